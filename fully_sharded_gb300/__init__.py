@@ -28,6 +28,9 @@ __all__ = [
     "fsdp_shard_step_grouped_plan", "fsdp_device_status", "fsdp_selftest_wait_timeout",
     "fsdp_offload_step", "OffloadUnit", "OffloadBatch", "fsdp_reduce_scatter_ranks",
     "fsdp_adam_shard_step_grouped", "AdamShard",
+    "fsdp_rmsnorm", "fsdp_rmsnorm_backward", "fsdp_rmsnorm_backward_workspace",
+    "NewtonSchulz", "NewtonSchulzBatch", "fsdp_newton_schulz", "fsdp_newton_schulz_workspace",
+    "Muon", "MuonTensor", "MuonUnit", "fsdp_muon_step", "fsdp_muon_workspace",
 ]
 
 FSDP_OK = 0
@@ -35,9 +38,11 @@ FSDP_EINVAL = -1
 FSDP_EALIAS = -2
 FSDP_ECUDA = -3
 FSDP_ENOSPACE = -4
+FSDP_EWORKSPACE = -5
 NOALLOC_STAGING_BYTES = 64 << 20  # FSDP_NOALLOC_STAGING_BYTES of include/fsdp.h
 FSDP_DTYPE_F32 = 0
 FSDP_DTYPE_BF16 = 1
+FSDP_DTYPE_E4M3 = 2
 MAX_WORLD = 64
 
 _c_i32, _c_i64, _c_dbl, _c_p = ctypes.c_int32, ctypes.c_int64, ctypes.c_double, ctypes.c_void_p
@@ -81,6 +86,64 @@ class OffloadUnit(ctypes.Structure):
 class AdamShard(ctypes.Structure):
     _fields_ = [("master", _c_p), ("exp_avg", _c_p), ("exp_avg_sq", _c_p), ("grad_shard", _c_p),
                 ("bf16_shard_out", _c_p), ("n", _c_i64)]
+
+
+class RmsNormArgs(ctypes.Structure):
+    _fields_ = [("rows", _c_i64), ("cols", _c_i64), ("x_stride", _c_i64), ("residual_stride", _c_i64),
+                ("h_stride", _c_i64), ("y_stride", _c_i64), ("dtype", _c_i32), ("gain_dtype", _c_i32),
+                ("y_dtype", _c_i32), ("group", _c_i32), ("eps", _c_dbl)]
+
+
+class RmsNormBackwardArgs(ctypes.Structure):
+    _fields_ = [("rows", _c_i64), ("cols", _c_i64), ("dy_stride", _c_i64), ("h_stride", _c_i64),
+                ("dh_stride", _c_i64), ("dx_stride", _c_i64), ("dtype", _c_i32), ("gain_dtype", _c_i32)]
+
+
+class NewtonSchulz(ctypes.Structure):
+    """Parameters of the orthogonalisation. `coefficients`: one (a, b, c) for every step, a list
+    of `steps` of them, or None for the default quintic; `terms`: 0, 1 or 3 (see include/fsdp.h)."""
+    _fields_ = [("steps", _c_i32), ("terms", _c_i32), ("coefficients", ctypes.POINTER(_c_dbl)), ("eps", _c_dbl)]
+
+    def __init__(self, steps=5, coefficients=None, eps=1e-7, terms=0):
+        super().__init__(steps, terms, None, eps)
+        if coefficients is not None:
+            per_step = [coefficients] * steps if not hasattr(coefficients[0], "__len__") else list(coefficients)
+            if len(per_step) != steps or any(len(abc) != 3 for abc in per_step):
+                raise ValueError("expected (a, b, c), or one (a, b, c) for each of %d steps" % steps)
+            self._values = (_c_dbl * max(1, 3 * steps))(*[v for abc in per_step for v in abc])
+            self.coefficients = ctypes.cast(self._values, ctypes.POINTER(_c_dbl))
+
+
+class MatrixArgs(ctypes.Structure):
+    _fields_ = [("source", _c_p), ("out", _c_p), ("rows", _c_i64), ("cols", _c_i64), ("source_stride", _c_i64),
+                ("out_stride", _c_i64), ("dtype", _c_i32)]
+
+
+class MuonTensor(ctypes.Structure):
+    """One tensor of a unit: a matrix (rows, cols) whose update is scaled by `scale`, or, with
+    cols = 0, a tensor of `rows` elements that Adam updates."""
+    _fields_ = [("rows", _c_i64), ("cols", _c_i64), ("scale", _c_dbl)]
+
+    def __init__(self, rows=0, cols=0, scale=1.0):
+        super().__init__(rows, cols, scale)
+
+
+class Muon(ctypes.Structure):
+    """Hyper-parameters of the Muon step; `adam` (an AdamHyper, with its own lr and step) serves
+    the tensors that are not matrices."""
+    _fields_ = [("lr", _c_dbl), ("momentum", _c_dbl), ("weight_decay", _c_dbl), ("nesterov", _c_i32),
+                ("newton_schulz", ctypes.POINTER(NewtonSchulz)), ("adam", AdamHyper)]
+
+    def __init__(self, lr=1e-3, momentum=0.95, weight_decay=0.0, nesterov=True, newton_schulz=None, adam=None):
+        super().__init__(lr, momentum, weight_decay, 1 if nesterov else 0, None, adam or AdamHyper())
+        if newton_schulz is not None:
+            self._newton_schulz = newton_schulz
+            self.newton_schulz = ctypes.pointer(newton_schulz)
+
+
+class MuonUnitArgs(ctypes.Structure):
+    _fields_ = [("layout", ctypes.POINTER(Layout)), ("tensors", ctypes.POINTER(MuonTensor)), ("grads", _c_p),
+                ("master", _c_p), ("exp_avg", _c_p), ("exp_avg_sq", _c_p), ("full_out", _c_p)]
 
 
 class ZeroAccount(ctypes.Structure):
@@ -148,6 +211,14 @@ def _load():
         "fsdp_selftest_wait_timeout": [P, P, _c_i64, _c_i64, P, ctypes.POINTER(ctypes.c_uint32)],
         "fsdp_offload_step": [ctypes.POINTER(OffloadUnit), _c_i32, _c_i32, P, _c_i64, _c_i32,
                               ctypes.POINTER(AdamHyper), P, P, P],
+        "fsdp_rmsnorm": [ctypes.POINTER(RmsNormArgs), P, P, P, P, P, P, P, P],
+        "fsdp_rmsnorm_backward": [ctypes.POINTER(RmsNormBackwardArgs), P, P, P, P, P, P, P, P, _c_i64, P],
+        "fsdp_rmsnorm_backward_workspace": [_c_i64, _c_i64, ctypes.POINTER(_c_i64)],
+        "fsdp_newton_schulz": [ctypes.POINTER(MatrixArgs), _c_i32, ctypes.POINTER(NewtonSchulz), P, _c_i64, P],
+        "fsdp_newton_schulz_workspace": [ctypes.POINTER(MatrixArgs), _c_i32, ctypes.POINTER(NewtonSchulz),
+                                         ctypes.POINTER(_c_i64)],
+        "fsdp_muon_step": [ctypes.POINTER(MuonUnitArgs), ctypes.POINTER(Muon), P, _c_i64, P],
+        "fsdp_muon_workspace": [ctypes.POINTER(MuonUnitArgs), ctypes.POINTER(Muon), ctypes.POINTER(_c_i64)],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -492,3 +563,186 @@ def fsdp_account(P: float, U: float, N: int, F: int | None = None, prefetch: int
     _check("fsdp_account", _lib.fsdp_account(float(P), float(U), N, N if F is None else F,
                                              prefetch, ctypes.byref(out)))
     return out.as_dict()
+
+
+# ------------------------------------------- operators of the training loop
+
+def _float_dtype(t, what: str) -> int:
+    import torch
+    if t.dtype == torch.float32:
+        return FSDP_DTYPE_F32
+    if t.dtype == torch.bfloat16:
+        return FSDP_DTYPE_BF16
+    raise ValueError("%s: expected float32 or bfloat16, got %s" % (what, t.dtype))
+
+
+def _matrix(t, what: str, rows: int, cols: int, dtype=None):
+    """(address, row stride) of a CUDA matrix of the given shape whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError("%s: expected a CUDA tensor, got one on %s" % (what, t.device))
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError("%s: expected shape (%d, %d), got %s" % (what, rows, cols, tuple(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s: expected %s, got %s" % (what, dtype, t.dtype))
+    row, col = t.stride()
+    if col != 1 and cols > 1:
+        raise ValueError("%s: expected contiguous rows" % what)
+    return t.data_ptr(), (row if rows > 1 else cols)
+
+
+def _vector(t, what: str, n: int, dtype=None):
+    if not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError("%s: expected a contiguous CUDA tensor of %d elements" % (what, n))
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("%s: expected %s, got %s" % (what, dtype, t.dtype))
+    return t.data_ptr()
+
+
+def _workspace(t):
+    if t is None:
+        return None, 0
+    return _dptr(t), t.numel() * t.element_size()
+
+
+def fsdp_rmsnorm(x, gain, y, residual=None, h_out=None, scales=None, rstd=None, group: int = 0, eps: float = 1e-6,
+                 stream=None):
+    """RMS norm of the rows of x (+ residual, the sum written to h_out) into y: y's type is x's,
+    or 8 bits (torch.float8_e4m3fn) with fp32 `scales` [rows, groups], one per `group` elements
+    (0: per row). rstd (fp32 [rows], optional) is what the backward pass needs."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x: expected a matrix, got shape %s" % (tuple(x.shape),))
+    rows, cols = x.shape
+    a = RmsNormArgs(rows=rows, cols=cols, dtype=_float_dtype(x, "x"), gain_dtype=_float_dtype(gain, "gain"),
+                    group=group, eps=eps)
+    xp, a.x_stride = _matrix(x, "x", rows, cols)
+    rp = hp = sp = None
+    if residual is not None:
+        rp, a.residual_stride = _matrix(residual, "residual", rows, cols, x.dtype)
+    if h_out is not None:
+        hp, a.h_stride = _matrix(h_out, "h_out", rows, cols, x.dtype)
+    if y.dtype == torch.float8_e4m3fn:
+        a.y_dtype = FSDP_DTYPE_E4M3
+        if scales is None:
+            raise ValueError("scales: needed for an 8-bit y")
+        sp = _vector(scales, "scales", rows * (-(-cols // group) if group > 0 else 1), torch.float32)
+    else:
+        a.y_dtype = a.dtype
+        if y.dtype != x.dtype:
+            raise ValueError("y: expected %s or torch.float8_e4m3fn, got %s" % (x.dtype, y.dtype))
+        if scales is not None:
+            raise ValueError("scales: only for an 8-bit y")
+    yp, a.y_stride = _matrix(y, "y", rows, cols)
+    dp = _vector(rstd, "rstd", rows, torch.float32) if rstd is not None else None
+    _check("fsdp_rmsnorm", _lib.fsdp_rmsnorm(ctypes.byref(a), xp, rp, _vector(gain, "gain", cols), hp, yp, sp, dp,
+                                             _stream(stream)))
+
+
+def fsdp_rmsnorm_backward_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace that fsdp_rmsnorm_backward needs (host only)."""
+    n = _c_i64(0)
+    _check("fsdp_rmsnorm_backward_workspace", _lib.fsdp_rmsnorm_backward_workspace(rows, cols, ctypes.byref(n)))
+    return n.value
+
+
+def fsdp_rmsnorm_backward(dy, h, gain, rstd, dx, dgain, workspace, dh=None, stream=None):
+    """Gradients of fsdp_rmsnorm: dx (of x, and of the residual) from dy, the forward's h and rstd,
+    and dh, the gradient that reaches h by the residual path; dgain in gain's type, summed over the rows
+    (it may be a view into a rank's gradient row)."""
+    import torch
+    if h.dim() != 2:
+        raise ValueError("h: expected a matrix, got shape %s" % (tuple(h.shape),))
+    rows, cols = h.shape
+    a = RmsNormBackwardArgs(rows=rows, cols=cols, dtype=_float_dtype(h, "h"), gain_dtype=_float_dtype(gain, "gain"))
+    hp, a.h_stride = _matrix(h, "h", rows, cols)
+    yp, a.dy_stride = _matrix(dy, "dy", rows, cols, h.dtype)
+    xp, a.dx_stride = _matrix(dx, "dx", rows, cols, h.dtype)
+    dhp = None
+    if dh is not None:
+        dhp, a.dh_stride = _matrix(dh, "dh", rows, cols, h.dtype)
+    ws, ws_bytes = _workspace(workspace)
+    _check("fsdp_rmsnorm_backward", _lib.fsdp_rmsnorm_backward(
+        ctypes.byref(a), yp, hp, _vector(gain, "gain", cols), _vector(rstd, "rstd", rows, torch.float32), dhp, xp,
+        _vector(dgain, "dgain", cols, gain.dtype), ws, ws_bytes, _stream(stream)))
+
+
+class NewtonSchulzBatch:
+    """Marshalled matrices for fsdp_newton_schulz: `sources` (float32 or bfloat16) and their bf16
+    results `outs`, kept alive together."""
+
+    def __init__(self, sources, outs):
+        import torch
+        if len(sources) != len(outs):
+            raise ValueError("expected one out for each of %d sources, got %d" % (len(sources), len(outs)))
+        self._keep = (list(sources), list(outs))
+        self.n = len(sources)
+        self.array = (MatrixArgs * max(1, self.n))()
+        for a, source, out in zip(self.array, sources, outs):
+            if source.dim() != 2:
+                raise ValueError("source: expected a matrix, got shape %s" % (tuple(source.shape),))
+            a.rows, a.cols = source.shape
+            a.dtype = _float_dtype(source, "source")
+            a.source, a.source_stride = _matrix(source, "source", a.rows, a.cols)
+            a.out, a.out_stride = _matrix(out, "out", a.rows, a.cols, torch.bfloat16)
+
+
+def _byref_or_none(x):
+    return ctypes.byref(x) if x is not None else None
+
+
+def fsdp_newton_schulz_workspace(batch: NewtonSchulzBatch, newton_schulz: NewtonSchulz | None = None) -> int:
+    """Bytes of workspace that fsdp_newton_schulz needs for these matrices (host only)."""
+    n = _c_i64(0)
+    _check("fsdp_newton_schulz_workspace", _lib.fsdp_newton_schulz_workspace(
+        batch.array, batch.n, _byref_or_none(newton_schulz), ctypes.byref(n)))
+    return n.value
+
+
+def fsdp_newton_schulz(batch: NewtonSchulzBatch, workspace, newton_schulz: NewtonSchulz | None = None, stream=None):
+    """Orthogonalises every matrix of the batch into its out by Newton-Schulz products."""
+    ws, ws_bytes = _workspace(workspace)
+    _check("fsdp_newton_schulz", _lib.fsdp_newton_schulz(batch.array, batch.n, _byref_or_none(newton_schulz), ws,
+                                                         ws_bytes, _stream(stream)))
+
+
+class MuonUnit:
+    """Marshalled arguments of one unit for fsdp_muon_step: its tensors in flat order
+    (MuonTensor each), the W bf16 gradient rows, the W fp32 shards of the state, the
+    gathered bf16 parameters. Kept alive together."""
+
+    def __init__(self, layout: Layout, tensors, grads, master, exp_avg, exp_avg_sq, full_out):
+        if len(tensors) != layout.n_tensors:
+            raise ValueError("expected %d tensors, got %d" % (layout.n_tensors, len(tensors)))
+        world, padded, shard = layout.world_size, layout.padded_numel, layout.shard_numel
+        for what, xs, n in (("grads", grads, padded), ("master", master, shard), ("exp_avg", exp_avg, shard),
+                            ("exp_avg_sq", exp_avg_sq, shard), ("full_out", [full_out] * world, padded)):
+            if len(xs) != world:
+                raise ValueError("%s: expected one per rank (%d), got %d" % (what, world, len(xs)))
+            for x in xs:
+                if x is not None and not isinstance(x, int) and x.numel() != n:
+                    raise ValueError("%s: expected %d elements, got %d" % (what, n, x.numel()))
+        self._tensors = (MuonTensor * max(1, len(tensors)))(*tensors)
+        arrays = dict(grads=_parray(grads, 2), master=_parray(master, 4), exp_avg=_parray(exp_avg, 4),
+                      exp_avg_sq=_parray(exp_avg_sq, 4))
+        self._keep = (layout, list(grads), list(master), list(exp_avg), list(exp_avg_sq), full_out, arrays)
+        self.args = MuonUnitArgs(layout=ctypes.pointer(layout),
+                                 tensors=ctypes.cast(self._tensors, ctypes.POINTER(MuonTensor)),
+                                 full_out=_dptr(full_out, 2))
+        for k, v in arrays.items():
+            setattr(self.args, k, ctypes.cast(v, _c_p))
+
+
+def fsdp_muon_workspace(unit: MuonUnit, muon: Muon | None = None) -> int:
+    """Bytes of workspace that fsdp_muon_step needs for this unit (host only)."""
+    n = _c_i64(0)
+    _check("fsdp_muon_workspace", _lib.fsdp_muon_workspace(ctypes.byref(unit.args), ctypes.byref(muon or Muon()),
+                                                           ctypes.byref(n)))
+    return n.value
+
+
+def fsdp_muon_step(unit: MuonUnit, muon: Muon, workspace, stream=None):
+    """The Muon step of one unit on all its ranks: reduce-scatter and momentum, every matrix's update
+    orthogonalised and applied, the other tensors by Adam, the bf16 cast and the gather."""
+    ws, ws_bytes = _workspace(workspace)
+    _check("fsdp_muon_step", _lib.fsdp_muon_step(ctypes.byref(unit.args), ctypes.byref(muon), ws, ws_bytes,
+                                                 _stream(stream)))

@@ -101,6 +101,7 @@ extern "C" const char* fsdp_status_string(int status) {
     case FSDP_EALIAS: return "an output overlaps an input or another output";
     case FSDP_ECUDA: return "CUDA launch error";
     case FSDP_ENOSPACE: return enospace_text();
+    case FSDP_EWORKSPACE: return "the workspace is smaller than the call needs";
     default: return "unknown status";
   }
 }

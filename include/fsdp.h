@@ -80,6 +80,7 @@ typedef struct CUstream_st *fsdp_stream_t;
 #define FSDP_ECUDA (-3)  /* a CUDA call or launch failed (cudaGetLastError) */
 #define FSDP_ENOSPACE (-4) /* the work does not fit the fixed staging capacity of
                               fsdp_pipeline_step_noalloc */
+#define FSDP_EWORKSPACE (-5) /* the given workspace is smaller than the call needs */
 
 #define FSDP_MAX_WORLD 64
 
@@ -508,6 +509,165 @@ typedef struct {
 
 int fsdp_account(double P, double U, int32_t N, int32_t F, int32_t prefetch,
                  fsdp_account_t *out);
+
+/* ------------------------------------------------------------------------
+ * Operators of the training loop around the step.
+ *
+ * A unit's tensors are matrices (projections) and vectors (norm gains,
+ * biases). The calls below are the norm that the gains belong to, forward and
+ * backward, and an optimizer for the matrices: the Muon step, which
+ * orthogonalises every matrix's update. (The FSDP pages have no counterpart.)
+ *
+ * Matrices are row-major with a row stride in elements (>= the row's length;
+ * any value for a single row). A workspace is device memory of the caller, of
+ * any alignment, at least as large as the call's ..._workspace function says
+ * for the same arguments; it holds nothing between calls, and calls whose
+ * work overlaps on the GPU need workspaces of their own. */
+
+#define FSDP_DTYPE_E4M3 2 /* 1-byte elements (8-bit floats: 4 exponent, 3 mantissa bits) */
+
+/* RMS norm of each row, with the residual's addition:
+ *   h = x + residual                  (h = x without a residual)
+ *   rstd = 1 / sqrt(mean_j h_j^2 + eps)
+ *   y_j = h_j rstd gain_j
+ * x, residual and h_out have type `dtype` (F32 or BF16), gain has gain_dtype,
+ * y has y_dtype: `dtype`'s own, or E4M3 with scales. All sums are fp32, and
+ * y comes from the unrounded h. residual and h_out are both null or both given;
+ * rstd (fp32 [rows]) may be null.
+ * E4M3: each row is cut into groups of `group` consecutive elements (32, 64, 128
+ * or 256; 0: the whole row; the last group may be short), and
+ *   scale = max(max|y| / 448, 2^-126),   y_out = round(y / scale)
+ * to the nearest even e4m3 value; scales is fp32 [rows][ceil(cols / group)],
+ * contiguous. Other y types: scales null and group 0. A row with an infinity or a NaN
+ * gives what the formulas give.
+ * In place: h_out may be x or residual, and y may be x (same address, stride
+ * and type), as long as the outputs are distinct; column slices of one
+ * buffer (equal strides, disjoint columns) may be mixed freely.
+ * rows = 0 launches nothing. EINVAL: cols < 1 or > 2^30, rows < 0, a stride below cols, a
+ * type, group or eps (finite, > 0) outside the above, a missing pointer, one not
+ * aligned to its elements. EALIAS: other overlaps. */
+typedef struct {
+  int64_t rows;
+  int64_t cols;
+  int64_t x_stride;
+  int64_t residual_stride;
+  int64_t h_stride;
+  int64_t y_stride;
+  int32_t dtype;
+  int32_t gain_dtype;
+  int32_t y_dtype;
+  int32_t group;
+  double eps;
+} fsdp_rmsnorm_t;
+
+int fsdp_rmsnorm(const fsdp_rmsnorm_t *args, const void *x, const void *residual, const void *gain, void *h_out,
+                 void *y, float *scales, float *rstd, fsdp_stream_t stream);
+
+/* Gradients of fsdp_rmsnorm. dy: gradient of y; h, rstd: the forward's (h is x
+ * where it had no residual); dh: gradient that reaches h by the residual path
+ * (null: none). With u_j = dy_j gain_j and n_j = h_j rstd:
+ *   dx_j = rstd (u_j - n_j mean_i(u_i n_i)) + dh_j   (also the residual's gradient)
+ *   dgain_j = sum over the rows of dy_j n_j
+ * dy, h, dh and dx have type `dtype`, gain and dgain gain_dtype. Sums are fp32
+ * in an order fixed by the sizes; each output is rounded once. dgain may lie
+ * anywhere in a rank's bf16 gradient row (2-byte alignment). dx may be dy or dh in place.
+ * rows = 0 sets dgain to zero. EINVAL and EALIAS as above. */
+typedef struct {
+  int64_t rows;
+  int64_t cols;
+  int64_t dy_stride;
+  int64_t h_stride;
+  int64_t dh_stride;
+  int64_t dx_stride;
+  int32_t dtype;
+  int32_t gain_dtype;
+} fsdp_rmsnorm_backward_t;
+
+int fsdp_rmsnorm_backward(const fsdp_rmsnorm_backward_t *args, const void *dy, const void *h, const void *gain,
+                          const float *rstd, const void *dh, void *dx, void *dgain, void *workspace,
+                          int64_t workspace_bytes, fsdp_stream_t stream);
+int fsdp_rmsnorm_backward_workspace(int64_t rows, int64_t cols, int64_t *bytes_out);
+
+/* Newton-Schulz orthogonalisation of matrices (Higham, "Functions of Matrices",
+ * 2008, chapter 8, gives the iteration family; the default quintic is the one
+ * that the Muon optimizer made common): with X_0 = G / (|G|_F + eps), each step
+ * with its a, b, c
+ *   A = X X^T,   X <- a X + (b A + c A^2) X
+ * (for a matrix with more rows than columns, of its transpose). The result has
+ * G's singular vectors and singular values near 1; a zero matrix stays zero.
+ * terms: how the products take their operands. 1: rounded to 11 bits (fp16,
+ * scaled by powers of two; the error is 0.1 to 0.3 % of the result's
+ * norm); 3: as two such parts each, three products (about 1e-5); 0: 3 where the
+ * short side is below 256 and 1 otherwise. Between steps X is held as two fp16
+ * parts, 22 bits; accumulation is fp32. */
+typedef struct {
+  int32_t steps;              /* 1 .. 32 */
+  int32_t terms;              /* 0, 1 or 3 */
+  const double *coefficients; /* host: a, b, c of each step (3 * steps values); null: 3.4445,
+                                 -4.7750, 2.0315 for every step */
+  double eps;                 /* finite, > 0 */
+} fsdp_newton_schulz_t;
+
+typedef struct {
+  const void *source; /* rows x cols, type dtype */
+  uint16_t *out;      /* rows x cols, bf16; may be source itself (same address, stride, BF16) */
+  int64_t rows;
+  int64_t cols;
+  int64_t source_stride;
+  int64_t out_stride;
+  int32_t dtype; /* F32 or BF16 */
+} fsdp_matrix_t;
+
+/* Orthogonalises n matrices (host array), together in each launch. Empty
+ * matrices are skipped. newton_schulz null: 5 steps, terms 0, eps 1e-7.
+ * EINVAL: also coefficients whose iterates leave [-7, 7] or whose b s + c s^2
+ * leaves [-60, 60] for some singular value in [0, 1] (the fp16 ranges); a side beyond
+ * 2^30. EALIAS: an out that overlaps another out or a source but its own. */
+int fsdp_newton_schulz(const fsdp_matrix_t *matrices, int32_t n, const fsdp_newton_schulz_t *newton_schulz,
+                       void *workspace, int64_t workspace_bytes, fsdp_stream_t stream);
+int fsdp_newton_schulz_workspace(const fsdp_matrix_t *matrices, int32_t n, const fsdp_newton_schulz_t *newton_schulz,
+                                 int64_t *bytes_out);
+
+/* The Muon step of one unit, all W ranks (F = W): as fsdp_shard_step, with the
+ * unit's matrices updated by
+ *   g = fold of the W gradients / W                        (a3)
+ *   m = momentum m + g                                     (exp_avg, in place)
+ *   u = g + momentum m  (nesterov)  or  m
+ *   p = p (1 - lr weight_decay) - lr scale O               (O: u orthogonalised)
+ * and its other tensors (and the padding) by Adam, then cast and gathered into
+ * full_out. A matrix's exp_avg_sq is left alone. `tensors` lists the unit's
+ * tensors in flat order: layout->n_tensors entries whose sizes add up to
+ * layout->numel. g, m, p are fp32 as in the step; O's precision is that of
+ * fsdp_newton_schulz. EINVAL: F != W, sizes that do not add up, non-finite
+ * hyper-parameters, momentum outside [0, 1). EALIAS, EWORKSPACE as above. */
+typedef struct {
+  int64_t rows; /* matrix: rows x cols; other tensor: rows elements, cols = 0 */
+  int64_t cols;
+  double scale; /* matrix: factor of its update */
+} fsdp_muon_tensor_t;
+
+typedef struct {
+  double lr;
+  double momentum;
+  double weight_decay;
+  int32_t nesterov;
+  const fsdp_newton_schulz_t *newton_schulz; /* null: the defaults */
+  fsdp_adam_t adam;                          /* for the other tensors; its own lr and step */
+} fsdp_muon_t;
+
+typedef struct {
+  const fsdp_layout_t *layout;
+  const fsdp_muon_tensor_t *tensors;
+  const uint16_t *const *grads; /* W device rows of padded_numel bf16 */
+  float *const *master;         /* W device shards of S fp32, in place */
+  float *const *exp_avg;
+  float *const *exp_avg_sq;
+  uint16_t *full_out; /* device bf16 [padded_numel] */
+} fsdp_muon_unit_t;
+
+int fsdp_muon_step(const fsdp_muon_unit_t *unit, const fsdp_muon_t *muon, void *workspace, int64_t workspace_bytes,
+                   fsdp_stream_t stream);
+int fsdp_muon_workspace(const fsdp_muon_unit_t *unit, const fsdp_muon_t *muon, int64_t *bytes_out);
 
 /* Text of a status code (static storage). */
 const char *fsdp_status_string(int status);
