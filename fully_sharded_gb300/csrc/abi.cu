@@ -655,6 +655,25 @@ extern "C" int fsdp_shard_step_grouped_plan(const fsdp_unit_args_t* units, int32
   return rc;
 }
 
+namespace fsdp {
+
+int device_status_word(unsigned int** out) {
+  static std::atomic<unsigned int*> cached[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return FSDP_ECUDA;
+  unsigned int* p = cached[dev].load(std::memory_order_acquire);
+  if (!p) {
+    void* addr = nullptr;
+    if (cudaGetSymbolAddress(&addr, g_fsdp_status) != cudaSuccess || !addr) return FSDP_ECUDA;
+    p = static_cast<unsigned int*>(addr);
+    cached[dev].store(p, std::memory_order_release);
+  }
+  *out = p;
+  return FSDP_OK;
+}
+
+}  // namespace fsdp
+
 extern "C" int fsdp_device_status(int32_t clear, uint32_t* status_out) {
   if (!status_out) return FSDP_EINVAL;
   // the symbol copy runs on the legacy default stream, which does not wait for

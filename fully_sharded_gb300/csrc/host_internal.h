@@ -163,6 +163,10 @@ struct EventSet {
 int launch(const SegmentList& list, const Scalars& s, cudaStream_t stream, int* count = nullptr,
            int* tma_count = nullptr, int* interleaved_count = nullptr);
 
+// Address of the current device's status word (see fsdp_device_status), for
+// kernels of other translation units. Looked up once per device.
+int device_status_word(unsigned int** out);
+
 // Layout consistent with its own definition (padding, shard length, W, F).
 bool layout_ok(const fsdp_layout_t* L);
 

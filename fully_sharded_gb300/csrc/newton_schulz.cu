@@ -2,9 +2,29 @@
 // fsdp_muon_step).
 //
 // X_0 = G / (|G|_F + eps); per step, with the Gram matrix on the short side,
-//   A = X X^T,  X <- a X + (b A + c A^2) X.
+//   A = X X^T,  P = b A + c A^2,  X <- a X + P X
+// (X^T X and X P for a matrix with more rows than columns: no transposes, the
+// tensor cores take operands whose long index is the contiguous one).
+//
+// Representation. The products run on fp16 operands with fp32 accumulation, at
+// the rate of bf16 and with 11 instead of 8 bits; powers of two keep the values in
+// fp16's range: X is held times 2^12, A and P times 2^10 (X's singular values
+// stay below 7 and P's below 60, which ns_plan() checks). X itself is held as two
+// fp16 parts, hi + lo, 22 bits: only the products see it rounded. A rounding of X
+// would put noise into the directions that X lacks, and each step multiplies
+// those by a = 3.4 (measured on matrices of low rank: 3 % of the result's
+// norm, 0.06 % with the two parts); the operands' rounding stays inside X's row or
+// column space. With terms = 3 every operand has both parts: hi hi + lo hi + hi lo.
+//
+// Each of the three products is one launch over all matrices of the call: a
+// persistent grid of 128 x kN tiles, one producer lane (TMA), one product lane
+// (tcgen05, two accumulators in tensor memory) and four epilogue warps per
+// block. A and P are symmetric: tiles above the diagonal are not computed, and
+// the others are written to both places.
+#include "host_internal.h"
 #include "newton_schulz.h"
 #include "strided.h"
+#include "tensor_core.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -12,112 +32,667 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <new>
 #include <vector>
 
 namespace fsdp {
 namespace {
 
-constexpr int kSumBlocks = 64;
+using namespace tc;
 
-__device__ __forceinline__ float load_source(const void* p, int32_t dtype, int64_t i) {
-  return dtype == FSDP_DTYPE_F32 ? static_cast<const float*>(p)[i]
-                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+constexpr float kScaleX = 4096.0f, kScaleA = 1024.0f;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+constexpr int kMaxMats = 32;                      // matrices of one launch (24 KB of parameters)
+
+// ------------------------------------------------- norm and first operands
+
+constexpr int kUnitCols = 1024;  // a warp's share of a row
+constexpr int kPassWarps = 8;
+constexpr int kMaxParts = 304;
+
+struct PassMat {
+  const void* source;
+  int64_t stride, rows, cols;
+  __half *hi, *lo;
+  int64_t ld;
+  float* partial;
+  int32_t dtype;
+  int32_t parts;      // blocks (and partial sums) of this matrix
+  int32_t block_end;  // running total of parts
+};
+
+struct PassParams {
+  PassMat mat[kMaxMats];
+  int32_t count;
+  float eps;
+};
+
+__device__ __forceinline__ float load_source(const PassMat& j, int64_t i) {
+  return j.dtype == FSDP_DTYPE_F32 ? static_cast<const float*>(j.source)[i]
+                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(j.source)[i]);
 }
 
-// Sum of squares of a matrix, one partial sum per block.
-__global__ void __launch_bounds__(256) ns_squares(const NsJob j, float* partial) {
-  __shared__ double shared[8];
-  double sum = 0.0;
-  for (int64_t r = blockIdx.x; r < j.rows; r += gridDim.x) {
-    float s = 0.0f;
-    for (int64_t c = threadIdx.x; c < j.cols; c += 256) {
-      const float v = load_source(j.source, j.dtype, r * j.source_stride + c);
-      s += v * v;
-    }
-    sum += s;
+__device__ __forceinline__ const PassMat& pass_mat(const PassParams& p, int* part) {
+  int i = 0, first = 0;
+  while (static_cast<int>(blockIdx.x) >= p.mat[i].block_end) first = p.mat[i++].block_end;
+  *part = blockIdx.x - first;
+  return p.mat[i];
+}
+
+__device__ __forceinline__ double warp_sum(double v) {
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Calls f(row, column) for this lane's elements of its block's units.
+template <typename F>
+__device__ __forceinline__ void each_element(const PassMat& j, int part, F f) {
+  const int64_t segs = (j.cols + kUnitCols - 1) / kUnitCols, units = j.rows * segs;
+  const int lane = threadIdx.x % 32;
+  for (int64_t u = static_cast<int64_t>(part) * kPassWarps + threadIdx.x / 32; u < units;
+       u += static_cast<int64_t>(j.parts) * kPassWarps) {
+    const int64_t r = u / segs, c0 = (u - r * segs) * kUnitCols, end = min(j.cols, c0 + kUnitCols);
+    for (int64_t c = c0 + lane; c < end; c += 32) f(r, c);
   }
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+}
+
+// Sums of squares, one per block: fp32 over a lane's elements of a unit, then fp64.
+__global__ void __launch_bounds__(32 * kPassWarps) ns_squares(const __grid_constant__ PassParams p) {
+  __shared__ double shared[kPassWarps];
+  int part;
+  const PassMat& j = pass_mat(p, &part);
+  double sum = 0.0;
+  float s = 0.0f;
+  int64_t row = -1;
+  each_element(j, part, [&](int64_t r, int64_t c) {
+    if (r != row) {
+      sum += s;
+      s = 0.0f;
+      row = r;
+    }
+    const float v = load_source(j, r * j.stride + c);
+    s += v * v;
+  });
+  sum = warp_sum(sum + s);
   if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < 8; ++i) sum += shared[i];
-    partial[blockIdx.x] = static_cast<float>(sum);
+    for (int i = 1; i < kPassWarps; ++i) sum += shared[i];
+    j.partial[part] = static_cast<float>(sum);
   }
 }
 
-__global__ void __launch_bounds__(256) ns_normalise(const NsJob j, const float* partial, float eps, float* x) {
-  double sum = 0.0;
-  for (int i = 0; i < kSumBlocks; ++i) sum += partial[i];
-  const float inv = static_cast<float>(1.0 / (sqrt(sum) + eps));
-  for (int64_t r = blockIdx.x; r < j.rows; r += gridDim.x)
-    for (int64_t c = threadIdx.x; c < j.cols; c += 256)
-      x[r * j.cols + c] = load_source(j.source, j.dtype, r * j.source_stride + c) * inv;
+__device__ __forceinline__ void split(float v, __half* hi, __half* lo) {
+  *hi = __float2half_rn(v);
+  *lo = __float2half_rn(v - __half2float(*hi));
 }
 
-// C = alpha A B + beta D with any strides; 64 x 64 tiles, 4 x 4 per thread.
-struct Product {
-  const float *a, *b, *d;
-  float* c;
-  int64_t m, n, k;
-  int64_t a_row, a_k, b_k, b_col, c_row;  // element strides (C and D: row stride, unit column stride)
-  float alpha, beta;
+// X_0 as two parts.
+__global__ void __launch_bounds__(32 * kPassWarps) ns_normalise(const __grid_constant__ PassParams p) {
+  int part;
+  const PassMat& j = pass_mat(p, &part);
+  double sum = 0.0;
+  for (int i = threadIdx.x % 32; i < j.parts; i += 32) sum += j.partial[i];
+  sum = warp_sum(sum);
+  const float inv = static_cast<float>(1.0 / (sqrt(sum) + p.eps));
+  each_element(j, part, [&](int64_t r, int64_t c) {
+    __half hi, lo;
+    split(load_source(j, r * j.stride + c) * inv * kScaleX, &hi, &lo);
+    j.hi[r * j.ld + c] = hi;
+    j.lo[r * j.ld + c] = lo;
+  });
+}
+
+// ----------------------------------------------------------------- products
+
+enum Kind : int32_t { kGram, kPoly, kUpdate };             // A = X X^T; P = b A + c A A; X <- a X + P X
+enum Result : int32_t { kParts, kOut, kApply };            // hi/lo parts; bf16 out; the master's update
+
+// C[m, n] = alpha sum_k p[i, k] q[j, k] + beta in[i, j].
+struct GemmMat {
+  CUtensorMap p[2], q[2];  // boxes of 64 x 64 elements of the operands' hi and lo parts
+  __half *hi, *lo;
+  const __half *in_hi, *in_lo;
+  int64_t ld;              // of the result and of `in`: a multiple of 64
+  int32_t m, n, k;
+  int32_t col_tiles, tiles;
+  uint8_t p_mn, q_mn;      // the operand's row index (of C's rows, columns) is the contiguous one
+  uint8_t symmetric;
+  uint16_t* out;
+  int64_t out_stride;
+  int64_t flat;
+  float step;
 };
 
-__global__ void __launch_bounds__(256) ns_product(const Product p) {
-  __shared__ float sa[16][65], sb[16][65];
-  const int64_t i0 = static_cast<int64_t>(blockIdx.y) * 64, j0 = static_cast<int64_t>(blockIdx.x) * 64;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < p.k; k0 += 16) {
-    for (int e = threadIdx.x; e < 64 * 16; e += 256) {
-      const int kk = e % 16, ii = e / 16;
-      const int64_t k = k0 + kk;
-      sa[kk][ii] = (k < p.k && i0 + ii < p.m) ? p.a[(i0 + ii) * p.a_row + k * p.a_k] : 0.0f;
-      sb[kk][ii] = (k < p.k && j0 + ii < p.n) ? p.b[k * p.b_k + (j0 + ii) * p.b_col] : 0.0f;
+template <int kMats>
+struct GemmParams {
+  GemmMat mat[kMats];
+  NsApply apply;
+  int32_t count, tiles, terms;
+  int32_t kind, result;
+  float alpha, beta;
+  unsigned int* status;
+};
+static_assert(sizeof(GemmParams<kMaxMats>) <= 32764, "kernel parameter block too large");
+
+constexpr int kTileM = 128, kTileK = 64;
+constexpr int kGemmThreads = 256;  // producer, product, two idle and four epilogue warps
+
+template <int kN>
+struct Tile {
+  static constexpr int kABytes = kTileM * kTileK * 2, kBBytes = kN * kTileK * 2;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = 196608 / kStageBytes;  // 192 KB of operands in flight
+  static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+  static constexpr int kTmemCols = 2 * kN;
+};
+
+// Tile t of a launch: its matrix and place. Calls come with growing t.
+template <int kN, typename P>
+struct Tiles {
+  const P& p;
+  int mat = 0, first = 0;
+  int row = 0, base = 0;  // symmetric: the current row of tiles and its first tile
+
+  __device__ __forceinline__ const GemmMat& at(int t, int* i, int* j) {
+    while (t - first >= p.mat[mat].tiles) {
+      first += p.mat[mat++].tiles;
+      row = base = 0;
     }
-    __syncthreads();
-    for (int kk = 0; kk < 16; ++kk)
-      for (int r = 0; r < 4; ++r)
-        for (int c = 0; c < 4; ++c) acc[r][c] += sa[kk][ty * 4 + r] * sb[kk][tx * 4 + c];
-    __syncthreads();
+    const GemmMat& g = p.mat[mat];
+    const int l = t - first;
+    if (!g.symmetric) {
+      *i = l / g.col_tiles;
+      *j = l - *i * g.col_tiles;
+      return g;
+    }
+    // row i holds the tiles with an element on or below the diagonal
+    constexpr int kRatio = kN / kTileM;
+    while (l - base > row / kRatio) base += row++ / kRatio + 1;
+    *i = row;
+    *j = l - base;
+    return g;
   }
-  for (int r = 0; r < 4; ++r)
-    for (int c = 0; c < 4; ++c) {
-      const int64_t i = i0 + ty * 4 + r, j = j0 + tx * 4 + c;
-      if (i >= p.m || j >= p.n) continue;
-      float v = p.alpha * acc[r][c];
-      if (p.d) v += p.beta * p.d[i * p.c_row + j];
-      p.c[i * p.c_row + j] = v;
-    }
-}
+};
 
-int product(const Product& p, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>((p.n + 63) / 64), static_cast<unsigned>((p.m + 63) / 64));
-  ns_product<<<grid, 256, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FSDP_OK : FSDP_ECUDA;
-}
-
-__global__ void __launch_bounds__(256) ns_output(const NsJob j, const float* x, const __grid_constant__ NsApply ap,
-                                                 bool apply) {
-  for (int64_t r = blockIdx.x; r < j.rows; r += gridDim.x)
-    for (int64_t c = threadIdx.x; c < j.cols; c += 256) {
-      const float o = x[r * j.cols + c];
-      if (!apply) {
-        j.out[r * j.out_stride + c] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
-        continue;
+// The thread's 32 results (row, col0 ..) as bf16, or applied to the master.
+__device__ __forceinline__ void finish(const GemmMat& g, const NsApply& ap, int32_t result, int64_t row, int col0,
+                                       const float (&v)[32]) {
+  const bool whole = col0 + 32 <= g.n;
+  if (result == kOut) {
+    uint16_t* o = g.out + row * g.out_stride + col0;
+    if (whole && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t r[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
+          r[e] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        reinterpret_cast<uint4*>(o)[q] = make_uint4(r[0], r[1], r[2], r[3]);
       }
-      const int64_t f = j.flat + r * j.cols + c;
-      float* master = ap.master[f / ap.shard] + f % ap.shard;
-      const float v = *master * ap.keep - j.step * o;
-      *master = v;
-      ap.full[f] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+      return;
     }
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (col0 + c < g.n) o[c] = __bfloat16_as_ushort(__float2bfloat16_rn(v[c]));
+    return;
+  }
+  const int64_t f = g.flat + row * g.n + col0;
+  int64_t rank = f / ap.shard, at = f - rank * ap.shard;
+  float* master = ap.master[rank] + at;
+  uint16_t* full = ap.full + f;
+  if (whole && at + 32 <= ap.shard &&
+      ((reinterpret_cast<uintptr_t>(master) | reinterpret_cast<uintptr_t>(full)) & 15u) == 0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float4 a = reinterpret_cast<float4*>(master)[2 * q], b = reinterpret_cast<float4*>(master)[2 * q + 1];
+      a.x = a.x * ap.keep - g.step * v[8 * q], a.y = a.y * ap.keep - g.step * v[8 * q + 1];
+      a.z = a.z * ap.keep - g.step * v[8 * q + 2], a.w = a.w * ap.keep - g.step * v[8 * q + 3];
+      b.x = b.x * ap.keep - g.step * v[8 * q + 4], b.y = b.y * ap.keep - g.step * v[8 * q + 5];
+      b.z = b.z * ap.keep - g.step * v[8 * q + 6], b.w = b.w * ap.keep - g.step * v[8 * q + 7];
+      reinterpret_cast<float4*>(master)[2 * q] = a;
+      reinterpret_cast<float4*>(master)[2 * q + 1] = b;
+      const __nv_bfloat162 c0 = __floats2bfloat162_rn(a.x, a.y), c1 = __floats2bfloat162_rn(a.z, a.w),
+                           c2 = __floats2bfloat162_rn(b.x, b.y), c3 = __floats2bfloat162_rn(b.z, b.w);
+      reinterpret_cast<uint4*>(full)[q] =
+          make_uint4(*reinterpret_cast<const uint32_t*>(&c0), *reinterpret_cast<const uint32_t*>(&c1),
+                     *reinterpret_cast<const uint32_t*>(&c2), *reinterpret_cast<const uint32_t*>(&c3));
+    }
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    if (col0 + c >= g.n) break;
+    if (at == ap.shard) {
+      at = 0;
+      master = ap.master[++rank];
+    }
+    const float w = *master * ap.keep - g.step * v[c];
+    *master++ = w;
+    ++at;
+    full[c] = __bfloat16_as_ushort(__float2bfloat16_rn(w));
+  }
 }
 
-int64_t matrix_floats(const NsJob& j) {
-  const int64_t k = std::min(j.rows, j.cols);
-  return 2 * j.rows * j.cols + 2 * k * k + kSumBlocks;
+// Stores 32 fp16 values of a row, and their mirror image when `mirror`: pairs of
+// lanes exchange halves so that each 4-byte store holds two rows of one column.
+__device__ __forceinline__ void store_part(__half* base, int64_t ld, int row, int col0, bool in_rows, bool mirror,
+                                           int m, int n, const uint32_t (&r)[16]) {
+  if (in_rows) {
+    __half* o = base + row * ld + col0;
+    store16(o, {r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7]});
+    store16(o + 16, {r[8], r[9], r[10], r[11], r[12], r[13], r[14], r[15]});
+  }
+  if (!mirror) return;
+  const bool odd = threadIdx.x & 1;
+  const int pair = row & ~1;
+#pragma unroll
+  for (int c = 0; c < 16; ++c) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, r[c], 1);
+    const uint32_t two = odd ? __byte_perm(r[c], other, 0x3276) : __byte_perm(r[c], other, 0x5410);
+    const int col = col0 + 2 * c + (odd ? 1 : 0);
+    if (col < n && pair < m) *reinterpret_cast<uint32_t*>(base + col * ld + pair) = two;
+  }
+}
+
+template <int kN, int kMats>
+__global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_constant__ GemmParams<kMats> p) {
+  using T = Tile<kN>;
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t full_bar[T::kStages], empty_bar[T::kStages], done_bar[2], free_bar[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int stop;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
+  const Guard guard{&stop, p.status, kWaitLimitNs};
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < T::kStages; ++s) {
+      bar_init(smem_addr(&full_bar[s]), 1);
+      bar_init(smem_addr(&empty_bar[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      bar_init(smem_addr(&done_bar[b]), 1);
+      bar_init(smem_addr(&free_bar[b]), 4);
+    }
+    stop = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), T::kTmemCols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  if (warp == 0 && lane == 0) {  // producer
+    Tiles<kN, GemmParams<kMats>> tiles{p};
+    uint32_t it = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
+      int i, j;
+      const GemmMat& g = tiles.at(t, &i, &j);
+      const int blocks = (g.k + kTileK - 1) / kTileK;
+      for (int term = 0; ok && term < p.terms; ++term) {
+        const CUtensorMap* mp = &g.p[term == 1 ? 1 : 0];
+        const CUtensorMap* mq = &g.q[term == 2 ? 1 : 0];
+        for (int kb = 0; kb < blocks; ++kb, ++it) {
+          const int s = it % T::kStages;
+          ok = bar_wait(smem_addr(&empty_bar[s]), ((it / T::kStages) & 1u) ^ 1u, guard);
+          if (!ok) break;
+          const uint32_t bar = smem_addr(&full_bar[s]), a = smem + s * T::kStageBytes, b = a + T::kABytes;
+          bar_expect(bar, T::kStageBytes);
+#pragma unroll
+          for (int q = 0; q < kTileM / 64; ++q) {
+            const int r = i * kTileM + 64 * q;
+            tma_box(a + q * 8192, mp, g.p_mn ? r : kb * kTileK, g.p_mn ? kb * kTileK : r, bar);
+          }
+#pragma unroll
+          for (int q = 0; q < kN / 64; ++q) {
+            const int c = j * kN + 64 * q;
+            tma_box(b + q * 8192, mq, g.q_mn ? c : kb * kTileK, g.q_mn ? kb * kTileK : c, bar);
+          }
+        }
+      }
+    }
+    // every copy lands before the block ends
+    for (uint32_t back = 1; back <= T::kStages && back <= it; ++back) {
+      const uint32_t last = it - back;
+      bar_drain(smem_addr(&full_bar[last % T::kStages]), (last / T::kStages) & 1u, kWaitLimitNs);
+    }
+  } else if (warp == 1 && lane == 0) {  // products
+    Tiles<kN, GemmParams<kMats>> tiles{p};
+    uint32_t it = 0, n = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, ++n) {
+      int i, j;
+      const GemmMat& g = tiles.at(t, &i, &j);
+      const int blocks = (g.k + kTileK - 1) / kTileK * p.terms;
+      const uint32_t buf = n & 1u, d = tmem + buf * kN;
+      ok = bar_wait(smem_addr(&free_bar[buf]), ((n >> 1) & 1u) ^ 1u, guard);
+      if (!ok) break;
+      fence_after();
+      const uint32_t kind = product_kind(kTileM, kN, g.p_mn, g.q_mn);
+      // bytes from one 16-deep product's operand to the next, and between blocks of 64 rows
+      const uint32_t a_step = g.p_mn ? 2048 : 32, b_step = g.q_mn ? 2048 : 32;
+      const uint32_t a_block = g.p_mn ? 8192 : 0, b_block = g.q_mn ? 8192 : 0;
+      for (int kb = 0; kb < blocks; ++kb, ++it) {
+        const int s = it % T::kStages;
+        ok = bar_wait(smem_addr(&full_bar[s]), (it / T::kStages) & 1u, guard);
+        if (!ok) break;
+        fence_after();
+        const uint32_t a = smem + s * T::kStageBytes, b = a + T::kABytes;
+#pragma unroll
+        for (int q = 0; q < kTileK / 16; ++q)
+          mma(d, operand(a + q * a_step, a_block, 1024), operand(b + q * b_step, b_block, 1024), kind, kb > 0 || q > 0);
+        mma_commit(smem_addr(&empty_bar[s]));
+      }
+      if (ok) mma_commit(smem_addr(&done_bar[buf]));
+    }
+    if (!ok) {  // products in flight end before the accumulators are freed
+      const uint32_t last = it > 0 ? it - 1 : 0;
+      if (it > 0) bar_drain(smem_addr(&empty_bar[last % T::kStages]), (last / T::kStages) & 1u, kWaitLimitNs);
+    }
+  } else if (warp >= 4) {  // epilogue
+    Tiles<kN, GemmParams<kMats>> tiles{p};
+    const int quarter = warp - 4;
+    uint32_t n = 0;
+    for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, ++n) {
+      int i, j;
+      const GemmMat& g = tiles.at(t, &i, &j);
+      const uint32_t buf = n & 1u;
+      if (!bar_wait(smem_addr(&done_bar[buf]), (n >> 1) & 1u, guard)) break;
+      fence_after();
+      const int row = i * kTileM + quarter * 32 + lane;
+      const bool in_rows = row < g.m;
+      for (int c = 0; c < kN; c += 32) {
+        const int col0 = j * kN + c;
+        const int sub = col0 / kTileM;
+        if (col0 >= g.n || (g.symmetric && sub > i)) continue;
+        float v[32];
+        tmem_load32(tmem + buf * kN + c + (static_cast<uint32_t>(quarter * 32) << 16), v);
+        if (p.kind == kGram) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] *= p.alpha;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] *= p.alpha;
+          if (in_rows) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+              const __half* in = part ? g.in_lo : g.in_hi;
+              if (!in) continue;
+              in += row * g.ld + col0;
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const Half16 h = load16(in + 16 * q);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h.r[e]));
+                  v[16 * q + 2 * e] += p.beta * f.x;
+                  v[16 * q + 2 * e + 1] += p.beta * f.y;
+                }
+              }
+            }
+          }
+        }
+        if (p.result != kParts) {
+          if (in_rows) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] *= 1.0f / kScaleX;
+            finish(g, p.apply, p.result, row, col0, v);
+          }
+          continue;
+        }
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const __half2 h = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+          const float2 f = __half22float2(h);
+          const __half2 l = __floats2half2_rn(v[2 * e] - f.x, v[2 * e + 1] - f.y);
+          hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+          lo[e] = *reinterpret_cast<const uint32_t*>(&l);
+        }
+        const bool mirror = g.symmetric && sub < i;
+        store_part(g.hi, g.ld, row, col0, in_rows, mirror, g.m, g.n, hi);
+        if (g.lo) store_part(g.lo, g.ld, row, col0, in_rows, mirror, g.m, g.n, lo);
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_addr(&free_bar[buf]));
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1) tmem_free(tmem, T::kTmemCols);
+}
+
+// ------------------------------------------------------------- host side
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+int terms_of(const NsJob& j, const NsPlan& plan) {
+  return plan.terms ? plan.terms : std::min(j.rows, j.cols) < 256 ? 3 : 1;
+}
+
+int parts_of(const NsJob& j) {
+  const int64_t units = j.rows * ((j.cols + kUnitCols - 1) / kUnitCols);
+  return static_cast<int>(std::min<int64_t>(kMaxParts, (units + kPassWarps - 1) / kPassWarps));
+}
+
+// A matrix's share of the workspace: X twice (read and written by turns) and A, P,
+// each as hi and, where it is used, lo part, rows a multiple of 128 bytes apart.
+struct Buffers {
+  __half *x[2][2], *a[2], *poly[2];
+  float* partial;
+  int64_t ld_x, ld_a;
+};
+
+int64_t carve(const NsJob& j, const NsPlan& plan, unsigned char* base, Buffers* out) {
+  const int terms = terms_of(j, plan);
+  const int64_t side = std::min(j.rows, j.cols);
+  Buffers b{};
+  b.ld_x = round_up(j.cols, 64);
+  b.ld_a = round_up(side, 64);
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    unsigned char* q = base ? base + at : nullptr;
+    at += round_up(bytes, 256);
+    return q;
+  };
+  for (int k = 0; k < 2; ++k)
+    for (int part = 0; part < 2; ++part)
+      b.x[k][part] = reinterpret_cast<__half*>(take(j.rows * b.ld_x * 2));
+  for (int part = 0; part < (terms == 3 ? 2 : 1); ++part) {
+    b.a[part] = reinterpret_cast<__half*>(take(side * b.ld_a * 2));
+    b.poly[part] = reinterpret_cast<__half*>(take(side * b.ld_a * 2));
+  }
+  b.partial = reinterpret_cast<float*>(take(kMaxParts * 4));
+  if (out) *out = b;
+  return at;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+
+// Boxes of 64 x 64 elements of a rows x cols fp16 matrix; outside it they read zeros.
+bool make_map(CUtensorMap* map, const __half* base, int64_t rows, int64_t cols, int64_t ld) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {64, 64}, step[2] = {1, 1};
+  return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<__half*>(base), dims, strides, box, step,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Device {
+  int sms = 0;
+  unsigned int* status = nullptr;
+};
+
+int device_facts(Device* d) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FSDP_ECUDA;
+  return device_status_word(&d->status);
+}
+
+// Launches a kernel so that its blocks may be placed while the previous kernel of
+// the stream ends; the kernels wait for that one's results themselves.
+template <typename K, typename P>
+int launch_after(K kernel, int grid, int threads, int smem, cudaStream_t stream, const P& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FSDP_OK : FSDP_ECUDA;
+}
+
+template <int kN, int kMats>
+int launch_product(GemmParams<kMats>& p, int sms, cudaStream_t stream) {
+  using T = Tile<kN>;
+  p.tiles = 0;
+  for (int i = 0; i < p.count; ++i) {
+    GemmMat& g = p.mat[i];
+    const int rows = (g.m + kTileM - 1) / kTileM;
+    g.col_tiles = (g.n + kN - 1) / kN;
+    g.tiles = rows * g.col_tiles;
+    if (g.symmetric) {
+      g.tiles = 0;
+      for (int r = 0; r < rows; ++r) g.tiles += r / (kN / kTileM) + 1;
+    }
+    p.tiles += g.tiles;
+  }
+  if (cudaFuncSetAttribute(ns_product<kN, kMats>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) !=
+      cudaSuccess)
+    return FSDP_ECUDA;
+  return launch_after(ns_product<kN, kMats>, std::min(p.tiles, sms), kGemmThreads, T::kSmemBytes, stream, p);
+}
+
+// One launch's matrices through all steps.
+template <int kMats>
+int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms, const NsApply* apply,
+              unsigned char* workspace, const Device& dev, cudaStream_t stream) {
+  static thread_local PassParams pass;
+  static thread_local GemmParams<kMats> p;
+  struct Maps {
+    CUtensorMap x[2][2], a[2], poly[2];
+  };
+  std::vector<Buffers> buffers(count);
+  std::vector<Maps> maps(count);
+  int blocks = 0;
+  for (int i = 0; i < count; ++i) {
+    const NsJob& j = *jobs[i];
+    Buffers& b = buffers[i];
+    workspace += carve(j, plan, workspace, &b);
+    const int64_t side = std::min(j.rows, j.cols);
+    bool ok = true;
+    for (int part = 0; part < (terms == 3 ? 2 : 1); ++part) {
+      for (int k = 0; k < 2; ++k) ok = ok && make_map(&maps[i].x[k][part], b.x[k][part], j.rows, j.cols, b.ld_x);
+      ok = ok && make_map(&maps[i].a[part], b.a[part], side, side, b.ld_a);
+      ok = ok && make_map(&maps[i].poly[part], b.poly[part], side, side, b.ld_a);
+    }
+    if (!ok) return FSDP_ECUDA;
+    blocks += parts_of(j);
+    pass.mat[i] = {j.source, j.source_stride, j.rows, j.cols, b.x[0][0], b.x[0][1], b.ld_x, b.partial, j.dtype,
+                   parts_of(j), blocks};
+  }
+  pass.count = count;
+  pass.eps = plan.eps;
+  ns_squares<<<blocks, 32 * kPassWarps, 0, stream>>>(pass);
+  ns_normalise<<<blocks, 32 * kPassWarps, 0, stream>>>(pass);
+  if (cudaGetLastError() != cudaSuccess) return FSDP_ECUDA;
+  p.count = count;
+  p.terms = terms;
+  p.status = dev.status;
+  if (apply) p.apply = *apply;
+  for (int s = 0; s < plan.steps; ++s) {
+    const bool last = s + 1 == plan.steps;
+    const int now = s & 1, next = now ^ 1;
+    for (int kind = kGram; kind <= kUpdate; ++kind) {
+      int64_t wide_tiles = 0;
+      for (int i = 0; i < count; ++i) {
+        const NsJob& j = *jobs[i];
+        const Buffers& b = buffers[i];
+        const Maps& q = maps[i];
+        GemmMat& g = p.mat[i];
+        const bool wide = j.rows <= j.cols;
+        const int32_t side = static_cast<int32_t>(std::min(j.rows, j.cols));
+        auto use = [&](CUtensorMap* to, const CUtensorMap* from) { std::memcpy(to, from, 2 * sizeof(CUtensorMap)); };
+        g.symmetric = kind != kUpdate;
+        g.m = g.n = g.k = side;
+        g.ld = b.ld_a;
+        g.in_hi = g.in_lo = nullptr;
+        g.p_mn = g.q_mn = 0;
+        if (kind == kGram) {
+          use(g.p, q.x[now]);
+          use(g.q, q.x[now]);
+          g.k = static_cast<int32_t>(std::max(j.rows, j.cols));
+          g.p_mn = g.q_mn = !wide;
+          g.hi = b.a[0];
+          g.lo = b.a[1];
+        } else if (kind == kPoly) {
+          use(g.p, q.a);
+          use(g.q, q.a);
+          g.in_hi = b.a[0];
+          g.in_lo = b.a[1];
+          g.hi = b.poly[0];
+          g.lo = b.poly[1];
+        } else {
+          use(g.p, wide ? q.poly : q.x[now]);
+          use(g.q, wide ? q.x[now] : q.poly);
+          g.q_mn = wide;
+          g.m = static_cast<int32_t>(j.rows);
+          g.n = static_cast<int32_t>(j.cols);
+          g.ld = b.ld_x;
+          g.in_hi = b.x[now][0];
+          g.in_lo = b.x[now][1];
+          g.hi = b.x[next][0];
+          g.lo = b.x[next][1];
+          g.out = j.out;
+          g.out_stride = j.out_stride;
+          g.flat = j.flat;
+          g.step = j.step;
+        }
+        const int64_t rows = (g.m + 127) / 128, cols = (g.n + 255) / 256;
+        wide_tiles += g.symmetric ? (rows + 1) * (rows + 1) / 4 : rows * cols;
+      }
+      p.kind = kind;
+      p.result = kind != kUpdate || !last ? kParts : apply ? kApply : kOut;
+      p.alpha = kind == kGram ? kScaleA / (kScaleX * kScaleX) : kind == kPoly ? plan.coef[3 * s + 2] / kScaleA
+                                                                               : 1.0f / kScaleA;
+      p.beta = kind == kPoly ? plan.coef[3 * s + 1] : plan.coef[3 * s];
+      // 256-column tiles where they are enough for every SM, else narrower ones
+      const int rc = wide_tiles >= dev.sms ? launch_product<256>(p, dev.sms, stream)
+                                           : launch_product<128>(p, dev.sms, stream);
+      if (rc != FSDP_OK) return rc;
+    }
+  }
+  return FSDP_OK;
 }
 
 }  // namespace
@@ -161,38 +736,29 @@ int ns_plan(const fsdp_newton_schulz_t* h, NsPlan* plan) {
   return FSDP_OK;
 }
 
-int64_t ns_workspace_bytes(const std::vector<NsJob>& jobs, const NsPlan&) {
-  int64_t floats = 0;
-  for (const NsJob& j : jobs) floats += matrix_floats(j);
-  return floats * 4 + 16;
+int64_t ns_workspace_bytes(const std::vector<NsJob>& jobs, const NsPlan& plan) {
+  int64_t bytes = 256;
+  for (const NsJob& j : jobs) bytes += carve(j, plan, nullptr, nullptr);
+  return bytes;
 }
 
 int ns_run(const std::vector<NsJob>& jobs, const NsPlan& plan, const NsApply* apply, void* workspace,
            cudaStream_t stream) {
-  float* at = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + 15) & ~uintptr_t(15));
-  const NsApply none{};
-  for (const NsJob& j : jobs) {
-    const int64_t m = j.rows, n = j.cols, k = std::min(m, n);
-    float *x = at, *y = x + m * n, *gram = y + m * n, *poly = gram + k * k, *partial = poly + k * k;
-    at += matrix_floats(j);
-    ns_squares<<<kSumBlocks, 256, 0, stream>>>(j, partial);
-    const int grid = static_cast<int>(std::min<int64_t>(m, 4096));
-    ns_normalise<<<grid, 256, 0, stream>>>(j, partial, plan.eps, x);
-    for (int s = 0; s < plan.steps; ++s) {
-      const float a = plan.coef[3 * s], b = plan.coef[3 * s + 1], c = plan.coef[3 * s + 2];
-      if (m <= n) {
-        if (int rc = product({x, x, nullptr, gram, k, k, n, n, 1, 1, n, k, 1.0f, 0.0f}, stream)) return rc;
-        if (int rc = product({gram, gram, gram, poly, k, k, k, k, 1, k, 1, k, c, b}, stream)) return rc;
-        if (int rc = product({poly, x, x, y, m, n, k, k, 1, n, 1, n, 1.0f, a}, stream)) return rc;
-      } else {
-        if (int rc = product({x, x, nullptr, gram, k, k, m, 1, n, n, 1, k, 1.0f, 0.0f}, stream)) return rc;
-        if (int rc = product({gram, gram, gram, poly, k, k, k, k, 1, k, 1, k, c, b}, stream)) return rc;
-        if (int rc = product({x, poly, x, y, m, n, k, n, 1, k, 1, n, 1.0f, a}, stream)) return rc;
-      }
-      std::swap(x, y);
+  Device dev;
+  if (int rc = device_facts(&dev)) return rc;
+  if (!encoder()) return FSDP_ECUDA;
+  auto* base = reinterpret_cast<unsigned char*>(round_up(reinterpret_cast<intptr_t>(workspace), 256));
+  for (int terms : {1, 3}) {
+    std::vector<const NsJob*> group;
+    for (const NsJob& j : jobs)
+      if (terms_of(j, plan) == terms) group.push_back(&j);
+    for (size_t at = 0; at < group.size(); at += kMaxMats) {
+      const int count = static_cast<int>(std::min<size_t>(kMaxMats, group.size() - at));
+      const int rc = count <= 8 ? run_group<8>(&group[at], count, plan, terms, apply, base, dev, stream)
+                                : run_group<kMaxMats>(&group[at], count, plan, terms, apply, base, dev, stream);
+      if (rc != FSDP_OK) return rc;
+      for (int i = 0; i < count; ++i) base += carve(*group[at + i], plan, nullptr, nullptr);
     }
-    ns_output<<<grid, 256, 0, stream>>>(j, x, apply ? *apply : none, apply != nullptr);
-    if (cudaGetLastError() != cudaSuccess) return FSDP_ECUDA;
   }
   return FSDP_OK;
 }

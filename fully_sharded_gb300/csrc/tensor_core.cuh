@@ -1,0 +1,150 @@
+// sm_103a building blocks of the tensor-core kernels: mbarriers with bounded
+// waits, tiled TMA loads, tcgen05 products into tensor memory.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace fsdp {
+namespace tc {
+
+__device__ __forceinline__ uint32_t smem_addr(const void* q) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(q));
+}
+__device__ __forceinline__ uint64_t clock_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// What every bounded wait of a block shares: when one runs out, `stop` is set,
+// bit 0 of the device's status word is set, and every other wait returns.
+struct Guard {
+  volatile int* stop;
+  unsigned int* status;
+  uint64_t limit_ns;
+};
+
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Guard& g) {
+  if (bar_try(bar, parity)) return true;
+  const uint64_t t0 = clock_ns();
+  for (;;) {
+    if (bar_try(bar, parity)) return true;
+    if (*g.stop) return false;
+    if (clock_ns() - t0 > g.limit_ns) {
+      *g.stop = 1;
+      atomicOr(g.status, 1u);
+      return false;
+    }
+  }
+}
+
+// A wait for copies or products already issued, after a stop too (bounded again).
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = clock_ns();
+  while (!bar_try(bar, parity) && clock_ns() - t0 <= limit_ns) {
+  }
+}
+
+// One box of a 2-D tensor map; x is a multiple of 64 two-byte elements everywhere here.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+// Shared-memory operand descriptor: 128-byte swizzle, byte strides between
+// 8-row groups (`group`) and, for operands whose M or N index is contiguous,
+// between 64-element blocks of it (`block`).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t block, uint32_t group) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((block >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((group >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// fp16 x fp16 -> fp32, M x N tile; a_mn / b_mn: the operand's M (N) index is the contiguous one.
+__device__ __forceinline__ uint32_t product_kind(int m, int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// Arrives on `bar` when every product issued so far has completed.
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols) : "memory");
+}
+
+// 32 columns of this warp's 32 lanes: v[c] = column c of the thread's own lane.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 16 fp16 values (32 bytes, aligned).
+struct Half16 {
+  uint32_t r[8];
+};
+__device__ __forceinline__ Half16 load16(const __half* p) {
+  Half16 h;
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(h.r[0]), "=r"(h.r[1]), "=r"(h.r[2]), "=r"(h.r[3]), "=r"(h.r[4]), "=r"(h.r[5]), "=r"(h.r[6]),
+                 "=r"(h.r[7])
+               : "l"(p)
+               : "memory");
+  return h;
+}
+__device__ __forceinline__ void store16(__half* p, const Half16& h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(h.r[0]), "r"(h.r[1]),
+               "r"(h.r[2]), "r"(h.r[3]), "r"(h.r[4]), "r"(h.r[5]), "r"(h.r[6]), "r"(h.r[7])
+               : "memory");
+}
+
+}  // namespace tc
+}  // namespace fsdp
