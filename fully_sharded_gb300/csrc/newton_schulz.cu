@@ -17,7 +17,7 @@
 // column space. With terms = 3 every operand has both parts: hi hi + lo hi + hi lo.
 //
 // Each of the three products is one launch over all matrices of the call: a
-// persistent grid of 128 x kN tiles, one producer lane (TMA), one product lane
+// persistent grid of tiles, one producer lane (TMA), one product lane
 // (tcgen05, two accumulators in tensor memory) and four epilogue warps per
 // block. A and P are symmetric: tiles above the diagonal are not computed, and
 // the others are written to both places.
@@ -30,6 +30,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -176,20 +177,29 @@ struct GemmParams {
 };
 static_assert(sizeof(GemmParams<kMaxMats>) <= 32764, "kernel parameter block too large");
 
-constexpr int kTileM = 128, kTileK = 64;
+constexpr int kTileK = 64;
 constexpr int kGemmThreads = 256;  // producer, product, two idle and four epilogue warps
 
-template <int kN>
+// A tile: 128 rows per block of the pair (or single block) and kN columns.
+template <int kN, int kPair>
 struct Tile {
-  static constexpr int kABytes = kTileM * kTileK * 2, kBBytes = kN * kTileK * 2;
+  static constexpr int kM = 128 * kPair;
+  static constexpr int kBRows = kN / kPair;  // a block's half of the second operand
+  static constexpr int kABytes = 128 * kTileK * 2, kBBytes = kBRows * kTileK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = 196608 / kStageBytes;  // 192 KB of operands in flight
   static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
   static constexpr int kTmemCols = 2 * kN;
+
+  // symmetric results: tiles of tile row i with an element on or below the diagonal
+  __host__ __device__ static int below(int i, int col_tiles) {
+    const int c = ((i + 1) * kM + kN - 1) / kN;
+    return c < col_tiles ? c : col_tiles;
+  }
 };
 
 // Tile t of a launch: its matrix and place. Calls come with growing t.
-template <int kN, typename P>
+template <typename T, typename P>
 struct Tiles {
   const P& p;
   int mat = 0, first = 0;
@@ -207,9 +217,7 @@ struct Tiles {
       *j = l - *i * g.col_tiles;
       return g;
     }
-    // row i holds the tiles with an element on or below the diagonal
-    constexpr int kRatio = kN / kTileM;
-    while (l - base > row / kRatio) base += row++ / kRatio + 1;
+    while (l - base >= T::below(row, g.col_tiles)) base += T::below(row++, g.col_tiles);
     *i = row;
     *j = l - base;
     return g;
@@ -298,15 +306,17 @@ __device__ __forceinline__ void store_part(__half* base, int64_t ld, int row, in
   }
 }
 
-template <int kN, int kMats>
+template <int kN, int kPair, int kMats>
 __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_constant__ GemmParams<kMats> p) {
-  using T = Tile<kN>;
+  using T = Tile<kN, kPair>;
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t full_bar[T::kStages], empty_bar[T::kStages], done_bar[2], free_bar[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int stop;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
+  const int rank = kPair == 2 ? static_cast<int>(block_rank()) : 0;
+  const int first_tile = blockIdx.x / kPair, tile_step = gridDim.x / kPair;
   const Guard guard{&stop, p.status, kWaitLimitNs};
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) {
@@ -315,27 +325,29 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     }
     for (int b = 0; b < 2; ++b) {
       bar_init(smem_addr(&done_bar[b]), 1);
-      bar_init(smem_addr(&free_bar[b]), 4);
+      bar_init(smem_addr(&free_bar[b]), 4 * kPair);
     }
     stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), T::kTmemCols);
+  if (warp == 1) tmem_alloc<kPair>(smem_addr(&tmem_slot), T::kTmemCols);
   fence_before();
   __syncthreads();
+  if constexpr (kPair == 2) cluster_sync();
   fence_after();
   const uint32_t tmem = tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
 
-  if (warp == 0 && lane == 0) {  // producer
-    Tiles<kN, GemmParams<kMats>> tiles{p};
+  if (warp == 0 && lane == 0) {  // producer: this block's rows of both operands
+    Tiles<T, GemmParams<kMats>> tiles{p};
     uint32_t it = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x) {
+    for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
       int i, j;
       const GemmMat& g = tiles.at(t, &i, &j);
       const int blocks = (g.k + kTileK - 1) / kTileK;
+      const int row0 = i * T::kM + rank * 128, col0 = j * kN + rank * T::kBRows;
       for (int term = 0; ok && term < p.terms; ++term) {
         const CUtensorMap* mp = &g.p[term == 1 ? 1 : 0];
         const CUtensorMap* mq = &g.q[term == 2 ? 1 : 0];
@@ -343,31 +355,36 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
           const int s = it % T::kStages;
           ok = bar_wait(smem_addr(&empty_bar[s]), ((it / T::kStages) & 1u) ^ 1u, guard);
           if (!ok) break;
-          const uint32_t bar = smem_addr(&full_bar[s]), a = smem + s * T::kStageBytes, b = a + T::kABytes;
-          bar_expect(bar, T::kStageBytes);
+          // the first block's barrier counts the bytes of both
+          const uint32_t own = smem_addr(&full_bar[s]), bar = kPair == 2 ? in_block(own, 0) : own;
+          const uint32_t a = smem + s * T::kStageBytes, b = a + T::kABytes;
+          if (rank == 0) bar_expect(own, T::kStageBytes * kPair);
 #pragma unroll
-          for (int q = 0; q < kTileM / 64; ++q) {
-            const int r = i * kTileM + 64 * q;
-            tma_box(a + q * 8192, mp, g.p_mn ? r : kb * kTileK, g.p_mn ? kb * kTileK : r, bar);
+          for (int q = 0; q < 2; ++q) {
+            const int r = row0 + 64 * q;
+            tma_box<kPair>(a + q * 8192, mp, g.p_mn ? r : kb * kTileK, g.p_mn ? kb * kTileK : r, bar);
           }
 #pragma unroll
-          for (int q = 0; q < kN / 64; ++q) {
-            const int c = j * kN + 64 * q;
-            tma_box(b + q * 8192, mq, g.q_mn ? c : kb * kTileK, g.q_mn ? kb * kTileK : c, bar);
+          for (int q = 0; q < T::kBRows / 64; ++q) {
+            const int c = col0 + 64 * q;
+            tma_box<kPair>(b + q * 8192, mq, g.q_mn ? c : kb * kTileK, g.q_mn ? kb * kTileK : c, bar);
           }
         }
       }
     }
-    // every copy lands before the block ends
+    // every copy lands (its stage is used and released) before the block ends
     for (uint32_t back = 1; back <= T::kStages && back <= it; ++back) {
       const uint32_t last = it - back;
-      bar_drain(smem_addr(&full_bar[last % T::kStages]), (last / T::kStages) & 1u, kWaitLimitNs);
+      if (rank == 0)
+        bar_drain(smem_addr(&full_bar[last % T::kStages]), (last / T::kStages) & 1u, kWaitLimitNs);
+      else
+        bar_drain(smem_addr(&empty_bar[last % T::kStages]), (last / T::kStages) & 1u, kWaitLimitNs);
     }
-  } else if (warp == 1 && lane == 0) {  // products
-    Tiles<kN, GemmParams<kMats>> tiles{p};
+  } else if (warp == 1 && lane == 0 && rank == 0) {  // products, for both blocks
+    Tiles<T, GemmParams<kMats>> tiles{p};
     uint32_t it = 0, n = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < p.tiles; t += gridDim.x, ++n) {
+    for (int t = first_tile; ok && t < p.tiles; t += tile_step, ++n) {
       int i, j;
       const GemmMat& g = tiles.at(t, &i, &j);
       const int blocks = (g.k + kTileK - 1) / kTileK * p.terms;
@@ -375,7 +392,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
       ok = bar_wait(smem_addr(&free_bar[buf]), ((n >> 1) & 1u) ^ 1u, guard);
       if (!ok) break;
       fence_after();
-      const uint32_t kind = product_kind(kTileM, kN, g.p_mn, g.q_mn);
+      const uint32_t kind = product_kind(T::kM, kN, g.p_mn, g.q_mn);
       // bytes from one 16-deep product's operand to the next, and between blocks of 64 rows
       const uint32_t a_step = g.p_mn ? 2048 : 32, b_step = g.q_mn ? 2048 : 32;
       const uint32_t a_block = g.p_mn ? 8192 : 0, b_block = g.q_mn ? 8192 : 0;
@@ -387,31 +404,31 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
         const uint32_t a = smem + s * T::kStageBytes, b = a + T::kABytes;
 #pragma unroll
         for (int q = 0; q < kTileK / 16; ++q)
-          mma(d, operand(a + q * a_step, a_block, 1024), operand(b + q * b_step, b_block, 1024), kind, kb > 0 || q > 0);
-        mma_commit(smem_addr(&empty_bar[s]));
+          mma<kPair>(d, operand(a + q * a_step, a_block, 1024), operand(b + q * b_step, b_block, 1024), kind,
+                     kb > 0 || q > 0);
+        mma_commit<kPair>(smem_addr(&empty_bar[s]));
       }
-      if (ok) mma_commit(smem_addr(&done_bar[buf]));
+      if (ok) mma_commit<kPair>(smem_addr(&done_bar[buf]));
     }
-    if (!ok) {  // products in flight end before the accumulators are freed
-      const uint32_t last = it > 0 ? it - 1 : 0;
-      if (it > 0) bar_drain(smem_addr(&empty_bar[last % T::kStages]), (last / T::kStages) & 1u, kWaitLimitNs);
-    }
-  } else if (warp >= 4) {  // epilogue
-    Tiles<kN, GemmParams<kMats>> tiles{p};
+    if (!ok && it > 0)  // products in flight end before the accumulators are freed
+      bar_drain(smem_addr(&empty_bar[(it - 1) % T::kStages]), ((it - 1) / T::kStages) & 1u, kWaitLimitNs);
+  } else if (warp >= 4) {  // epilogue: this block's 128 rows
+    Tiles<T, GemmParams<kMats>> tiles{p};
     const int quarter = warp - 4;
     uint32_t n = 0;
-    for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, ++n) {
+    for (int t = first_tile; t < p.tiles; t += tile_step, ++n) {
       int i, j;
       const GemmMat& g = tiles.at(t, &i, &j);
       const uint32_t buf = n & 1u;
       if (!bar_wait(smem_addr(&done_bar[buf]), (n >> 1) & 1u, guard)) break;
       fence_after();
-      const int row = i * kTileM + quarter * 32 + lane;
+      const int block = i * kPair + rank;  // in rows of 128, as `sub` in columns
+      const int row = block * 128 + quarter * 32 + lane;
       const bool in_rows = row < g.m;
       for (int c = 0; c < kN; c += 32) {
         const int col0 = j * kN + c;
-        const int sub = col0 / kTileM;
-        if (col0 >= g.n || (g.symmetric && sub > i)) continue;
+        const int sub = col0 / 128;
+        if (col0 >= g.n || (g.symmetric && sub > block)) continue;
         float v[32];
         tmem_load32(tmem + buf * kN + c + (static_cast<uint32_t>(quarter * 32) << 16), v);
         if (p.kind == kGram) {
@@ -456,19 +473,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
           hi[e] = *reinterpret_cast<const uint32_t*>(&h);
           lo[e] = *reinterpret_cast<const uint32_t*>(&l);
         }
-        const bool mirror = g.symmetric && sub < i;
+        const bool mirror = g.symmetric && sub < block;
         store_part(g.hi, g.ld, row, col0, in_rows, mirror, g.m, g.n, hi);
         if (g.lo) store_part(g.lo, g.ld, row, col0, in_rows, mirror, g.m, g.n, lo);
       }
       fence_before();
       __syncwarp();
-      if (lane == 0) bar_arrive(smem_addr(&free_bar[buf]));
+      if (lane == 0) {
+        if constexpr (kPair == 2)
+          bar_arrive_cluster(in_block(smem_addr(&free_bar[buf]), 0));
+        else
+          bar_arrive(smem_addr(&free_bar[buf]));
+      }
     }
   }
   fence_before();
   __syncthreads();
+  if constexpr (kPair == 2) cluster_sync();  // neither block leaves while the other may signal it
   fence_after();
-  if (warp == 1) tmem_free(tmem, T::kTmemCols);
+  if (warp == 1) tmem_free<kPair>(tmem, T::kTmemCols);
 }
 
 // ------------------------------------------------------------- host side
@@ -543,14 +566,13 @@ bool make_map(CUtensorMap* map, const __half* base, int64_t rows, int64_t cols, 
 }
 
 struct Device {
-  int sms = 0;
+  int id = 0, sms = 0;
   unsigned int* status = nullptr;
 };
 
 int device_facts(Device* d) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+  if (cudaGetDevice(&d->id) != cudaSuccess ||
+      cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->id) != cudaSuccess)
     return FSDP_ECUDA;
   return device_status_word(&d->status);
 }
@@ -558,39 +580,71 @@ int device_facts(Device* d) {
 // Launches a kernel so that its blocks may be placed while the previous kernel of
 // the stream ends; the kernels wait for that one's results themselves.
 template <typename K, typename P>
-int launch_after(K kernel, int grid, int threads, int smem, cudaStream_t stream, const P& p) {
+int launch_after(K kernel, int grid, int cluster, int threads, int smem, cudaStream_t stream, const P& p) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FSDP_OK : FSDP_ECUDA;
 }
 
-template <int kN, int kMats>
-int launch_product(GemmParams<kMats>& p, int sms, cudaStream_t stream) {
-  using T = Tile<kN>;
+// How many clusters of the kernel run at once (looked up once per device).
+template <int kN, int kPair, int kMats>
+int resident_clusters(const Device& dev) {
+  using T = Tile<kN, kPair>;
+  static std::atomic<int> cached[64];
+  if (dev.id >= 64) return 0;
+  int n = cached[dev.id].load(std::memory_order_acquire);
+  if (n) return n;
+  const auto kernel = ns_product<kN, kPair, kMats>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess) return 0;
+  if (kPair == 1) {
+    n = dev.sms;
+  } else {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(dev.sms / kPair * kPair);
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = T::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPair;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 0;
+  }
+  cached[dev.id].store(n, std::memory_order_release);
+  return n;
+}
+
+template <int kN, int kPair, int kMats>
+int launch_product(GemmParams<kMats>& p, const Device& dev, cudaStream_t stream) {
+  using T = Tile<kN, kPair>;
   p.tiles = 0;
   for (int i = 0; i < p.count; ++i) {
     GemmMat& g = p.mat[i];
-    const int rows = (g.m + kTileM - 1) / kTileM;
+    const int rows = (g.m + T::kM - 1) / T::kM;
     g.col_tiles = (g.n + kN - 1) / kN;
     g.tiles = rows * g.col_tiles;
     if (g.symmetric) {
       g.tiles = 0;
-      for (int r = 0; r < rows; ++r) g.tiles += r / (kN / kTileM) + 1;
+      for (int r = 0; r < rows; ++r) g.tiles += T::below(r, g.col_tiles);
     }
     p.tiles += g.tiles;
   }
-  if (cudaFuncSetAttribute(ns_product<kN, kMats>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) !=
-      cudaSuccess)
-    return FSDP_ECUDA;
-  return launch_after(ns_product<kN, kMats>, std::min(p.tiles, sms), kGemmThreads, T::kSmemBytes, stream, p);
+  const int room = resident_clusters<kN, kPair, kMats>(dev);
+  if (room < 1) return FSDP_ECUDA;
+  return launch_after(ns_product<kN, kPair, kMats>, std::min(p.tiles, room) * kPair, kPair, kGemmThreads, T::kSmemBytes,
+                      stream, p);
 }
 
 // One launch's matrices through all steps.
@@ -634,7 +688,7 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
     const bool last = s + 1 == plan.steps;
     const int now = s & 1, next = now ^ 1;
     for (int kind = kGram; kind <= kUpdate; ++kind) {
-      int64_t wide_tiles = 0;
+      int64_t large_tiles = 0;
       for (int i = 0; i < count; ++i) {
         const NsJob& j = *jobs[i];
         const Buffers& b = buffers[i];
@@ -679,16 +733,16 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
           g.step = j.step;
         }
         const int64_t rows = (g.m + 127) / 128, cols = (g.n + 255) / 256;
-        wide_tiles += g.symmetric ? (rows + 1) * (rows + 1) / 4 : rows * cols;
+        large_tiles += g.symmetric ? cols * (cols + 1) / 2 : (rows + 1) / 2 * cols;
       }
       p.kind = kind;
       p.result = kind != kUpdate || !last ? kParts : apply ? kApply : kOut;
       p.alpha = kind == kGram ? kScaleA / (kScaleX * kScaleX) : kind == kPoly ? plan.coef[3 * s + 2] / kScaleA
                                                                                : 1.0f / kScaleA;
       p.beta = kind == kPoly ? plan.coef[3 * s + 1] : plan.coef[3 * s];
-      // 256-column tiles where they are enough for every SM, else narrower ones
-      const int rc = wide_tiles >= dev.sms ? launch_product<256>(p, dev.sms, stream)
-                                           : launch_product<128>(p, dev.sms, stream);
+      // pairs of blocks on 256 x 256 tiles where these fill the SMs, else single blocks on 128 x 128
+      const int rc = 2 * large_tiles >= dev.sms ? launch_product<256, 2>(p, dev, stream)
+                                                : launch_product<128, 1>(p, dev, stream);
       if (rc != FSDP_OK) return rc;
     }
   }
