@@ -9,7 +9,6 @@
 #include "newton_schulz.h"
 #include "strided.h"
 
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -19,33 +18,6 @@
 
 namespace fsdp {
 namespace {
-
-struct MomentumParams {
-  const uint16_t* grads[FSDP_MAX_WORLD];
-  float* momentum[FSDP_MAX_WORLD];
-  float* u;      // this matrix's update, contiguous
-  int64_t flat;  // its first element in the unit
-  int64_t n;
-  int64_t shard;
-  int32_t w;
-  float mu;
-  float inv_w;   // 1 / W where W is a power of two, else 0
-  bool nesterov;
-};
-
-__global__ void __launch_bounds__(256) muon_momentum(const __grid_constant__ MomentumParams p) {
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < p.n;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t f = p.flat + i;
-    float g = 0.0f;
-    for (int k = 0; k < p.w; ++k) g += __bfloat162float(__ushort_as_bfloat16(p.grads[k][f]));
-    g = p.inv_w != 0.0f ? g * p.inv_w : g / static_cast<float>(p.w);
-    float* mp = p.momentum[f / p.shard] + f % p.shard;
-    const float m = p.mu * *mp + g;
-    *mp = m;
-    p.u[i] = p.nesterov ? g + p.mu * m : m;
-  }
-}
 
 struct Muon {
   std::vector<NsJob> jobs;
@@ -117,7 +89,9 @@ int make(const fsdp_muon_unit_t* unit, const fsdp_muon_t* h, bool pointers, Muon
       adam(pending, flat);
       out->jobs.push_back({nullptr, t.cols, t.rows, t.cols, nullptr, 0, flat, static_cast<float>(h->lr * t.scale),
                            FSDP_DTYPE_F32});
-      out->u_elems += t.rows * t.cols;
+      // each u starts at its place in the unit modulo 8, so that groups of 8 elements
+      // are aligned in both
+      out->u_elems += (t.rows * t.cols + 7) / 8 * 8 + 8;
       flat += t.rows * t.cols;
       pending = flat;
     }
@@ -165,7 +139,11 @@ extern "C" int fsdp_muon_step(const fsdp_muon_unit_t* unit, const fsdp_muon_t* h
   if (m.jobs.empty()) return FSDP_OK;
   float* u = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + 15) & ~uintptr_t(15));
   void* rest = u + m.u_elems;
-  MomentumParams p{};
+  for (NsJob& j : m.jobs) {
+    j.source = u + j.flat % 8;
+    u += (j.rows * j.cols + 7) / 8 * 8 + 8;
+  }
+  NsMomentum p{};
   for (int k = 0; k < W; ++k) {
     p.grads[k] = unit->grads[k];
     p.momentum[k] = unit->exp_avg[k];
@@ -175,16 +153,7 @@ extern "C" int fsdp_muon_step(const fsdp_muon_unit_t* unit, const fsdp_muon_t* h
   p.mu = static_cast<float>(h->momentum);
   p.inv_w = m.scalars.inv_w;
   p.nesterov = h->nesterov != 0;
-  for (NsJob& j : m.jobs) {
-    p.u = u;
-    p.flat = j.flat;
-    p.n = j.rows * j.cols;
-    j.source = u;
-    u += p.n;
-    muon_momentum<<<static_cast<int>(std::min<int64_t>((p.n + 255) / 256, 152 * 8)), 256, 0, st>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return FSDP_ECUDA;
-  }
-  return ns_run(m.jobs, m.plan, &m.apply, rest, st);
+  return ns_run(m.jobs, m.plan, &p, &m.apply, rest, st);
 } catch (const std::bad_alloc&) {
   return FSDP_ECUDA;
 }

@@ -48,9 +48,11 @@ constexpr int kMaxMats = 32;                      // matrices of one launch (24 
 
 // ------------------------------------------------- norm and first operands
 
-constexpr int kUnitCols = 1024;  // a warp's share of a row
+// Warps take units of up to 1024 consecutive elements (of a row), each lane four
+// times 8 elements: 128 bytes of fp32 in flight per lane.
+constexpr int kUnit = 1024;
 constexpr int kPassWarps = 8;
-constexpr int kMaxParts = 304;
+constexpr int kMaxParts = 608;
 
 struct PassMat {
   const void* source;
@@ -58,6 +60,7 @@ struct PassMat {
   __half *hi, *lo;
   int64_t ld;
   float* partial;
+  int64_t flat;       // the first element's place in the unit (momentum)
   int32_t dtype;
   int32_t parts;      // blocks (and partial sums) of this matrix
   int32_t block_end;  // running total of parts
@@ -69,10 +72,10 @@ struct PassParams {
   float eps;
 };
 
-__device__ __forceinline__ float load_source(const PassMat& j, int64_t i) {
-  return j.dtype == FSDP_DTYPE_F32 ? static_cast<const float*>(j.source)[i]
-                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(j.source)[i]);
-}
+struct MomentumParams {
+  PassParams pass;
+  NsMomentum m;
+};
 
 __device__ __forceinline__ const PassMat& pass_mat(const PassParams& p, int* part) {
   int i = 0, first = 0;
@@ -86,47 +89,153 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-// Calls f(row, column) for this lane's elements of its block's units.
+__device__ __forceinline__ void block_sum_to(double sum, float* out) {
+  __shared__ double shared[kPassWarps];
+  sum = warp_sum(sum);
+  if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = sum;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int i = 1; i < kPassWarps; ++i) sum += shared[i];
+  *out = static_cast<float>(sum);
+}
+
+__device__ __forceinline__ void unpack_bf16(uint32_t two, float* v) {
+  v[0] = __uint_as_float(two << 16);
+  v[1] = __uint_as_float(two & 0xffff0000u);
+}
+
+// 8 elements from element i of the source, zeros from `count` on.
+__device__ __forceinline__ void load8(const PassMat& j, int64_t i, int count, float (&v)[8]) {
+  if (j.dtype == FSDP_DTYPE_F32) {
+    const float* q = static_cast<const float*>(j.source) + i;
+    if (count >= 8 && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
+      const float4 a = __ldcs(reinterpret_cast<const float4*>(q)), b = __ldcs(reinterpret_cast<const float4*>(q) + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < count ? q[e] : 0.0f;
+    return;
+  }
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(j.source) + i;
+  if (count >= 8 && (reinterpret_cast<uintptr_t>(q) & 15u) == 0) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(q));
+    unpack_bf16(a.x, v), unpack_bf16(a.y, v + 2), unpack_bf16(a.z, v + 4), unpack_bf16(a.w, v + 6);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = e < count ? __bfloat162float(q[e]) : 0.0f;
+}
+
+// Calls f(row, column, values) for this lane's groups of 8 elements of its block's
+// units (column beyond the row's end: not called; values beyond it: zero).
 template <typename F>
-__device__ __forceinline__ void each_element(const PassMat& j, int part, F f) {
-  const int64_t segs = (j.cols + kUnitCols - 1) / kUnitCols, units = j.rows * segs;
+__device__ __forceinline__ void each_group(const PassMat& j, int part, F f) {
+  const int64_t segs = (j.cols + kUnit - 1) / kUnit, units = j.rows * segs;
   const int lane = threadIdx.x % 32;
   for (int64_t u = static_cast<int64_t>(part) * kPassWarps + threadIdx.x / 32; u < units;
        u += static_cast<int64_t>(j.parts) * kPassWarps) {
-    const int64_t r = u / segs, c0 = (u - r * segs) * kUnitCols, end = min(j.cols, c0 + kUnitCols);
-    for (int64_t c = c0 + lane; c < end; c += 32) f(r, c);
+    const int64_t r = u / segs, c0 = (u - r * segs) * kUnit + lane * 8;
+    float v[4][8];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t c = c0 + q * 256;
+      if (c < j.cols) load8(j, r * j.stride + c, static_cast<int>(min(j.cols - c, int64_t(8))), v[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (c0 + q * 256 < j.cols) f(r, c0 + q * 256, v[q]);
   }
 }
 
-// Sums of squares, one per block: fp32 over a lane's elements of a unit, then fp64.
+// Sums of squares, one per block: fp32 over a group of 8, then fp64.
 __global__ void __launch_bounds__(32 * kPassWarps) ns_squares(const __grid_constant__ PassParams p) {
-  __shared__ double shared[kPassWarps];
   int part;
   const PassMat& j = pass_mat(p, &part);
   double sum = 0.0;
-  float s = 0.0f;
-  int64_t row = -1;
-  each_element(j, part, [&](int64_t r, int64_t c) {
-    if (r != row) {
-      sum += s;
-      s = 0.0f;
-      row = r;
-    }
-    const float v = load_source(j, r * j.stride + c);
-    s += v * v;
+  each_group(j, part, [&](int64_t, int64_t, const float (&v)[8]) {
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += v[e] * v[e];
+    sum += s;
   });
-  sum = warp_sum(sum + s);
-  if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kPassWarps; ++i) sum += shared[i];
-    j.partial[part] = static_cast<float>(sum);
-  }
+  block_sum_to(sum, &j.partial[part]);
 }
 
-__device__ __forceinline__ void split(float v, __half* hi, __half* lo) {
-  *hi = __float2half_rn(v);
-  *lo = __float2half_rn(v - __half2float(*hi));
+__device__ __forceinline__ float mean_of(float sum, const NsMomentum& m) {
+  return m.inv_w != 0.0f ? sum * m.inv_w : sum / static_cast<float>(m.w);
+}
+
+// The momentum update of a unit's matrices (W = kWorld ranks; 0: any), and the sums
+// of squares of u. Bound by HBM: 2 W + 12 bytes an element.
+template <int kWorld>
+__global__ void __launch_bounds__(32 * kPassWarps) ns_momentum(const __grid_constant__ MomentumParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int part;
+  const PassMat& j = pass_mat(p.pass, &part);
+  const NsMomentum& m = p.m;
+  const int world = kWorld ? kWorld : m.w;
+  float* out = static_cast<float*>(const_cast<void*>(j.source));
+  const int64_t begin = j.flat, end = j.flat + j.rows * j.cols;
+  const int64_t units = (end - (begin & ~int64_t(7)) + 255) / 256;  // of 256 elements: 8 per lane
+  uintptr_t bits = 0;
+  for (int k = 0; k < world; ++k) bits |= reinterpret_cast<uintptr_t>(m.grads[k]);
+  double sum = 0.0;
+  for (int64_t u = static_cast<int64_t>(part) * kPassWarps + threadIdx.x / 32; u < units;
+       u += static_cast<int64_t>(j.parts) * kPassWarps) {
+    const int64_t f = (begin & ~int64_t(7)) + u * 256 + threadIdx.x % 32 * 8;
+    if (f >= end) continue;
+    const int64_t rank = f / m.shard, at = f - rank * m.shard;
+    float* mom = m.momentum[rank] + at;
+    float* to = out + (f - begin);
+    float s = 0.0f;
+    if (f >= begin && f + 8 <= end && at + 8 <= m.shard &&
+        ((bits | reinterpret_cast<uintptr_t>(mom) | reinterpret_cast<uintptr_t>(to)) & 15u) == 0) {
+      float4 a = __ldcs(reinterpret_cast<const float4*>(mom)), b = __ldcs(reinterpret_cast<const float4*>(mom) + 1);
+      float g[8] = {};
+      constexpr int kBatch = kWorld ? (kWorld < 8 ? kWorld : 8) : 4;
+      for (int k0 = 0; k0 < world; k0 += kBatch) {
+        uint4 r[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (kWorld || k0 + k < world) r[k] = __ldcs(reinterpret_cast<const uint4*>(m.grads[k0 + k] + f));
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          if (!kWorld && k0 + k >= world) break;
+          float w[8];
+          unpack_bf16(r[k].x, w), unpack_bf16(r[k].y, w + 2), unpack_bf16(r[k].z, w + 4), unpack_bf16(r[k].w, w + 6);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) g[e] += w[e];
+        }
+      }
+      float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}, w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float mean = mean_of(g[e], m);
+        v[e] = m.mu * v[e] + mean;
+        w[e] = m.nesterov ? mean + m.mu * v[e] : v[e];
+        s += w[e] * w[e];
+      }
+      __stcs(reinterpret_cast<float4*>(mom), make_float4(v[0], v[1], v[2], v[3]));
+      __stcs(reinterpret_cast<float4*>(mom) + 1, make_float4(v[4], v[5], v[6], v[7]));
+      reinterpret_cast<float4*>(to)[0] = make_float4(w[0], w[1], w[2], w[3]);
+      reinterpret_cast<float4*>(to)[1] = make_float4(w[4], w[5], w[6], w[7]);
+    } else {
+      for (int64_t q = max(f, begin); q < min(f + 8, end); ++q) {
+        float g = 0.0f;
+        for (int k = 0; k < world; ++k) g += __bfloat162float(__ushort_as_bfloat16(m.grads[k][q]));
+        g = mean_of(g, m);
+        float* mq = m.momentum[q / m.shard] + q % m.shard;
+        const float v = m.mu * *mq + g;
+        *mq = v;
+        const float w = m.nesterov ? g + m.mu * v : v;
+        out[q - begin] = w;
+        s += w * w;
+      }
+    }
+    sum += s;
+  }
+  block_sum_to(sum, &j.partial[part]);
 }
 
 // X_0 as two parts.
@@ -137,11 +246,20 @@ __global__ void __launch_bounds__(32 * kPassWarps) ns_normalise(const __grid_con
   for (int i = threadIdx.x % 32; i < j.parts; i += 32) sum += j.partial[i];
   sum = warp_sum(sum);
   const float inv = static_cast<float>(1.0 / (sqrt(sum) + p.eps));
-  each_element(j, part, [&](int64_t r, int64_t c) {
-    __half hi, lo;
-    split(load_source(j, r * j.stride + c) * inv * kScaleX, &hi, &lo);
-    j.hi[r * j.ld + c] = hi;
-    j.lo[r * j.ld + c] = lo;
+  each_group(j, part, [&](int64_t r, int64_t c, const float (&v)[8]) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      // inv first: a tiny norm's reciprocal times 2^12 may not fit
+      const float a = v[2 * e] * inv * kScaleX, b = v[2 * e + 1] * inv * kScaleX;
+      const __half2 h = __floats2half2_rn(a, b);
+      const float2 f = __half22float2(h);
+      const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+      hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+      lo[e] = *reinterpret_cast<const uint32_t*>(&l);
+    }
+    *reinterpret_cast<uint4*>(j.hi + r * j.ld + c) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(j.lo + r * j.ld + c) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   });
 }
 
@@ -503,7 +621,7 @@ int terms_of(const NsJob& j, const NsPlan& plan) {
 }
 
 int parts_of(const NsJob& j) {
-  const int64_t units = j.rows * ((j.cols + kUnitCols - 1) / kUnitCols);
+  const int64_t units = j.rows * ((j.cols + kUnit - 1) / kUnit);
   return static_cast<int>(std::min<int64_t>(kMaxParts, (units + kPassWarps - 1) / kPassWarps));
 }
 
@@ -647,11 +765,24 @@ int launch_product(GemmParams<kMats>& p, const Device& dev, cudaStream_t stream)
                       stream, p);
 }
 
+int launch_momentum(const MomentumParams& p, int blocks, cudaStream_t stream) {
+  const auto go = [&](auto kernel) { return launch_after(kernel, blocks, 1, 32 * kPassWarps, 0, stream, p); };
+  switch (p.m.w) {
+    case 1: return go(ns_momentum<1>);
+    case 2: return go(ns_momentum<2>);
+    case 4: return go(ns_momentum<4>);
+    case 8: return go(ns_momentum<8>);
+    case 16: return go(ns_momentum<16>);
+    default: return go(ns_momentum<0>);
+  }
+}
+
 // One launch's matrices through all steps.
 template <int kMats>
-int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms, const NsApply* apply,
-              unsigned char* workspace, const Device& dev, cudaStream_t stream) {
-  static thread_local PassParams pass;
+int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms, const NsMomentum* momentum,
+              const NsApply* apply, unsigned char* workspace, const Device& dev, cudaStream_t stream) {
+  static thread_local MomentumParams first;
+  PassParams& pass = first.pass;
   static thread_local GemmParams<kMats> p;
   struct Maps {
     CUtensorMap x[2][2], a[2], poly[2];
@@ -672,12 +803,17 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
     }
     if (!ok) return FSDP_ECUDA;
     blocks += parts_of(j);
-    pass.mat[i] = {j.source, j.source_stride, j.rows, j.cols, b.x[0][0], b.x[0][1], b.ld_x, b.partial, j.dtype,
-                   parts_of(j), blocks};
+    pass.mat[i] = {j.source, j.source_stride, j.rows, j.cols, b.x[0][0], b.x[0][1], b.ld_x, b.partial, j.flat,
+                   j.dtype, parts_of(j), blocks};
   }
   pass.count = count;
   pass.eps = plan.eps;
-  ns_squares<<<blocks, 32 * kPassWarps, 0, stream>>>(pass);
+  if (momentum) {
+    first.m = *momentum;
+    if (int rc = launch_momentum(first, blocks, stream)) return rc;
+  } else {
+    ns_squares<<<blocks, 32 * kPassWarps, 0, stream>>>(pass);
+  }
   ns_normalise<<<blocks, 32 * kPassWarps, 0, stream>>>(pass);
   if (cudaGetLastError() != cudaSuccess) return FSDP_ECUDA;
   p.count = count;
@@ -796,8 +932,8 @@ int64_t ns_workspace_bytes(const std::vector<NsJob>& jobs, const NsPlan& plan) {
   return bytes;
 }
 
-int ns_run(const std::vector<NsJob>& jobs, const NsPlan& plan, const NsApply* apply, void* workspace,
-           cudaStream_t stream) {
+int ns_run(const std::vector<NsJob>& jobs, const NsPlan& plan, const NsMomentum* momentum, const NsApply* apply,
+           void* workspace, cudaStream_t stream) {
   Device dev;
   if (int rc = device_facts(&dev)) return rc;
   if (!encoder()) return FSDP_ECUDA;
@@ -808,8 +944,8 @@ int ns_run(const std::vector<NsJob>& jobs, const NsPlan& plan, const NsApply* ap
       if (terms_of(j, plan) == terms) group.push_back(&j);
     for (size_t at = 0; at < group.size(); at += kMaxMats) {
       const int count = static_cast<int>(std::min<size_t>(kMaxMats, group.size() - at));
-      const int rc = count <= 8 ? run_group<8>(&group[at], count, plan, terms, apply, base, dev, stream)
-                                : run_group<kMaxMats>(&group[at], count, plan, terms, apply, base, dev, stream);
+      const int rc = count <= 8 ? run_group<8>(&group[at], count, plan, terms, momentum, apply, base, dev, stream)
+                                : run_group<kMaxMats>(&group[at], count, plan, terms, momentum, apply, base, dev, stream);
       if (rc != FSDP_OK) return rc;
       for (int i = 0; i < count; ++i) base += carve(*group[at + i], plan, nullptr, nullptr);
     }
@@ -877,7 +1013,7 @@ extern "C" int fsdp_newton_schulz(const fsdp_matrix_t* matrices, int32_t n, cons
     if (ws.overlaps({j.source, j.rows, j.cols, j.source_stride, size_of_dtype(j.dtype)}) ||
         ws.overlaps({j.out, j.rows, j.cols, j.out_stride, 2}))
       return FSDP_EALIAS;
-  return ns_run(jobs, plan, nullptr, workspace, reinterpret_cast<cudaStream_t>(stream));
+  return ns_run(jobs, plan, nullptr, nullptr, workspace, reinterpret_cast<cudaStream_t>(stream));
 } catch (const std::bad_alloc&) {
   return FSDP_ECUDA;
 }

@@ -32,6 +32,19 @@ struct NsApply {
   float keep;     // 1 - lr * weight_decay
 };
 
+// The step's first part, where the matrices are a unit's momentum updates: the
+// pass that sums squares also folds the gradients and updates the momentum, and
+// writes each u to its job's (fp32, contiguous) source.
+struct NsMomentum {
+  const uint16_t* grads[FSDP_MAX_WORLD];
+  float* momentum[FSDP_MAX_WORLD];
+  int64_t shard;
+  int32_t w;
+  float mu;
+  float inv_w;  // 1 / W where W is a power of two, else 0
+  int32_t nesterov;
+};
+
 // The checked parameters of a call.
 struct NsPlan {
   int steps = 5;
@@ -42,7 +55,7 @@ struct NsPlan {
 
 int ns_plan(const fsdp_newton_schulz_t* h, NsPlan* plan);
 int64_t ns_workspace_bytes(const std::vector<NsJob>& jobs, const NsPlan& plan);
-int ns_run(const std::vector<NsJob>& jobs, const NsPlan& plan, const NsApply* apply, void* workspace,
-           cudaStream_t stream);
+int ns_run(const std::vector<NsJob>& jobs, const NsPlan& plan, const NsMomentum* momentum, const NsApply* apply,
+           void* workspace, cudaStream_t stream);
 
 }  // namespace fsdp

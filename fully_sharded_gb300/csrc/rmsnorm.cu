@@ -4,6 +4,12 @@
 // With h = x + residual, r = (mean h^2 + eps)^(-1/2), n = h r: y = n gain, and
 // for u = dy gain, from dr/dh_j = -r^3 h_j / cols,
 //   dx_j = r (u_j - n_j mean_i(u_i n_i)) + dh_j,   dgain_j = sum_rows dy_j n_j.
+//
+// Both are bound by HBM (5 to 10 operations for 4 to 8 bytes moved per element at
+// bf16), so a row is read once: it stays in its threads' registers between the
+// sum over the row and the writes. A row belongs to one warp (short rows, several
+// to a block) or to one block; each thread holds up to kV groups of 8 elements.
+// Rows longer than that are read twice (norm_long_rows and its like).
 #include "fsdp.h"
 #include "strided.h"
 
@@ -11,45 +17,161 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
 namespace fsdp {
 namespace {
 
-constexpr int kNormThreads = 256;
 constexpr int64_t kMaxCols = int64_t(1) << 30;
+constexpr int kMaxV = 4;              // groups of 8 elements per thread
+constexpr int kMaxThreads = 512;      // of a row held in registers
+constexpr int kLongThreads = 256;     // rows beyond the registers
 
-template <typename T>
-__device__ __forceinline__ float load1(const T* p);
-template <>
+// Where a thread's 8 kV elements of a row lie.
+//   kVector: groups of 8 consecutive elements, read and written as vectors: every
+//     row of every array starts on a 16-byte boundary.
+//   kGroups: the same elements one by one (rows off that alignment, 8-bit groups).
+//   kStrided: element by element across the row's threads, so that a warp's
+//     accesses stay contiguous (rows off alignment, no groups).
+enum Map { kVector, kGroups, kStrided };
+
 __device__ __forceinline__ float load1(const float* p) { return *p; }
-template <>
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ uint8_t to_e4m3(float v) {
+  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));
+}
+__device__ __forceinline__ void store1(uint8_t* p, float v) { *p = to_e4m3(v); }
+
+__device__ __forceinline__ void load_vec(const float* p, float* v) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void unpack(uint32_t two, float* v) {
+  v[0] = __uint_as_float(two << 16);
+  v[1] = __uint_as_float(two & 0xffff0000u);
+}
+__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float* v) {
+  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+  unpack(a.x, v), unpack(a.y, v + 2), unpack(a.z, v + 4), unpack(a.w, v + 6);
+}
+__device__ __forceinline__ void store_vec(float* p, const float* v) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  const __nv_bfloat162 two = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&two);
+}
+__device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float* v) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7]));
+}
+__device__ __forceinline__ void store_vec(uint8_t* p, const float* v) {
+  uint32_t two[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    two[e] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * e], v[2 * e + 1]), __NV_SATFINITE, __NV_E4M3);
+  *reinterpret_cast<uint2*>(p) = make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
+}
 
 __device__ __forceinline__ float load_gain(const void* gain, int32_t dtype, int64_t j) {
   return dtype == FSDP_DTYPE_F32 ? load1(static_cast<const float*>(gain) + j)
                                  : load1(static_cast<const __nv_bfloat16*>(gain) + j);
 }
+// 8 gains from j on (zeros past the end); as vectors where their place allows it.
+__device__ __forceinline__ void load_gain8(const void* gain, int32_t dtype, int64_t j, int64_t cols, float* v) {
+  if (dtype == FSDP_DTYPE_F32) {
+    const float* p = static_cast<const float*>(gain) + j;
+    if (j + 8 <= cols && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+      const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      return;
+    }
+  } else {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(gain) + j;
+    if (j + 8 <= cols && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p);
+      unpack(a.x, v), unpack(a.y, v + 2), unpack(a.z, v + 4), unpack(a.w, v + 6);
+      return;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = j + e < cols ? load_gain(gain, dtype, j + e) : 0.0f;
+}
 
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));
+// The row's threads: `t` of `n` (n = 32: a warp of its own row; else the block).
+struct RowThreads {
+  int t, n;
+};
+
+// First element of group v, or element (v, e) in the strided map.
+template <Map kMap>
+__device__ __forceinline__ int64_t place(const RowThreads& r, int v, int e) {
+  return kMap == kStrided ? static_cast<int64_t>(v * 8 + e) * r.n + r.t : (static_cast<int64_t>(v) * r.n + r.t) * 8 + e;
+}
+
+template <Map kMap, typename T>
+__device__ __forceinline__ void load_group(const T* p, const RowThreads& r, int v, int64_t cols, float* out) {
+  if (kMap == kVector && place<kMap>(r, v, 0) + 8 <= cols) {
+    load_vec(p + place<kMap>(r, v, 0), out);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int64_t j = place<kMap>(r, v, e);
+    out[e] = j < cols ? load1(p + j) : 0.0f;
+  }
+}
+
+template <Map kMap, typename T>
+__device__ __forceinline__ void store_group(T* p, const RowThreads& r, int v, int64_t cols, const float* in) {
+  if (kMap == kVector && place<kMap>(r, v, 0) + 8 <= cols) {
+    store_vec(p + place<kMap>(r, v, 0), in);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int64_t j = place<kMap>(r, v, e);
+    if (j < cols) store1(p + j, in[e]);
+  }
+}
+
+template <Map kMap>
+__device__ __forceinline__ void gain_group(const void* gain, int32_t dtype, const RowThreads& r, int v, int64_t cols,
+                                           float* out) {
+  if (kMap != kStrided) {
+    load_gain8(gain, dtype, place<kMap>(r, v, 0), cols, out);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int64_t j = place<kMap>(r, v, e);
+    out[e] = j < cols ? load_gain(gain, dtype, j) : 0.0f;
+  }
 }
 
 template <bool kMax>
-__device__ __forceinline__ float block_reduce(float v, float* shared) {
-  for (int o = 16; o > 0; o >>= 1) {
+__device__ __forceinline__ float warp_reduce(float v, int lanes = 32) {
+  for (int o = lanes / 2; o > 0; o >>= 1) {
     const float w = __shfl_xor_sync(0xffffffffu, v, o);
     v = kMax ? fmaxf(v, w) : v + w;
   }
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = shared[0];
-  for (int i = 1; i < kNormThreads / 32; ++i) v = kMax ? fmaxf(v, shared[i]) : v + shared[i];
   return v;
+}
+
+// Over the row's threads; every one gets the result. `shared`: 32 floats, free to
+// be written (the caller's previous reduction used another one).
+template <bool kMax>
+__device__ __forceinline__ float row_reduce(float v, const RowThreads& r, float* shared) {
+  v = warp_reduce<kMax>(v);
+  if (r.n == 32) return v;
+  if (r.t % 32 == 0) shared[r.t / 32] = v;
+  __syncthreads();
+  const int warps = r.n / 32;
+  return warp_reduce<kMax>(r.t % 32 < warps ? shared[r.t % 32] : 0.0f);  // zero is neutral: maxima are of |y|
 }
 
 struct NormParams {
@@ -57,47 +179,148 @@ struct NormParams {
   const void *x, *residual, *gain;
   void *h, *y;
   float *scales, *rstd;
+  int32_t threads;  // of a row
 };
 
-// One block per row, the row read twice.
-template <typename T, bool kE4m3>
-__global__ void __launch_bounds__(kNormThreads) norm_rows(const NormParams p) {
-  __shared__ float shared[kNormThreads / 32];
+// kQuant 0: y of the inputs' type; 1: 8 bits, one scale per row; 2: 8 bits, scales per group.
+template <typename T, int kQuant, Map kMap, int kV>
+__global__ void __launch_bounds__(kMaxThreads) norm_rows(const __grid_constant__ NormParams p) {
+  __shared__ float shared[3][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int64_t cols = p.a.cols;
+  const RowThreads r{static_cast<int>(threadIdx.x) % p.threads, p.threads};
+  const int per_block = blockDim.x / p.threads;
+  int turn = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / p.threads; row < p.a.rows;
+       row += static_cast<int64_t>(gridDim.x) * per_block) {
+    float v[kV][8], sum = 0.0f;
+    const T* x = static_cast<const T*>(p.x) + row * p.a.x_stride;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) load_group<kMap>(x, r, k, cols, v[k]);
+    if (p.residual) {
+      const T* res = static_cast<const T*>(p.residual) + row * p.a.residual_stride;
+      float w[kV][8];
+#pragma unroll
+      for (int k = 0; k < kV; ++k) load_group<kMap>(res, r, k, cols, w[k]);
+#pragma unroll
+      for (int k = 0; k < kV; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[k][e] += w[k][e];
+      T* h = static_cast<T*>(p.h) + row * p.a.h_stride;
+#pragma unroll
+      for (int k = 0; k < kV; ++k) store_group<kMap>(h, r, k, cols, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kV; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += v[k][e] * v[k][e];
+    // a block alternates between two sets of partial sums: the barrier inside one
+    // reduction ends every read of the one before the last
+    float* room = shared[turn];
+    turn ^= 1;
+    const float rstd = rsqrtf(row_reduce<false>(sum, r, room) / static_cast<float>(cols) + static_cast<float>(p.a.eps));
+    if (p.rstd && r.t == 0) p.rstd[row] = rstd;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      float g[8];
+      gain_group<kMap>(p.gain, p.a.gain_dtype, r, k, cols, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[k][e] *= rstd * g[e];
+    }
+    if constexpr (kQuant == 0) {
+      T* y = static_cast<T*>(p.y) + row * p.a.y_stride;
+#pragma unroll
+      for (int k = 0; k < kV; ++k) store_group<kMap>(y, r, k, cols, v[k]);
+    } else {
+      uint8_t* y = static_cast<uint8_t*>(p.y) + row * p.a.y_stride;
+      float top[kV], all = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kV; ++k) {
+        top[k] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top[k] = fmaxf(top[k], fabsf(v[k][e]));
+        all = fmaxf(all, top[k]);
+      }
+      if constexpr (kQuant == 1) {
+        all = row_reduce<true>(all, r, shared[2]);
+        // the next row's first reduction has a barrier before shared[2] is written again
+      }
+      const int64_t groups = kQuant == 1 ? 1 : (cols + p.a.group - 1) / p.a.group;
+#pragma unroll
+      for (int k = 0; k < kV; ++k) {
+        if constexpr (kQuant == 2) all = warp_reduce<true>(top[k], p.a.group / 8);
+        const float scale = fmaxf(all / 448.0f, 0x1p-126f);
+        const int64_t j = place<kMap>(r, k, 0);
+        if (kQuant == 1 ? (k == 0 && r.t == 0) : (j < cols && j % p.a.group == 0))
+          p.scales[row * groups + (kQuant == 1 ? 0 : j / p.a.group)] = scale;
+        float q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = v[k][e] / scale;
+        store_group<kMap>(y, r, k, cols, q);
+      }
+    }
+  }
+}
+
+template <bool kMax>
+__device__ __forceinline__ float long_reduce(float v, float* shared) {
+  __syncthreads();
+  return row_reduce<kMax>(v, RowThreads{static_cast<int>(threadIdx.x), kLongThreads}, shared);
+}
+
+// Rows beyond the registers: one block per row, the row read twice (thrice with 8-bit groups).
+template <typename T, int kQuant>
+__global__ void __launch_bounds__(kLongThreads) norm_long_rows(const __grid_constant__ NormParams p) {
+  __shared__ float shared[32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t cols = p.a.cols;
   for (int64_t row = blockIdx.x; row < p.a.rows; row += gridDim.x) {
     const T* x = static_cast<const T*>(p.x) + row * p.a.x_stride;
     const T* res = p.residual ? static_cast<const T*>(p.residual) + row * p.a.residual_stride : nullptr;
     T* h = p.h ? static_cast<T*>(p.h) + row * p.a.h_stride : nullptr;
     float sum = 0.0f;
-    for (int64_t j = threadIdx.x; j < cols; j += kNormThreads) {
+    for (int64_t j = threadIdx.x; j < cols; j += kLongThreads) {
       const float v = load1(x + j) + (res ? load1(res + j) : 0.0f);
       sum += v * v;
     }
-    const float rstd = rsqrtf(block_reduce<false>(sum, shared) / static_cast<float>(cols) + static_cast<float>(p.a.eps));
+    const float rstd = rsqrtf(long_reduce<false>(sum, shared) / static_cast<float>(cols) + static_cast<float>(p.a.eps));
     if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
-    if constexpr (kE4m3) {
-      uint8_t* y = static_cast<uint8_t*>(p.y) + row * p.a.y_stride;
-      const int64_t group = p.a.group ? p.a.group : cols;
-      const int64_t groups = (cols + group - 1) / group;
-      for (int64_t g = 0; g < groups; ++g) {
-        const int64_t end = min(cols, (g + 1) * group);
-        float top = 0.0f;
-        for (int64_t j = g * group + threadIdx.x; j < end; j += kNormThreads)
-          top = fmaxf(top, fabsf((load1(x + j) + (res ? load1(res + j) : 0.0f)) * rstd * load_gain(p.gain, p.a.gain_dtype, j)));
-        const float scale = fmaxf(block_reduce<true>(top, shared) / 448.0f, 0x1p-126f);
-        if (threadIdx.x == 0) p.scales[row * groups + g] = scale;
-        for (int64_t j = g * group + threadIdx.x; j < end; j += kNormThreads) {
-          const float v = load1(x + j) + (res ? load1(res + j) : 0.0f);
-          y[j] = to_e4m3(v * rstd * load_gain(p.gain, p.a.gain_dtype, j) / scale);
-          if (h) store1(h + j, v);
-        }
+    const auto value = [&](int64_t j) { return load1(x + j) + (res ? load1(res + j) : 0.0f); };
+    const auto gain = [&](int64_t j) { return rstd * load_gain(p.gain, p.a.gain_dtype, j); };
+    if constexpr (kQuant == 0) {
+      T* y = static_cast<T*>(p.y) + row * p.a.y_stride;
+      for (int64_t j = threadIdx.x; j < cols; j += kLongThreads) {
+        const float v = value(j);
+        if (h) store1(h + j, v);
+        store1(y + j, v * gain(j));
       }
     } else {
-      T* y = static_cast<T*>(p.y) + row * p.a.y_stride;
-      for (int64_t j = threadIdx.x; j < cols; j += kNormThreads) {
-        const float v = load1(x + j) + (res ? load1(res + j) : 0.0f);
-        if (h) store1(h + j, v);
-        store1(y + j, v * rstd * load_gain(p.gain, p.a.gain_dtype, j));
+      uint8_t* y = static_cast<uint8_t*>(p.y) + row * p.a.y_stride;
+      float all = 0.0f;
+      if constexpr (kQuant == 1) {
+        for (int64_t j = threadIdx.x; j < cols; j += kLongThreads) all = fmaxf(all, fabsf(value(j) * gain(j)));
+        all = long_reduce<true>(all, shared);
+        if (threadIdx.x == 0) p.scales[row] = fmaxf(all / 448.0f, 0x1p-126f);
+      }
+      const int64_t groups = kQuant == 1 ? 1 : (cols + p.a.group - 1) / p.a.group;
+      // a lane holds 8 consecutive elements, a group 4 to 32 lanes of a warp
+      for (int64_t j0 = 0; j0 < cols; j0 += kLongThreads * 8) {
+        const int64_t j = j0 + threadIdx.x * 8;
+        float v[8], top = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[e] = j + e < cols ? value(j + e) : 0.0f;
+          if (j + e < cols && h) store1(h + j + e, v[e]);
+          v[e] *= j + e < cols ? gain(j + e) : 0.0f;
+          top = fmaxf(top, fabsf(v[e]));
+        }
+        if constexpr (kQuant == 2) all = warp_reduce<true>(top, p.a.group / 8);
+        const float scale = fmaxf(all / 448.0f, 0x1p-126f);
+        if (kQuant == 2 && j < cols && j % p.a.group == 0) p.scales[row * groups + j / p.a.group] = scale;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (j + e < cols) y[j + e] = to_e4m3(v[e] / scale);
       }
     }
   }
@@ -108,30 +331,112 @@ struct NormBwdParams {
   const void *dy, *h, *gain, *dh;
   const float* rstd;
   void *dx, *dgain;
-  float* partial;  // [gridDim.x][cols]
+  float* partial;   // [parts][cols]
+  int32_t threads;  // of a row
+  int32_t parts;
 };
 
-// One block per row in turn; its share of dgain in its own row of `partial`.
+// A block takes every gridDim-th row (or, with a warp per row, set of rows); a
+// thread keeps its columns' share of dgain in registers over all its rows. The
+// warps' shares are added in order, then written as the block's row of `partial`.
+template <typename T, Map kMap, int kV>
+__global__ void __launch_bounds__(kMaxThreads) norm_rows_backward(const __grid_constant__ NormBwdParams p) {
+  __shared__ float shared[2][32];
+  extern __shared__ float total[];  // [cols], with a warp per row
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int64_t cols = p.a.cols;
+  const RowThreads r{static_cast<int>(threadIdx.x) % p.threads, p.threads};
+  const int per_block = blockDim.x / p.threads;
+  float acc[kV][8] = {};
+  int turn = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / p.threads; row < p.a.rows;
+       row += static_cast<int64_t>(gridDim.x) * per_block) {
+    const T* dy = static_cast<const T*>(p.dy) + row * p.a.dy_stride;
+    const T* h = static_cast<const T*>(p.h) + row * p.a.h_stride;
+    float u[kV][8], n[kV][8], sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      load_group<kMap>(dy, r, k, cols, u[k]);
+      load_group<kMap>(h, r, k, cols, n[k]);
+    }
+    const float rstd = p.rstd[row];
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      float g[8];
+      gain_group<kMap>(p.gain, p.a.gain_dtype, r, k, cols, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        n[k][e] *= rstd;
+        acc[k][e] += u[k][e] * n[k][e];
+        u[k][e] *= g[e];
+        sum += u[k][e] * n[k][e];
+      }
+    }
+    const float mean = row_reduce<false>(sum, r, shared[turn]) / static_cast<float>(cols);
+    turn ^= 1;
+    T* dx = static_cast<T*>(p.dx) + row * p.a.dx_stride;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      float d[8];
+      if (p.dh) {
+        load_group<kMap>(static_cast<const T*>(p.dh) + row * p.a.dh_stride, r, k, cols, d);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] = 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] += rstd * (u[k][e] - n[k][e] * mean);
+      store_group<kMap>(dx, r, k, cols, d);
+    }
+  }
+  float* mine = p.partial + blockIdx.x * cols;
+  if (per_block > 1) {
+    const int slot = threadIdx.x / p.threads;
+    for (int w = 0; w < per_block; ++w) {
+      if (w == slot) {
+#pragma unroll
+        for (int k = 0; k < kV; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int64_t j = place<kMap>(r, k, e);
+            if (j >= cols) continue;
+            if (w + 1 < per_block)
+              total[j] = (w > 0 ? total[j] : 0.0f) + acc[k][e];
+            else
+              mine[j] = total[j] + acc[k][e];
+          }
+      }
+      __syncthreads();
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kV; ++k) store_group<kMap == kVector ? kGroups : kMap>(mine, r, k, cols, acc[k]);
+  }
+}
+
+// Rows beyond the registers: the row read twice, dgain's share kept in `partial`.
 template <typename T>
-__global__ void __launch_bounds__(kNormThreads) norm_rows_backward(const NormBwdParams p) {
-  __shared__ float shared[kNormThreads / 32];
+__global__ void __launch_bounds__(kLongThreads) norm_long_rows_backward(const __grid_constant__ NormBwdParams p) {
+  __shared__ float shared[32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t cols = p.a.cols;
   float* mine = p.partial + blockIdx.x * cols;
-  for (int64_t j = threadIdx.x; j < cols; j += kNormThreads) mine[j] = 0.0f;
-  for (int64_t row = blockIdx.x; row < p.a.rows; row += gridDim.x) {
+  bool first = true;
+  for (int64_t row = blockIdx.x; row < p.a.rows; row += gridDim.x, first = false) {
     const T* dy = static_cast<const T*>(p.dy) + row * p.a.dy_stride;
     const T* h = static_cast<const T*>(p.h) + row * p.a.h_stride;
     const T* dh = p.dh ? static_cast<const T*>(p.dh) + row * p.a.dh_stride : nullptr;
     T* dx = static_cast<T*>(p.dx) + row * p.a.dx_stride;
     const float r = p.rstd[row];
     float sum = 0.0f;
-    for (int64_t j = threadIdx.x; j < cols; j += kNormThreads) {
+    for (int64_t j = threadIdx.x; j < cols; j += kLongThreads) {
       const float g = load1(dy + j), n = load1(h + j) * r;
       sum += g * load_gain(p.gain, p.a.gain_dtype, j) * n;
-      mine[j] += g * n;
+      mine[j] = (first ? 0.0f : mine[j]) + g * n;
     }
-    const float mean = block_reduce<false>(sum, shared) / static_cast<float>(cols);
-    for (int64_t j = threadIdx.x; j < cols; j += kNormThreads) {
+    const float mean = long_reduce<false>(sum, shared) / static_cast<float>(cols);
+    for (int64_t j = threadIdx.x; j < cols; j += kLongThreads) {
       const float n = load1(h + j) * r;
       float v = r * (load1(dy + j) * load_gain(p.gain, p.a.gain_dtype, j) - n * mean);
       if (dh) v += load1(dh + j);
@@ -140,18 +445,142 @@ __global__ void __launch_bounds__(kNormThreads) norm_rows_backward(const NormBwd
   }
 }
 
-__global__ void __launch_bounds__(kNormThreads) sum_partials(const NormBwdParams p, int parts) {
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x;
-  if (j >= p.a.cols) return;
+// dgain: 32 columns per block, its 8 warps share the rows of `partial`.
+__global__ void __launch_bounds__(256) sum_partials(const __grid_constant__ NormBwdParams p) {
+  __shared__ float shared[8][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float sum = 0.0f;
-  for (int i = 0; i < parts; ++i) sum += p.partial[i * p.a.cols + j];
+  if (j < p.a.cols) {
+    int i = warp;
+    for (; i + 24 < p.parts; i += 32) {
+      const float a = p.partial[i * p.a.cols + j], b = p.partial[(i + 8) * p.a.cols + j];
+      const float c = p.partial[(i + 16) * p.a.cols + j], d = p.partial[(i + 24) * p.a.cols + j];
+      sum += (a + b) + (c + d);
+    }
+    for (; i < p.parts; i += 8) sum += p.partial[i * p.a.cols + j];
+  }
+  shared[warp][lane] = sum;
+  __syncthreads();
+  if (warp != 0 || j >= p.a.cols) return;
+  for (int w = 1; w < 8; ++w) sum += shared[w][lane];
   if (p.a.gain_dtype == FSDP_DTYPE_F32)
     static_cast<float*>(p.dgain)[j] = sum;
   else
     store1(static_cast<__nv_bfloat16*>(p.dgain) + j, sum);
 }
 
-int backward_blocks(int64_t rows) { return static_cast<int>(std::min<int64_t>(std::max<int64_t>(rows, 1), 608)); }
+// ------------------------------------------------------------- host side
+
+template <typename P>
+int launch_rows(void (*kernel)(P), int grid, int threads, int smem, cudaStream_t stream, const P& p) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FSDP_OK : FSDP_ECUDA;
+}
+
+// How a row is spread: kV groups of 8 elements for each of `threads` threads.
+struct Spread {
+  int v = 0, threads = 0, per_block = 1;  // v = 0: a long row
+};
+
+int warps_for(int64_t cols, int v) { return static_cast<int>((cols + 256 * v - 1) / (256 * v)); }
+
+constexpr int kFewRows = 512;  // about as many rows as blocks run at once
+
+Spread forward_spread(int64_t rows, int64_t cols) {
+  Spread s;
+  if (cols > kMaxThreads * 8 * kMaxV) return s;
+  s.v = rows < kFewRows ? 1 : static_cast<int>(std::min<int64_t>(kMaxV, (cols + 1023) / 1024));
+  if (rows >= kFewRows && cols <= 1024) s.v = warps_for(cols, 1);  // a warp per row
+  while (warps_for(cols, s.v) > kMaxThreads / 32) ++s.v;
+  s.threads = 32 * warps_for(cols, s.v);
+  if (s.threads == 32) s.per_block = 4;
+  return s;
+}
+
+Spread backward_spread(int64_t rows, int64_t cols) {
+  Spread s;
+  if (cols > kMaxThreads * 8 * kMaxV) return s;
+  s.v = rows < kFewRows ? 1 : static_cast<int>(std::min<int64_t>(kMaxV, (cols + 2047) / 2048));
+  if (rows >= kFewRows && cols <= 1024) s.v = warps_for(cols, 1);
+  while (warps_for(cols, s.v) > kMaxThreads / 32) ++s.v;
+  s.threads = 32 * warps_for(cols, s.v);
+  if (s.threads == 32) s.per_block = 8;
+  return s;
+}
+
+// Blocks of the backward pass: rows of `partial`.
+int backward_parts(int64_t rows, int64_t cols) {
+  const Spread s = backward_spread(rows, cols);
+  return static_cast<int>(std::min<int64_t>((std::max<int64_t>(rows, 1) + s.per_block - 1) / s.per_block, 456));
+}
+
+template <typename T, int kQuant, Map kMap>
+int run_forward(const NormParams& p, const Spread& s, int grid, cudaStream_t st) {
+  const int threads = s.threads * s.per_block;
+  switch (s.v) {
+    case 1: return launch_rows(norm_rows<T, kQuant, kMap, 1>, grid, threads, 0, st, p);
+    case 2: return launch_rows(norm_rows<T, kQuant, kMap, 2>, grid, threads, 0, st, p);
+    case 3: return launch_rows(norm_rows<T, kQuant, kMap, 3>, grid, threads, 0, st, p);
+    default: return launch_rows(norm_rows<T, kQuant, kMap, 4>, grid, threads, 0, st, p);
+  }
+}
+
+template <typename T>
+int forward(NormParams p, bool aligned, cudaStream_t st) {
+  const Spread s = forward_spread(p.a.rows, p.a.cols);
+  p.threads = s.threads;
+  const bool quant = p.a.y_dtype == FSDP_DTYPE_E4M3;
+  const int grid = static_cast<int>(std::min<int64_t>((p.a.rows + s.per_block - 1) / s.per_block, 1 << 20));
+  if (s.v == 0) {
+    return launch_rows(!quant ? norm_long_rows<T, 0> : p.a.group == 0 ? norm_long_rows<T, 1> : norm_long_rows<T, 2>, grid,
+                       kLongThreads, 0, st, p);
+  }
+  if (!quant) return aligned ? run_forward<T, 0, kVector>(p, s, grid, st) : run_forward<T, 0, kStrided>(p, s, grid, st);
+  if (p.a.group == 0)
+    return aligned ? run_forward<T, 1, kVector>(p, s, grid, st) : run_forward<T, 1, kStrided>(p, s, grid, st);
+  return aligned ? run_forward<T, 2, kVector>(p, s, grid, st) : run_forward<T, 2, kGroups>(p, s, grid, st);
+}
+
+template <typename T, Map kMap>
+int run_backward(const NormBwdParams& p, const Spread& s, cudaStream_t st) {
+  const int threads = s.threads * s.per_block, smem = s.per_block > 1 ? static_cast<int>(p.a.cols * 4) : 0;
+  switch (s.v) {
+    case 1: return launch_rows(norm_rows_backward<T, kMap, 1>, p.parts, threads, smem, st, p);
+    case 2: return launch_rows(norm_rows_backward<T, kMap, 2>, p.parts, threads, smem, st, p);
+    case 3: return launch_rows(norm_rows_backward<T, kMap, 3>, p.parts, threads, smem, st, p);
+    default: return launch_rows(norm_rows_backward<T, kMap, 4>, p.parts, threads, smem, st, p);
+  }
+}
+
+template <typename T>
+int backward(NormBwdParams p, bool aligned, cudaStream_t st) {
+  const Spread s = backward_spread(p.a.rows, p.a.cols);
+  p.threads = s.threads;
+  p.parts = backward_parts(p.a.rows, p.a.cols);
+  int rc;
+  if (s.v == 0)
+    rc = launch_rows(norm_long_rows_backward<T>, p.parts, kLongThreads, 0, st, p);
+  else
+    rc = aligned ? run_backward<T, kVector>(p, s, st) : run_backward<T, kStrided>(p, s, st);
+  if (rc != FSDP_OK) return rc;
+  return launch_rows(sum_partials, static_cast<int>((p.a.cols + 31) / 32), 256, 0, st, p);
+}
+
+// Every row of the array starts on a boundary of `bytes`.
+bool rows_aligned(const void* q, int64_t rows, int64_t stride, int size, int bytes = 16) {
+  return !q || (reinterpret_cast<uintptr_t>(q) % bytes == 0 && (rows < 2 || stride * size % bytes == 0));
+}
 
 }  // namespace
 }  // namespace fsdp
@@ -189,20 +618,17 @@ extern "C" int fsdp_rmsnorm(const fsdp_rmsnorm_t* a, const void* x, const void* 
       if (!in_place) return FSDP_EALIAS;
     }
   }
-  const NormParams p{*a, x, residual, gain, h_out, y, scales, rstd};
-  const int grid = static_cast<int>(std::min<int64_t>(a->rows, 1 << 16));
+  const NormParams p{*a, x, residual, gain, h_out, y, scales, rstd, 0};
+  const bool aligned = rows_aligned(x, a->rows, a->x_stride, es) && rows_aligned(residual, a->rows, a->residual_stride, es) &&
+                       rows_aligned(h_out, a->rows, a->h_stride, es) &&
+                       rows_aligned(y, a->rows, a->y_stride, size_of_dtype(a->y_dtype), e4m3 ? 8 : 16);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (a->dtype == FSDP_DTYPE_F32)
-    e4m3 ? norm_rows<float, true><<<grid, kNormThreads, 0, st>>>(p) : norm_rows<float, false><<<grid, kNormThreads, 0, st>>>(p);
-  else
-    e4m3 ? norm_rows<__nv_bfloat16, true><<<grid, kNormThreads, 0, st>>>(p)
-         : norm_rows<__nv_bfloat16, false><<<grid, kNormThreads, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FSDP_OK : FSDP_ECUDA;
+  return a->dtype == FSDP_DTYPE_F32 ? forward<float>(p, aligned, st) : forward<__nv_bfloat16>(p, aligned, st);
 }
 
 extern "C" int fsdp_rmsnorm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes_out) {
   if (!bytes_out || rows < 0 || cols < 1 || cols > kMaxCols) return FSDP_EINVAL;
-  *bytes_out = backward_blocks(rows) * cols * 4 + 16;
+  *bytes_out = backward_parts(rows, cols) * cols * 4 + 16;
   return FSDP_OK;
 }
 
@@ -234,12 +660,8 @@ extern "C" int fsdp_rmsnorm_backward(const fsdp_rmsnorm_backward_t* a, const voi
       if (i && o->overlaps(*i) && !(o == &sdx && (i == &sdy || i == &sdh) && o->same_place(*i))) return FSDP_EALIAS;
   }
   float* partial = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + 15) & ~uintptr_t(15));
-  const NormBwdParams p{*a, dy, h, gain, dh, rstd, dx, dgain, partial};
-  const int grid = backward_blocks(a->rows);
-  if (a->dtype == FSDP_DTYPE_F32)
-    norm_rows_backward<float><<<grid, kNormThreads, 0, st>>>(p);
-  else
-    norm_rows_backward<__nv_bfloat16><<<grid, kNormThreads, 0, st>>>(p);
-  sum_partials<<<static_cast<int>((a->cols + kNormThreads - 1) / kNormThreads), kNormThreads, 0, st>>>(p, grid);
-  return cudaGetLastError() == cudaSuccess ? FSDP_OK : FSDP_ECUDA;
+  const NormBwdParams p{*a, dy, h, gain, dh, rstd, dx, dgain, partial, 0, 0};
+  const bool aligned = rows_aligned(dy, a->rows, a->dy_stride, es) && rows_aligned(h, a->rows, a->h_stride, es) &&
+                       rows_aligned(dh, a->rows, a->dh_stride, es) && rows_aligned(dx, a->rows, a->dx_stride, es);
+  return a->dtype == FSDP_DTYPE_F32 ? backward<float>(p, aligned, st) : backward<__nv_bfloat16>(p, aligned, st);
 }
