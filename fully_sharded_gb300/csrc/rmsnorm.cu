@@ -30,11 +30,13 @@ constexpr int kMaxThreads = 512;      // of a row held in registers
 constexpr int kLongThreads = 256;     // rows beyond the registers
 
 // Where a thread's 8 kV elements of a row lie.
-//   kVector: groups of 8 consecutive elements, read and written as vectors: every
-//     row of every array starts on a 16-byte boundary.
-//   kGroups: the same elements one by one (rows off that alignment, 8-bit groups).
+//   kVector: groups of 8 consecutive elements, read and written as vectors: cols is a
+//     multiple of 8 and every row of every array starts on a 16-byte boundary. (A group
+//     is whole or absent: one predicate and no branch around a load, so that all of
+//     a thread's loads are in flight together.)
+//   kGroups: the same elements one by one (other rows, 8-bit groups).
 //   kStrided: element by element across the row's threads, so that a warp's
-//     accesses stay contiguous (rows off alignment, no groups).
+//     accesses stay contiguous (other rows, no groups).
 enum Map { kVector, kGroups, kStrided };
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
@@ -46,18 +48,34 @@ __device__ __forceinline__ uint8_t to_e4m3(float v) {
 }
 __device__ __forceinline__ void store1(uint8_t* p, float v) { *p = to_e4m3(v); }
 
-__device__ __forceinline__ void load_vec(const float* p, float* v) {
-  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
+// 8 elements as loaded, and as floats.
+template <typename T>
+struct Raw8;
 __device__ __forceinline__ void unpack(uint32_t two, float* v) {
   v[0] = __uint_as_float(two << 16);
   v[1] = __uint_as_float(two & 0xffff0000u);
 }
-__device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float* v) {
-  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-  unpack(a.x, v), unpack(a.y, v + 2), unpack(a.z, v + 4), unpack(a.w, v + 6);
-}
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p, bool there) {
+    a = there ? __ldcs(reinterpret_cast<const float4*>(p)) : make_float4(0, 0, 0, 0);
+    b = there ? __ldcs(reinterpret_cast<const float4*>(p) + 1) : make_float4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void to(float* v) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool there) {
+    a = there ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void to(float* v) const {
+    unpack(a.x, v), unpack(a.y, v + 2), unpack(a.z, v + 4), unpack(a.w, v + 6);
+  }
+};
 __device__ __forceinline__ void store_vec(float* p, const float* v) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -81,27 +99,6 @@ __device__ __forceinline__ float load_gain(const void* gain, int32_t dtype, int6
   return dtype == FSDP_DTYPE_F32 ? load1(static_cast<const float*>(gain) + j)
                                  : load1(static_cast<const __nv_bfloat16*>(gain) + j);
 }
-// 8 gains from j on (zeros past the end); as vectors where their place allows it.
-__device__ __forceinline__ void load_gain8(const void* gain, int32_t dtype, int64_t j, int64_t cols, float* v) {
-  if (dtype == FSDP_DTYPE_F32) {
-    const float* p = static_cast<const float*>(gain) + j;
-    if (j + 8 <= cols && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-      const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-      return;
-    }
-  } else {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(gain) + j;
-    if (j + 8 <= cols && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-      const uint4 a = *reinterpret_cast<const uint4*>(p);
-      unpack(a.x, v), unpack(a.y, v + 2), unpack(a.z, v + 4), unpack(a.w, v + 6);
-      return;
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = j + e < cols ? load_gain(gain, dtype, j + e) : 0.0f;
-}
-
 // The row's threads: `t` of `n` (n = 32: a warp of its own row; else the block).
 struct RowThreads {
   int t, n;
@@ -109,47 +106,81 @@ struct RowThreads {
 
 // First element of group v, or element (v, e) in the strided map.
 template <Map kMap>
-__device__ __forceinline__ int64_t place(const RowThreads& r, int v, int e) {
-  return kMap == kStrided ? static_cast<int64_t>(v * 8 + e) * r.n + r.t : (static_cast<int64_t>(v) * r.n + r.t) * 8 + e;
+__device__ __forceinline__ int place(const RowThreads& r, int v, int e) {
+  return kMap == kStrided ? (v * 8 + e) * r.n + r.t : (v * r.n + r.t) * 8 + e;
 }
 
+// A thread's kV groups of a row, as loaded.
+template <Map kMap, int kV, typename T>
+struct RowLoad {
+  Raw8<T> raw[kMap == kVector ? kV : 1];
+  float v[kMap == kVector ? 1 : kV][8];
+  __device__ __forceinline__ void load(const T* p, const RowThreads& r, int cols, bool there = true) {
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      if constexpr (kMap == kVector) {
+        const int j = place<kMap>(r, k, 0);
+        raw[k].load(p + j, there && j < cols);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int j = place<kMap>(r, k, e);
+          v[k][e] = there && j < cols ? load1(p + j) : 0.0f;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void to(int k, float* out) const {
+    if constexpr (kMap == kVector) {
+      raw[k].to(out);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[e] = v[k][e];
+    }
+  }
+};
+
 template <Map kMap, typename T>
-__device__ __forceinline__ void load_group(const T* p, const RowThreads& r, int v, int64_t cols, float* out) {
-  if (kMap == kVector && place<kMap>(r, v, 0) + 8 <= cols) {
-    load_vec(p + place<kMap>(r, v, 0), out);
+__device__ __forceinline__ void store_group(T* p, const RowThreads& r, int v, int cols, const float* in) {
+  if constexpr (kMap == kVector) {
+    const int j = place<kMap>(r, v, 0);
+    if (j < cols) store_vec(p + j, in);
     return;
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int64_t j = place<kMap>(r, v, e);
-    out[e] = j < cols ? load1(p + j) : 0.0f;
-  }
-}
-
-template <Map kMap, typename T>
-__device__ __forceinline__ void store_group(T* p, const RowThreads& r, int v, int64_t cols, const float* in) {
-  if (kMap == kVector && place<kMap>(r, v, 0) + 8 <= cols) {
-    store_vec(p + place<kMap>(r, v, 0), in);
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int64_t j = place<kMap>(r, v, e);
+    const int j = place<kMap>(r, v, e);
     if (j < cols) store1(p + j, in[e]);
   }
 }
 
+// The gains of group v (zeros past the end); `vectors`: the gain starts on a
+// 16-byte boundary and the map is kVector.
 template <Map kMap>
-__device__ __forceinline__ void gain_group(const void* gain, int32_t dtype, const RowThreads& r, int v, int64_t cols,
-                                           float* out) {
-  if (kMap != kStrided) {
-    load_gain8(gain, dtype, place<kMap>(r, v, 0), cols, out);
+__device__ __forceinline__ void gain_group(const void* gain, int32_t dtype, bool vectors, const RowThreads& r, int v,
+                                           int cols, float* out) {
+  const int j = place<kMap>(r, v, 0);
+  if (kMap == kVector && vectors) {
+    if (dtype == FSDP_DTYPE_F32) {
+      Raw8<float> raw;
+      raw.a = raw.b = make_float4(0, 0, 0, 0);
+      if (j < cols) {
+        raw.a = *reinterpret_cast<const float4*>(static_cast<const float*>(gain) + j);
+        raw.b = *reinterpret_cast<const float4*>(static_cast<const float*>(gain) + j + 4);
+      }
+      raw.to(out);
+    } else {
+      Raw8<__nv_bfloat16> raw;
+      raw.a = make_uint4(0, 0, 0, 0);
+      if (j < cols) raw.a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(gain) + j);
+      raw.to(out);
+    }
     return;
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int64_t j = place<kMap>(r, v, e);
-    out[e] = j < cols ? load_gain(gain, dtype, j) : 0.0f;
+    const int i = place<kMap>(r, v, e);
+    out[e] = i < cols ? load_gain(gain, dtype, i) : 0.0f;
   }
 }
 
@@ -180,6 +211,7 @@ struct NormParams {
   void *h, *y;
   float *scales, *rstd;
   int32_t threads;  // of a row
+  bool gain_vectors;
 };
 
 // kQuant 0: y of the inputs' type; 1: 8 bits, one scale per row; 2: 8 bits, scales per group.
@@ -188,25 +220,25 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows(const __grid_constant__
   __shared__ float shared[3][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int64_t cols = p.a.cols;
+  const int cols = static_cast<int>(p.a.cols);
   const RowThreads r{static_cast<int>(threadIdx.x) % p.threads, p.threads};
   const int per_block = blockDim.x / p.threads;
   int turn = 0;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / p.threads; row < p.a.rows;
        row += static_cast<int64_t>(gridDim.x) * per_block) {
+    RowLoad<kMap, kV, T> x, res;
+    x.load(static_cast<const T*>(p.x) + row * p.a.x_stride, r, cols);
+    res.load(static_cast<const T*>(p.residual) + row * p.a.residual_stride, r, cols, p.residual != nullptr);
     float v[kV][8], sum = 0.0f;
-    const T* x = static_cast<const T*>(p.x) + row * p.a.x_stride;
 #pragma unroll
-    for (int k = 0; k < kV; ++k) load_group<kMap>(x, r, k, cols, v[k]);
+    for (int k = 0; k < kV; ++k) {
+      float w[8];
+      x.to(k, v[k]);
+      res.to(k, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[k][e] += w[e];
+    }
     if (p.residual) {
-      const T* res = static_cast<const T*>(p.residual) + row * p.a.residual_stride;
-      float w[kV][8];
-#pragma unroll
-      for (int k = 0; k < kV; ++k) load_group<kMap>(res, r, k, cols, w[k]);
-#pragma unroll
-      for (int k = 0; k < kV; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[k][e] += w[k][e];
       T* h = static_cast<T*>(p.h) + row * p.a.h_stride;
 #pragma unroll
       for (int k = 0; k < kV; ++k) store_group<kMap>(h, r, k, cols, v[k]);
@@ -215,6 +247,8 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows(const __grid_constant__
     for (int k = 0; k < kV; ++k)
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum += v[k][e] * v[k][e];
+    float g[kV][8];
+    if constexpr (kV == 1) gain_group<kMap>(p.gain, p.a.gain_dtype, p.gain_vectors, r, 0, cols, g[0]);
     // a block alternates between two sets of partial sums: the barrier inside one
     // reduction ends every read of the one before the last
     float* room = shared[turn];
@@ -223,10 +257,9 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows(const __grid_constant__
     if (p.rstd && r.t == 0) p.rstd[row] = rstd;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      float g[8];
-      gain_group<kMap>(p.gain, p.a.gain_dtype, r, k, cols, g);
+      if constexpr (kV > 1) gain_group<kMap>(p.gain, p.a.gain_dtype, p.gain_vectors, r, k, cols, g[k]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] *= rstd * g[e];
+      for (int e = 0; e < 8; ++e) v[k][e] *= rstd * g[k][e];
     }
     if constexpr (kQuant == 0) {
       T* y = static_cast<T*>(p.y) + row * p.a.y_stride;
@@ -246,17 +279,18 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows(const __grid_constant__
         all = row_reduce<true>(all, r, shared[2]);
         // the next row's first reduction has a barrier before shared[2] is written again
       }
-      const int64_t groups = kQuant == 1 ? 1 : (cols + p.a.group - 1) / p.a.group;
+      const int groups = kQuant == 1 ? 1 : (cols + p.a.group - 1) / p.a.group;
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
         if constexpr (kQuant == 2) all = warp_reduce<true>(top[k], p.a.group / 8);
         const float scale = fmaxf(all / 448.0f, 0x1p-126f);
-        const int64_t j = place<kMap>(r, k, 0);
+        const int j = place<kMap>(r, k, 0);
         if (kQuant == 1 ? (k == 0 && r.t == 0) : (j < cols && j % p.a.group == 0))
           p.scales[row * groups + (kQuant == 1 ? 0 : j / p.a.group)] = scale;
+        const float inverse = 1.0f / scale;
         float q[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = v[k][e] / scale;
+        for (int e = 0; e < 8; ++e) q[e] = v[k][e] * inverse;
         store_group<kMap>(y, r, k, cols, q);
       }
     }
@@ -320,7 +354,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_rows(const __grid_cons
         if (kQuant == 2 && j < cols && j % p.a.group == 0) p.scales[row * groups + j / p.a.group] = scale;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (j + e < cols) y[j + e] = to_e4m3(v[e] / scale);
+          if (j + e < cols) y[j + e] = to_e4m3(v[e] * (1.0f / scale));
       }
     }
   }
@@ -334,6 +368,7 @@ struct NormBwdParams {
   float* partial;   // [parts][cols]
   int32_t threads;  // of a row
   int32_t parts;
+  bool gain_vectors;
 };
 
 // A block takes every gridDim-th row (or, with a warp per row, set of rows); a
@@ -345,26 +380,26 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_backward(const __grid_c
   extern __shared__ float total[];  // [cols], with a warp per row
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int64_t cols = p.a.cols;
+  const int cols = static_cast<int>(p.a.cols);
   const RowThreads r{static_cast<int>(threadIdx.x) % p.threads, p.threads};
   const int per_block = blockDim.x / p.threads;
   float acc[kV][8] = {};
   int turn = 0;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / p.threads; row < p.a.rows;
        row += static_cast<int64_t>(gridDim.x) * per_block) {
-    const T* dy = static_cast<const T*>(p.dy) + row * p.a.dy_stride;
-    const T* h = static_cast<const T*>(p.h) + row * p.a.h_stride;
+    RowLoad<kMap, kV, T> dy, h, dh;
+    dy.load(static_cast<const T*>(p.dy) + row * p.a.dy_stride, r, cols);
+    h.load(static_cast<const T*>(p.h) + row * p.a.h_stride, r, cols);
+    const T* dh_row = static_cast<const T*>(p.dh) + row * p.a.dh_stride;
+    if constexpr (kMap == kVector) dh.load(dh_row, r, cols, p.dh != nullptr);  // early: it costs 4 registers a group
     float u[kV][8], n[kV][8], sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kV; ++k) {
-      load_group<kMap>(dy, r, k, cols, u[k]);
-      load_group<kMap>(h, r, k, cols, n[k]);
-    }
     const float rstd = p.rstd[row];
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
       float g[8];
-      gain_group<kMap>(p.gain, p.a.gain_dtype, r, k, cols, g);
+      dy.to(k, u[k]);
+      h.to(k, n[k]);
+      gain_group<kMap>(p.gain, p.a.gain_dtype, p.gain_vectors, r, k, cols, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         n[k][e] *= rstd;
@@ -375,22 +410,18 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_backward(const __grid_c
     }
     const float mean = row_reduce<false>(sum, r, shared[turn]) / static_cast<float>(cols);
     turn ^= 1;
+    if constexpr (kMap != kVector) dh.load(dh_row, r, cols, p.dh != nullptr);
     T* dx = static_cast<T*>(p.dx) + row * p.a.dx_stride;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
       float d[8];
-      if (p.dh) {
-        load_group<kMap>(static_cast<const T*>(p.dh) + row * p.a.dh_stride, r, k, cols, d);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = 0.0f;
-      }
+      dh.to(k, d);
 #pragma unroll
       for (int e = 0; e < 8; ++e) d[e] += rstd * (u[k][e] - n[k][e] * mean);
       store_group<kMap>(dx, r, k, cols, d);
     }
   }
-  float* mine = p.partial + blockIdx.x * cols;
+  float* mine = p.partial + static_cast<int64_t>(blockIdx.x) * cols;
   if (per_block > 1) {
     const int slot = threadIdx.x / p.threads;
     for (int w = 0; w < per_block; ++w) {
@@ -399,7 +430,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_backward(const __grid_c
         for (int k = 0; k < kV; ++k)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int64_t j = place<kMap>(r, k, e);
+            const int j = place<kMap>(r, k, e);
             if (j >= cols) continue;
             if (w + 1 < per_block)
               total[j] = (w > 0 ? total[j] : 0.0f) + acc[k][e];
@@ -618,8 +649,8 @@ extern "C" int fsdp_rmsnorm(const fsdp_rmsnorm_t* a, const void* x, const void* 
       if (!in_place) return FSDP_EALIAS;
     }
   }
-  const NormParams p{*a, x, residual, gain, h_out, y, scales, rstd, 0};
-  const bool aligned = rows_aligned(x, a->rows, a->x_stride, es) && rows_aligned(residual, a->rows, a->residual_stride, es) &&
+  const NormParams p{*a, x, residual, gain, h_out, y, scales, rstd, 0, reinterpret_cast<uintptr_t>(gain) % 16 == 0};
+  const bool aligned = a->cols % 8 == 0 && rows_aligned(x, a->rows, a->x_stride, es) && rows_aligned(residual, a->rows, a->residual_stride, es) &&
                        rows_aligned(h_out, a->rows, a->h_stride, es) &&
                        rows_aligned(y, a->rows, a->y_stride, size_of_dtype(a->y_dtype), e4m3 ? 8 : 16);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
@@ -660,8 +691,9 @@ extern "C" int fsdp_rmsnorm_backward(const fsdp_rmsnorm_backward_t* a, const voi
       if (i && o->overlaps(*i) && !(o == &sdx && (i == &sdy || i == &sdh) && o->same_place(*i))) return FSDP_EALIAS;
   }
   float* partial = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + 15) & ~uintptr_t(15));
-  const NormBwdParams p{*a, dy, h, gain, dh, rstd, dx, dgain, partial, 0, 0};
-  const bool aligned = rows_aligned(dy, a->rows, a->dy_stride, es) && rows_aligned(h, a->rows, a->h_stride, es) &&
+  const NormBwdParams p{*a, dy, h, gain, dh, rstd, dx, dgain, partial, 0, 0,
+                        reinterpret_cast<uintptr_t>(gain) % 16 == 0};
+  const bool aligned = a->cols % 8 == 0 && rows_aligned(dy, a->rows, a->dy_stride, es) && rows_aligned(h, a->rows, a->h_stride, es) &&
                        rows_aligned(dh, a->rows, a->dh_stride, es) && rows_aligned(dx, a->rows, a->dx_stride, es);
   return a->dtype == FSDP_DTYPE_F32 ? backward<float>(p, aligned, st) : backward<__nv_bfloat16>(p, aligned, st);
 }

@@ -536,8 +536,8 @@ int fsdp_account(double P, double U, int32_t N, int32_t F, int32_t prefetch,
  * rstd (fp32 [rows]) may be null.
  * E4M3: each row is cut into groups of `group` consecutive elements (32, 64, 128
  * or 256; 0: the whole row; the last group may be short), and
- *   scale = max(max|y| / 448, 2^-126),   y_out = round(y / scale)
- * to the nearest even e4m3 value; scales is fp32 [rows][ceil(cols / group)],
+ *   scale = max(max|y| / 448, 2^-126),   y_out = round(y (1 / scale))
+ * to the nearest even e4m3 value, at most 448; scales is fp32 [rows][ceil(cols / group)],
  * contiguous. Other y types: scales null and group 0. A row with an infinity or a NaN
  * gives what the formulas give.
  * In place: h_out may be x or residual, and y may be x (same address, stride
