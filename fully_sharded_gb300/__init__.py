@@ -567,27 +567,46 @@ def fsdp_account(P: float, U: float, N: int, F: int | None = None, prefetch: int
 
 # ------------------------------------------- operators of the training loop
 
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_torch_module = None
+
+
+def _cuda_stream(stream):
+    """The stream's handle; None: the current stream (of a caller that holds CUDA tensors)."""
+    if stream is None:
+        return _torch().cuda.current_stream().cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _float_dtype(t, what: str) -> int:
-    import torch
-    if t.dtype == torch.float32:
-        return FSDP_DTYPE_F32
-    if t.dtype == torch.bfloat16:
+    torch = _torch()
+    dtype = t.dtype
+    if dtype == torch.bfloat16:
         return FSDP_DTYPE_BF16
-    raise ValueError("%s: expected float32 or bfloat16, got %s" % (what, t.dtype))
+    if dtype == torch.float32:
+        return FSDP_DTYPE_F32
+    raise ValueError("%s: expected float32 or bfloat16, got %s" % (what, dtype))
 
 
-def _matrix(t, what: str, rows: int, cols: int, dtype=None):
+def _matrix(t, what: str, shape, dtype=None):
     """(address, row stride) of a CUDA matrix of the given shape whose rows are contiguous."""
     if not t.is_cuda:
         raise ValueError("%s: expected a CUDA tensor, got one on %s" % (what, t.device))
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError("%s: expected shape (%d, %d), got %s" % (what, rows, cols, tuple(t.shape)))
+    if t.shape != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
     if dtype is not None and t.dtype != dtype:
         raise ValueError("%s: expected %s, got %s" % (what, dtype, t.dtype))
     row, col = t.stride()
-    if col != 1 and cols > 1:
+    if col != 1 and shape[1] > 1:
         raise ValueError("%s: expected contiguous rows" % what)
-    return t.data_ptr(), (row if rows > 1 else cols)
+    return t.data_ptr(), (row if shape[0] > 1 else shape[1])
 
 
 def _vector(t, what: str, n: int, dtype=None):
@@ -604,38 +623,47 @@ def _workspace(t):
     return _dptr(t), t.numel() * t.element_size()
 
 
+def _shape2(t, what: str):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("%s: expected a matrix, got shape %s" % (what, tuple(shape)))
+    return shape
+
+
 def fsdp_rmsnorm(x, gain, y, residual=None, h_out=None, scales=None, rstd=None, group: int = 0, eps: float = 1e-6,
                  stream=None):
     """RMS norm of the rows of x (+ residual, the sum written to h_out) into y: y's type is x's,
     or 8 bits (torch.float8_e4m3fn) with fp32 `scales` [rows, groups], one per `group` elements
     (0: per row). rstd (fp32 [rows], optional) is what the backward pass needs."""
-    import torch
-    if x.dim() != 2:
-        raise ValueError("x: expected a matrix, got shape %s" % (tuple(x.shape),))
-    rows, cols = x.shape
-    a = RmsNormArgs(rows=rows, cols=cols, dtype=_float_dtype(x, "x"), gain_dtype=_float_dtype(gain, "gain"),
-                    group=group, eps=eps)
-    xp, a.x_stride = _matrix(x, "x", rows, cols)
+    torch = _torch()
+    shape = _shape2(x, "x")
+    rows, cols = shape
+    dtype, y_dtype = x.dtype, y.dtype
+    code = _float_dtype(x, "x")
+    xp, x_stride = _matrix(x, "x", shape)
     rp = hp = sp = None
+    r_stride = h_stride = cols
     if residual is not None:
-        rp, a.residual_stride = _matrix(residual, "residual", rows, cols, x.dtype)
+        rp, r_stride = _matrix(residual, "residual", shape, dtype)
     if h_out is not None:
-        hp, a.h_stride = _matrix(h_out, "h_out", rows, cols, x.dtype)
-    if y.dtype == torch.float8_e4m3fn:
-        a.y_dtype = FSDP_DTYPE_E4M3
+        hp, h_stride = _matrix(h_out, "h_out", shape, dtype)
+    y_code = code
+    if y_dtype == torch.float8_e4m3fn:
+        y_code = FSDP_DTYPE_E4M3
         if scales is None:
             raise ValueError("scales: needed for an 8-bit y")
         sp = _vector(scales, "scales", rows * (-(-cols // group) if group > 0 else 1), torch.float32)
     else:
-        a.y_dtype = a.dtype
-        if y.dtype != x.dtype:
-            raise ValueError("y: expected %s or torch.float8_e4m3fn, got %s" % (x.dtype, y.dtype))
+        if y_dtype != dtype:
+            raise ValueError("y: expected %s or torch.float8_e4m3fn, got %s" % (dtype, y_dtype))
         if scales is not None:
             raise ValueError("scales: only for an 8-bit y")
-    yp, a.y_stride = _matrix(y, "y", rows, cols)
+    yp, y_stride = _matrix(y, "y", shape)
     dp = _vector(rstd, "rstd", rows, torch.float32) if rstd is not None else None
+    a = RmsNormArgs(rows, cols, x_stride, r_stride, h_stride, y_stride, code, _float_dtype(gain, "gain"), y_code, group,
+                    eps)
     _check("fsdp_rmsnorm", _lib.fsdp_rmsnorm(ctypes.byref(a), xp, rp, _vector(gain, "gain", cols), hp, yp, sp, dp,
-                                             _stream(stream)))
+                                             _cuda_stream(stream)))
 
 
 def fsdp_rmsnorm_backward_workspace(rows: int, cols: int) -> int:
@@ -649,21 +677,19 @@ def fsdp_rmsnorm_backward(dy, h, gain, rstd, dx, dgain, workspace, dh=None, stre
     """Gradients of fsdp_rmsnorm: dx (of x, and of the residual) from dy, the forward's h and rstd,
     and dh, the gradient that reaches h by the residual path; dgain in gain's type, summed over the rows
     (it may be a view into a rank's gradient row)."""
-    import torch
-    if h.dim() != 2:
-        raise ValueError("h: expected a matrix, got shape %s" % (tuple(h.shape),))
-    rows, cols = h.shape
-    a = RmsNormBackwardArgs(rows=rows, cols=cols, dtype=_float_dtype(h, "h"), gain_dtype=_float_dtype(gain, "gain"))
-    hp, a.h_stride = _matrix(h, "h", rows, cols)
-    yp, a.dy_stride = _matrix(dy, "dy", rows, cols, h.dtype)
-    xp, a.dx_stride = _matrix(dx, "dx", rows, cols, h.dtype)
-    dhp = None
-    if dh is not None:
-        dhp, a.dh_stride = _matrix(dh, "dh", rows, cols, h.dtype)
+    shape = _shape2(h, "h")
+    rows, cols = shape
+    dtype = h.dtype
+    hp, h_stride = _matrix(h, "h", shape)
+    yp, dy_stride = _matrix(dy, "dy", shape, dtype)
+    xp, dx_stride = _matrix(dx, "dx", shape, dtype)
+    dhp, dh_stride = _matrix(dh, "dh", shape, dtype) if dh is not None else (None, cols)
+    a = RmsNormBackwardArgs(rows, cols, dy_stride, h_stride, dh_stride, dx_stride, _float_dtype(h, "h"),
+                            _float_dtype(gain, "gain"))
     ws, ws_bytes = _workspace(workspace)
     _check("fsdp_rmsnorm_backward", _lib.fsdp_rmsnorm_backward(
-        ctypes.byref(a), yp, hp, _vector(gain, "gain", cols), _vector(rstd, "rstd", rows, torch.float32), dhp, xp,
-        _vector(dgain, "dgain", cols, gain.dtype), ws, ws_bytes, _stream(stream)))
+        ctypes.byref(a), yp, hp, _vector(gain, "gain", cols), _vector(rstd, "rstd", rows, _torch().float32), dhp, xp,
+        _vector(dgain, "dgain", cols, gain.dtype), ws, ws_bytes, _cuda_stream(stream)))
 
 
 class NewtonSchulzBatch:
@@ -671,19 +697,17 @@ class NewtonSchulzBatch:
     results `outs`, kept alive together."""
 
     def __init__(self, sources, outs):
-        import torch
         if len(sources) != len(outs):
             raise ValueError("expected one out for each of %d sources, got %d" % (len(sources), len(outs)))
         self._keep = (list(sources), list(outs))
         self.n = len(sources)
         self.array = (MatrixArgs * max(1, self.n))()
         for a, source, out in zip(self.array, sources, outs):
-            if source.dim() != 2:
-                raise ValueError("source: expected a matrix, got shape %s" % (tuple(source.shape),))
-            a.rows, a.cols = source.shape
+            shape = _shape2(source, "source")
+            a.rows, a.cols = shape
             a.dtype = _float_dtype(source, "source")
-            a.source, a.source_stride = _matrix(source, "source", a.rows, a.cols)
-            a.out, a.out_stride = _matrix(out, "out", a.rows, a.cols, torch.bfloat16)
+            a.source, a.source_stride = _matrix(source, "source", shape)
+            a.out, a.out_stride = _matrix(out, "out", shape, _torch().bfloat16)
 
 
 def _byref_or_none(x):
@@ -702,7 +726,7 @@ def fsdp_newton_schulz(batch: NewtonSchulzBatch, workspace, newton_schulz: Newto
     """Orthogonalises every matrix of the batch into its out by Newton-Schulz products."""
     ws, ws_bytes = _workspace(workspace)
     _check("fsdp_newton_schulz", _lib.fsdp_newton_schulz(batch.array, batch.n, _byref_or_none(newton_schulz), ws,
-                                                         ws_bytes, _stream(stream)))
+                                                         ws_bytes, _cuda_stream(stream)))
 
 
 class MuonUnit:
@@ -745,4 +769,4 @@ def fsdp_muon_step(unit: MuonUnit, muon: Muon, workspace, stream=None):
     orthogonalised and applied, the other tensors by Adam, the bf16 cast and the gather."""
     ws, ws_bytes = _workspace(workspace)
     _check("fsdp_muon_step", _lib.fsdp_muon_step(ctypes.byref(unit.args), ctypes.byref(muon), ws, ws_bytes,
-                                                 _stream(stream)))
+                                                 _cuda_stream(stream)))

@@ -214,9 +214,18 @@ struct NormParams {
   bool gain_vectors;
 };
 
+// Threads of a row at most, and blocks of them that an SM's registers are to hold:
+// more rows in flight while others wait at their reductions. kWide: rows that need
+// more threads at kMaxV groups each.
+constexpr int forward_threads(int v, bool wide) { return v < 3 || wide ? 512 : 384; }
+constexpr int forward_blocks(int v, bool wide) { return v == 2 || wide ? 1 : 2; }
+constexpr int backward_threads(bool wide) { return wide ? 512 : 256; }
+constexpr int backward_blocks(int v, bool wide) { return wide ? 1 : v == 1 ? 4 : v == 2 ? 3 : 2; }
+
 // kQuant 0: y of the inputs' type; 1: 8 bits, one scale per row; 2: 8 bits, scales per group.
-template <typename T, int kQuant, Map kMap, int kV>
-__global__ void __launch_bounds__(kMaxThreads) norm_rows(const __grid_constant__ NormParams p) {
+template <typename T, int kQuant, Map kMap, int kV, bool kWide = false>
+__global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV, kWide))
+    norm_rows(const __grid_constant__ NormParams p) {
   __shared__ float shared[3][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
@@ -374,8 +383,9 @@ struct NormBwdParams {
 // A block takes every gridDim-th row (or, with a warp per row, set of rows); a
 // thread keeps its columns' share of dgain in registers over all its rows. The
 // warps' shares are added in order, then written as the block's row of `partial`.
-template <typename T, Map kMap, int kV>
-__global__ void __launch_bounds__(kMaxThreads) norm_rows_backward(const __grid_constant__ NormBwdParams p) {
+template <typename T, Map kMap, int kV, bool kWide = false>
+__global__ void __launch_bounds__(backward_threads(kWide), backward_blocks(kV, kWide))
+    norm_rows_backward(const __grid_constant__ NormBwdParams p) {
   __shared__ float shared[2][32];
   extern __shared__ float total[];  // [cols], with a warp per row
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -392,20 +402,19 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_backward(const __grid_c
     h.load(static_cast<const T*>(p.h) + row * p.a.h_stride, r, cols);
     const T* dh_row = static_cast<const T*>(p.dh) + row * p.a.dh_stride;
     if constexpr (kMap == kVector) dh.load(dh_row, r, cols, p.dh != nullptr);  // early: it costs 4 registers a group
-    float u[kV][8], n[kV][8], sum = 0.0f;
     const float rstd = p.rstd[row];
+    float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      float g[8];
-      dy.to(k, u[k]);
-      h.to(k, n[k]);
+      float u[8], n[8], g[8];
+      dy.to(k, u);
+      h.to(k, n);
       gain_group<kMap>(p.gain, p.a.gain_dtype, p.gain_vectors, r, k, cols, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        n[k][e] *= rstd;
-        acc[k][e] += u[k][e] * n[k][e];
-        u[k][e] *= g[e];
-        sum += u[k][e] * n[k][e];
+        const float t = u[e] * (n[e] * rstd);
+        acc[k][e] += t;
+        sum += t * g[e];
       }
     }
     const float mean = row_reduce<false>(sum, r, shared[turn]) / static_cast<float>(cols);
@@ -413,11 +422,14 @@ __global__ void __launch_bounds__(kMaxThreads) norm_rows_backward(const __grid_c
     if constexpr (kMap != kVector) dh.load(dh_row, r, cols, p.dh != nullptr);
     T* dx = static_cast<T*>(p.dx) + row * p.a.dx_stride;
 #pragma unroll
-    for (int k = 0; k < kV; ++k) {
-      float d[8];
+    for (int k = 0; k < kV; ++k) {  // formed again from the row as loaded: fewer registers over the reduction
+      float u[8], n[8], g[8], d[8];
+      dy.to(k, u);
+      h.to(k, n);
       dh.to(k, d);
+      gain_group<kMap>(p.gain, p.a.gain_dtype, p.gain_vectors, r, k, cols, g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] += rstd * (u[k][e] - n[k][e] * mean);
+      for (int e = 0; e < 8; ++e) d[e] += rstd * (u[e] * g[e] - n[e] * rstd * mean);
       store_group<kMap>(dx, r, k, cols, d);
     }
   }
@@ -476,30 +488,31 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_rows_backward(const __
   }
 }
 
-// dgain: 32 columns per block, its 8 warps share the rows of `partial`.
-__global__ void __launch_bounds__(256) sum_partials(const __grid_constant__ NormBwdParams p) {
-  __shared__ float shared[8][32];
+// dgain: 32 columns per block, its 32 warps share the rows of `partial`.
+__global__ void __launch_bounds__(1024) sum_partials(const __grid_constant__ NormBwdParams p) {
+  __shared__ float shared[32][33];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float sum = 0.0f;
   if (j < p.a.cols) {
-    int i = warp;
-    for (; i + 24 < p.parts; i += 32) {
-      const float a = p.partial[i * p.a.cols + j], b = p.partial[(i + 8) * p.a.cols + j];
-      const float c = p.partial[(i + 16) * p.a.cols + j], d = p.partial[(i + 24) * p.a.cols + j];
-      sum += (a + b) + (c + d);
+    for (int i = warp; i < p.parts; i += 256) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = i + 32 * k < p.parts ? p.partial[(i + 32 * k) * p.a.cols + j] : 0.0f;
+      sum += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     }
-    for (; i < p.parts; i += 8) sum += p.partial[i * p.a.cols + j];
   }
   shared[warp][lane] = sum;
   __syncthreads();
-  if (warp != 0 || j >= p.a.cols) return;
-  for (int w = 1; w < 8; ++w) sum += shared[w][lane];
+  // warp w adds up column w
+  sum = warp_reduce<false>(shared[lane][warp]);
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + warp;
+  if (lane != 0 || c >= p.a.cols) return;
   if (p.a.gain_dtype == FSDP_DTYPE_F32)
-    static_cast<float*>(p.dgain)[j] = sum;
+    static_cast<float*>(p.dgain)[c] = sum;
   else
-    store1(static_cast<__nv_bfloat16*>(p.dgain) + j, sum);
+    store1(static_cast<__nv_bfloat16*>(p.dgain) + c, sum);
 }
 
 // ------------------------------------------------------------- host side
@@ -533,7 +546,7 @@ Spread forward_spread(int64_t rows, int64_t cols) {
   if (cols > kMaxThreads * 8 * kMaxV) return s;
   s.v = rows < kFewRows ? 1 : static_cast<int>(std::min<int64_t>(kMaxV, (cols + 1023) / 1024));
   if (rows >= kFewRows && cols <= 1024) s.v = warps_for(cols, 1);  // a warp per row
-  while (warps_for(cols, s.v) > kMaxThreads / 32) ++s.v;
+  while (s.v < kMaxV && 32 * warps_for(cols, s.v) > forward_threads(s.v, false)) ++s.v;
   s.threads = 32 * warps_for(cols, s.v);
   if (s.threads == 32) s.per_block = 4;
   return s;
@@ -544,7 +557,7 @@ Spread backward_spread(int64_t rows, int64_t cols) {
   if (cols > kMaxThreads * 8 * kMaxV) return s;
   s.v = rows < kFewRows ? 1 : static_cast<int>(std::min<int64_t>(kMaxV, (cols + 2047) / 2048));
   if (rows >= kFewRows && cols <= 1024) s.v = warps_for(cols, 1);
-  while (warps_for(cols, s.v) > kMaxThreads / 32) ++s.v;
+  while (s.v < kMaxV && 32 * warps_for(cols, s.v) > backward_threads(false)) ++s.v;
   s.threads = 32 * warps_for(cols, s.v);
   if (s.threads == 32) s.per_block = 8;
   return s;
@@ -553,7 +566,7 @@ Spread backward_spread(int64_t rows, int64_t cols) {
 // Blocks of the backward pass: rows of `partial`.
 int backward_parts(int64_t rows, int64_t cols) {
   const Spread s = backward_spread(rows, cols);
-  return static_cast<int>(std::min<int64_t>((std::max<int64_t>(rows, 1) + s.per_block - 1) / s.per_block, 456));
+  return static_cast<int>(std::min<int64_t>((std::max<int64_t>(rows, 1) + s.per_block - 1) / s.per_block, 608));
 }
 
 template <typename T, int kQuant, Map kMap>
@@ -563,7 +576,10 @@ int run_forward(const NormParams& p, const Spread& s, int grid, cudaStream_t st)
     case 1: return launch_rows(norm_rows<T, kQuant, kMap, 1>, grid, threads, 0, st, p);
     case 2: return launch_rows(norm_rows<T, kQuant, kMap, 2>, grid, threads, 0, st, p);
     case 3: return launch_rows(norm_rows<T, kQuant, kMap, 3>, grid, threads, 0, st, p);
-    default: return launch_rows(norm_rows<T, kQuant, kMap, 4>, grid, threads, 0, st, p);
+    default:
+      return launch_rows(threads > forward_threads(kMaxV, false) ? norm_rows<T, kQuant, kMap, kMaxV, true>
+                                                                 : norm_rows<T, kQuant, kMap, kMaxV>,
+                         grid, threads, 0, st, p);
   }
 }
 
@@ -590,7 +606,10 @@ int run_backward(const NormBwdParams& p, const Spread& s, cudaStream_t st) {
     case 1: return launch_rows(norm_rows_backward<T, kMap, 1>, p.parts, threads, smem, st, p);
     case 2: return launch_rows(norm_rows_backward<T, kMap, 2>, p.parts, threads, smem, st, p);
     case 3: return launch_rows(norm_rows_backward<T, kMap, 3>, p.parts, threads, smem, st, p);
-    default: return launch_rows(norm_rows_backward<T, kMap, 4>, p.parts, threads, smem, st, p);
+    default:
+      return launch_rows(threads > backward_threads(false) ? norm_rows_backward<T, kMap, kMaxV, true>
+                                                           : norm_rows_backward<T, kMap, kMaxV>,
+                         p.parts, threads, smem, st, p);
   }
 }
 
@@ -605,7 +624,7 @@ int backward(NormBwdParams p, bool aligned, cudaStream_t st) {
   else
     rc = aligned ? run_backward<T, kVector>(p, s, st) : run_backward<T, kStrided>(p, s, st);
   if (rc != FSDP_OK) return rc;
-  return launch_rows(sum_partials, static_cast<int>((p.a.cols + 31) / 32), 256, 0, st, p);
+  return launch_rows(sum_partials, static_cast<int>((p.a.cols + 31) / 32), 1024, 0, st, p);
 }
 
 // Every row of the array starts on a boundary of `bytes`.
