@@ -10,8 +10,9 @@
 // sum over the row and the writes. A row belongs to one warp (short rows, several
 // to a block) or to one block; each thread holds up to kV groups of 8 elements.
 // Rows longer than that are read twice (norm_long_rows and its like).
-#include "fsdp.h"
+#include "host_internal.h"
 #include "strided.h"
+#include "tensor_core.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -62,6 +63,10 @@ struct Raw8<float> {
     a = there ? __ldcs(reinterpret_cast<const float4*>(p)) : make_float4(0, 0, 0, 0);
     b = there ? __ldcs(reinterpret_cast<const float4*>(p) + 1) : make_float4(0, 0, 0, 0);
   }
+  __device__ __forceinline__ void take(const float* p, bool there) {
+    a = there ? *reinterpret_cast<const float4*>(p) : make_float4(0, 0, 0, 0);
+    b = there ? *(reinterpret_cast<const float4*>(p) + 1) : make_float4(0, 0, 0, 0);
+  }
   __device__ __forceinline__ void to(float* v) const {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
@@ -71,6 +76,9 @@ struct Raw8<__nv_bfloat16> {
   uint4 a;
   __device__ __forceinline__ void load(const __nv_bfloat16* p, bool there) {
     a = there ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void take(const __nv_bfloat16* p, bool there) {
+    a = there ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ void to(float* v) const {
     unpack(a.x, v), unpack(a.y, v + 2), unpack(a.z, v + 4), unpack(a.w, v + 6);
@@ -128,6 +136,13 @@ struct RowLoad {
           v[k][e] = there && j < cols ? load1(p + j) : 0.0f;
         }
       }
+    }
+  }
+  __device__ __forceinline__ void take(const T* p, const RowThreads& r, int cols, bool there = true) {  // shared memory
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      const int j = place<kMap>(r, k, 0);
+      raw[k].take(p + j, there && j < cols);
     }
   }
   __device__ __forceinline__ void to(int k, float* out) const {
@@ -211,8 +226,12 @@ struct NormParams {
   void *h, *y;
   float *scales, *rstd;
   int32_t threads;  // of a row
+  int32_t group_bits;  // log2 of the group
   bool gain_vectors;
 };
+
+// The scale of a group whose largest |y| is `top`.
+__device__ __forceinline__ float scale_of(float top) { return fmaxf(top * (1.0f / 448.0f), 0x1p-126f); }
 
 // Threads of a row at most, and blocks of them that an SM's registers are to hold:
 // more rows in flight while others wait at their reductions. kWide: rows that need
@@ -223,7 +242,7 @@ constexpr int backward_threads(bool wide) { return wide ? 512 : 256; }
 constexpr int backward_blocks(int v, bool wide) { return wide ? 1 : v == 1 ? 4 : v == 2 ? 3 : 2; }
 
 // kQuant 0: y of the inputs' type; 1: 8 bits, one scale per row; 2: 8 bits, scales per group.
-template <typename T, int kQuant, Map kMap, int kV, bool kWide = false>
+template <typename T, bool kResidual, int kQuant, Map kMap, int kV, bool kWide = false>
 __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV, kWide))
     norm_rows(const __grid_constant__ NormParams p) {
   __shared__ float shared[3][32];
@@ -237,20 +256,19 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV,
        row += static_cast<int64_t>(gridDim.x) * per_block) {
     RowLoad<kMap, kV, T> x, res;
     x.load(static_cast<const T*>(p.x) + row * p.a.x_stride, r, cols);
-    res.load(static_cast<const T*>(p.residual) + row * p.a.residual_stride, r, cols, p.residual != nullptr);
+    if constexpr (kResidual) res.load(static_cast<const T*>(p.residual) + row * p.a.residual_stride, r, cols);
     float v[kV][8], sum = 0.0f;
+    T* h = static_cast<T*>(p.h) + row * p.a.h_stride;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      float w[8];
       x.to(k, v[k]);
-      res.to(k, w);
+      if constexpr (kResidual) {
+        float w[8];
+        res.to(k, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] += w[e];
-    }
-    if (p.residual) {
-      T* h = static_cast<T*>(p.h) + row * p.a.h_stride;
-#pragma unroll
-      for (int k = 0; k < kV; ++k) store_group<kMap>(h, r, k, cols, v[k]);
+        for (int e = 0; e < 8; ++e) v[k][e] += w[e];
+        store_group<kMap>(h, r, k, cols, v[k]);
+      }
     }
 #pragma unroll
     for (int k = 0; k < kV; ++k)
@@ -288,15 +306,15 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV,
         all = row_reduce<true>(all, r, shared[2]);
         // the next row's first reduction has a barrier before shared[2] is written again
       }
-      const int groups = kQuant == 1 ? 1 : (cols + p.a.group - 1) / p.a.group;
+      const int groups = kQuant == 1 ? 1 : (cols + p.a.group - 1) >> p.group_bits;
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
         if constexpr (kQuant == 2) all = warp_reduce<true>(top[k], p.a.group / 8);
-        const float scale = fmaxf(all / 448.0f, 0x1p-126f);
+        const float scale = scale_of(all);
         const int j = place<kMap>(r, k, 0);
-        if (kQuant == 1 ? (k == 0 && r.t == 0) : (j < cols && j % p.a.group == 0))
-          p.scales[row * groups + (kQuant == 1 ? 0 : j / p.a.group)] = scale;
-        const float inverse = 1.0f / scale;
+        if (kQuant == 1 ? (k == 0 && r.t == 0) : (j < cols && (j & (p.a.group - 1)) == 0))
+          p.scales[row * groups + (kQuant == 1 ? 0 : j >> p.group_bits)] = scale;
+        const float inverse = __frcp_rn(scale);
         float q[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] = v[k][e] * inverse;
@@ -344,9 +362,9 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_rows(const __grid_cons
       if constexpr (kQuant == 1) {
         for (int64_t j = threadIdx.x; j < cols; j += kLongThreads) all = fmaxf(all, fabsf(value(j) * gain(j)));
         all = long_reduce<true>(all, shared);
-        if (threadIdx.x == 0) p.scales[row] = fmaxf(all / 448.0f, 0x1p-126f);
+        if (threadIdx.x == 0) p.scales[row] = scale_of(all);
       }
-      const int64_t groups = kQuant == 1 ? 1 : (cols + p.a.group - 1) / p.a.group;
+      const int64_t groups = kQuant == 1 ? 1 : (cols + p.a.group - 1) >> p.group_bits;
       // a lane holds 8 consecutive elements, a group 4 to 32 lanes of a warp
       for (int64_t j0 = 0; j0 < cols; j0 += kLongThreads * 8) {
         const int64_t j = j0 + threadIdx.x * 8;
@@ -359,11 +377,11 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_rows(const __grid_cons
           top = fmaxf(top, fabsf(v[e]));
         }
         if constexpr (kQuant == 2) all = warp_reduce<true>(top, p.a.group / 8);
-        const float scale = fmaxf(all / 448.0f, 0x1p-126f);
-        if (kQuant == 2 && j < cols && j % p.a.group == 0) p.scales[row * groups + j / p.a.group] = scale;
+        const float scale = scale_of(all), inverse = __frcp_rn(scale);
+        if (kQuant == 2 && j < cols && (j & (p.a.group - 1)) == 0) p.scales[row * groups + (j >> p.group_bits)] = scale;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (j + e < cols) y[j + e] = to_e4m3(v[e] * (1.0f / scale));
+          if (j + e < cols) y[j + e] = to_e4m3(v[e] * inverse);
       }
     }
   }
@@ -377,8 +395,14 @@ struct NormBwdParams {
   float* partial;   // [parts][cols]
   int32_t threads;  // of a row
   int32_t parts;
+  int32_t stages;   // rows in shared memory (norm_staged_backward)
   bool gain_vectors;
+  unsigned int* status;
 };
+
+constexpr int kMaxStages = 8;
+constexpr int kStagedBytes = 216 * 1024;  // of an SM, for all its blocks
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
 // A block takes every gridDim-th row (or, with a warp per row, set of rows); a
 // thread keeps its columns' share of dgain in registers over all its rows. The
@@ -456,6 +480,104 @@ __global__ void __launch_bounds__(backward_threads(kWide), backward_blocks(kV, k
 #pragma unroll
     for (int k = 0; k < kV; ++k) store_group<kMap == kVector ? kGroups : kMap>(mine, r, k, cols, acc[k]);
   }
+}
+
+// The same for many aligned rows of a block each, the rows staged in shared memory by
+// bulk copies: `stages` rows ahead of the one at work. The row's values are read
+// into registers, and after the barrier inside the sum over the row its stage is free
+// for the next copy, so that the memory stays busy through the reductions.
+// (16384 x 4096 bf16 with dh: 131 us without the stages.)
+template <typename T, int kV, bool kWide>
+__global__ void __launch_bounds__(backward_threads(kWide), backward_blocks(kV, kWide))
+    norm_staged_backward(const __grid_constant__ NormBwdParams p) {
+  __shared__ float shared[2][32];
+  __shared__ __align__(8) uint64_t full[kMaxStages];
+  __shared__ int stop;
+  extern __shared__ __align__(128) unsigned char staged[];  // stages x {dy, h, dh} rows
+  const int cols = static_cast<int>(p.a.cols);
+  const RowThreads r{static_cast<int>(threadIdx.x), p.threads};
+  const uint32_t row_bytes = static_cast<uint32_t>(cols) * sizeof(T), arrays = p.dh ? 3 : 2;
+  const tc::Guard guard{&stop, p.status, kWaitLimitNs};
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) tc::bar_init(tc::smem_addr(&full[s]), 1);
+    stop = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const auto fetch = [&](int64_t row, int s) {
+    const uint32_t bar = tc::smem_addr(&full[s]), to = tc::smem_addr(staged) + s * arrays * row_bytes;
+    tc::bar_expect(bar, arrays * row_bytes);
+    tc::bulk_load(to, static_cast<const T*>(p.dy) + row * p.a.dy_stride, row_bytes, bar);
+    tc::bulk_load(to + row_bytes, static_cast<const T*>(p.h) + row * p.a.h_stride, row_bytes, bar);
+    if (p.dh) tc::bulk_load(to + 2 * row_bytes, static_cast<const T*>(p.dh) + row * p.a.dh_stride, row_bytes, bar);
+  };
+  if (threadIdx.x == 0)
+    for (int s = 0; s < p.stages; ++s) {
+      const int64_t row = blockIdx.x + static_cast<int64_t>(s) * gridDim.x;
+      if (row < p.a.rows) fetch(row, s);
+    }
+  float acc[kV][8] = {};
+  int turn = 0, stage = 0;
+  uint32_t parity = 0, turns = 0;
+  bool failed = false;
+  for (int64_t row = blockIdx.x; row < p.a.rows; row += gridDim.x) {
+    const float rstd = p.rstd[row];
+    failed = !tc::bar_wait(tc::smem_addr(&full[stage]), parity, guard);
+    const unsigned char* at = staged + stage * arrays * row_bytes;
+    RowLoad<kVector, kV, T> dy, h, dh;
+    dy.take(reinterpret_cast<const T*>(at), r, cols);
+    h.take(reinterpret_cast<const T*>(at + row_bytes), r, cols);
+    dh.take(reinterpret_cast<const T*>(at + 2 * row_bytes), r, cols, p.dh != nullptr);
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      float u[8], n[8], g[8];
+      dy.to(k, u);
+      h.to(k, n);
+      gain_group<kVector>(p.gain, p.a.gain_dtype, p.gain_vectors, r, k, cols, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float t = u[e] * (n[e] * rstd);
+        acc[k][e] += t;
+        sum += t * g[e];
+      }
+    }
+    sum = warp_reduce<false>(sum);
+    if (r.t % 32 == 0) shared[turn][r.t / 32] = sum;
+    failed = __syncthreads_or(failed);
+    if (failed) break;
+    const int64_t next = row + static_cast<int64_t>(p.stages) * gridDim.x;
+    if (threadIdx.x == 0 && next < p.a.rows) fetch(next, stage);
+    const float mean =
+        warp_reduce<false>(r.t % 32 < r.n / 32 ? shared[turn][r.t % 32] : 0.0f) / static_cast<float>(cols);
+    turn ^= 1;
+    T* dx = static_cast<T*>(p.dx) + row * p.a.dx_stride;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      float u[8], n[8], g[8], d[8];
+      dy.to(k, u);
+      h.to(k, n);
+      dh.to(k, d);
+      gain_group<kVector>(p.gain, p.a.gain_dtype, p.gain_vectors, r, k, cols, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] += rstd * (u[e] * g[e] - n[e] * rstd * mean);
+      store_group<kVector>(dx, r, k, cols, d);
+    }
+    if (++stage == p.stages) stage = 0, parity ^= 1u;
+    ++turns;
+  }
+  if (failed && threadIdx.x == 0) {  // copies in flight land before the block ends
+    for (int s = 0; s < p.stages; ++s) {
+      if (blockIdx.x + static_cast<int64_t>(turns + s) * gridDim.x < p.a.rows)
+        tc::bar_drain(tc::smem_addr(&full[stage]), parity, kWaitLimitNs);
+      if (++stage == p.stages) stage = 0, parity ^= 1u;
+    }
+  }
+  float* mine = p.partial + static_cast<int64_t>(blockIdx.x) * cols;
+#pragma unroll
+  for (int k = 0; k < kV; ++k) store_group<kGroups>(mine, r, k, cols, acc[k]);
 }
 
 // Rows beyond the registers: the row read twice, dgain's share kept in `partial`.
@@ -563,24 +685,50 @@ Spread backward_spread(int64_t rows, int64_t cols) {
   return s;
 }
 
-// Blocks of the backward pass: rows of `partial`.
-int backward_parts(int64_t rows, int64_t cols) {
-  const Spread s = backward_spread(rows, cols);
-  return static_cast<int>(std::min<int64_t>((std::max<int64_t>(rows, 1) + s.per_block - 1) / s.per_block, 608));
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    sms = 152;
+  return sms;
 }
 
-template <typename T, int kQuant, Map kMap>
+// Blocks of the backward pass (rows of `partial`): as many as run at once.
+int backward_parts(int64_t rows, int64_t cols) {
+  const Spread s = backward_spread(rows, cols);
+  int per_sm = 4;
+  if (s.v > 0) {
+    const int threads = s.threads * s.per_block;
+    const bool wide = threads > backward_threads(false);
+    per_sm = std::max(1, backward_blocks(s.v, wide) * backward_threads(wide) / threads);
+  }
+  return static_cast<int>(
+      std::min<int64_t>((std::max<int64_t>(rows, 1) + s.per_block - 1) / s.per_block, static_cast<int64_t>(per_sm) * sm_count()));
+}
+
+template <typename T, bool kResidual, int kQuant, Map kMap>
 int run_forward(const NormParams& p, const Spread& s, int grid, cudaStream_t st) {
   const int threads = s.threads * s.per_block;
   switch (s.v) {
-    case 1: return launch_rows(norm_rows<T, kQuant, kMap, 1>, grid, threads, 0, st, p);
-    case 2: return launch_rows(norm_rows<T, kQuant, kMap, 2>, grid, threads, 0, st, p);
-    case 3: return launch_rows(norm_rows<T, kQuant, kMap, 3>, grid, threads, 0, st, p);
+    case 1: return launch_rows(norm_rows<T, kResidual, kQuant, kMap, 1>, grid, threads, 0, st, p);
+    case 2: return launch_rows(norm_rows<T, kResidual, kQuant, kMap, 2>, grid, threads, 0, st, p);
+    case 3: return launch_rows(norm_rows<T, kResidual, kQuant, kMap, 3>, grid, threads, 0, st, p);
     default:
-      return launch_rows(threads > forward_threads(kMaxV, false) ? norm_rows<T, kQuant, kMap, kMaxV, true>
-                                                                 : norm_rows<T, kQuant, kMap, kMaxV>,
+      return launch_rows(threads > forward_threads(kMaxV, false) ? norm_rows<T, kResidual, kQuant, kMap, kMaxV, true>
+                                                                 : norm_rows<T, kResidual, kQuant, kMap, kMaxV>,
                          grid, threads, 0, st, p);
   }
+}
+
+template <typename T, bool kResidual>
+int run_forward_as(const NormParams& p, const Spread& s, bool aligned, int grid, cudaStream_t st) {
+  if (p.a.y_dtype != FSDP_DTYPE_E4M3)
+    return aligned ? run_forward<T, kResidual, 0, kVector>(p, s, grid, st)
+                   : run_forward<T, kResidual, 0, kStrided>(p, s, grid, st);
+  if (p.a.group == 0)
+    return aligned ? run_forward<T, kResidual, 1, kVector>(p, s, grid, st)
+                   : run_forward<T, kResidual, 1, kStrided>(p, s, grid, st);
+  return aligned ? run_forward<T, kResidual, 2, kVector>(p, s, grid, st)
+                 : run_forward<T, kResidual, 2, kGroups>(p, s, grid, st);
 }
 
 template <typename T>
@@ -589,14 +737,10 @@ int forward(NormParams p, bool aligned, cudaStream_t st) {
   p.threads = s.threads;
   const bool quant = p.a.y_dtype == FSDP_DTYPE_E4M3;
   const int grid = static_cast<int>(std::min<int64_t>((p.a.rows + s.per_block - 1) / s.per_block, 1 << 20));
-  if (s.v == 0) {
+  if (s.v == 0)
     return launch_rows(!quant ? norm_long_rows<T, 0> : p.a.group == 0 ? norm_long_rows<T, 1> : norm_long_rows<T, 2>, grid,
                        kLongThreads, 0, st, p);
-  }
-  if (!quant) return aligned ? run_forward<T, 0, kVector>(p, s, grid, st) : run_forward<T, 0, kStrided>(p, s, grid, st);
-  if (p.a.group == 0)
-    return aligned ? run_forward<T, 1, kVector>(p, s, grid, st) : run_forward<T, 1, kStrided>(p, s, grid, st);
-  return aligned ? run_forward<T, 2, kVector>(p, s, grid, st) : run_forward<T, 2, kGroups>(p, s, grid, st);
+  return p.residual ? run_forward_as<T, true>(p, s, aligned, grid, st) : run_forward_as<T, false>(p, s, aligned, grid, st);
 }
 
 template <typename T, Map kMap>
@@ -614,15 +758,41 @@ int run_backward(const NormBwdParams& p, const Spread& s, cudaStream_t st) {
 }
 
 template <typename T>
+int run_staged(const NormBwdParams& p, const Spread& s, int smem, cudaStream_t st) {
+  const auto go = [&](auto kernel) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedBytes) != cudaSuccess)
+      return FSDP_ECUDA;
+    return launch_rows(kernel, p.parts, s.threads, smem, st, p);
+  };
+  switch (s.v) {
+    case 1: return go(norm_staged_backward<T, 1, false>);
+    case 2: return go(norm_staged_backward<T, 2, false>);
+    case 3: return go(norm_staged_backward<T, 3, false>);
+    default:
+      return s.threads > backward_threads(false) ? go(norm_staged_backward<T, kMaxV, true>)
+                                                 : go(norm_staged_backward<T, kMaxV, false>);
+  }
+}
+
+template <typename T>
 int backward(NormBwdParams p, bool aligned, cudaStream_t st) {
   const Spread s = backward_spread(p.a.rows, p.a.cols);
   p.threads = s.threads;
   p.parts = backward_parts(p.a.rows, p.a.cols);
+  // several rows per block: staged, if an SM's shared memory holds two for each of its blocks
+  const int64_t row_bytes = p.a.cols * static_cast<int64_t>(sizeof(T)) * (p.dh ? 3 : 2);
+  const int per_sm = (p.parts + sm_count() - 1) / sm_count();
+  const int64_t stages = std::min<int64_t>(kMaxStages, (kStagedBytes / per_sm - 1024) / row_bytes);
   int rc;
-  if (s.v == 0)
+  if (s.v == 0) {
     rc = launch_rows(norm_long_rows_backward<T>, p.parts, kLongThreads, 0, st, p);
-  else
+  } else if (aligned && s.per_block == 1 && p.a.rows > p.parts && stages >= 2) {
+    p.stages = static_cast<int32_t>(stages);
+    rc = device_status_word(&p.status);
+    if (rc == FSDP_OK) rc = run_staged<T>(p, s, static_cast<int>(stages * row_bytes), st);
+  } else {
     rc = aligned ? run_backward<T, kVector>(p, s, st) : run_backward<T, kStrided>(p, s, st);
+  }
   if (rc != FSDP_OK) return rc;
   return launch_rows(sum_partials, static_cast<int>((p.a.cols + 31) / 32), 1024, 0, st, p);
 }
@@ -668,7 +838,10 @@ extern "C" int fsdp_rmsnorm(const fsdp_rmsnorm_t* a, const void* x, const void* 
       if (!in_place) return FSDP_EALIAS;
     }
   }
-  const NormParams p{*a, x, residual, gain, h_out, y, scales, rstd, 0, reinterpret_cast<uintptr_t>(gain) % 16 == 0};
+  int group_bits = 0;
+  while (a->group >> (group_bits + 1)) ++group_bits;
+  const NormParams p{*a, x, residual, gain, h_out, y, scales, rstd, 0, group_bits,
+                     reinterpret_cast<uintptr_t>(gain) % 16 == 0};
   const bool aligned = a->cols % 8 == 0 && rows_aligned(x, a->rows, a->x_stride, es) && rows_aligned(residual, a->rows, a->residual_stride, es) &&
                        rows_aligned(h_out, a->rows, a->h_stride, es) &&
                        rows_aligned(y, a->rows, a->y_stride, size_of_dtype(a->y_dtype), e4m3 ? 8 : 16);
@@ -710,8 +883,8 @@ extern "C" int fsdp_rmsnorm_backward(const fsdp_rmsnorm_backward_t* a, const voi
       if (i && o->overlaps(*i) && !(o == &sdx && (i == &sdy || i == &sdh) && o->same_place(*i))) return FSDP_EALIAS;
   }
   float* partial = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + 15) & ~uintptr_t(15));
-  const NormBwdParams p{*a, dy, h, gain, dh, rstd, dx, dgain, partial, 0, 0,
-                        reinterpret_cast<uintptr_t>(gain) % 16 == 0};
+  const NormBwdParams p{*a, dy, h, gain, dh, rstd, dx, dgain, partial, 0, 0, 0,
+                        reinterpret_cast<uintptr_t>(gain) % 16 == 0, nullptr};
   const bool aligned = a->cols % 8 == 0 && rows_aligned(dy, a->rows, a->dy_stride, es) && rows_aligned(h, a->rows, a->h_stride, es) &&
                        rows_aligned(dh, a->rows, a->dh_stride, es) && rows_aligned(dx, a->rows, a->dx_stride, es);
   return a->dtype == FSDP_DTYPE_F32 ? backward<float>(p, aligned, st) : backward<__nv_bfloat16>(p, aligned, st);

@@ -67,6 +67,13 @@ __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity, uint64_
   }
 }
 
+// An untiled copy: both addresses and the size are multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 // The same barrier (or any shared address) in block `rank` of the cluster.
 __device__ __forceinline__ uint32_t in_block(uint32_t addr, uint32_t rank) {
   uint32_t r;
