@@ -84,19 +84,20 @@ __device__ __forceinline__ const PassMat& pass_mat(const PassParams& p, int* par
   return p.mat[i];
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
+__device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-__device__ __forceinline__ void block_sum_to(double sum, float* out) {
-  __shared__ double shared[kPassWarps];
+// The block's sum, at `out` after the caller's next barrier.
+__device__ __forceinline__ void block_sum_to(float sum, float* out) {
+  __shared__ float shared[kPassWarps];
   sum = warp_sum(sum);
   if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = sum;
   __syncthreads();
   if (threadIdx.x != 0) return;
   for (int i = 1; i < kPassWarps; ++i) sum += shared[i];
-  *out = static_cast<float>(sum);
+  *out = sum;
 }
 
 __device__ __forceinline__ void unpack_bf16(uint32_t two, float* v) {
@@ -148,11 +149,12 @@ __device__ __forceinline__ void each_group(const PassMat& j, int part, F f) {
   }
 }
 
-// Sums of squares, one per block: fp32 over a group of 8, then fp64.
+// Sums of squares, one per block: a lane adds its groups of 8, then trees. fp32
+// throughout (a few hundred terms in sequence at most; fp64 runs at 1/64 of the rate).
 __global__ void __launch_bounds__(32 * kPassWarps) ns_squares(const __grid_constant__ PassParams p) {
   int part;
   const PassMat& j = pass_mat(p, &part);
-  double sum = 0.0;
+  float sum = 0.0f;
   each_group(j, part, [&](int64_t, int64_t, const float (&v)[8]) {
     float s = 0.0f;
 #pragma unroll
@@ -180,7 +182,7 @@ __global__ void __launch_bounds__(32 * kPassWarps) ns_momentum(const __grid_cons
   const int64_t units = (end - (begin & ~int64_t(7)) + 255) / 256;  // of 256 elements: 8 per lane
   uintptr_t bits = 0;
   for (int k = 0; k < world; ++k) bits |= reinterpret_cast<uintptr_t>(m.grads[k]);
-  double sum = 0.0;
+  float sum = 0.0f;
   for (int64_t u = static_cast<int64_t>(part) * kPassWarps + threadIdx.x / 32; u < units;
        u += static_cast<int64_t>(j.parts) * kPassWarps) {
     const int64_t f = (begin & ~int64_t(7)) + u * 256 + threadIdx.x % 32 * 8;
@@ -235,17 +237,16 @@ __global__ void __launch_bounds__(32 * kPassWarps) ns_momentum(const __grid_cons
     }
     sum += s;
   }
-  block_sum_to(sum, &j.partial[part]);
+  if (j.partial) block_sum_to(sum, &j.partial[part]);
 }
 
 // X_0 as two parts.
 __global__ void __launch_bounds__(32 * kPassWarps) ns_normalise(const __grid_constant__ PassParams p) {
   int part;
   const PassMat& j = pass_mat(p, &part);
-  double sum = 0.0;
+  float sum = 0.0f;
   for (int i = threadIdx.x % 32; i < j.parts; i += 32) sum += j.partial[i];
-  sum = warp_sum(sum);
-  const float inv = static_cast<float>(1.0 / (sqrt(sum) + p.eps));
+  const float inv = 1.0f / (sqrtf(warp_sum(sum)) + p.eps);
   each_group(j, part, [&](int64_t r, int64_t c, const float (&v)[8]) {
     uint32_t hi[4], lo[4];
 #pragma unroll
@@ -548,6 +549,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
         const int sub = col0 / 128;
         if (col0 >= g.n || (g.symmetric && sub > block)) continue;
         float v[32];
+        __syncwarp();
         tmem_load32(tmem + buf * kN + c + (static_cast<uint32_t>(quarter * 32) << 16), v);
         if (p.kind == kGram) {
 #pragma unroll
@@ -612,12 +614,279 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
   if (warp == 1) tmem_free<kPair>(tmem, T::kTmemCols);
 }
 
+// ----------------------------------------------------------- small matrices
+
+// A matrix with a short side of at most 128 that fits the shared memory of one
+// block goes through all its steps there, in one launch: X's two parts and those
+// of A (then of P, in the same place) as 128-byte-swizzled operand tiles, the
+// products in tensor memory, the short side's rows on its lanes. The three products
+// of a step follow one another, so it is bound by their latency (about 1 us each
+// with the passes between them). Tall matrices are transposed as they are read.
+constexpr int kSmallSide = 128;
+constexpr int kSmallThreads = 256;
+constexpr int kSmallBytes = 220 * 1024;
+constexpr int kSmallSlack = 128 * 128;  // a product reads 128 rows whatever the short side
+constexpr int kSmallMats = 48;
+constexpr int kSmallCols = 256;         // of X per product
+
+struct SmallMat {
+  const void* source;
+  int64_t source_stride;
+  uint16_t* out;
+  int64_t out_stride;
+  int64_t flat;
+  int32_t rows, cols;
+  int32_t dtype;
+  float step;
+};
+
+struct SmallParams {
+  SmallMat mat[kSmallMats];
+  NsApply apply;
+  float coef[3 * 32];
+  int32_t steps, terms;
+  float eps;
+  bool applies;
+  unsigned int* status;
+};
+static_assert(sizeof(SmallParams) <= 32764, "kernel parameter block too large");
+
+struct SmallShape {
+  int side, length;      // of the wide orientation
+  int side16, blocks;    // padded short side; 64-column blocks of X
+  int part_x, part_a;    // bytes of one part
+  __host__ __device__ SmallShape(int rows, int cols) {
+    side = rows < cols ? rows : cols;
+    length = rows < cols ? cols : rows;
+    side16 = (side + 15) / 16 * 16;
+    blocks = (length + 63) / 64;
+    part_x = side16 * blocks * 128;
+    part_a = side16 * ((side16 + 63) / 64) * 128;
+  }
+  __host__ __device__ int bytes() const { return 2 * part_x + 2 * part_a + kSmallSlack + 1024; }
+};
+
+// Byte of element (row, col) in a part: 64-column blocks of rows of 128 bytes, whose
+// 16-byte pieces are exchanged by the row's place in its group of 8.
+__device__ __forceinline__ int small_at(int rows, int row, int col) {
+  return (col >> 6) * rows * 128 + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4) + (col & 7) * 2;
+}
+
+__global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant__ SmallParams p) {
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t done_bar;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int stop;
+  __shared__ float norm;
+  const SmallMat& g = p.mat[blockIdx.x];
+  const SmallShape s(g.rows, g.cols);
+  const bool wide = g.rows <= g.cols;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
+  unsigned char* x = raw + (base - smem_addr(raw));
+  unsigned char* a = x + 2 * s.part_x;
+  const uint32_t x_addr = base, a_addr = base + 2 * s.part_x;
+  const Guard guard{&stop, p.status, kWaitLimitNs};
+  if (threadIdx.x == 0) {
+    bar_init(smem_addr(&done_bar), 1);
+    stop = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) tmem_alloc<1>(smem_addr(&tmem_slot), kSmallCols);
+  for (int i = threadIdx.x * 16; i < 2 * s.part_x; i += kSmallThreads * 16)
+    *reinterpret_cast<uint4*>(x + i) = make_uint4(0, 0, 0, 0);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const auto source = [&](int r, int c) {
+    const int64_t i = r * g.source_stride + c;
+    return g.dtype == FSDP_DTYPE_F32 ? static_cast<const float*>(g.source)[i]
+                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(g.source)[i]);
+  };
+  const int count = g.rows * g.cols;
+  float squares = 0.0f;
+  for (int i = threadIdx.x; i < count; i += kSmallThreads) {
+    const int r = i / g.cols;
+    const float v = source(r, i - r * g.cols);
+    squares += v * v;
+  }
+  block_sum_to(squares, &norm);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_slot;
+  const float inv = 1.0f / (sqrtf(norm) + p.eps);
+  for (int i = threadIdx.x; i < count; i += kSmallThreads) {
+    const int r = i / g.cols, c = i - r * g.cols;
+    const int at = wide ? small_at(s.side16, r, c) : small_at(s.side16, c, r);
+    const float v = source(r, c) * inv * kScaleX;
+    const __half hi = __float2half_rn(v);
+    *reinterpret_cast<__half*>(x + at) = hi;
+    *reinterpret_cast<__half*>(x + s.part_x + at) = __float2half_rn(v - __half2float(hi));
+  }
+  uint32_t phase = 0;
+  // a wait of this thread ran out; some thread's did (the same for all, known at the next barrier)
+  bool lost = false, failed = false;
+  // Makes what the threads wrote visible to the products, lets thread 0 issue them, and waits for them.
+  const auto run = [&](auto issue) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    fence_before();
+    failed = __syncthreads_or(lost);
+    if (failed) return;
+    if (threadIdx.x == 0) {
+      fence_after();
+      issue();
+      mma_commit<1>(smem_addr(&done_bar));
+    }
+    lost = !bar_wait(smem_addr(&done_bar), phase & 1u, guard);
+    ++phase;
+    fence_after();
+  };
+  const int row = (warp & 3) * 32 + lane;
+  const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  const bool busy = (warp & 3) * 32 < s.side16;  // some lane of the warp has a row
+  // Calls f(column, results, hi parts, lo parts) for 8-column pieces [0, cols) of this thread's
+  // row of a region at `to`; the two warps of a lane quarter take 32 columns by turns.
+  const auto pieces = [&](unsigned char* to, int part, int col0, int cols, auto f) {
+    if (!busy) return;
+    for (int c = (warp >> 2) * 32; c < cols; c += 64) {
+      float v[32];
+      __syncwarp();
+      tmem_load32(lanes + c, v);
+      if (row >= s.side16) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (c + 8 * q >= cols) break;
+        unsigned char* at = to + small_at(s.side16, row, col0 + c + 8 * q);
+        f(&v[8 * q], reinterpret_cast<uint4*>(at), reinterpret_cast<uint4*>(at + part));
+      }
+    }
+  };
+  // old = hi + lo of a piece; stores `v` as two parts
+  const auto sum_of = [](const uint4& hi, const uint4& lo, float* out) {
+    const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+      const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&l[e]));
+      out[2 * e] = f.x + t.x;
+      out[2 * e + 1] = f.y + t.y;
+    }
+  };
+  const auto put = [](const float* v, uint4* hi, uint4* lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __half2 t = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+      const float2 f = __half22float2(t);
+      const __half2 u = __floats2half2_rn(v[2 * e] - f.x, v[2 * e + 1] - f.y);
+      h[e] = *reinterpret_cast<const uint32_t*>(&t);
+      l[e] = *reinterpret_cast<const uint32_t*>(&u);
+    }
+    *hi = make_uint4(h[0], h[1], h[2], h[3]);
+    *lo = make_uint4(l[0], l[1], l[2], l[3]);
+  };
+  const uint32_t block = static_cast<uint32_t>(s.side16) * 128;
+  const uint32_t square = product_kind(128, s.side16, false, false);
+  for (int step = 0; step < p.steps && !failed; ++step) {
+    const float ca = p.coef[3 * step], cb = p.coef[3 * step + 1], cc = p.coef[3 * step + 2];
+    run([&] {  // A = X X^T
+      for (int t = 0; t < p.terms; ++t) {
+        const uint32_t l = x_addr + (t == 1 ? s.part_x : 0), r = x_addr + (t == 2 ? s.part_x : 0);
+        for (int k = 0; k < (s.length + 15) / 16; ++k) {
+          const uint32_t at = (k >> 2) * block + (k & 3) * 32;
+          mma<1>(tmem, operand(l + at, 0, 1024), operand(r + at, 0, 1024), square, t > 0 || k > 0);
+        }
+      }
+    });
+    if (failed) break;
+    pieces(a, s.part_a, 0, s.side16, [&](float* v, uint4* hi, uint4* lo) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= kScaleA / (kScaleX * kScaleX);
+      put(v, hi, lo);
+    });
+    run([&] {  // A A
+      for (int t = 0; t < p.terms; ++t) {
+        const uint32_t l = a_addr + (t == 1 ? s.part_a : 0), r = a_addr + (t == 2 ? s.part_a : 0);
+        for (int k = 0; k < s.side16 / 16; ++k) {
+          const uint32_t at = (k >> 2) * block + (k & 3) * 32;
+          mma<1>(tmem, operand(l + at, 0, 1024), operand(r + at, 0, 1024), square, t > 0 || k > 0);
+        }
+      }
+    });
+    if (failed) break;
+    pieces(a, s.part_a, 0, s.side16, [&](float* v, uint4* hi, uint4* lo) {
+      float old[8];
+      sum_of(*hi, *lo, old);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = cb * old[e] + cc / kScaleA * v[e];
+      put(v, hi, lo);
+    });
+    for (int col0 = 0; col0 < s.length && !failed; col0 += kSmallCols) {
+      const int cols = min(kSmallCols, (s.length - col0 + 15) / 16 * 16);
+      run([&] {  // P X, columns from col0 on
+        const uint32_t kind = product_kind(128, cols, false, true);
+        for (int t = 0; t < p.terms; ++t) {
+          const uint32_t l = a_addr + (t == 1 ? s.part_a : 0), r = x_addr + (t == 2 ? s.part_x : 0) + (col0 >> 6) * block;
+          for (int k = 0; k < s.side16 / 16; ++k)
+            mma<1>(tmem, operand(l + (k >> 2) * block + (k & 3) * 32, 0, 1024), operand(r + k * 2048, block, 1024), kind,
+                   t > 0 || k > 0);
+        }
+      });
+      if (failed) break;
+      pieces(x, s.part_x, col0, cols, [&](float* v, uint4* hi, uint4* lo) {
+        float old[8];
+        sum_of(*hi, *lo, old);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = ca * old[e] + v[e] / kScaleA;
+        put(v, hi, lo);
+      });
+    }
+  }
+  fence_before();
+  failed = __syncthreads_or(lost);
+  if (!failed) {
+    int64_t f = g.flat + threadIdx.x, rank = 0;
+    if (p.applies) {
+      rank = f / p.apply.shard;
+      f -= rank * p.apply.shard;
+    }
+    for (int i = threadIdx.x; i < count; i += kSmallThreads, f += kSmallThreads) {
+      const int r = i / g.cols, c = i - r * g.cols;
+      const int at = wide ? small_at(s.side16, r, c) : small_at(s.side16, c, r);
+      const float v = (__half2float(*reinterpret_cast<const __half*>(x + at)) +
+                       __half2float(*reinterpret_cast<const __half*>(x + s.part_x + at))) *
+                      (1.0f / kScaleX);
+      if (!p.applies) {
+        g.out[r * g.out_stride + c] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        continue;
+      }
+      while (f >= p.apply.shard) {
+        f -= p.apply.shard;
+        ++rank;
+      }
+      float* master = p.apply.master[rank] + f;
+      const float w = *master * p.apply.keep - g.step * v;
+      *master = w;
+      p.apply.full[g.flat + i] = __bfloat16_as_ushort(__float2bfloat16_rn(w));
+    }
+  }
+  if (warp == 0) {
+    fence_after();
+    tmem_free<1>(tmem, kSmallCols);
+  }
+}
+
 // ------------------------------------------------------------- host side
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 int terms_of(const NsJob& j, const NsPlan& plan) {
   return plan.terms ? plan.terms : std::min(j.rows, j.cols) < 256 ? 3 : 1;
+}
+
+bool is_small(const NsJob& j) {
+  if (std::min(j.rows, j.cols) > kSmallSide || std::max(j.rows, j.cols) > kSmallBytes) return false;
+  return SmallShape(static_cast<int>(j.rows), static_cast<int>(j.cols)).bytes() <= kSmallBytes;
 }
 
 int parts_of(const NsJob& j) {
@@ -639,6 +908,7 @@ int64_t carve(const NsJob& j, const NsPlan& plan, unsigned char* base, Buffers* 
   Buffers b{};
   b.ld_x = round_up(j.cols, 64);
   b.ld_a = round_up(side, 64);
+  if (is_small(j)) return 0;
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     unsigned char* q = base ? base + at : nullptr;
@@ -775,6 +1045,44 @@ int launch_momentum(const MomentumParams& p, int blocks, cudaStream_t stream) {
     case 16: return go(ns_momentum<16>);
     default: return go(ns_momentum<0>);
   }
+}
+
+// Small matrices: one block each, all steps in one launch.
+int run_small(const NsJob* const* jobs, int count, const NsPlan& plan, const NsMomentum* momentum, const NsApply* apply,
+              const Device& dev, cudaStream_t stream) {
+  static thread_local SmallParams p;
+  if (momentum) {
+    static thread_local MomentumParams first;
+    for (int at = 0; at < count; at += kMaxMats) {
+      int blocks = 0;
+      first.pass.count = std::min(kMaxMats, count - at);
+      for (int i = 0; i < first.pass.count; ++i) {
+        const NsJob& j = *jobs[at + i];
+        blocks += parts_of(j);
+        first.pass.mat[i] = {j.source, j.source_stride, j.rows, j.cols, nullptr, nullptr, 0, nullptr, j.flat, j.dtype,
+                             parts_of(j), blocks};
+      }
+      first.m = *momentum;
+      if (int rc = launch_momentum(first, blocks, stream)) return rc;
+    }
+  }
+  int smem = 0;
+  for (int i = 0; i < count; ++i) {
+    const NsJob& j = *jobs[i];
+    p.mat[i] = {j.source, j.source_stride, j.out, j.out_stride, j.flat, static_cast<int32_t>(j.rows),
+                static_cast<int32_t>(j.cols), j.dtype, j.step};
+    smem = std::max(smem, SmallShape(static_cast<int>(j.rows), static_cast<int>(j.cols)).bytes());
+  }
+  if (apply) p.apply = *apply;
+  p.applies = apply != nullptr;
+  std::copy(plan.coef.begin(), plan.coef.end(), p.coef);
+  p.steps = plan.steps;
+  p.terms = plan.terms ? plan.terms : 3;
+  p.eps = plan.eps;
+  p.status = dev.status;
+  if (cudaFuncSetAttribute(ns_small, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallBytes) != cudaSuccess)
+    return FSDP_ECUDA;
+  return launch_after(ns_small, count, 1, kSmallThreads, smem, stream, p);
 }
 
 // One launch's matrices through all steps.
@@ -938,10 +1246,17 @@ int ns_run(const std::vector<NsJob>& jobs, const NsPlan& plan, const NsMomentum*
   if (int rc = device_facts(&dev)) return rc;
   if (!encoder()) return FSDP_ECUDA;
   auto* base = reinterpret_cast<unsigned char*>(round_up(reinterpret_cast<intptr_t>(workspace), 256));
+  std::vector<const NsJob*> small;
+  for (const NsJob& j : jobs)
+    if (is_small(j)) small.push_back(&j);
+  for (size_t at = 0; at < small.size(); at += kSmallMats) {
+    const int count = static_cast<int>(std::min<size_t>(kSmallMats, small.size() - at));
+    if (int rc = run_small(&small[at], count, plan, momentum, apply, dev, stream)) return rc;
+  }
   for (int terms : {1, 3}) {
     std::vector<const NsJob*> group;
     for (const NsJob& j : jobs)
-      if (terms_of(j, plan) == terms) group.push_back(&j);
+      if (!is_small(j) && terms_of(j, plan) == terms) group.push_back(&j);
     for (size_t at = 0; at < group.size(); at += kMaxMats) {
       const int count = static_cast<int>(std::min<size_t>(kMaxMats, group.size() - at));
       const int rc = count <= 8 ? run_group<8>(&group[at], count, plan, terms, momentum, apply, base, dev, stream)
