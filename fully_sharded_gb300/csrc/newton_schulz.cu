@@ -17,10 +17,11 @@
 // column space. With terms = 3 every operand has both parts: hi hi + lo hi + hi lo.
 //
 // Each of the three products is one launch over all matrices of the call: a
-// persistent grid of tiles, one producer lane (TMA), one product lane
-// (tcgen05, two accumulators in tensor memory) and four epilogue warps per
-// block. A and P are symmetric: tiles above the diagonal are not computed, and
-// the others are written to both places.
+// persistent grid of tiles; in each block a producer lane (TMA), a product lane
+// (tcgen05, two accumulators in tensor memory), a lane that fetches what the result
+// is added to, and eight epilogue warps. Results leave through shared memory, 64
+// columns at a time, as tiled stores. A and P are symmetric: tiles above the
+// diagonal are not computed, and the others are written to both places.
 #include "host_internal.h"
 #include "newton_schulz.h"
 #include "strided.h"
@@ -271,14 +272,12 @@ enum Result : int32_t { kParts, kOut, kApply };            // hi/lo parts; bf16 
 
 // C[m, n] = alpha sum_k p[i, k] q[j, k] + beta in[i, j].
 struct GemmMat {
-  CUtensorMap p[2], q[2];  // boxes of 64 x 64 elements of the operands' hi and lo parts
-  __half *hi, *lo;
-  const __half *in_hi, *in_lo;
-  int64_t ld;              // of the result and of `in`: a multiple of 64
+  CUtensorMap p[2], q[2], result[2];  // boxes of 64 x 64 elements of the hi and lo parts
   int32_t m, n, k;
   int32_t col_tiles, tiles;
   uint8_t p_mn, q_mn;      // the operand's row index (of C's rows, columns) is the contiguous one
   uint8_t symmetric;
+  uint8_t in_q;            // `in` is q (else p)
   uint16_t* out;
   int64_t out_stride;
   int64_t flat;
@@ -297,17 +296,26 @@ struct GemmParams {
 static_assert(sizeof(GemmParams<kMaxMats>) <= 32764, "kernel parameter block too large");
 
 constexpr int kTileK = 64;
-constexpr int kGemmThreads = 256;  // producer, product, two idle and four epilogue warps
+constexpr int kChunk = 64;          // columns of a tile that leave together
+constexpr int kEpilogueWarps = 8;
+constexpr int kGemmThreads = 128 + 32 * kEpilogueWarps;  // producer, products, fetch of `in`, an idle warp, epilogue
+constexpr int kSlotBytes = 128 * kChunk * 2;              // one part of a chunk
+constexpr int kSlots = 4;
+constexpr int kShareBytes = 128 * kChunk * 4;             // a chunk's fp32 sums from the other block (kSplit = 2)
 
-// A tile: 128 rows per block of the pair (or single block) and kN columns.
-template <int kN, int kPair>
+// A tile: 128 rows per block of the pair (or single block) and kN columns. kSplit = 2:
+// the two blocks of a cluster share a tile, each takes half of the inner dimension,
+// sends the other the sums of the chunk that it does not finish, and finishes one.
+template <int kN, int kPair, int kSplit>
 struct Tile {
   static constexpr int kM = 128 * kPair;
+  static constexpr int kCluster = kPair * kSplit;
   static constexpr int kBRows = kN / kPair;  // a block's half of the second operand
   static constexpr int kABytes = 128 * kTileK * 2, kBBytes = kBRows * kTileK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = 196608 / kStageBytes;  // 192 KB of operands in flight
-  static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+  static constexpr int kShare = kSplit == 2 ? kShareBytes : 0;
+  static constexpr int kStages = (230400 - 1024 - kSlots * kSlotBytes - kShare) / kStageBytes;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kSlots * kSlotBytes + kShare + 1024;
   static constexpr int kTmemCols = 2 * kN;
 
   // symmetric results: tiles of tile row i with an element on or below the diagonal
@@ -343,99 +351,119 @@ struct Tiles {
   }
 };
 
-// The thread's 32 results (row, col0 ..) as bf16, or applied to the master.
-__device__ __forceinline__ void finish(const GemmMat& g, const NsApply& ap, int32_t result, int64_t row, int col0,
-                                       const float (&v)[32]) {
-  const bool whole = col0 + 32 <= g.n;
-  if (result == kOut) {
-    uint16_t* o = g.out + row * g.out_stride + col0;
-    if (whole && (reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+// Byte of the 16-byte piece `piece` of row `row` in a slot (rows of 128 bytes, swizzled as TMA does).
+__device__ __forceinline__ uint32_t slot_at(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
+
+__device__ __forceinline__ uint4 shared_load(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void shared_store(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Writes the thread's 32 fp16 values (columns 32 half .. of row `row`) into a slot.
+__device__ __forceinline__ void put_part(uint32_t slot, int row, int half, const uint32_t (&r)[16]) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t r[4];
+  for (int q = 0; q < 4; ++q)
+    shared_store(slot + slot_at(row, half * 4 + q), r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+}
+
+// The same values as columns of the transposed chunk: two boxes of 64 x 64, box b
+// with rows 64 b .. of the tile as its columns. Pairs of lanes exchange two columns at a
+// time, so that a store holds two rows of one column; the even lanes' columns and
+// the odd lanes' are 4 apart, which puts them in different banks.
+__device__ __forceinline__ void put_mirror(uint32_t slot, int row, int half, const uint32_t (&r)[16]) {
+  const bool odd = row & 1;
+  const int pair = row & 63 & ~1;
+  const uint32_t base = slot + (row >> 6) * 8192 + (pair & 7) * 2;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]);
-          r[e] = *reinterpret_cast<const uint32_t*>(&b);
+  for (int c = 0; c < 16; c += 4) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {  // columns 2 (c + k), + 1 of the even lane; 4 more of the odd lane
+      const uint32_t mine = odd ? r[c + 2 + k] : r[c + k];
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? r[c + k] : r[c + 2 + k], 1);
+      const uint32_t first = odd ? __byte_perm(other, mine, 0x5410) : __byte_perm(mine, other, 0x5410);
+      const uint32_t second = odd ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x7632);
+      const int col = half * 32 + 2 * (c + k) + (odd ? 4 : 0);
+      const uint32_t a = base + col * 128 + (((pair >> 3) ^ (col & 7)) << 4);
+      const uint32_t b = base + (col + 1) * 128 + (((pair >> 3) ^ ((col + 1) & 7)) << 4);
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(first) : "memory");
+      asm volatile("st.shared.b32 [%0], %1;" ::"r"(b), "r"(second) : "memory");
+    }
+  }
+}
+
+// The last step's chunk, fp32 in the slots: written as bf16, or applied to the
+// master, a row by a warp at a time (any alignment, whole lines per access).
+__device__ __forceinline__ void finish_rows(const GemmMat& g, const NsApply& ap, int32_t result, uint32_t slots, int row0,
+                                            int col0, int warp, int lane) {
+  constexpr int kRows = 128 / kEpilogueWarps, kBatch = 4;
+  const int first = warp * kRows;
+  int64_t at = 0, rank = 0;  // of element (row, col0)
+  if (result == kApply) {
+    const int64_t f = g.flat + static_cast<int64_t>(row0 + first) * g.n + col0;
+    rank = f / ap.shard;
+    at = f - rank * ap.shard;
+  }
+  for (int r0 = 0; r0 < kRows; r0 += kBatch) {
+    float v[kBatch][2], old[kBatch][2];
+    float* where[kBatch][2];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int row = first + r0 + b;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int col = 32 * h + lane;
+        const bool there = row0 + row < g.m && col0 + col < g.n;
+        asm volatile("ld.shared.f32 %0, [%1];"
+                     : "=f"(v[b][h])
+                     : "r"(slots + (lane >> 4) * kSlotBytes + slot_at(row, h * 4 + ((lane & 15) >> 2)) + (lane & 3) * 4)
+                     : "memory");
+        where[b][h] = nullptr;
+        if (result == kApply && there) {
+          int64_t a = at + col, r = rank;
+          while (a >= ap.shard) a -= ap.shard, ++r;
+          where[b][h] = ap.master[r] + a;
+          old[b][h] = *where[b][h];
+        } else if (result == kOut && there) {
+          g.out[(row0 + row) * g.out_stride + col0 + col] = __bfloat16_as_ushort(__float2bfloat16_rn(v[b][h]));
         }
-        reinterpret_cast<uint4*>(o)[q] = make_uint4(r[0], r[1], r[2], r[3]);
       }
-      return;
+      at += g.n;
+      if (result == kApply)
+        while (at >= ap.shard) at -= ap.shard, ++rank;
     }
+    if (result != kApply) continue;
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
-      if (col0 + c < g.n) o[c] = __bfloat16_as_ushort(__float2bfloat16_rn(v[c]));
-    return;
-  }
-  const int64_t f = g.flat + row * g.n + col0;
-  int64_t rank = f / ap.shard, at = f - rank * ap.shard;
-  float* master = ap.master[rank] + at;
-  uint16_t* full = ap.full + f;
-  if (whole && at + 32 <= ap.shard &&
-      ((reinterpret_cast<uintptr_t>(master) | reinterpret_cast<uintptr_t>(full)) & 15u) == 0) {
+    for (int b = 0; b < kBatch; ++b)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float4 a = reinterpret_cast<float4*>(master)[2 * q], b = reinterpret_cast<float4*>(master)[2 * q + 1];
-      a.x = a.x * ap.keep - g.step * v[8 * q], a.y = a.y * ap.keep - g.step * v[8 * q + 1];
-      a.z = a.z * ap.keep - g.step * v[8 * q + 2], a.w = a.w * ap.keep - g.step * v[8 * q + 3];
-      b.x = b.x * ap.keep - g.step * v[8 * q + 4], b.y = b.y * ap.keep - g.step * v[8 * q + 5];
-      b.z = b.z * ap.keep - g.step * v[8 * q + 6], b.w = b.w * ap.keep - g.step * v[8 * q + 7];
-      reinterpret_cast<float4*>(master)[2 * q] = a;
-      reinterpret_cast<float4*>(master)[2 * q + 1] = b;
-      const __nv_bfloat162 c0 = __floats2bfloat162_rn(a.x, a.y), c1 = __floats2bfloat162_rn(a.z, a.w),
-                           c2 = __floats2bfloat162_rn(b.x, b.y), c3 = __floats2bfloat162_rn(b.z, b.w);
-      reinterpret_cast<uint4*>(full)[q] =
-          make_uint4(*reinterpret_cast<const uint32_t*>(&c0), *reinterpret_cast<const uint32_t*>(&c1),
-                     *reinterpret_cast<const uint32_t*>(&c2), *reinterpret_cast<const uint32_t*>(&c3));
-    }
-    return;
-  }
-#pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    if (col0 + c >= g.n) break;
-    if (at == ap.shard) {
-      at = 0;
-      master = ap.master[++rank];
-    }
-    const float w = *master * ap.keep - g.step * v[c];
-    *master++ = w;
-    ++at;
-    full[c] = __bfloat16_as_ushort(__float2bfloat16_rn(w));
+      for (int h = 0; h < 2; ++h) {
+        if (!where[b][h]) continue;
+        const float w = old[b][h] * ap.keep - g.step * v[b][h];
+        *where[b][h] = w;
+        ap.full[g.flat + static_cast<int64_t>(row0 + first + r0 + b) * g.n + col0 + 32 * h + lane] =
+            __bfloat16_as_ushort(__float2bfloat16_rn(w));
+      }
   }
 }
 
-// Stores 32 fp16 values of a row, and their mirror image when `mirror`: pairs of
-// lanes exchange halves so that each 4-byte store holds two rows of one column.
-__device__ __forceinline__ void store_part(__half* base, int64_t ld, int row, int col0, bool in_rows, bool mirror,
-                                           int m, int n, const uint32_t (&r)[16]) {
-  if (in_rows) {
-    __half* o = base + row * ld + col0;
-    store16(o, {r[0], r[1], r[2], r[3], r[4], r[5], r[6], r[7]});
-    store16(o + 16, {r[8], r[9], r[10], r[11], r[12], r[13], r[14], r[15]});
-  }
-  if (!mirror) return;
-  const bool odd = threadIdx.x & 1;
-  const int pair = row & ~1;
-#pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, r[c], 1);
-    const uint32_t two = odd ? __byte_perm(r[c], other, 0x3276) : __byte_perm(r[c], other, 0x5410);
-    const int col = col0 + 2 * c + (odd ? 1 : 0);
-    if (col < n && pair < m) *reinterpret_cast<uint32_t*>(base + col * ld + pair) = two;
-  }
-}
-
-template <int kN, int kPair, int kMats>
+template <int kN, int kPair, int kSplit, int kMats>
 __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_constant__ GemmParams<kMats> p) {
-  using T = Tile<kN, kPair>;
+  using T = Tile<kN, kPair, kSplit>;
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t full_bar[T::kStages], empty_bar[T::kStages], done_bar[2], free_bar[2];
+  __shared__ __align__(8) uint64_t in_bar[2], out_bar[2];     // a set of slots: `in` has come; the result has left
+  __shared__ __align__(8) uint64_t shared_bar, taken_bar;     // kSplit: sums have come from, were taken by the other block
   __shared__ uint32_t tmem_slot;
   __shared__ int stop;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
-  const int rank = kPair == 2 ? static_cast<int>(block_rank()) : 0;
-  const int first_tile = blockIdx.x / kPair, tile_step = gridDim.x / kPair;
+  const uint32_t slots = smem + T::kStages * T::kStageBytes, share = slots + kSlots * kSlotBytes;
+  const int rank = T::kCluster == 2 ? static_cast<int>(block_rank()) : 0;
+  const int pair_rank = kPair == 2 ? rank : 0;
+  const int first_tile = blockIdx.x / T::kCluster, tile_step = gridDim.x / T::kCluster;
   const Guard guard{&stop, p.status, kWaitLimitNs};
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) {
@@ -444,69 +472,86 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     }
     for (int b = 0; b < 2; ++b) {
       bar_init(smem_addr(&done_bar[b]), 1);
-      bar_init(smem_addr(&free_bar[b]), 4 * kPair);
+      bar_init(smem_addr(&free_bar[b]), kEpilogueWarps * kPair);
+      bar_init(smem_addr(&in_bar[b]), 1);
+      bar_init(smem_addr(&out_bar[b]), 1);
     }
+    bar_init(smem_addr(&shared_bar), kEpilogueWarps);
+    bar_init(smem_addr(&taken_bar), kEpilogueWarps);
     stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<kPair>(smem_addr(&tmem_slot), T::kTmemCols);
   fence_before();
   __syncthreads();
-  if constexpr (kPair == 2) cluster_sync();
+  if constexpr (T::kCluster == 2) cluster_sync();
   fence_after();
   const uint32_t tmem = tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
+
+  // this block's steps of the inner dimension, over all terms: [lo, hi)
+  const auto steps_of = [&](const GemmMat& g, int* lo, int* hi) {
+    const int all = (g.k + kTileK - 1) / kTileK * p.terms;
+    *lo = kSplit == 2 ? all * rank / 2 : 0;
+    *hi = kSplit == 2 ? all * (rank + 1) / 2 : all;
+  };
+  // sets of slots: a chunk needs hi and lo, or a part and its mirror image, or all four
+  const int sets = p.terms == 3 && p.kind != kUpdate ? 1 : 2;
+  const uint32_t set_bytes = sets == 1 ? kSlots * kSlotBytes : 2 * kSlotBytes;
+  // whether this block finishes the chunk of a tile
+  const auto has_chunk = [&](const GemmMat& g, int block, int col0, int c) {
+    return !(col0 >= g.n || block * 128 >= g.m || (g.symmetric && col0 / 128 > block) || (kSplit == 2 && c != rank));
+  };
 
   if (warp == 0 && lane == 0) {  // producer: this block's rows of both operands
     Tiles<T, GemmParams<kMats>> tiles{p};
     uint32_t it = 0;
     bool ok = true;
     for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
-      int i, j;
+      int i, j, lo, hi;
       const GemmMat& g = tiles.at(t, &i, &j);
+      steps_of(g, &lo, &hi);
       const int blocks = (g.k + kTileK - 1) / kTileK;
-      const int row0 = i * T::kM + rank * 128, col0 = j * kN + rank * T::kBRows;
-      for (int term = 0; ok && term < p.terms; ++term) {
+      const int row0 = i * T::kM + pair_rank * 128, col0 = j * kN + pair_rank * T::kBRows;
+      int term = lo / blocks, kb = lo - term * blocks;
+      for (int step = lo; step < hi; ++step, ++it) {
         const CUtensorMap* mp = &g.p[term == 1 ? 1 : 0];
         const CUtensorMap* mq = &g.q[term == 2 ? 1 : 0];
-        for (int kb = 0; kb < blocks; ++kb, ++it) {
-          const int s = it % T::kStages;
-          ok = bar_wait(smem_addr(&empty_bar[s]), ((it / T::kStages) & 1u) ^ 1u, guard);
-          if (!ok) break;
-          // the first block's barrier counts the bytes of both
-          const uint32_t own = smem_addr(&full_bar[s]), bar = kPair == 2 ? in_block(own, 0) : own;
-          const uint32_t a = smem + s * T::kStageBytes, b = a + T::kABytes;
-          if (rank == 0) bar_expect(own, T::kStageBytes * kPair);
+        const int s = it % T::kStages;
+        ok = bar_wait(smem_addr(&empty_bar[s]), ((it / T::kStages) & 1u) ^ 1u, guard);
+        if (!ok) break;
+        // the first block's barrier counts the bytes of both
+        const uint32_t own = smem_addr(&full_bar[s]), bar = kPair == 2 ? in_block(own, 0) : own;
+        const uint32_t a = smem + s * T::kStageBytes, b = a + T::kABytes;
+        if (pair_rank == 0) bar_expect(own, T::kStageBytes * kPair);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int r = row0 + 64 * q;
-            tma_box<kPair>(a + q * 8192, mp, g.p_mn ? r : kb * kTileK, g.p_mn ? kb * kTileK : r, bar);
-          }
-#pragma unroll
-          for (int q = 0; q < T::kBRows / 64; ++q) {
-            const int c = col0 + 64 * q;
-            tma_box<kPair>(b + q * 8192, mq, g.q_mn ? c : kb * kTileK, g.q_mn ? kb * kTileK : c, bar);
-          }
+        for (int q = 0; q < 2; ++q) {
+          const int r = row0 + 64 * q;
+          tma_box<kPair>(a + q * 8192, mp, g.p_mn ? r : kb * kTileK, g.p_mn ? kb * kTileK : r, bar);
         }
+#pragma unroll
+        for (int q = 0; q < T::kBRows / 64; ++q) {
+          const int c = col0 + 64 * q;
+          tma_box<kPair>(b + q * 8192, mq, g.q_mn ? c : kb * kTileK, g.q_mn ? kb * kTileK : c, bar);
+        }
+        if (++kb == blocks) kb = 0, ++term;
       }
     }
     // every copy lands (its stage is used and released) before the block ends
     for (uint32_t back = 1; back <= T::kStages && back <= it; ++back) {
       const uint32_t last = it - back;
-      if (rank == 0)
-        bar_drain(smem_addr(&full_bar[last % T::kStages]), (last / T::kStages) & 1u, kWaitLimitNs);
-      else
-        bar_drain(smem_addr(&empty_bar[last % T::kStages]), (last / T::kStages) & 1u, kWaitLimitNs);
+      const uint64_t* bar = pair_rank == 0 ? full_bar : empty_bar;
+      bar_drain(smem_addr(&bar[last % T::kStages]), (last / T::kStages) & 1u, kWaitLimitNs);
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {  // products, for both blocks
+  } else if (warp == 1 && lane == 0 && pair_rank == 0) {  // products, for both blocks of a pair
     Tiles<T, GemmParams<kMats>> tiles{p};
     uint32_t it = 0, n = 0;
     bool ok = true;
     for (int t = first_tile; ok && t < p.tiles; t += tile_step, ++n) {
-      int i, j;
+      int i, j, lo, hi;
       const GemmMat& g = tiles.at(t, &i, &j);
-      const int blocks = (g.k + kTileK - 1) / kTileK * p.terms;
+      steps_of(g, &lo, &hi);
       const uint32_t buf = n & 1u, d = tmem + buf * kN;
       ok = bar_wait(smem_addr(&free_bar[buf]), ((n >> 1) & 1u) ^ 1u, guard);
       if (!ok) break;
@@ -515,7 +560,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
       // bytes from one 16-deep product's operand to the next, and between blocks of 64 rows
       const uint32_t a_step = g.p_mn ? 2048 : 32, b_step = g.q_mn ? 2048 : 32;
       const uint32_t a_block = g.p_mn ? 8192 : 0, b_block = g.q_mn ? 8192 : 0;
-      for (int kb = 0; kb < blocks; ++kb, ++it) {
+      for (int step = lo; step < hi; ++step, ++it) {
         const int s = it % T::kStages;
         ok = bar_wait(smem_addr(&full_bar[s]), (it / T::kStages) & 1u, guard);
         if (!ok) break;
@@ -524,78 +569,175 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
 #pragma unroll
         for (int q = 0; q < kTileK / 16; ++q)
           mma<kPair>(d, operand(a + q * a_step, a_block, 1024), operand(b + q * b_step, b_block, 1024), kind,
-                     kb > 0 || q > 0);
+                     step > lo || q > 0);
         mma_commit<kPair>(smem_addr(&empty_bar[s]));
       }
       if (ok) mma_commit<kPair>(smem_addr(&done_bar[buf]));
     }
     if (!ok && it > 0)  // products in flight end before the accumulators are freed
       bar_drain(smem_addr(&empty_bar[(it - 1) % T::kStages]), ((it - 1) / T::kStages) & 1u, kWaitLimitNs);
-  } else if (warp >= 4) {  // epilogue: this block's 128 rows
+  } else if (warp == 2 && lane == 0 && p.kind != kGram) {  // fetch of `in`, ahead of the epilogue
     Tiles<T, GemmParams<kMats>> tiles{p};
-    const int quarter = warp - 4;
-    uint32_t n = 0;
-    for (int t = first_tile; t < p.tiles; t += tile_step, ++n) {
+    const int parts = p.kind == kUpdate || p.terms == 3 ? 2 : 1;
+    uint32_t e = 0;
+    bool ok = true;
+    for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
       int i, j;
       const GemmMat& g = tiles.at(t, &i, &j);
+      const int block = i * kPair + pair_rank;
+      const CUtensorMap* in = g.in_q ? g.q : g.p;
+      for (int c = 0; c < kN / kChunk; ++c) {
+        const int col0 = j * kN + c * kChunk;
+        if (!has_chunk(g, block, col0, c)) continue;
+        const uint32_t set = e % sets, bar = smem_addr(&in_bar[set]), to = slots + set * set_bytes;
+        ok = bar_wait(smem_addr(&out_bar[set]), ((e / sets) & 1u) ^ 1u, guard);
+        if (!ok) break;
+        bar_expect(bar, parts * kSlotBytes);
+        for (int part = 0; part < parts; ++part)
+          for (int b = 0; b < 2; ++b)
+            tma_box<1>(to + part * kSlotBytes + b * 8192, &in[part], col0, block * 128 + 64 * b, bar);
+        ++e;
+      }
+    }
+    for (uint32_t back = 1; back <= static_cast<uint32_t>(sets) && back <= e; ++back)
+      bar_drain(smem_addr(&in_bar[(e - back) % sets]), ((e - back) / sets) & 1u, kWaitLimitNs);
+  } else if (warp >= 4) {  // epilogue: this block's 128 rows
+    Tiles<T, GemmParams<kMats>> tiles{p};
+    const int own = warp - 4, quarter = own & 3, half = own >> 2;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const bool leader = own == 0 && lane == 0;  // issues the stores
+    uint32_t n = 0, e = 0, left = 0;            // tiles, chunks, chunks whose slots are released
+    // a wait of this thread ran out; some thread's did (the same for all, known at the next barrier)
+    bool lost = false, failed = false;
+    for (int t = first_tile; !failed && t < p.tiles; t += tile_step, ++n) {
+      int i, j, lo, hi;
+      const GemmMat& g = tiles.at(t, &i, &j);
+      steps_of(g, &lo, &hi);
+      const int block = i * kPair + pair_rank;  // in rows of 128, as col0 / 128 in columns
       const uint32_t buf = n & 1u;
-      if (!bar_wait(smem_addr(&done_bar[buf]), (n >> 1) & 1u, guard)) break;
+      lost |= !bar_wait(smem_addr(&done_bar[buf]), (n >> 1) & 1u, guard);
       fence_after();
-      const int block = i * kPair + rank;  // in rows of 128, as `sub` in columns
-      const int row = block * 128 + quarter * 32 + lane;
-      const bool in_rows = row < g.m;
-      for (int c = 0; c < kN; c += 32) {
-        const int col0 = j * kN + c;
-        const int sub = col0 / 128;
-        if (col0 >= g.n || (g.symmetric && sub > block)) continue;
-        float v[32];
+      const auto sums = [&](int c, float (&v)[32]) {
         __syncwarp();
-        tmem_load32(tmem + buf * kN + c + (static_cast<uint32_t>(quarter * 32) << 16), v);
+        tmem_load32(lanes + buf * kN + c * kChunk + half * 32, v);
+        if (kSplit == 2 && lo == hi) {  // no step of this tile was this block's
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[q] = 0.0f;
+        }
+      };
+      if constexpr (kSplit == 2) {  // the other block's chunk
+        float v[32];
+        sums(1 - rank, v);
+        lost |= !bar_wait_cluster(smem_addr(&taken_bar), (n & 1u) ^ 1u, guard);
+        const uint32_t to = in_block(share, 1 - rank);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) store_cluster(to + ((half * 8 + q) * 128 + row) * 16, &v[4 * q]);
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive_cluster(in_block(smem_addr(&shared_bar), 1 - rank));
+      }
+      bool any = false;
+      for (int c = 0; c < kN / kChunk; ++c) {
+        const int col0 = j * kN + c * kChunk;
+        if (!has_chunk(g, block, col0, c)) continue;
+        any = true;
+        const uint32_t set = e % sets, base = slots + set * set_bytes;
+        float v[32];
+        sums(c, v);
+        if constexpr (kSplit == 2) {
+          lost |= !bar_wait_cluster(smem_addr(&shared_bar), n & 1u, guard);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint4 w = shared_load(share + ((half * 8 + q) * 128 + row) * 16);
+            v[4 * q] += __uint_as_float(w.x), v[4 * q + 1] += __uint_as_float(w.y);
+            v[4 * q + 2] += __uint_as_float(w.z), v[4 * q + 3] += __uint_as_float(w.w);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 32; ++q) v[q] *= p.alpha;
         if (p.kind == kGram) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= p.alpha;
+          lost |= !bar_wait(smem_addr(&out_bar[set]), ((e / sets) & 1u) ^ 1u, guard);
         } else {
+          lost |= !bar_wait(smem_addr(&in_bar[set]), (e / sets) & 1u, guard);
+          for (int part = 0; part < (p.kind == kUpdate || p.terms == 3 ? 2 : 1); ++part) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= p.alpha;
-          if (in_rows) {
+            for (int q = 0; q < 4; ++q) {
+              const uint4 w = shared_load(base + part * kSlotBytes + slot_at(row, half * 4 + q));
+              const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-              const __half* in = part ? g.in_lo : g.in_hi;
-              if (!in) continue;
-              in += row * g.ld + col0;
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const Half16 h = load16(in + 16 * q);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h.r[e]));
-                  v[16 * q + 2 * e] += p.beta * f.x;
-                  v[16 * q + 2 * e + 1] += p.beta * f.y;
-                }
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[k]));
+                v[8 * q + 2 * k] += p.beta * f.x;
+                v[8 * q + 2 * k + 1] += p.beta * f.y;
               }
             }
           }
         }
-        if (p.result != kParts) {
-          if (in_rows) {
+        const bool mirror = g.symmetric && col0 / 128 < block;
+        if (p.result != kParts) {  // fp32 where the thread's own hi and lo were
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= 1.0f / kScaleX;
-            finish(g, p.apply, p.result, row, col0, v);
+          for (int q = 0; q < 8; ++q)
+            shared_store(base + (q >> 2) * kSlotBytes + slot_at(row, half * 4 + (q & 3)),
+                         __float_as_uint(v[4 * q] * (1.0f / kScaleX)), __float_as_uint(v[4 * q + 1] * (1.0f / kScaleX)),
+                         __float_as_uint(v[4 * q + 2] * (1.0f / kScaleX)), __float_as_uint(v[4 * q + 3] * (1.0f / kScaleX)));
+        } else {
+          uint32_t r[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const __half2 h = __floats2half2_rn(v[2 * q], v[2 * q + 1]);
+            const float2 f = __half22float2(h);
+            v[2 * q] -= f.x, v[2 * q + 1] -= f.y;
+            r[q] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          continue;
-        }
-        uint32_t hi[16], lo[16];
+          const bool lo_too = p.kind == kUpdate || p.terms == 3;
+          put_part(base, row, half, r);
+          if (mirror) put_mirror(base + (lo_too ? 2 : 1) * kSlotBytes, row, half, r);
+          if (lo_too) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const __half2 h = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
-          const float2 f = __half22float2(h);
-          const __half2 l = __floats2half2_rn(v[2 * e] - f.x, v[2 * e + 1] - f.y);
-          hi[e] = *reinterpret_cast<const uint32_t*>(&h);
-          lo[e] = *reinterpret_cast<const uint32_t*>(&l);
+            for (int q = 0; q < 16; ++q) {
+              const __half2 l = __floats2half2_rn(v[2 * q], v[2 * q + 1]);
+              r[q] = *reinterpret_cast<const uint32_t*>(&l);
+            }
+            put_part(base + kSlotBytes, row, half, r);
+            if (mirror) put_mirror(base + 3 * kSlotBytes, row, half, r);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        const bool mirror = g.symmetric && sub < block;
-        store_part(g.hi, g.ld, row, col0, in_rows, mirror, g.m, g.n, hi);
-        if (g.lo) store_part(g.lo, g.ld, row, col0, in_rows, mirror, g.m, g.n, lo);
+        failed = named_or(1, 32 * kEpilogueWarps, lost);
+        if (failed) break;
+        if (p.result != kParts) {
+          finish_rows(g, p.apply, p.result, base, block * 128, col0, own, lane);
+          // the slots were read by every warp, and may be written by the next fetch
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          named_or(1, 32 * kEpilogueWarps, false);
+          if (leader) bar_arrive(smem_addr(&out_bar[set]));
+        } else if (leader) {
+          const int parts = p.kind == kUpdate || p.terms == 3 ? 2 : 1;
+          for (int part = 0; part < parts; ++part)
+            for (int b = 0; b < 2; ++b) {
+              const int at = block * 128 + 64 * b;
+              if (at >= g.m) continue;
+              tma_store(&g.result[part], col0, at, base + part * kSlotBytes + b * 8192);
+              if (mirror) tma_store(&g.result[part], at, col0, base + (parts + part) * kSlotBytes + b * 8192);
+            }
+          bulk_commit();
+          // the chunk before this one (this one, with a single set) has left its slots
+          if (sets == 2)
+            bulk_wait_read<1>();
+          else
+            bulk_wait_read<0>();
+          for (const uint32_t gone = sets == 2 ? e : e + 1; left < gone; ++left) bar_arrive(smem_addr(&out_bar[left % sets]));
+        }
+        ++e;
+      }
+      if (kSplit == 2 && !any && !failed) {  // nothing to finish: what came is let go
+        lost |= !bar_wait_cluster(smem_addr(&shared_bar), n & 1u, guard);
+        failed = named_or(1, 32 * kEpilogueWarps, lost);
+      }
+      if constexpr (kSplit == 2) {
+        __syncwarp();
+        if (lane == 0) bar_arrive_cluster(in_block(smem_addr(&taken_bar), 1 - rank));
       }
       fence_before();
       __syncwarp();
@@ -606,10 +748,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
           bar_arrive(smem_addr(&free_bar[buf]));
       }
     }
+    if (leader) bulk_wait_all();
   }
+  __syncwarp();
   fence_before();
   __syncthreads();
-  if constexpr (kPair == 2) cluster_sync();  // neither block leaves while the other may signal it
+  if constexpr (T::kCluster == 2) cluster_sync();  // neither block leaves while the other may signal it
   fence_after();
   if (warp == 1) tmem_free<kPair>(tmem, T::kTmemCols);
 }
@@ -889,6 +1033,12 @@ bool is_small(const NsJob& j) {
   return SmallShape(static_cast<int>(j.rows), static_cast<int>(j.cols)).bytes() <= kSmallBytes;
 }
 
+// Matrices whose symmetric products are shared by two blocks a tile: those with so
+// few tiles (66 or fewer of 128 x 128) that two blocks for each still run at once. It
+// goes by the matrix alone, not by its company, so that a matrix gives the same
+// bits in every call.
+bool splits(const NsJob& j) { return std::min(j.rows, j.cols) <= 1408; }
+
 int parts_of(const NsJob& j) {
   const int64_t units = j.rows * ((j.cols + kUnit - 1) / kUnit);
   return static_cast<int>(std::min<int64_t>(kMaxParts, (units + kPassWarps - 1) / kPassWarps));
@@ -986,25 +1136,25 @@ int launch_after(K kernel, int grid, int cluster, int threads, int smem, cudaStr
 }
 
 // How many clusters of the kernel run at once (looked up once per device).
-template <int kN, int kPair, int kMats>
+template <int kN, int kPair, int kSplit, int kMats>
 int resident_clusters(const Device& dev) {
-  using T = Tile<kN, kPair>;
+  using T = Tile<kN, kPair, kSplit>;
   static std::atomic<int> cached[64];
   if (dev.id >= 64) return 0;
   int n = cached[dev.id].load(std::memory_order_acquire);
   if (n) return n;
-  const auto kernel = ns_product<kN, kPair, kMats>;
+  const auto kernel = ns_product<kN, kPair, kSplit, kMats>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess) return 0;
-  if (kPair == 1) {
+  if (T::kCluster == 1) {
     n = dev.sms;
   } else {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(dev.sms / kPair * kPair);
+    cfg.gridDim = dim3(dev.sms / T::kCluster * T::kCluster);
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = T::kSmemBytes;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kPair;
+    attr[0].val.clusterDim.x = T::kCluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -1014,9 +1164,9 @@ int resident_clusters(const Device& dev) {
   return n;
 }
 
-template <int kN, int kPair, int kMats>
+template <int kN, int kPair, int kSplit, int kMats>
 int launch_product(GemmParams<kMats>& p, const Device& dev, cudaStream_t stream) {
-  using T = Tile<kN, kPair>;
+  using T = Tile<kN, kPair, kSplit>;
   p.tiles = 0;
   for (int i = 0; i < p.count; ++i) {
     GemmMat& g = p.mat[i];
@@ -1029,10 +1179,10 @@ int launch_product(GemmParams<kMats>& p, const Device& dev, cudaStream_t stream)
     }
     p.tiles += g.tiles;
   }
-  const int room = resident_clusters<kN, kPair, kMats>(dev);
+  const int room = resident_clusters<kN, kPair, kSplit, kMats>(dev);
   if (room < 1) return FSDP_ECUDA;
-  return launch_after(ns_product<kN, kPair, kMats>, std::min(p.tiles, room) * kPair, kPair, kGemmThreads, T::kSmemBytes,
-                      stream, p);
+  return launch_after(ns_product<kN, kPair, kSplit, kMats>, std::min(p.tiles, room) * T::kCluster, T::kCluster,
+                      kGemmThreads, T::kSmemBytes, stream, p);
 }
 
 int launch_momentum(const MomentumParams& p, int blocks, cudaStream_t stream) {
@@ -1087,8 +1237,8 @@ int run_small(const NsJob* const* jobs, int count, const NsPlan& plan, const NsM
 
 // One launch's matrices through all steps.
 template <int kMats>
-int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms, const NsMomentum* momentum,
-              const NsApply* apply, unsigned char* workspace, const Device& dev, cudaStream_t stream) {
+int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms, bool split,
+              const NsMomentum* momentum, const NsApply* apply, unsigned char* workspace, const Device& dev, cudaStream_t stream) {
   static thread_local MomentumParams first;
   PassParams& pass = first.pass;
   static thread_local GemmParams<kMats> p;
@@ -1104,8 +1254,9 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
     workspace += carve(j, plan, workspace, &b);
     const int64_t side = std::min(j.rows, j.cols);
     bool ok = true;
-    for (int part = 0; part < (terms == 3 ? 2 : 1); ++part) {
+    for (int part = 0; part < 2; ++part) {
       for (int k = 0; k < 2; ++k) ok = ok && make_map(&maps[i].x[k][part], b.x[k][part], j.rows, j.cols, b.ld_x);
+      if (part == 1 && terms == 1) continue;
       ok = ok && make_map(&maps[i].a[part], b.a[part], side, side, b.ld_a);
       ok = ok && make_map(&maps[i].poly[part], b.poly[part], side, side, b.ld_a);
     }
@@ -1143,34 +1294,24 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
         auto use = [&](CUtensorMap* to, const CUtensorMap* from) { std::memcpy(to, from, 2 * sizeof(CUtensorMap)); };
         g.symmetric = kind != kUpdate;
         g.m = g.n = g.k = side;
-        g.ld = b.ld_a;
-        g.in_hi = g.in_lo = nullptr;
-        g.p_mn = g.q_mn = 0;
+        g.p_mn = g.q_mn = g.in_q = 0;
         if (kind == kGram) {
           use(g.p, q.x[now]);
           use(g.q, q.x[now]);
+          use(g.result, q.a);
           g.k = static_cast<int32_t>(std::max(j.rows, j.cols));
           g.p_mn = g.q_mn = !wide;
-          g.hi = b.a[0];
-          g.lo = b.a[1];
         } else if (kind == kPoly) {
           use(g.p, q.a);
           use(g.q, q.a);
-          g.in_hi = b.a[0];
-          g.in_lo = b.a[1];
-          g.hi = b.poly[0];
-          g.lo = b.poly[1];
+          use(g.result, q.poly);
         } else {
           use(g.p, wide ? q.poly : q.x[now]);
           use(g.q, wide ? q.x[now] : q.poly);
-          g.q_mn = wide;
+          use(g.result, q.x[next]);
+          g.q_mn = g.in_q = wide;
           g.m = static_cast<int32_t>(j.rows);
           g.n = static_cast<int32_t>(j.cols);
-          g.ld = b.ld_x;
-          g.in_hi = b.x[now][0];
-          g.in_lo = b.x[now][1];
-          g.hi = b.x[next][0];
-          g.lo = b.x[next][1];
           g.out = j.out;
           g.out_stride = j.out_stride;
           g.flat = j.flat;
@@ -1184,9 +1325,11 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
       p.alpha = kind == kGram ? kScaleA / (kScaleX * kScaleX) : kind == kPoly ? plan.coef[3 * s + 2] / kScaleA
                                                                                : 1.0f / kScaleA;
       p.beta = kind == kPoly ? plan.coef[3 * s + 1] : plan.coef[3 * s];
-      // pairs of blocks on 256 x 256 tiles where these fill the SMs, else single blocks on 128 x 128
-      const int rc = 2 * large_tiles >= dev.sms ? launch_product<256, 2>(p, dev, stream)
-                                                : launch_product<128, 1>(p, dev, stream);
+      // pairs of blocks on 256 x 256 tiles where these fill the SMs, else 128 x 128 tiles: one
+      // block each (the same sums in the same order), or two (see splits())
+      const int rc = split && kind != kUpdate         ? launch_product<128, 1, 2>(p, dev, stream)
+                     : 2 * large_tiles >= dev.sms ? launch_product<256, 2, 1>(p, dev, stream)
+                                                  : launch_product<128, 1, 1>(p, dev, stream);
       if (rc != FSDP_OK) return rc;
     }
   }
@@ -1253,14 +1396,21 @@ int ns_run(const std::vector<NsJob>& jobs, const NsPlan& plan, const NsMomentum*
     const int count = static_cast<int>(std::min<size_t>(kSmallMats, small.size() - at));
     if (int rc = run_small(&small[at], count, plan, momentum, apply, dev, stream)) return rc;
   }
-  for (int terms : {1, 3}) {
+  for (int kind = 0; kind < 4; ++kind) {
+    const int terms = kind & 1 ? 3 : 1;
+    const bool split = kind & 2;
     std::vector<const NsJob*> group;
     for (const NsJob& j : jobs)
-      if (!is_small(j) && terms_of(j, plan) == terms) group.push_back(&j);
+      if (!is_small(j) && terms_of(j, plan) == terms && splits(j) == split) group.push_back(&j);
+    // the tiles that take longest first, so that the short ones fill up the end
+    std::stable_sort(group.begin(), group.end(), [](const NsJob* a, const NsJob* b) {
+      return std::max(a->rows, a->cols) > std::max(b->rows, b->cols);
+    });
     for (size_t at = 0; at < group.size(); at += kMaxMats) {
       const int count = static_cast<int>(std::min<size_t>(kMaxMats, group.size() - at));
-      const int rc = count <= 8 ? run_group<8>(&group[at], count, plan, terms, momentum, apply, base, dev, stream)
-                                : run_group<kMaxMats>(&group[at], count, plan, terms, momentum, apply, base, dev, stream);
+      const int rc = count <= 8
+                         ? run_group<8>(&group[at], count, plan, terms, split, momentum, apply, base, dev, stream)
+                         : run_group<kMaxMats>(&group[at], count, plan, terms, split, momentum, apply, base, dev, stream);
       if (rc != FSDP_OK) return rc;
       for (int i = 0; i < count; ++i) base += carve(*group[at + i], plan, nullptr, nullptr);
     }

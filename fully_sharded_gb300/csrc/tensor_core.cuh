@@ -60,6 +60,27 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Gu
   }
 }
 
+// As bar_wait, for data that another block of the cluster wrote.
+__device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity, const Guard& g) {
+  const uint64_t t0 = clock_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, "
+        "p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (*g.stop) return false;
+    if (clock_ns() - t0 > g.limit_ns) {
+      *g.stop = 1;
+      atomicOr(g.status, 1u);
+      return false;
+    }
+  }
+}
+
 // A wait for copies or products already issued, after a stop too (bounded again).
 __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = clock_ns();
@@ -109,6 +130,35 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
         "[%4];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(bar)
         : "memory");
+}
+
+// A box back to memory (parts outside the matrix are dropped), in the thread's current bulk group.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+               "r"(y), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// At most kLeft of the thread's groups have yet to read shared memory.
+template <int kLeft>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Barrier of the `threads` threads that use `id`; returns whether any came with `flag`.
+__device__ __forceinline__ bool named_or(int id, int threads, bool flag) {
+  uint32_t any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n barrier.cta.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(any)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(flag))
+      : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void store_cluster(uint32_t addr, const float* v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+               : "memory");
 }
 
 // Shared-memory operand descriptor: 128-byte swizzle, byte strides between
@@ -188,25 +238,6 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// 16 fp16 values (32 bytes, aligned).
-struct Half16 {
-  uint32_t r[8];
-};
-__device__ __forceinline__ Half16 load16(const __half* p) {
-  Half16 h;
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(h.r[0]), "=r"(h.r[1]), "=r"(h.r[2]), "=r"(h.r[3]), "=r"(h.r[4]), "=r"(h.r[5]), "=r"(h.r[6]),
-                 "=r"(h.r[7])
-               : "l"(p)
-               : "memory");
-  return h;
-}
-__device__ __forceinline__ void store16(__half* p, const Half16& h) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(h.r[0]), "r"(h.r[1]),
-               "r"(h.r[2]), "r"(h.r[3]), "r"(h.r[4]), "r"(h.r[5]), "r"(h.r[6]), "r"(h.r[7])
-               : "memory");
 }
 
 }  // namespace tc
