@@ -395,56 +395,76 @@ __device__ __forceinline__ void put_mirror(uint32_t slot, int row, int half, con
   }
 }
 
-// The last step's chunk, fp32 in the slots: written as bf16, or applied to the
-// master, a row by a warp at a time (any alignment, whole lines per access).
+__device__ __forceinline__ float shared_load1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
+
+// The last step's chunk, fp32 in the slots (the caller's barrier ordered the writes):
+// written as bf16, or applied to the master, a row by a warp at a time (any
+// alignment, whole lines per access), eight rows in flight.
 __device__ __forceinline__ void finish_rows(const GemmMat& g, const NsApply& ap, int32_t result, uint32_t slots, int row0,
                                             int col0, int warp, int lane) {
-  constexpr int kRows = 128 / kEpilogueWarps, kBatch = 4;
-  const int first = warp * kRows;
-  int64_t at = 0, rank = 0;  // of element (row, col0)
-  if (result == kApply) {
-    const int64_t f = g.flat + static_cast<int64_t>(row0 + first) * g.n + col0;
-    rank = f / ap.shard;
-    at = f - rank * ap.shard;
+  constexpr int kRows = 128 / kEpilogueWarps, kBatch = 8;
+  const int first = row0 + warp * kRows, rows = min(kRows, g.m - first);
+  const int n = g.n;
+  const bool there[2] = {col0 + lane < n, col0 + 32 + lane < n};
+  uint32_t from[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) from[h] = slots + (lane >> 4) * kSlotBytes + (lane & 3) * 4;
+  if (result == kOut) {
+    uint16_t* out = g.out + first * g.out_stride + col0 + lane;
+    const int64_t stride = g.out_stride;
+#pragma unroll
+    for (int r0 = 0; r0 < kRows; r0 += kBatch) {
+      float v[kBatch][2];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          v[b][h] = shared_load1(from[h] + slot_at(warp * kRows + r0 + b, h * 4 + ((lane & 15) >> 2)));
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b, out += stride)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (r0 + b < rows && there[h]) out[32 * h] = __bfloat16_as_ushort(__float2bfloat16_rn(v[b][h]));
+    }
+    return;
   }
+  const int64_t shard = ap.shard;
+  const float keep = ap.keep, step = g.step;
+  int64_t f = g.flat + static_cast<int64_t>(first) * n + col0 + lane;
+  int64_t rank = f / shard, at = f - rank * shard;  // of element (row, col0 + lane)
+  uint16_t* full = ap.full + f;
+#pragma unroll
   for (int r0 = 0; r0 < kRows; r0 += kBatch) {
     float v[kBatch][2], old[kBatch][2];
     float* where[kBatch][2];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int row = first + r0 + b;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int col = 32 * h + lane;
-        const bool there = row0 + row < g.m && col0 + col < g.n;
-        asm volatile("ld.shared.f32 %0, [%1];"
-                     : "=f"(v[b][h])
-                     : "r"(slots + (lane >> 4) * kSlotBytes + slot_at(row, h * 4 + ((lane & 15) >> 2)) + (lane & 3) * 4)
-                     : "memory");
-        where[b][h] = nullptr;
-        if (result == kApply && there) {
-          int64_t a = at + col, r = rank;
-          while (a >= ap.shard) a -= ap.shard, ++r;
-          where[b][h] = ap.master[r] + a;
-          old[b][h] = *where[b][h];
-        } else if (result == kOut && there) {
-          g.out[(row0 + row) * g.out_stride + col0 + col] = __bfloat16_as_ushort(__float2bfloat16_rn(v[b][h]));
-        }
+        v[b][h] = shared_load1(from[h] + slot_at(warp * kRows + r0 + b, h * 4 + ((lane & 15) >> 2)));
+        const bool use = r0 + b < rows && there[h];
+        int64_t a = at + 32 * h, r = rank;
+        if (use)
+          while (a >= shard) a -= shard, ++r;
+        where[b][h] = use ? ap.master[r] + a : nullptr;
+        old[b][h] = use ? *where[b][h] : 0.0f;
       }
-      at += g.n;
-      if (result == kApply)
-        while (at >= ap.shard) at -= ap.shard, ++rank;
+      at += n;
+      if (r0 + b + 1 < rows)
+        while (at >= shard) at -= shard, ++rank;
     }
-    if (result != kApply) continue;
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b)
+    for (int b = 0; b < kBatch; ++b, full += n)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (!where[b][h]) continue;
-        const float w = old[b][h] * ap.keep - g.step * v[b][h];
+        const float w = old[b][h] * keep - step * v[b][h];
         *where[b][h] = w;
-        ap.full[g.flat + static_cast<int64_t>(row0 + first + r0 + b) * g.n + col0 + 32 * h + lane] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(w));
+        full[32 * h] = __bfloat16_as_ushort(__float2bfloat16_rn(w));
       }
   }
 }
@@ -474,21 +494,28 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
       bar_init(smem_addr(&done_bar[b]), 1);
       bar_init(smem_addr(&free_bar[b]), kEpilogueWarps * kPair);
       bar_init(smem_addr(&in_bar[b]), 1);
-      bar_init(smem_addr(&out_bar[b]), 1);
+      bar_init(smem_addr(&out_bar[b]), kEpilogueWarps);
     }
-    bar_init(smem_addr(&shared_bar), kEpilogueWarps);
+    bar_init(smem_addr(&shared_bar), 1);
     bar_init(smem_addr(&taken_bar), kEpilogueWarps);
     stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) tmem_alloc<kPair>(smem_addr(&tmem_slot), T::kTmemCols);
+  if (warp == 2 && lane < 3) {  // the first matrix's maps
+    const GemmMat& g = p.mat[0];
+    prefetch_map(lane == 0 ? g.p : lane == 1 ? g.q : g.result);
+  }
   fence_before();
   __syncthreads();
   if constexpr (T::kCluster == 2) cluster_sync();
   fence_after();
   const uint32_t tmem = tmem_slot;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The previous kernel's results: each role waits for them right before its first
+  // access, after it has read its part of the parameters (their first reads miss the
+  // constant cache, about 1 us in all).
   asm volatile("griddepcontrol.launch_dependents;");
+  const auto await_inputs = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
 
   // this block's steps of the inner dimension, over all terms: [lo, hi)
   const auto steps_of = [&](const GemmMat& g, int* lo, int* hi) {
@@ -525,6 +552,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
         const uint32_t own = smem_addr(&full_bar[s]), bar = kPair == 2 ? in_block(own, 0) : own;
         const uint32_t a = smem + s * T::kStageBytes, b = a + T::kABytes;
         if (pair_rank == 0) bar_expect(own, T::kStageBytes * kPair);
+        if (it == 0) await_inputs();
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int r = row0 + 64 * q;
@@ -593,6 +621,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
         ok = bar_wait(smem_addr(&out_bar[set]), ((e / sets) & 1u) ^ 1u, guard);
         if (!ok) break;
         bar_expect(bar, parts * kSlotBytes);
+        if (e == 0) await_inputs();
         for (int part = 0; part < parts; ++part)
           for (int b = 0; b < 2; ++b)
             tma_box<1>(to + part * kSlotBytes + b * 8192, &in[part], col0, block * 128 + 64 * b, bar);
@@ -606,8 +635,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     const int own = warp - 4, quarter = own & 3, half = own >> 2;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const bool leader = own == 0 && lane == 0;  // issues the stores
-    uint32_t n = 0, e = 0, left = 0;            // tiles, chunks, chunks whose slots are released
+    const bool leader = own == 0 && lane == 0;
+    await_inputs();
+    uint32_t n = 0, e = 0, left = 0;            // tiles, chunks, chunks whose slots this warp has released
     // a wait of this thread ran out; some thread's did (the same for all, known at the next barrier)
     bool lost = false, failed = false;
     for (int t = first_tile; !failed && t < p.tiles; t += tile_step, ++n) {
@@ -630,12 +660,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
         float v[32];
         sums(1 - rank, v);
         lost |= !bar_wait_cluster(smem_addr(&taken_bar), (n & 1u) ^ 1u, guard);
-        const uint32_t to = in_block(share, 1 - rank);
+        if (leader) bar_expect(smem_addr(&shared_bar), kShareBytes);  // what comes the other way
+        const uint32_t to = in_block(share, 1 - rank), bar = in_block(smem_addr(&shared_bar), 1 - rank);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) store_cluster(to + ((half * 8 + q) * 128 + row) * 16, &v[4 * q]);
-        asm volatile("fence.acq_rel.cluster;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) bar_arrive_cluster(in_block(smem_addr(&shared_bar), 1 - rank));
+        for (int q = 0; q < 8; ++q) store_async(to + ((half * 8 + q) * 128 + row) * 16, &v[4 * q], bar);
       }
       bool any = false;
       for (int c = 0; c < kN / kChunk; ++c) {
@@ -711,18 +739,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
           // the slots were read by every warp, and may be written by the next fetch
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           named_or(1, 32 * kEpilogueWarps, false);
-          if (leader) bar_arrive(smem_addr(&out_bar[set]));
-        } else if (leader) {
+          if (lane == 0) bar_arrive(smem_addr(&out_bar[set]));
+        } else if (lane == 0) {
+          // up to eight boxes, one for each warp to send: part, half of the rows, direct or mirrored
           const int parts = p.kind == kUpdate || p.terms == 3 ? 2 : 1;
-          for (int part = 0; part < parts; ++part)
-            for (int b = 0; b < 2; ++b) {
-              const int at = block * 128 + 64 * b;
-              if (at >= g.m) continue;
+          const int b = own & 1, part = own >> 1 & 1, at = block * 128 + 64 * b;
+          if (part < parts && at < g.m) {
+            if (own < 4)
               tma_store(&g.result[part], col0, at, base + part * kSlotBytes + b * 8192);
-              if (mirror) tma_store(&g.result[part], at, col0, base + (parts + part) * kSlotBytes + b * 8192);
-            }
+            else if (mirror)
+              tma_store(&g.result[part], at, col0, base + (parts + part) * kSlotBytes + b * 8192);
+          }
           bulk_commit();
-          // the chunk before this one (this one, with a single set) has left its slots
+          // this warp's box of the chunk before this one (of this one, with a single set) has left its slot
           if (sets == 2)
             bulk_wait_read<1>();
           else
@@ -748,7 +777,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
           bar_arrive(smem_addr(&free_bar[buf]));
       }
     }
-    if (leader) bulk_wait_all();
+    if (lane == 0) bulk_wait_all();
   }
   __syncwarp();
   fence_before();
@@ -1235,6 +1264,22 @@ int run_small(const NsJob* const* jobs, int count, const NsPlan& plan, const NsM
   return launch_after(ns_small, count, 1, kSmallThreads, smem, stream, p);
 }
 
+// Estimated times, in microseconds, of a launch of `tiles` tiles of `steps` steps of 64
+// of the inner dimension. Measured on GB300: a step of a 256 x 256 tile takes a pair 0.36 (93 %
+// of the measured cuBLAS rate), one of a 128 x 128 tile takes a block 0.33 (bound by
+// L2: 32 KB of operands for a quarter of the products); a tile's results leave in
+// 7.5 and 1.6, while the next tile's products run, the last one's after them.
+// Updates of a GPT-2 block's matrices (12 steps): pairs 292, single blocks
+// 268 us for all; of 4096 x 11008 (64 steps) pairs 268, single blocks 446 us each.
+double pair_time(int64_t tiles, int steps, int sms) {
+  const double rounds = static_cast<double>((tiles + sms / 2 - 1) / (sms / 2));
+  return rounds * std::max(0.36 * steps, 7.5) + 7.5;
+}
+double block_time(int64_t tiles, int steps, int sms) {
+  const double rounds = static_cast<double>((tiles + sms - 1) / sms);
+  return rounds * std::max(0.33 * steps, 1.6) + 1.6;
+}
+
 // One launch's matrices through all steps.
 template <int kMats>
 int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms, bool split,
@@ -1283,7 +1328,8 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
     const bool last = s + 1 == plan.steps;
     const int now = s & 1, next = now ^ 1;
     for (int kind = kGram; kind <= kUpdate; ++kind) {
-      int64_t large_tiles = 0;
+      int64_t large_tiles = 0, small_tiles = 0;
+      int steps = 0;
       for (int i = 0; i < count; ++i) {
         const NsJob& j = *jobs[i];
         const Buffers& b = buffers[i];
@@ -1319,17 +1365,20 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
         }
         const int64_t rows = (g.m + 127) / 128, cols = (g.n + 255) / 256;
         large_tiles += g.symmetric ? cols * (cols + 1) / 2 : (rows + 1) / 2 * cols;
+        small_tiles += g.symmetric ? rows * (rows + 1) / 2 : rows * ((g.n + 127) / 128);
+        steps = std::max(steps, (g.k + kTileK - 1) / kTileK * terms);
       }
       p.kind = kind;
       p.result = kind != kUpdate || !last ? kParts : apply ? kApply : kOut;
       p.alpha = kind == kGram ? kScaleA / (kScaleX * kScaleX) : kind == kPoly ? plan.coef[3 * s + 2] / kScaleA
                                                                                : 1.0f / kScaleA;
       p.beta = kind == kPoly ? plan.coef[3 * s + 1] : plan.coef[3 * s];
-      // pairs of blocks on 256 x 256 tiles where these fill the SMs, else 128 x 128 tiles: one
-      // block each (the same sums in the same order), or two (see splits())
-      const int rc = split && kind != kUpdate         ? launch_product<128, 1, 2>(p, dev, stream)
-                     : 2 * large_tiles >= dev.sms ? launch_product<256, 2, 1>(p, dev, stream)
-                                                  : launch_product<128, 1, 1>(p, dev, stream);
+      // pairs of blocks on 256 x 256 tiles, or single ones on 128 x 128 (the same sums in the
+      // same order), whichever is estimated faster; or two blocks a tile (see splits())
+      const bool pairs = pair_time(large_tiles, steps, dev.sms) < block_time(small_tiles, steps, dev.sms);
+      const int rc = split && kind == kGram ? launch_product<128, 1, 2>(p, dev, stream)
+                     : pairs                ? launch_product<256, 2, 1>(p, dev, stream)
+                                            : launch_product<128, 1, 1>(p, dev, stream);
       if (rc != FSDP_OK) return rc;
     }
   }

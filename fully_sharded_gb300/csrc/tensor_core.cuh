@@ -156,9 +156,16 @@ __device__ __forceinline__ bool named_or(int id, int threads, bool flag) {
       : "memory");
   return any != 0;
 }
-__device__ __forceinline__ void store_cluster(uint32_t addr, const float* v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
-               : "memory");
+// 16 bytes into another block's shared memory, counted there by that block's barrier `bar`.
+__device__ __forceinline__ void store_async(uint32_t addr, const float* v, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+      "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // Shared-memory operand descriptor: 128-byte swizzle, byte strides between
