@@ -581,16 +581,20 @@ _torch_module = None
 def _cuda_stream(stream):
     """The stream's handle; None: the current stream (of a caller that holds CUDA tensors)."""
     if stream is None:
-        return _torch().cuda.current_stream().cuda_stream
+        torch = _torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 2.8 us less than the Stream object
+        if raw is not None:
+            return raw(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _float_dtype(t, what: str) -> int:
     torch = _torch()
     dtype = t.dtype
-    if dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return FSDP_DTYPE_BF16
-    if dtype == torch.float32:
+    if dtype is torch.float32:
         return FSDP_DTYPE_F32
     raise ValueError("%s: expected float32 or bfloat16, got %s" % (what, dtype))
 
@@ -601,12 +605,13 @@ def _matrix(t, what: str, shape, dtype=None):
         raise ValueError("%s: expected a CUDA tensor, got one on %s" % (what, t.device))
     if t.shape != shape:
         raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError("%s: expected %s, got %s" % (what, dtype, t.dtype))
+    rows, cols = shape
     row, col = t.stride()
-    if col != 1 and shape[1] > 1:
+    if col != 1 and cols > 1:
         raise ValueError("%s: expected contiguous rows" % what)
-    return t.data_ptr(), (row if shape[0] > 1 else shape[1])
+    return t.data_ptr(), (row if rows > 1 else cols)
 
 
 def _vector(t, what: str, n: int, dtype=None):

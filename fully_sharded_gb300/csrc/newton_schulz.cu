@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(32 * kPassWarps) ns_momentum(const __grid_cons
     }
     sum += s;
   }
-  if (j.partial) block_sum_to(sum, &j.partial[part]);
+  block_sum_to(sum, &j.partial[part]);
 }
 
 // X_0 as two parts.
@@ -816,6 +816,7 @@ struct SmallMat {
 struct SmallParams {
   SmallMat mat[kSmallMats];
   NsApply apply;
+  NsMomentum momentum;  // applies: the step's first part, done here too
   float coef[3 * 32];
   int32_t steps, terms;
   float eps;
@@ -877,6 +878,23 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
   };
   const int count = g.rows * g.cols;
   float squares = 0.0f;
+  if (p.applies) {  // u, written to where it is read again below by the same thread
+    const NsMomentum& m = p.momentum;
+    float* u = static_cast<float*>(const_cast<void*>(g.source));
+    int64_t at = g.flat + threadIdx.x, rank = at / m.shard;
+    at -= rank * m.shard;
+    for (int i = threadIdx.x; i < count; i += kSmallThreads, at += kSmallThreads) {
+      while (at >= m.shard) at -= m.shard, ++rank;
+      float sum = 0.0f;
+#pragma unroll 4
+      for (int k = 0; k < m.w; ++k) sum += __bfloat162float(__ushort_as_bfloat16(m.grads[k][g.flat + i]));
+      const float mean = mean_of(sum, m);
+      float* mom = m.momentum[rank] + at;
+      const float v = m.mu * *mom + mean;
+      *mom = v;
+      u[i] = m.nesterov ? mean + m.mu * v : v;
+    }
+  }
   for (int i = threadIdx.x; i < count; i += kSmallThreads) {
     const int r = i / g.cols;
     const float v = source(r, i - r * g.cols);
@@ -1230,21 +1248,7 @@ int launch_momentum(const MomentumParams& p, int blocks, cudaStream_t stream) {
 int run_small(const NsJob* const* jobs, int count, const NsPlan& plan, const NsMomentum* momentum, const NsApply* apply,
               const Device& dev, cudaStream_t stream) {
   static thread_local SmallParams p;
-  if (momentum) {
-    static thread_local MomentumParams first;
-    for (int at = 0; at < count; at += kMaxMats) {
-      int blocks = 0;
-      first.pass.count = std::min(kMaxMats, count - at);
-      for (int i = 0; i < first.pass.count; ++i) {
-        const NsJob& j = *jobs[at + i];
-        blocks += parts_of(j);
-        first.pass.mat[i] = {j.source, j.source_stride, j.rows, j.cols, nullptr, nullptr, 0, nullptr, j.flat, j.dtype,
-                             parts_of(j), blocks};
-      }
-      first.m = *momentum;
-      if (int rc = launch_momentum(first, blocks, stream)) return rc;
-    }
-  }
+  if (momentum) p.momentum = *momentum;
   int smem = 0;
   for (int i = 0; i < count; ++i) {
     const NsJob& j = *jobs[i];

@@ -237,13 +237,13 @@ __device__ __forceinline__ float scale_of(float top) { return fmaxf(top * (1.0f 
 // more rows in flight while others wait at their reductions. kWide: rows that need
 // more threads at kMaxV groups each.
 constexpr int forward_threads(int v, bool wide) { return v < 3 || wide ? 512 : 384; }
-constexpr int forward_blocks(int v, bool wide) { return v == 2 || wide ? 1 : 2; }
+constexpr int forward_blocks(int v, bool wide, bool residual) { return v == 2 || wide ? 1 : v > 2 && !residual ? 3 : 2; }
 constexpr int backward_threads(bool wide) { return wide ? 512 : 256; }
 constexpr int backward_blocks(int v, bool wide) { return wide ? 1 : v == 1 ? 4 : v == 2 ? 3 : 2; }
 
 // kQuant 0: y of the inputs' type; 1: 8 bits, one scale per row; 2: 8 bits, scales per group.
 template <typename T, bool kResidual, int kQuant, Map kMap, int kV, bool kWide = false>
-__global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV, kWide))
+__global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV, kWide, kResidual))
     norm_rows(const __grid_constant__ NormParams p) {
   __shared__ float shared[3][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV,
     for (int k = 0; k < kV; ++k) {
       if constexpr (kV > 1) gain_group<kMap>(p.gain, p.a.gain_dtype, p.gain_vectors, r, k, cols, g[k]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[k][e] *= rstd * g[k][e];
+      for (int e = 0; e < 8; ++e) v[k][e] *= kQuant == 0 ? rstd * g[k][e] : g[k][e];  // 8 bits: rstd goes into the scale
     }
     if constexpr (kQuant == 0) {
       T* y = static_cast<T*>(p.y) + row * p.a.y_stride;
@@ -310,12 +310,17 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV,
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
         if constexpr (kQuant == 2) all = warp_reduce<true>(top[k], p.a.group / 8);
-        const float scale = scale_of(all);
+        const float scale = scale_of(all * rstd);
         const int j = place<kMap>(r, k, 0);
         if (kQuant == 1 ? (k == 0 && r.t == 0) : (j < cols && (j & (p.a.group - 1)) == 0))
           p.scales[row * groups + (kQuant == 1 ? 0 : j >> p.group_bits)] = scale;
-        const float inverse = __frcp_rn(scale);
-        float q[8];
+        float inverse = __frcp_rn(scale), q[8];
+        if (rstd * inverse <= 0x1p127f) {
+          inverse *= rstd;
+        } else {  // a group of zeros or next to them: the product of the two factors would overflow
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[k][e] *= rstd;
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) q[e] = v[k][e] * inverse;
         store_group<kMap>(y, r, k, cols, q);
