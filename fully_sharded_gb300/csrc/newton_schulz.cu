@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
   __shared__ uint32_t tmem_slot;
   __shared__ int stop;
   __shared__ float norm;
-  const SmallMat& g = p.mat[blockIdx.x];
+  const SmallMat g = p.mat[blockIdx.x];
   const SmallShape s(g.rows, g.cols);
   const bool wide = g.rows <= g.cols;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -871,11 +871,6 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
     *reinterpret_cast<uint4*>(x + i) = make_uint4(0, 0, 0, 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const auto source = [&](int r, int c) {
-    const int64_t i = r * g.source_stride + c;
-    return g.dtype == FSDP_DTYPE_F32 ? static_cast<const float*>(g.source)[i]
-                                     : __bfloat162float(static_cast<const __nv_bfloat16*>(g.source)[i]);
-  };
   const int count = g.rows * g.cols;
   float squares = 0.0f;
   if (p.applies) {  // u, written to where it is read again below by the same thread
@@ -883,22 +878,78 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
     float* u = static_cast<float*>(const_cast<void*>(g.source));
     int64_t at = g.flat + threadIdx.x, rank = at / m.shard;
     at -= rank * m.shard;
-    for (int i = threadIdx.x; i < count; i += kSmallThreads, at += kSmallThreads) {
-      while (at >= m.shard) at -= m.shard, ++rank;
-      float sum = 0.0f;
+    constexpr int kBatch = 4;  // elements of a thread whose loads are in flight together
+    for (int i0 = threadIdx.x; i0 < count; i0 += kBatch * kSmallThreads) {
+      float* mom[kBatch];
+      float old[kBatch], sum[kBatch] = {};
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b, at += kSmallThreads) {
+        const bool there = i0 + b * kSmallThreads < count;
+        if (there)
+          while (at >= m.shard) at -= m.shard, ++rank;
+        mom[b] = there ? m.momentum[rank] + at : nullptr;
+        old[b] = there ? *mom[b] : 0.0f;
+      }
 #pragma unroll 4
-      for (int k = 0; k < m.w; ++k) sum += __bfloat162float(__ushort_as_bfloat16(m.grads[k][g.flat + i]));
-      const float mean = mean_of(sum, m);
-      float* mom = m.momentum[rank] + at;
-      const float v = m.mu * *mom + mean;
-      *mom = v;
-      u[i] = m.nesterov ? mean + m.mu * v : v;
+      for (int k = 0; k < m.w; ++k) {
+        const uint16_t* row = m.grads[k] + g.flat + i0;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          sum[b] += __bfloat162float(__ushort_as_bfloat16(mom[b] ? row[b * kSmallThreads] : uint16_t(0)));
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (!mom[b]) continue;
+        const float mean = mean_of(sum[b], m);
+        const float v = m.mu * old[b] + mean;
+        *mom[b] = v;
+        u[i0 + b * kSmallThreads] = m.nesterov ? mean + m.mu * v : v;
+      }
     }
   }
-  for (int i = threadIdx.x; i < count; i += kSmallThreads) {
-    const int r = i / g.cols;
-    const float v = source(r, i - r * g.cols);
-    squares += v * v;
+  // Everything outside the products goes by pieces of 8 columns of X: piece t lies in row
+  // `row` from column `col` on, `n` of its elements are inside, element e is at (r, c) of the
+  // matrix. Neighbouring threads have neighbouring elements of the matrix.
+  struct Piece {
+    int row, col, n, at;
+  };
+  const int per_row = (s.length + 7) / 8, all = s.side * per_row;
+  const auto piece = [&](int t) {
+    const int q = wide ? t / per_row : t / s.side;
+    const int row = wide ? q : t - q * s.side, col = 8 * (wide ? t - q * per_row : q);
+    return Piece{row, col, min(8, s.length - col), small_at(s.side16, row, col)};
+  };
+  const int64_t along = wide ? 1 : g.source_stride, across = wide ? g.source_stride : 1;
+  __syncthreads();  // the zeros, and u, are written
+  // The source is read once: its fp32 bits wait where the element's two parts will be,
+  // until the norm is known.
+  for (int t = threadIdx.x; t < all; t += kSmallThreads) {
+    const Piece q = piece(t);
+    const int64_t from = q.row * across + q.col * along;
+    float v[8];
+    if (g.dtype == FSDP_DTYPE_F32) {
+      const float* src = static_cast<const float*>(g.source) + from;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = src[(e < q.n ? e : 0) * along];
+    } else {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(g.source) + from;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __bfloat162float(src[(e < q.n ? e : 0) * along]);
+    }
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = e < q.n ? v[e] : 0.0f;
+      squares += v[e] * v[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t a0 = __float_as_uint(v[2 * e]), a1 = __float_as_uint(v[2 * e + 1]);
+      hi[e] = __byte_perm(a0, a1, 0x7632);
+      lo[e] = __byte_perm(a0, a1, 0x5410);
+    }
+    *reinterpret_cast<uint4*>(x + q.at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(x + s.part_x + q.at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
   block_sum_to(squares, &norm);
   fence_before();
@@ -906,13 +957,23 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
   fence_after();
   const uint32_t tmem = tmem_slot;
   const float inv = 1.0f / (sqrtf(norm) + p.eps);
-  for (int i = threadIdx.x; i < count; i += kSmallThreads) {
-    const int r = i / g.cols, c = i - r * g.cols;
-    const int at = wide ? small_at(s.side16, r, c) : small_at(s.side16, c, r);
-    const float v = source(r, c) * inv * kScaleX;
-    const __half hi = __float2half_rn(v);
-    *reinterpret_cast<__half*>(x + at) = hi;
-    *reinterpret_cast<__half*>(x + s.part_x + at) = __float2half_rn(v - __half2float(hi));
+  for (int t = threadIdx.x; t < all; t += kSmallThreads) {
+    const Piece q = piece(t);
+    const uint4 h = *reinterpret_cast<const uint4*>(x + q.at), l = *reinterpret_cast<const uint4*>(x + s.part_x + q.at);
+    const uint32_t hi[4] = {h.x, h.y, h.z, h.w}, lo[4] = {l.x, l.y, l.z, l.w};
+    uint32_t first[4], second[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float a0 = __uint_as_float(__byte_perm(lo[e], hi[e], 0x5410)) * inv * kScaleX;
+      const float a1 = __uint_as_float(__byte_perm(lo[e], hi[e], 0x7632)) * inv * kScaleX;
+      const __half2 t0 = __floats2half2_rn(a0, a1);
+      const float2 f = __half22float2(t0);
+      const __half2 t1 = __floats2half2_rn(a0 - f.x, a1 - f.y);
+      first[e] = *reinterpret_cast<const uint32_t*>(&t0);
+      second[e] = *reinterpret_cast<const uint32_t*>(&t1);
+    }
+    *reinterpret_cast<uint4*>(x + q.at) = make_uint4(first[0], first[1], first[2], first[3]);
+    *reinterpret_cast<uint4*>(x + s.part_x + q.at) = make_uint4(second[0], second[1], second[2], second[3]);
   }
   uint32_t phase = 0;
   // a wait of this thread ran out; some thread's did (the same for all, known at the next barrier)
@@ -1036,29 +1097,41 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
   fence_before();
   failed = __syncthreads_or(lost);
   if (!failed) {
-    int64_t f = g.flat + threadIdx.x, rank = 0;
-    if (p.applies) {
-      rank = f / p.apply.shard;
-      f -= rank * p.apply.shard;
-    }
-    for (int i = threadIdx.x; i < count; i += kSmallThreads, f += kSmallThreads) {
-      const int r = i / g.cols, c = i - r * g.cols;
-      const int at = wide ? small_at(s.side16, r, c) : small_at(s.side16, c, r);
-      const float v = (__half2float(*reinterpret_cast<const __half*>(x + at)) +
-                       __half2float(*reinterpret_cast<const __half*>(x + s.part_x + at))) *
-                      (1.0f / kScaleX);
+    for (int t = threadIdx.x; t < all; t += kSmallThreads) {
+      const Piece q = piece(t);
+      float v[8];
+      sum_of(*reinterpret_cast<const uint4*>(x + q.at), *reinterpret_cast<const uint4*>(x + s.part_x + q.at), v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= 1.0f / kScaleX;
       if (!p.applies) {
-        g.out[r * g.out_stride + c] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+        const int64_t step = wide ? 1 : g.out_stride;
+        uint16_t* out = g.out + (wide ? q.row * g.out_stride + q.col : q.col * g.out_stride + q.row);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e < q.n) out[e * step] = __bfloat16_as_ushort(__float2bfloat16_rn(v[e]));
         continue;
       }
-      while (f >= p.apply.shard) {
-        f -= p.apply.shard;
-        ++rank;
+      const int64_t shard = p.apply.shard, step = wide ? 1 : g.cols;
+      const int64_t f = g.flat + (wide ? static_cast<int64_t>(q.row) * g.cols + q.col : static_cast<int64_t>(q.col) * g.cols + q.row);
+      int64_t rank = f / shard, at = f - rank * shard;
+      float* master[8];
+      float old[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e, at += step) {
+        master[e] = nullptr;
+        if (e < q.n) {
+          while (at >= shard) at -= shard, ++rank;
+          master[e] = p.apply.master[rank] + at;
+        }
+        old[e] = master[e] ? *master[e] : 0.0f;
       }
-      float* master = p.apply.master[rank] + f;
-      const float w = *master * p.apply.keep - g.step * v;
-      *master = w;
-      p.apply.full[g.flat + i] = __bfloat16_as_ushort(__float2bfloat16_rn(w));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (!master[e]) continue;
+        const float w = old[e] * p.apply.keep - g.step * v[e];
+        *master[e] = w;
+        p.apply.full[f + e * step] = __bfloat16_as_ushort(__float2bfloat16_rn(w));
+      }
     }
   }
   if (warp == 0) {
