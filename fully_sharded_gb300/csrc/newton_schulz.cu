@@ -9,12 +9,20 @@
 // Representation. The products run on fp16 operands with fp32 accumulation, at
 // the rate of bf16 and with 11 instead of 8 bits; powers of two keep the values in
 // fp16's range: X is held times 2^12, A and P times 2^10 (X's singular values
-// stay below 7 and P's below 60, which ns_plan() checks). X itself is held as two
+// stay below 7 and P's below 30, which ns_plan() checks). X itself is held as two
 // fp16 parts, hi + lo, 22 bits: only the products see it rounded. A rounding of X
 // would put noise into the directions that X lacks, and each step multiplies
 // those by a = 3.4 (measured on matrices of low rank: 3 % of the result's
 // norm, 0.06 % with the two parts); the operands' rounding stays inside X's row or
 // column space. With terms = 3 every operand has both parts: hi hi + lo hi + hi lo.
+//
+// Late steps round less still. Once the mean squared singular value m = |X|^2 / side
+// is large (1/4 or more: most of the space is filled, nothing is left to keep clean)
+// A is close to m I, and what is rounded is only the rest, A' = A - m I:
+//   b A + c A^2 = d I + P',  d = b m + c m^2,  P' = (b + 2 c m) A' + c A'^2,
+//   X <- (a + d) X + P' X.
+// P' is several times smaller than P, and so is the part of X' that comes from rounded
+// operands (error of a 768 x 2304 matrix 1.5e-3 -> 0.5e-3 of its norm).
 //
 // Each of the three products is one launch over all matrices of the call: a
 // persistent grid of tiles; in each block a producer lane (TMA), a product lane
@@ -278,6 +286,9 @@ struct GemmMat {
   uint8_t p_mn, q_mn;      // the operand's row index (of C's rows, columns) is the contiguous one
   uint8_t symmetric;
   uint8_t in_q;            // `in` is q (else p)
+  const float* squares;    // sums of squares of X over 32 x 32 blocks (null: X_0, no shift)
+  float* new_squares;      // those of the next X
+  int32_t squares_count;
   uint16_t* out;
   int64_t out_stride;
   int64_t flat;
@@ -290,10 +301,12 @@ struct GemmParams {
   NsApply apply;
   int32_t count, tiles, terms;
   int32_t kind, result;
-  float alpha, beta;
+  float a, b, c;           // the step's coefficients
   unsigned int* status;
 };
 static_assert(sizeof(GemmParams<kMaxMats>) <= 32764, "kernel parameter block too large");
+
+constexpr float kShiftFrom = 0.25f;  // mean squared singular value from which A is shifted
 
 constexpr int kTileK = 64;
 constexpr int kChunk = 64;          // columns of a tile that leave together
@@ -478,6 +491,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
   __shared__ __align__(8) uint64_t shared_bar, taken_bar;     // kSplit: sums have come from, were taken by the other block
   __shared__ uint32_t tmem_slot;
   __shared__ int stop;
+  __shared__ float squares[2][kEpilogueWarps];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
   const uint32_t slots = smem + T::kStages * T::kStageBytes, share = slots + kSlots * kSlotBytes;
@@ -640,10 +654,34 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     uint32_t n = 0, e = 0, left = 0;            // tiles, chunks, chunks whose slots this warp has released
     // a wait of this thread ran out; some thread's did (the same for all, known at the next barrier)
     bool lost = false, failed = false;
+    int known = -1, turn = 0;                   // the matrix whose m is `shift`
+    float shift = 0.0f;
     for (int t = first_tile; !failed && t < p.tiles; t += tile_step, ++n) {
       int i, j, lo, hi;
       const GemmMat& g = tiles.at(t, &i, &j);
       steps_of(g, &lo, &hi);
+      if (known != tiles.mat) {  // its m, from all blocks' sums in a fixed order
+        known = tiles.mat;
+        shift = 0.0f;
+        if (g.squares) {
+          float sum = 0.0f;
+          const int count = g.squares_count;
+#pragma unroll 8
+          for (int k = threadIdx.x - 128; k < count; k += 32 * kEpilogueWarps) sum += g.squares[k];
+          sum = warp_sum(sum);
+          if (lane == 0) squares[turn][own] = sum;
+          failed = named_or(1, 32 * kEpilogueWarps, lost);
+          if (failed) break;
+          sum = 0.0f;
+#pragma unroll
+          for (int k = 0; k < kEpilogueWarps; ++k) sum += squares[turn][k];
+          turn ^= 1;  // the next matrix's barrier comes before this set is written again
+          shift = sum / (kScaleX * kScaleX) / static_cast<float>(min(g.m, min(g.n, g.k)));
+          if (shift < kShiftFrom) shift = 0.0f;
+        }
+      }
+      const float alpha = p.kind == kGram ? kScaleA / (kScaleX * kScaleX) : p.kind == kPoly ? p.c / kScaleA : 1.0f / kScaleA;
+      const float beta = p.kind == kPoly ? p.b + 2.0f * p.c * shift : p.a + p.b * shift + p.c * shift * shift;
       const int block = i * kPair + pair_rank;  // in rows of 128, as col0 / 128 in columns
       const uint32_t buf = n & 1u;
       lost |= !bar_wait(smem_addr(&done_bar[buf]), (n >> 1) & 1u, guard);
@@ -683,9 +721,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
           }
         }
 #pragma unroll
-        for (int q = 0; q < 32; ++q) v[q] *= p.alpha;
+        for (int q = 0; q < 32; ++q) v[q] *= alpha;
         if (p.kind == kGram) {
           lost |= !bar_wait(smem_addr(&out_bar[set]), ((e / sets) & 1u) ^ 1u, guard);
+          const int diagonal = block * 128 + row - (col0 + half * 32);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[q] -= q == diagonal ? shift * kScaleA : 0.0f;
         } else {
           lost |= !bar_wait(smem_addr(&in_bar[set]), (e / sets) & 1u, guard);
           for (int part = 0; part < (p.kind == kUpdate || p.terms == 3 ? 2 : 1); ++part) {
@@ -696,8 +737,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[k]));
-                v[8 * q + 2 * k] += p.beta * f.x;
-                v[8 * q + 2 * k + 1] += p.beta * f.y;
+                v[8 * q + 2 * k] += beta * f.x;
+                v[8 * q + 2 * k + 1] += beta * f.y;
               }
             }
           }
@@ -710,6 +751,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
                          __float_as_uint(v[4 * q] * (1.0f / kScaleX)), __float_as_uint(v[4 * q + 1] * (1.0f / kScaleX)),
                          __float_as_uint(v[4 * q + 2] * (1.0f / kScaleX)), __float_as_uint(v[4 * q + 3] * (1.0f / kScaleX)));
         } else {
+          if (p.kind == kUpdate) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 32; ++q) sum += v[q] * v[q];
+            sum = warp_sum(sum);
+            if (lane == 0) g.new_squares[(block * 4 + quarter) * ((g.n + 63) / 64 * 2) + col0 / 32 + half] = sum;
+          }
           uint32_t r[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
@@ -1168,8 +1216,9 @@ int parts_of(const NsJob& j) {
 // each as hi and, where it is used, lo part, rows a multiple of 128 bytes apart.
 struct Buffers {
   __half *x[2][2], *a[2], *poly[2];
-  float* partial;
+  float *partial, *squares[2];
   int64_t ld_x, ld_a;
+  int64_t squares_count;
 };
 
 int64_t carve(const NsJob& j, const NsPlan& plan, unsigned char* base, Buffers* out) {
@@ -1193,6 +1242,8 @@ int64_t carve(const NsJob& j, const NsPlan& plan, unsigned char* base, Buffers* 
     b.poly[part] = reinterpret_cast<__half*>(take(side * b.ld_a * 2));
   }
   b.partial = reinterpret_cast<float*>(take(kMaxParts * 4));
+  b.squares_count = (j.rows + 127) / 128 * 4 * (b.ld_x / 32);
+  for (int k = 0; k < 2; ++k) b.squares[k] = reinterpret_cast<float*>(take(b.squares_count * 4));
   if (out) *out = b;
   return at;
 }
@@ -1418,6 +1469,9 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
         g.symmetric = kind != kUpdate;
         g.m = g.n = g.k = side;
         g.p_mn = g.q_mn = g.in_q = 0;
+        g.squares = s > 0 ? b.squares[now] : nullptr;
+        g.new_squares = b.squares[next];
+        g.squares_count = static_cast<int32_t>(b.squares_count);
         if (kind == kGram) {
           use(g.p, q.x[now]);
           use(g.q, q.x[now]);
@@ -1447,9 +1501,9 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
       }
       p.kind = kind;
       p.result = kind != kUpdate || !last ? kParts : apply ? kApply : kOut;
-      p.alpha = kind == kGram ? kScaleA / (kScaleX * kScaleX) : kind == kPoly ? plan.coef[3 * s + 2] / kScaleA
-                                                                               : 1.0f / kScaleA;
-      p.beta = kind == kPoly ? plan.coef[3 * s + 1] : plan.coef[3 * s];
+      p.a = plan.coef[3 * s];
+      p.b = plan.coef[3 * s + 1];
+      p.c = plan.coef[3 * s + 2];
       // pairs of blocks on 256 x 256 tiles, or single ones on 128 x 128 (the same sums in the
       // same order), whichever is estimated faster; or two blocks a tile (see splits())
       const bool pairs = pair_time(large_tiles, steps, dev.sms) < block_time(small_tiles, steps, dev.sms);
@@ -1494,7 +1548,7 @@ int ns_plan(const fsdp_newton_schulz_t* h, NsPlan* plan) {
     for (double s : at) {
       if (!(s >= 0.0 && s <= top * top)) continue;
       next = std::max(next, std::fabs(std::sqrt(s) * (a + b * s + c * s * s)));
-      if (std::fabs(b * s + c * s * s) > 60.0) return FSDP_EINVAL;
+      if (std::fabs(b * s + c * s * s) > 30.0) return FSDP_EINVAL;
     }
     if (!(next <= 7.0)) return FSDP_EINVAL;
     top = next;

@@ -596,8 +596,8 @@ int fsdp_rmsnorm_backward_workspace(int64_t rows, int64_t cols, int64_t *bytes_o
  * (for a matrix with more rows than columns, of its transpose). The result has
  * G's singular vectors and singular values near 1; a zero matrix stays zero.
  * terms: how the products take their operands. 1: rounded to 11 bits (fp16,
- * scaled by powers of two; the error is 0.1 to 0.3 % of the result's
- * norm); 3: as two such parts each, three products (about 1e-5); 0: 3 where the
+ * scaled by powers of two; the error is below 0.3 % of the result's norm,
+ * typically 0.03 to 0.1 %); 3: as two such parts each, three products (about 1e-5); 0: 3 where the
  * short side is below 256 and 1 otherwise. Between steps X is held as two fp16
  * parts, 22 bits; accumulation is fp32. */
 typedef struct {
@@ -621,7 +621,7 @@ typedef struct {
 /* Orthogonalises n matrices (host array), together in each launch. Empty
  * matrices are skipped. newton_schulz null: 5 steps, terms 0, eps 1e-7.
  * EINVAL: also coefficients whose iterates leave [-7, 7] or whose b s + c s^2
- * leaves [-60, 60] for some singular value in [0, 1] (the fp16 ranges); a side beyond
+ * leaves [-30, 30] for some singular value in [0, 1] (the fp16 ranges); a side beyond
  * 2^30. EALIAS: an out that overlaps another out or a source but its own. */
 int fsdp_newton_schulz(const fsdp_matrix_t *matrices, int32_t n, const fsdp_newton_schulz_t *newton_schulz,
                        void *workspace, int64_t workspace_bytes, fsdp_stream_t stream);
