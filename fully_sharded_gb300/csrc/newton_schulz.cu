@@ -353,8 +353,12 @@ struct Tiles {
     const GemmMat& g = p.mat[mat];
     const int l = t - first;
     if (!g.symmetric) {
-      *i = l / g.col_tiles;
-      *j = l - *i * g.col_tiles;
+      // along the short side first: the tiles at work share the long operand's rows or
+      // columns and the whole of the short one, which stays in L2
+      const int short_tiles = g.in_q ? g.tiles / g.col_tiles : g.col_tiles;
+      const int a = l / short_tiles, b = l - a * short_tiles;
+      *i = g.in_q ? b : a;
+      *j = g.in_q ? a : b;
       return g;
     }
     while (l - base >= T::below(row, g.col_tiles)) base += T::below(row++, g.col_tiles);
