@@ -112,7 +112,7 @@ extern "C" int fsdp_muon_workspace(const fsdp_muon_unit_t* unit, const fsdp_muon
   if (int rc = make(unit, muon, false, &m)) return rc;
   *bytes_out = m.bytes();
   return FSDP_OK;
-} catch (const std::bad_alloc&) {
+} catch (...) {
   return FSDP_ECUDA;
 }
 
@@ -154,6 +154,6 @@ extern "C" int fsdp_muon_step(const fsdp_muon_unit_t* unit, const fsdp_muon_t* h
   p.inv_w = m.scalars.inv_w;
   p.nesterov = h->nesterov != 0;
   return ns_run(m.jobs, m.plan, &p, &m.apply, rest, st);
-} catch (const std::bad_alloc&) {
+} catch (...) {
   return FSDP_ECUDA;
 }

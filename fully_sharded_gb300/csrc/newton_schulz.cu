@@ -1644,7 +1644,7 @@ extern "C" int fsdp_newton_schulz_workspace(const fsdp_matrix_t* matrices, int32
   if (int rc = make_jobs(matrices, n, false, &jobs)) return rc;
   *bytes_out = ns_workspace_bytes(jobs, plan);
   return FSDP_OK;
-} catch (const std::bad_alloc&) {
+} catch (...) {
   return FSDP_ECUDA;
 }
 
@@ -1663,6 +1663,6 @@ extern "C" int fsdp_newton_schulz(const fsdp_matrix_t* matrices, int32_t n, cons
         ws.overlaps({j.out, j.rows, j.cols, j.out_stride, 2}))
       return FSDP_EALIAS;
   return ns_run(jobs, plan, nullptr, nullptr, workspace, reinterpret_cast<cudaStream_t>(stream));
-} catch (const std::bad_alloc&) {
+} catch (...) {
   return FSDP_ECUDA;
 }
