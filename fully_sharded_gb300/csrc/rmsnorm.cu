@@ -208,6 +208,16 @@ __device__ __forceinline__ float warp_reduce(float v, int lanes = 32) {
   return v;
 }
 
+// Over aligned groups of 4, 8, 16 or 32 lanes.
+__device__ __forceinline__ float group_max(float v, int lanes) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+  if (lanes > 4) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  if (lanes > 8) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  if (lanes > 16) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+  return v;
+}
+
 // Over the row's threads; every one gets the result. `shared`: 32 floats, free to
 // be written (the caller's previous reduction used another one).
 template <bool kMax>
@@ -237,13 +247,13 @@ __device__ __forceinline__ float scale_of(float top) { return fmaxf(top * (1.0f 
 // more rows in flight while others wait at their reductions. kWide: rows that need
 // more threads at kMaxV groups each.
 constexpr int forward_threads(int v, bool wide) { return v < 3 || wide ? 512 : 384; }
-constexpr int forward_blocks(int v, bool wide, bool residual) { return v == 2 || wide ? 1 : v > 2 && !residual ? 3 : 2; }
+constexpr int forward_blocks(int v, bool wide) { return v == 2 || wide ? 1 : 2; }
 constexpr int backward_threads(bool wide) { return wide ? 512 : 256; }
 constexpr int backward_blocks(int v, bool wide) { return wide ? 1 : v == 1 ? 4 : v == 2 ? 3 : 2; }
 
 // kQuant 0: y of the inputs' type; 1: 8 bits, one scale per row; 2: 8 bits, scales per group.
 template <typename T, bool kResidual, int kQuant, Map kMap, int kV, bool kWide = false>
-__global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV, kWide, kResidual))
+__global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV, kWide))
     norm_rows(const __grid_constant__ NormParams p) {
   __shared__ float shared[3][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -252,10 +262,15 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV,
   const RowThreads r{static_cast<int>(threadIdx.x) % p.threads, p.threads};
   const int per_block = blockDim.x / p.threads;
   int turn = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / p.threads; row < p.a.rows;
-       row += static_cast<int64_t>(gridDim.x) * per_block) {
-    RowLoad<kMap, kV, T> x, res;
-    x.load(static_cast<const T*>(p.x) + row * p.a.x_stride, r, cols);
+  const int64_t row_step = static_cast<int64_t>(gridDim.x) * per_block;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / p.threads;
+  // kAhead: the next row is on its way while this one is worked on
+  constexpr bool kAhead = !kResidual && kMap == kVector && kV > 1;
+  RowLoad<kMap, kV, T> x, res;
+  if constexpr (kAhead)
+    x.load(static_cast<const T*>(p.x) + row * p.a.x_stride, r, cols, row < p.a.rows);
+  for (; row < p.a.rows; row += row_step) {
+    if constexpr (!kAhead) x.load(static_cast<const T*>(p.x) + row * p.a.x_stride, r, cols);
     if constexpr (kResidual) res.load(static_cast<const T*>(p.residual) + row * p.a.residual_stride, r, cols);
     float v[kV][8], sum = 0.0f;
     T* h = static_cast<T*>(p.h) + row * p.a.h_stride;
@@ -270,6 +285,8 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV,
         store_group<kMap>(h, r, k, cols, v[k]);
       }
     }
+    if constexpr (kAhead)
+      x.load(static_cast<const T*>(p.x) + (row + row_step) * p.a.x_stride, r, cols, row + row_step < p.a.rows);
 #pragma unroll
     for (int k = 0; k < kV; ++k)
 #pragma unroll
@@ -284,7 +301,8 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV,
     if (p.rstd && r.t == 0) p.rstd[row] = rstd;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      if constexpr (kV > 1) gain_group<kMap>(p.gain, p.a.gain_dtype, p.gain_vectors, r, k, cols, g[k]);
+      if constexpr (kV > 1)
+        gain_group<kMap>(p.gain, p.a.gain_dtype, p.gain_vectors, r, k, cols, g[k]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[k][e] *= kQuant == 0 ? rstd * g[k][e] : g[k][e];  // 8 bits: rstd goes into the scale
     }
@@ -309,7 +327,7 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV,
       const int groups = kQuant == 1 ? 1 : (cols + p.a.group - 1) >> p.group_bits;
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
-        if constexpr (kQuant == 2) all = warp_reduce<true>(top[k], p.a.group / 8);
+        if constexpr (kQuant == 2) all = group_max(top[k], p.a.group / 8);
         const float scale = scale_of(all * rstd);
         const int j = place<kMap>(r, k, 0);
         if (kQuant == 1 ? (k == 0 && r.t == 0) : (j < cols && (j & (p.a.group - 1)) == 0))
@@ -741,7 +759,11 @@ int forward(NormParams p, bool aligned, cudaStream_t st) {
   const Spread s = forward_spread(p.a.rows, p.a.cols);
   p.threads = s.threads;
   const bool quant = p.a.y_dtype == FSDP_DTYPE_E4M3;
-  const int grid = static_cast<int>(std::min<int64_t>((p.a.rows + s.per_block - 1) / s.per_block, 1 << 20));
+  // as many blocks as run at once where a block works ahead, else one for each row
+  int64_t most = 1 << 20;
+  if (s.v > 1 && aligned && !p.residual)
+    most = static_cast<int64_t>(sm_count()) * std::max(1, 768 / (s.threads * s.per_block));
+  const int grid = static_cast<int>(std::min<int64_t>((p.a.rows + s.per_block - 1) / s.per_block, most));
   if (s.v == 0)
     return launch_rows(!quant ? norm_long_rows<T, 0> : p.a.group == 0 ? norm_long_rows<T, 1> : norm_long_rows<T, 2>, grid,
                        kLongThreads, 0, st, p);
