@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 namespace fsdp {
 namespace {
@@ -35,10 +36,18 @@ constexpr int kLongThreads = 256;     // rows beyond the registers
 //     multiple of 8 and every row of every array starts on a 16-byte boundary. (A group
 //     is whole or absent: one predicate and no branch around a load, so that all of
 //     a thread's loads are in flight together.)
-//   kGroups: the same elements one by one (other rows, 8-bit groups).
+//   kShifted: the same groups moved back by the row's own distance from a 16-byte
+//     boundary (`phase` elements, the same for all arrays), so that rows of any
+//     length are read and written as aligned vectors too; the first and the last group
+//     of a row are partly outside, where a load's surplus is dropped (it lies in
+//     a 16-byte piece that holds an element of the row) and stores go one by one.
+//     (43633 x 769 bf16 with the residual, 268 MB: 224 us strided, see below.)
+//   kGroups: 8 consecutive elements one by one (other rows, 8-bit groups).
 //   kStrided: element by element across the row's threads, so that a warp's
 //     accesses stay contiguous (other rows, no groups).
-enum Map { kVector, kGroups, kStrided };
+enum RowMap { kVector, kShifted, kGroups, kStrided };
+template <RowMap kMap>
+constexpr bool kByVectors = kMap == kVector || kMap == kShifted;
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -59,9 +68,10 @@ __device__ __forceinline__ void unpack(uint32_t two, float* v) {
 template <>
 struct Raw8<float> {
   float4 a, b;
-  __device__ __forceinline__ void load(const float* p, bool there) {
-    a = there ? __ldcs(reinterpret_cast<const float4*>(p)) : make_float4(0, 0, 0, 0);
-    b = there ? __ldcs(reinterpret_cast<const float4*>(p) + 1) : make_float4(0, 0, 0, 0);
+  // first, second: whether the 4 elements of each half are wanted
+  __device__ __forceinline__ void load(const float* p, bool first, bool second) {
+    a = first ? __ldcs(reinterpret_cast<const float4*>(p)) : make_float4(0, 0, 0, 0);
+    b = second ? __ldcs(reinterpret_cast<const float4*>(p) + 1) : make_float4(0, 0, 0, 0);
   }
   __device__ __forceinline__ void take(const float* p, bool there) {
     a = there ? *reinterpret_cast<const float4*>(p) : make_float4(0, 0, 0, 0);
@@ -74,8 +84,8 @@ struct Raw8<float> {
 template <>
 struct Raw8<__nv_bfloat16> {
   uint4 a;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool there) {
-    a = there ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool first, bool second) {
+    a = first || second ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
   }
   __device__ __forceinline__ void take(const __nv_bfloat16* p, bool there) {
     a = there ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
@@ -107,33 +117,37 @@ __device__ __forceinline__ float load_gain(const void* gain, int32_t dtype, int6
   return dtype == FSDP_DTYPE_F32 ? load1(static_cast<const float*>(gain) + j)
                                  : load1(static_cast<const __nv_bfloat16*>(gain) + j);
 }
-// The row's threads: `t` of `n` (n = 32: a warp of its own row; else the block).
+// The row's threads: `t` of `n` (n up to 32: part of a warp or a warp; else the block).
 struct RowThreads {
   int t, n;
+  int phase;  // kShifted: elements from the last 16-byte boundary to the row's first
 };
 
 // First element of group v, or element (v, e) in the strided map.
-template <Map kMap>
+template <RowMap kMap>
 __device__ __forceinline__ int place(const RowThreads& r, int v, int e) {
-  return kMap == kStrided ? (v * 8 + e) * r.n + r.t : (v * r.n + r.t) * 8 + e;
+  const int j = kMap == kStrided ? (v * 8 + e) * r.n + r.t : (v * r.n + r.t) * 8 + e;
+  return kMap == kShifted ? j - r.phase : j;
 }
 
 // A thread's kV groups of a row, as loaded.
-template <Map kMap, int kV, typename T>
+template <RowMap kMap, int kV, typename T>
 struct RowLoad {
-  Raw8<T> raw[kMap == kVector ? kV : 1];
-  float v[kMap == kVector ? 1 : kV][8];
+  Raw8<T> raw[kByVectors<kMap> ? kV : 1];
+  float v[kByVectors<kMap> ? 1 : kV][8];
   __device__ __forceinline__ void load(const T* p, const RowThreads& r, int cols, bool there = true) {
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
+      const int j = place<kMap>(r, k, 0);
       if constexpr (kMap == kVector) {
-        const int j = place<kMap>(r, k, 0);
-        raw[k].load(p + j, there && j < cols);
+        raw[k].load(p + j, there && j < cols, there && j < cols);
+      } else if constexpr (kMap == kShifted) {
+        raw[k].load(p + j, there && j + 4 > 0 && j < cols, there && j + 8 > 0 && j + 4 < cols);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int j = place<kMap>(r, k, e);
-          v[k][e] = there && j < cols ? load1(p + j) : 0.0f;
+          const int i = place<kMap>(r, k, e);
+          v[k][e] = there && i < cols ? load1(p + i) : 0.0f;
         }
       }
     }
@@ -145,9 +159,15 @@ struct RowLoad {
       raw[k].take(p + j, there && j < cols);
     }
   }
-  __device__ __forceinline__ void to(int k, float* out) const {
-    if constexpr (kMap == kVector) {
+  // Group k as floats, zeros outside the row.
+  __device__ __forceinline__ void to(int k, const RowThreads& r, int cols, float* out) const {
+    if constexpr (kByVectors<kMap>) {
       raw[k].to(out);
+      const int j = place<kMap>(r, k, 0);
+      if (kMap == kShifted && (j < 0 || j + 8 > cols)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[e] = j + e >= 0 && j + e < cols ? out[e] : 0.0f;
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) out[e] = v[k][e];
@@ -155,23 +175,55 @@ struct RowLoad {
   }
 };
 
-template <Map kMap, typename T>
+template <RowMap kMap, typename T>
 __device__ __forceinline__ void store_group(T* p, const RowThreads& r, int v, int cols, const float* in) {
+  const int j = place<kMap>(r, v, 0);
   if constexpr (kMap == kVector) {
-    const int j = place<kMap>(r, v, 0);
     if (j < cols) store_vec(p + j, in);
-    return;
+  } else if (kMap == kShifted && j >= 0 && j + 8 <= cols) {
+    store_vec(p + j, in);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int i = place<kMap>(r, v, e);
+      if (i >= 0 && i < cols) store1(p + i, in[e]);
+    }
   }
+}
+
+// The same one by one, to a place of any alignment.
+template <RowMap kMap>
+__device__ __forceinline__ void store_each(float* p, const RowThreads& r, int v, int cols, const float* in) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int j = place<kMap>(r, v, e);
-    if (j < cols) store1(p + j, in[e]);
+    const int i = place<kMap>(r, v, e);
+    if (i >= 0 && i < cols) p[i] = in[e];
   }
+}
+
+// kWords 4-byte words from any 2-byte boundary, out of aligned vectors that each hold some of them.
+template <int kWords>
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&out)[kWords]) {
+  constexpr int kVecs = kWords / 4 + 1;
+  const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p) - s);
+  uint32_t w[4 * kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const uint4 t = 16 * i < static_cast<int>(s) + 4 * kWords ? q[i] : make_uint4(0, 0, 0, 0);
+    w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
+  }
+#pragma unroll
+  for (int i = 0; i + 2 < 4 * kVecs; ++i) w[i] = s & 8u ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i + 1 < 4 * kVecs; ++i) w[i] = s & 4u ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], (s & 2u) * 8u);
 }
 
 // The gains of group v (zeros past the end); `vectors`: the gain starts on a
 // 16-byte boundary and the map is kVector.
-template <Map kMap>
+template <RowMap kMap>
 __device__ __forceinline__ void gain_group(const void* gain, int32_t dtype, bool vectors, const RowThreads& r, int v,
                                            int cols, float* out) {
   const int j = place<kMap>(r, v, 0);
@@ -192,10 +244,24 @@ __device__ __forceinline__ void gain_group(const void* gain, int32_t dtype, bool
     }
     return;
   }
+  if (kMap == kShifted && j >= 0 && j + 8 <= cols) {
+    if (dtype == FSDP_DTYPE_F32) {
+      uint32_t w[8];
+      load_words(static_cast<const float*>(gain) + j, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[e] = __uint_as_float(w[e]);
+    } else {
+      uint32_t w[4];
+      load_words(static_cast<const __nv_bfloat16*>(gain) + j, w);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) unpack(w[e], out + 2 * e);
+    }
+    return;
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const int i = place<kMap>(r, v, e);
-    out[e] = i < cols ? load_gain(gain, dtype, i) : 0.0f;
+    out[e] = i >= 0 && i < cols ? load_gain(gain, dtype, i) : 0.0f;
   }
 }
 
@@ -222,8 +288,8 @@ __device__ __forceinline__ float group_max(float v, int lanes) {
 // be written (the caller's previous reduction used another one).
 template <bool kMax>
 __device__ __forceinline__ float row_reduce(float v, const RowThreads& r, float* shared) {
-  v = warp_reduce<kMax>(v);
-  if (r.n == 32) return v;
+  v = warp_reduce<kMax>(v, min(r.n, 32));
+  if (r.n <= 32) return v;
   if (r.t % 32 == 0) shared[r.t / 32] = v;
   __syncthreads();
   const int warps = r.n / 32;
@@ -252,41 +318,46 @@ constexpr int backward_threads(bool wide) { return wide ? 512 : 256; }
 constexpr int backward_blocks(int v, bool wide) { return wide ? 1 : v == 1 ? 4 : v == 2 ? 3 : 2; }
 
 // kQuant 0: y of the inputs' type; 1: 8 bits, one scale per row; 2: 8 bits, scales per group.
-template <typename T, bool kResidual, int kQuant, Map kMap, int kV, bool kWide = false>
+template <typename T, bool kResidual, int kQuant, RowMap kMap, int kV, bool kWide = false>
 __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV, kWide))
     norm_rows(const __grid_constant__ NormParams p) {
   __shared__ float shared[3][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int cols = static_cast<int>(p.a.cols);
-  const RowThreads r{static_cast<int>(threadIdx.x) % p.threads, p.threads};
+  const int all = static_cast<int>(p.a.cols);
+  RowThreads r{static_cast<int>(threadIdx.x) % p.threads, p.threads, 0};
   const int per_block = blockDim.x / p.threads;
   int turn = 0;
   const int64_t row_step = static_cast<int64_t>(gridDim.x) * per_block;
+  // a warp of several short rows stays together while its first one is there
+  const int lead = p.threads < 32 ? static_cast<int>(threadIdx.x) % 32 / p.threads : 0;
   int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / p.threads;
   // kAhead: the next row is on its way while this one is worked on
   constexpr bool kAhead = !kResidual && kMap == kVector && kV > 1;
   RowLoad<kMap, kV, T> x, res;
   if constexpr (kAhead)
-    x.load(static_cast<const T*>(p.x) + row * p.a.x_stride, r, cols, row < p.a.rows);
-  for (; row < p.a.rows; row += row_step) {
-    if constexpr (!kAhead) x.load(static_cast<const T*>(p.x) + row * p.a.x_stride, r, cols);
+    x.load(static_cast<const T*>(p.x) + row * p.a.x_stride, r, all, row < p.a.rows);
+  for (; row - lead < p.a.rows; row += row_step) {
+    const int cols = row < p.a.rows ? all : 0;
+    const T* x_row = static_cast<const T*>(p.x) + row * p.a.x_stride;
+    if constexpr (kMap == kShifted) r.phase = static_cast<int>((reinterpret_cast<uintptr_t>(x_row) & 15u) / sizeof(T));
+    if constexpr (!kAhead) x.load(x_row, r, cols);
     if constexpr (kResidual) res.load(static_cast<const T*>(p.residual) + row * p.a.residual_stride, r, cols);
     float v[kV][8], sum = 0.0f;
     T* h = static_cast<T*>(p.h) + row * p.a.h_stride;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
-      x.to(k, v[k]);
+      x.to(k, r, cols, v[k]);
       if constexpr (kResidual) {
         float w[8];
-        res.to(k, w);
+        res.to(k, r, cols, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[k][e] += w[e];
         store_group<kMap>(h, r, k, cols, v[k]);
       }
     }
     if constexpr (kAhead)
-      x.load(static_cast<const T*>(p.x) + (row + row_step) * p.a.x_stride, r, cols, row + row_step < p.a.rows);
+      x.load(static_cast<const T*>(p.x) + (row + row_step) * p.a.x_stride, r, all, row + row_step < p.a.rows);
 #pragma unroll
     for (int k = 0; k < kV; ++k)
 #pragma unroll
@@ -297,8 +368,8 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV,
     // reduction ends every read of the one before the last
     float* room = shared[turn];
     turn ^= 1;
-    const float rstd = rsqrtf(row_reduce<false>(sum, r, room) / static_cast<float>(cols) + static_cast<float>(p.a.eps));
-    if (p.rstd && r.t == 0) p.rstd[row] = rstd;
+    const float rstd = rsqrtf(row_reduce<false>(sum, r, room) / static_cast<float>(all) + static_cast<float>(p.a.eps));
+    if (p.rstd && r.t == 0 && cols > 0) p.rstd[row] = rstd;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
       if constexpr (kV > 1)
@@ -312,25 +383,25 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV,
       for (int k = 0; k < kV; ++k) store_group<kMap>(y, r, k, cols, v[k]);
     } else {
       uint8_t* y = static_cast<uint8_t*>(p.y) + row * p.a.y_stride;
-      float top[kV], all = 0.0f;
+      float top[kV], most = 0.0f;
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
         top[k] = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) top[k] = fmaxf(top[k], fabsf(v[k][e]));
-        all = fmaxf(all, top[k]);
+        most = fmaxf(most, top[k]);
       }
       if constexpr (kQuant == 1) {
-        all = row_reduce<true>(all, r, shared[2]);
+        most = row_reduce<true>(most, r, shared[2]);
         // the next row's first reduction has a barrier before shared[2] is written again
       }
-      const int groups = kQuant == 1 ? 1 : (cols + p.a.group - 1) >> p.group_bits;
+      const int groups = kQuant == 1 ? 1 : (all + p.a.group - 1) >> p.group_bits;
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
-        if constexpr (kQuant == 2) all = group_max(top[k], p.a.group / 8);
-        const float scale = scale_of(all * rstd);
+        if constexpr (kQuant == 2) most = group_max(top[k], p.a.group / 8);
+        const float scale = scale_of(most * rstd);
         const int j = place<kMap>(r, k, 0);
-        if (kQuant == 1 ? (k == 0 && r.t == 0) : (j < cols && (j & (p.a.group - 1)) == 0))
+        if (kQuant == 1 ? (k == 0 && r.t == 0 && cols > 0) : (j < cols && (j & (p.a.group - 1)) == 0))
           p.scales[row * groups + (kQuant == 1 ? 0 : j >> p.group_bits)] = scale;
         float inverse = __frcp_rn(scale), q[8];
         if (rstd * inverse <= 0x1p127f) {
@@ -350,7 +421,7 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV,
 template <bool kMax>
 __device__ __forceinline__ float long_reduce(float v, float* shared) {
   __syncthreads();
-  return row_reduce<kMax>(v, RowThreads{static_cast<int>(threadIdx.x), kLongThreads}, shared);
+  return row_reduce<kMax>(v, RowThreads{static_cast<int>(threadIdx.x), kLongThreads, 0}, shared);
 }
 
 // Rows beyond the registers: one block per row, the row read twice (thrice with 8-bit groups).
@@ -430,32 +501,38 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 // A block takes every gridDim-th row (or, with a warp per row, set of rows); a
 // thread keeps its columns' share of dgain in registers over all its rows. The
 // warps' shares are added in order, then written as the block's row of `partial`.
-template <typename T, Map kMap, int kV, bool kWide = false>
+template <typename T, RowMap kMap, int kV, bool kWide = false>
 __global__ void __launch_bounds__(backward_threads(kWide), backward_blocks(kV, kWide))
     norm_rows_backward(const __grid_constant__ NormBwdParams p) {
   __shared__ float shared[2][32];
   extern __shared__ float total[];  // [cols], with a warp per row
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int cols = static_cast<int>(p.a.cols);
-  const RowThreads r{static_cast<int>(threadIdx.x) % p.threads, p.threads};
+  const int all = static_cast<int>(p.a.cols);
+  RowThreads r{static_cast<int>(threadIdx.x) % p.threads, p.threads, 0};
   const int per_block = blockDim.x / p.threads;
   float acc[kV][8] = {};
   int turn = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / p.threads; row < p.a.rows;
+  const int lead = p.threads < 32 ? static_cast<int>(threadIdx.x) % 32 / p.threads : 0;  // as in norm_rows
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + threadIdx.x / p.threads; row - lead < p.a.rows;
        row += static_cast<int64_t>(gridDim.x) * per_block) {
+    const int cols = row < p.a.rows ? all : 0;
+    const T* dy_row = static_cast<const T*>(p.dy) + row * p.a.dy_stride;
+    // kShifted: the rows of a thread are a multiple of 8 apart and have one phase
+    if constexpr (kMap == kShifted)
+      if (cols > 0) r.phase = static_cast<int>((reinterpret_cast<uintptr_t>(dy_row) & 15u) / sizeof(T));
     RowLoad<kMap, kV, T> dy, h, dh;
-    dy.load(static_cast<const T*>(p.dy) + row * p.a.dy_stride, r, cols);
+    dy.load(dy_row, r, cols);
     h.load(static_cast<const T*>(p.h) + row * p.a.h_stride, r, cols);
     const T* dh_row = static_cast<const T*>(p.dh) + row * p.a.dh_stride;
-    if constexpr (kMap == kVector) dh.load(dh_row, r, cols, p.dh != nullptr);  // early: it costs 4 registers a group
-    const float rstd = p.rstd[row];
+    if constexpr (kByVectors<kMap>) dh.load(dh_row, r, cols, p.dh != nullptr);  // early: it costs 4 registers a group
+    const float rstd = cols > 0 ? p.rstd[row] : 0.0f;
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
       float u[8], n[8], g[8];
-      dy.to(k, u);
-      h.to(k, n);
+      dy.to(k, r, cols, u);
+      h.to(k, r, cols, n);
       gain_group<kMap>(p.gain, p.a.gain_dtype, p.gain_vectors, r, k, cols, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -464,23 +541,23 @@ __global__ void __launch_bounds__(backward_threads(kWide), backward_blocks(kV, k
         sum += t * g[e];
       }
     }
-    const float mean = row_reduce<false>(sum, r, shared[turn]) / static_cast<float>(cols);
+    const float mean = row_reduce<false>(sum, r, shared[turn]) / static_cast<float>(all);
     turn ^= 1;
-    if constexpr (kMap != kVector) dh.load(dh_row, r, cols, p.dh != nullptr);
+    if constexpr (!kByVectors<kMap>) dh.load(dh_row, r, cols, p.dh != nullptr);
     T* dx = static_cast<T*>(p.dx) + row * p.a.dx_stride;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {  // formed again from the row as loaded: fewer registers over the reduction
       float u[8], n[8], g[8], d[8];
-      dy.to(k, u);
-      h.to(k, n);
-      dh.to(k, d);
+      dy.to(k, r, cols, u);
+      h.to(k, r, cols, n);
+      dh.to(k, r, cols, d);
       gain_group<kMap>(p.gain, p.a.gain_dtype, p.gain_vectors, r, k, cols, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) d[e] += rstd * (u[e] * g[e] - n[e] * rstd * mean);
       store_group<kMap>(dx, r, k, cols, d);
     }
   }
-  float* mine = p.partial + static_cast<int64_t>(blockIdx.x) * cols;
+  float* mine = p.partial + static_cast<int64_t>(blockIdx.x) * all;
   if (per_block > 1) {
     const int slot = threadIdx.x / p.threads;
     for (int w = 0; w < per_block; ++w) {
@@ -490,7 +567,7 @@ __global__ void __launch_bounds__(backward_threads(kWide), backward_blocks(kV, k
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int j = place<kMap>(r, k, e);
-            if (j >= cols) continue;
+            if (j < 0 || j >= all) continue;
             if (w + 1 < per_block)
               total[j] = (w > 0 ? total[j] : 0.0f) + acc[k][e];
             else
@@ -501,7 +578,7 @@ __global__ void __launch_bounds__(backward_threads(kWide), backward_blocks(kV, k
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < kV; ++k) store_group<kMap == kVector ? kGroups : kMap>(mine, r, k, cols, acc[k]);
+    for (int k = 0; k < kV; ++k) store_each<kMap>(mine, r, k, all, acc[k]);
   }
 }
 
@@ -518,7 +595,7 @@ __global__ void __launch_bounds__(backward_threads(kWide), backward_blocks(kV, k
   __shared__ int stop;
   extern __shared__ __align__(128) unsigned char staged[];  // stages x {dy, h, dh} rows
   const int cols = static_cast<int>(p.a.cols);
-  const RowThreads r{static_cast<int>(threadIdx.x), p.threads};
+  const RowThreads r{static_cast<int>(threadIdx.x), p.threads, 0};
   const uint32_t row_bytes = static_cast<uint32_t>(cols) * sizeof(T), arrays = p.dh ? 3 : 2;
   const tc::Guard guard{&stop, p.status, kWaitLimitNs};
   if (threadIdx.x == 0) {
@@ -557,8 +634,8 @@ __global__ void __launch_bounds__(backward_threads(kWide), backward_blocks(kV, k
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
       float u[8], n[8], g[8];
-      dy.to(k, u);
-      h.to(k, n);
+      dy.to(k, r, cols, u);
+      h.to(k, r, cols, n);
       gain_group<kVector>(p.gain, p.a.gain_dtype, p.gain_vectors, r, k, cols, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -580,9 +657,9 @@ __global__ void __launch_bounds__(backward_threads(kWide), backward_blocks(kV, k
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
       float u[8], n[8], g[8], d[8];
-      dy.to(k, u);
-      h.to(k, n);
-      dh.to(k, d);
+      dy.to(k, r, cols, u);
+      h.to(k, r, cols, n);
+      dh.to(k, r, cols, d);
       gain_group<kVector>(p.gain, p.a.gain_dtype, p.gain_vectors, r, k, cols, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) d[e] += rstd * (u[e] * g[e] - n[e] * rstd * mean);
@@ -600,7 +677,7 @@ __global__ void __launch_bounds__(backward_threads(kWide), backward_blocks(kV, k
   }
   float* mine = p.partial + static_cast<int64_t>(blockIdx.x) * cols;
 #pragma unroll
-  for (int k = 0; k < kV; ++k) store_group<kGroups>(mine, r, k, cols, acc[k]);
+  for (int k = 0; k < kV; ++k) store_each<kVector>(mine, r, k, cols, acc[k]);
 }
 
 // Rows beyond the registers: the row read twice, dgain's share kept in `partial`.
@@ -686,25 +763,34 @@ int warps_for(int64_t cols, int v) { return static_cast<int>((cols + 256 * v - 1
 
 constexpr int kFewRows = 512;  // about as many rows as blocks run at once
 
+// `cols`: of the row, with up to 7 more where its groups are shifted. Short rows share a
+// warp: 8 or 16 lanes each, so that few lanes are idle.
+int threads_for(int64_t rows, int64_t cols, int v) {
+  if (rows >= kFewRows && v == 1 && cols <= 128) return cols <= 64 ? 8 : 16;
+  return 32 * warps_for(cols, v);
+}
+
 Spread forward_spread(int64_t rows, int64_t cols) {
   Spread s;
   if (cols > kMaxThreads * 8 * kMaxV) return s;
   s.v = rows < kFewRows ? 1 : static_cast<int>(std::min<int64_t>(kMaxV, (cols + 1023) / 1024));
   if (rows >= kFewRows && cols <= 1024) s.v = warps_for(cols, 1);  // a warp per row
   while (s.v < kMaxV && 32 * warps_for(cols, s.v) > forward_threads(s.v, false)) ++s.v;
-  s.threads = 32 * warps_for(cols, s.v);
-  if (s.threads == 32) s.per_block = 4;
+  s.threads = threads_for(rows, cols, s.v);
+  if (s.threads <= 32) s.per_block = 128 / s.threads;
   return s;
 }
 
+// A warp per row up to 512 columns only: beyond that the staged rows are faster
+// (43690 x 768 bf16: 63 us with a warp per row).
 Spread backward_spread(int64_t rows, int64_t cols) {
   Spread s;
   if (cols > kMaxThreads * 8 * kMaxV) return s;
   s.v = rows < kFewRows ? 1 : static_cast<int>(std::min<int64_t>(kMaxV, (cols + 2047) / 2048));
-  if (rows >= kFewRows && cols <= 1024) s.v = warps_for(cols, 1);
+  if (rows >= kFewRows && cols <= 512) s.v = warps_for(cols, 1);
   while (s.v < kMaxV && 32 * warps_for(cols, s.v) > backward_threads(false)) ++s.v;
-  s.threads = 32 * warps_for(cols, s.v);
-  if (s.threads == 32) s.per_block = 8;
+  s.threads = threads_for(rows, cols, s.v);
+  if (s.threads <= 32) s.per_block = 256 / s.threads;
   return s;
 }
 
@@ -715,20 +801,23 @@ int sm_count() {
   return sms;
 }
 
-// Blocks of the backward pass (rows of `partial`): as many as run at once.
-int backward_parts(int64_t rows, int64_t cols) {
-  const Spread s = backward_spread(rows, cols);
+// Blocks of the backward pass (rows of `partial`): as many as run at once, a multiple of 8
+// where a block has several rows.
+int backward_parts(int64_t rows, const Spread& s) {
   int per_sm = 4;
   if (s.v > 0) {
     const int threads = s.threads * s.per_block;
     const bool wide = threads > backward_threads(false);
     per_sm = std::max(1, backward_blocks(s.v, wide) * backward_threads(wide) / threads);
   }
-  return static_cast<int>(
-      std::min<int64_t>((std::max<int64_t>(rows, 1) + s.per_block - 1) / s.per_block, static_cast<int64_t>(per_sm) * sm_count()));
+  const int64_t most = std::max<int64_t>(8, static_cast<int64_t>(per_sm) * sm_count() / 8 * 8);
+  return static_cast<int>(std::min<int64_t>((std::max<int64_t>(rows, 1) + s.per_block - 1) / s.per_block, most));
 }
 
-template <typename T, bool kResidual, int kQuant, Map kMap>
+// The columns that a row's groups have to cover.
+int64_t covered(int64_t cols, RowMap map) { return map == kShifted ? cols + 7 : cols; }
+
+template <typename T, bool kResidual, int kQuant, RowMap kMap>
 int run_forward(const NormParams& p, const Spread& s, int grid, cudaStream_t st) {
   const int threads = s.threads * s.per_block;
   switch (s.v) {
@@ -743,34 +832,36 @@ int run_forward(const NormParams& p, const Spread& s, int grid, cudaStream_t st)
 }
 
 template <typename T, bool kResidual>
-int run_forward_as(const NormParams& p, const Spread& s, bool aligned, int grid, cudaStream_t st) {
-  if (p.a.y_dtype != FSDP_DTYPE_E4M3)
-    return aligned ? run_forward<T, kResidual, 0, kVector>(p, s, grid, st)
-                   : run_forward<T, kResidual, 0, kStrided>(p, s, grid, st);
-  if (p.a.group == 0)
-    return aligned ? run_forward<T, kResidual, 1, kVector>(p, s, grid, st)
-                   : run_forward<T, kResidual, 1, kStrided>(p, s, grid, st);
-  return aligned ? run_forward<T, kResidual, 2, kVector>(p, s, grid, st)
-                 : run_forward<T, kResidual, 2, kGroups>(p, s, grid, st);
+int run_forward_as(const NormParams& p, const Spread& s, RowMap map, int grid, cudaStream_t st) {
+  const int quant = p.a.y_dtype != FSDP_DTYPE_E4M3 ? 0 : p.a.group == 0 ? 1 : 2;
+  if (map == kVector)
+    return quant == 0   ? run_forward<T, kResidual, 0, kVector>(p, s, grid, st)
+           : quant == 1 ? run_forward<T, kResidual, 1, kVector>(p, s, grid, st)
+                        : run_forward<T, kResidual, 2, kVector>(p, s, grid, st);
+  if (map == kShifted) return run_forward<T, kResidual, 0, kShifted>(p, s, grid, st);
+  return quant == 0   ? run_forward<T, kResidual, 0, kStrided>(p, s, grid, st)
+         : quant == 1 ? run_forward<T, kResidual, 1, kStrided>(p, s, grid, st)
+                      : run_forward<T, kResidual, 2, kGroups>(p, s, grid, st);
 }
 
 template <typename T>
-int forward(NormParams p, bool aligned, cudaStream_t st) {
-  const Spread s = forward_spread(p.a.rows, p.a.cols);
-  p.threads = s.threads;
+int forward(NormParams p, RowMap map, cudaStream_t st) {
   const bool quant = p.a.y_dtype == FSDP_DTYPE_E4M3;
+  if (quant && map == kShifted) map = kStrided;  // y's rows have a distance of their own
+  const Spread s = forward_spread(p.a.rows, covered(p.a.cols, map));
+  p.threads = s.threads;
   // as many blocks as run at once where a block works ahead, else one for each row
   int64_t most = 1 << 20;
-  if (s.v > 1 && aligned && !p.residual)
+  if (s.v > 1 && map == kVector && !p.residual)
     most = static_cast<int64_t>(sm_count()) * std::max(1, 768 / (s.threads * s.per_block));
   const int grid = static_cast<int>(std::min<int64_t>((p.a.rows + s.per_block - 1) / s.per_block, most));
   if (s.v == 0)
     return launch_rows(!quant ? norm_long_rows<T, 0> : p.a.group == 0 ? norm_long_rows<T, 1> : norm_long_rows<T, 2>, grid,
                        kLongThreads, 0, st, p);
-  return p.residual ? run_forward_as<T, true>(p, s, aligned, grid, st) : run_forward_as<T, false>(p, s, aligned, grid, st);
+  return p.residual ? run_forward_as<T, true>(p, s, map, grid, st) : run_forward_as<T, false>(p, s, map, grid, st);
 }
 
-template <typename T, Map kMap>
+template <typename T, RowMap kMap>
 int run_backward(const NormBwdParams& p, const Spread& s, cudaStream_t st) {
   const int threads = s.threads * s.per_block, smem = s.per_block > 1 ? static_cast<int>(p.a.cols * 4) : 0;
   switch (s.v) {
@@ -802,10 +893,10 @@ int run_staged(const NormBwdParams& p, const Spread& s, int smem, cudaStream_t s
 }
 
 template <typename T>
-int backward(NormBwdParams p, bool aligned, cudaStream_t st) {
-  const Spread s = backward_spread(p.a.rows, p.a.cols);
+int backward(NormBwdParams p, RowMap map, cudaStream_t st) {
+  const Spread s = backward_spread(p.a.rows, covered(p.a.cols, map));
   p.threads = s.threads;
-  p.parts = backward_parts(p.a.rows, p.a.cols);
+  p.parts = backward_parts(p.a.rows, s);
   // several rows per block: staged, if an SM's shared memory holds two for each of its blocks
   const int64_t row_bytes = p.a.cols * static_cast<int64_t>(sizeof(T)) * (p.dh ? 3 : 2);
   const int per_sm = (p.parts + sm_count() - 1) / sm_count();
@@ -813,20 +904,36 @@ int backward(NormBwdParams p, bool aligned, cudaStream_t st) {
   int rc;
   if (s.v == 0) {
     rc = launch_rows(norm_long_rows_backward<T>, p.parts, kLongThreads, 0, st, p);
-  } else if (aligned && s.per_block == 1 && p.a.rows > p.parts && stages >= 2) {
+  } else if (map == kVector && s.per_block == 1 && p.a.rows > p.parts && stages >= 2) {
     p.stages = static_cast<int32_t>(stages);
     rc = device_status_word(&p.status);
     if (rc == FSDP_OK) rc = run_staged<T>(p, s, static_cast<int>(stages * row_bytes), st);
   } else {
-    rc = aligned ? run_backward<T, kVector>(p, s, st) : run_backward<T, kStrided>(p, s, st);
+    rc = map == kVector    ? run_backward<T, kVector>(p, s, st)
+         : map == kShifted ? run_backward<T, kShifted>(p, s, st)
+                           : run_backward<T, kStrided>(p, s, st);
   }
   if (rc != FSDP_OK) return rc;
   return launch_rows(sum_partials, static_cast<int>((p.a.cols + 31) / 32), 1024, 0, st, p);
 }
 
-// Every row of the array starts on a boundary of `bytes`.
-bool rows_aligned(const void* q, int64_t rows, int64_t stride, int size, int bytes = 16) {
-  return !q || (reinterpret_cast<uintptr_t>(q) % bytes == 0 && (rows < 2 || stride * size % bytes == 0));
+struct Rows {
+  const void* p;  // null: no such array
+  int64_t stride;
+};
+
+// How rows of `size`-byte elements in these arrays can be read and written.
+RowMap map_of(std::initializer_list<Rows> arrays, int64_t rows, int64_t cols, int size) {
+  const Rows* first = nullptr;
+  bool aligned = cols % 8 == 0, together = true;
+  for (const Rows& q : arrays) {
+    if (!q.p) continue;
+    if (!first) first = &q;
+    const auto at = reinterpret_cast<uintptr_t>(q.p), at0 = reinterpret_cast<uintptr_t>(first->p);
+    aligned = aligned && at % 16 == 0 && (rows < 2 || q.stride * size % 16 == 0);
+    together = together && at % 16 == at0 % 16 && (rows < 2 || (q.stride - first->stride) * size % 16 == 0);
+  }
+  return aligned ? kVector : together ? kShifted : kStrided;
 }
 
 }  // namespace
@@ -869,16 +976,19 @@ extern "C" int fsdp_rmsnorm(const fsdp_rmsnorm_t* a, const void* x, const void* 
   while (a->group >> (group_bits + 1)) ++group_bits;
   const NormParams p{*a, x, residual, gain, h_out, y, scales, rstd, 0, group_bits,
                      reinterpret_cast<uintptr_t>(gain) % 16 == 0};
-  const bool aligned = a->cols % 8 == 0 && rows_aligned(x, a->rows, a->x_stride, es) && rows_aligned(residual, a->rows, a->residual_stride, es) &&
-                       rows_aligned(h_out, a->rows, a->h_stride, es) &&
-                       rows_aligned(y, a->rows, a->y_stride, size_of_dtype(a->y_dtype), e4m3 ? 8 : 16);
+  RowMap map = map_of({{x, a->x_stride}, {residual, a->residual_stride}, {h_out, a->h_stride}, {e4m3 ? nullptr : y, a->y_stride}},
+                   a->rows, a->cols, es);
+  if (e4m3 && (reinterpret_cast<uintptr_t>(y) % 8 != 0 || (a->rows > 1 && a->y_stride % 8 != 0))) map = kStrided;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return a->dtype == FSDP_DTYPE_F32 ? forward<float>(p, aligned, st) : forward<__nv_bfloat16>(p, aligned, st);
+  return a->dtype == FSDP_DTYPE_F32 ? forward<float>(p, map, st) : forward<__nv_bfloat16>(p, map, st);
 }
 
 extern "C" int fsdp_rmsnorm_backward_workspace(int64_t rows, int64_t cols, int64_t* bytes_out) {
   if (!bytes_out || rows < 0 || cols < 1 || cols > kMaxCols) return FSDP_EINVAL;
-  *bytes_out = backward_parts(rows, cols) * cols * 4 + 16;
+  // whatever the rows' alignment will be
+  const int parts = std::max(backward_parts(rows, backward_spread(rows, cols)),
+                             backward_parts(rows, backward_spread(rows, covered(cols, kShifted))));
+  *bytes_out = parts * cols * 4 + 16;
   return FSDP_OK;
 }
 
@@ -912,7 +1022,7 @@ extern "C" int fsdp_rmsnorm_backward(const fsdp_rmsnorm_backward_t* a, const voi
   float* partial = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + 15) & ~uintptr_t(15));
   const NormBwdParams p{*a, dy, h, gain, dh, rstd, dx, dgain, partial, 0, 0, 0,
                         reinterpret_cast<uintptr_t>(gain) % 16 == 0, nullptr};
-  const bool aligned = a->cols % 8 == 0 && rows_aligned(dy, a->rows, a->dy_stride, es) && rows_aligned(h, a->rows, a->h_stride, es) &&
-                       rows_aligned(dh, a->rows, a->dh_stride, es) && rows_aligned(dx, a->rows, a->dx_stride, es);
-  return a->dtype == FSDP_DTYPE_F32 ? backward<float>(p, aligned, st) : backward<__nv_bfloat16>(p, aligned, st);
+  const RowMap map =
+      map_of({{dy, a->dy_stride}, {h, a->h_stride}, {dh, a->dh_stride}, {dx, a->dx_stride}}, a->rows, a->cols, es);
+  return a->dtype == FSDP_DTYPE_F32 ? backward<float>(p, map, st) : backward<__nv_bfloat16>(p, map, st);
 }
