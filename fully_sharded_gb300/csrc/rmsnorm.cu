@@ -313,13 +313,13 @@ __device__ __forceinline__ float scale_of(float top) { return fmaxf(top * (1.0f 
 // more rows in flight while others wait at their reductions. kWide: rows that need
 // more threads at kMaxV groups each.
 constexpr int forward_threads(int v, bool wide) { return v < 3 || wide ? 512 : 384; }
-constexpr int forward_blocks(int v, bool wide) { return v == 2 || wide ? 1 : 2; }
+constexpr int forward_blocks(bool wide) { return wide ? 1 : 2; }
 constexpr int backward_threads(bool wide) { return wide ? 512 : 256; }
 constexpr int backward_blocks(int v, bool wide) { return wide ? 1 : v == 1 ? 4 : v == 2 ? 3 : 2; }
 
 // kQuant 0: y of the inputs' type; 1: 8 bits, one scale per row; 2: 8 bits, scales per group.
 template <typename T, bool kResidual, int kQuant, RowMap kMap, int kV, bool kWide = false>
-__global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kV, kWide))
+__global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kWide))
     norm_rows(const __grid_constant__ NormParams p) {
   __shared__ float shared[3][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
