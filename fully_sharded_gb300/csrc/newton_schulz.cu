@@ -145,7 +145,8 @@ __device__ __forceinline__ void each_group(const PassMat& j, int part, F f) {
   const int lane = threadIdx.x % 32;
   for (int64_t u = static_cast<int64_t>(part) * kPassWarps + threadIdx.x / 32; u < units;
        u += static_cast<int64_t>(j.parts) * kPassWarps) {
-    const int64_t r = u / segs, c0 = (u - r * segs) * kUnit + lane * 8;
+    const int64_t r = units >> 31 ? u / segs : static_cast<uint32_t>(u) / static_cast<uint32_t>(segs);
+    const int64_t c0 = (u - r * segs) * kUnit + lane * 8;
     float v[4][8];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -162,7 +163,9 @@ __device__ __forceinline__ void each_group(const PassMat& j, int part, F f) {
 // throughout (a few hundred terms in sequence at most; fp64 runs at 1/64 of the rate).
 __global__ void __launch_bounds__(32 * kPassWarps) ns_squares(const __grid_constant__ PassParams p) {
   int part;
-  const PassMat& j = pass_mat(p, &part);
+  const PassMat j = pass_mat(p, &part);  // read ahead of the wait, as in ns_product
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float sum = 0.0f;
   each_group(j, part, [&](int64_t, int64_t, const float (&v)[8]) {
     float s = 0.0f;
@@ -181,9 +184,10 @@ __device__ __forceinline__ float mean_of(float sum, const NsMomentum& m) {
 // of squares of u. Bound by HBM: 2 W + 12 bytes an element.
 template <int kWorld>
 __global__ void __launch_bounds__(32 * kPassWarps) ns_momentum(const __grid_constant__ MomentumParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   int part;
-  const PassMat& j = pass_mat(p.pass, &part);
+  const PassMat j = pass_mat(p.pass, &part);
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const NsMomentum& m = p.m;
   const int world = kWorld ? kWorld : m.w;
   float* out = static_cast<float*>(const_cast<void*>(j.source));
@@ -252,7 +256,9 @@ __global__ void __launch_bounds__(32 * kPassWarps) ns_momentum(const __grid_cons
 // X_0 as two parts.
 __global__ void __launch_bounds__(32 * kPassWarps) ns_normalise(const __grid_constant__ PassParams p) {
   int part;
-  const PassMat& j = pass_mat(p, &part);
+  const PassMat j = pass_mat(p, &part);  // read ahead of the wait, as in ns_product
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float sum = 0.0f;
   for (int i = threadIdx.x % 32; i < j.parts; i += 32) sum += j.partial[i];
   const float inv = 1.0f / (sqrtf(warp_sum(sum)) + p.eps);
@@ -501,7 +507,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
   const uint32_t slots = smem + T::kStages * T::kStageBytes, share = slots + kSlots * kSlotBytes;
   const int rank = T::kCluster == 2 ? static_cast<int>(block_rank()) : 0;
   const int pair_rank = kPair == 2 ? rank : 0;
-  const int first_tile = blockIdx.x / T::kCluster, tile_step = gridDim.x / T::kCluster;
+  // Tiles go round the clusters forwards, then backwards, and so on: they are sorted by
+  // length, so who had a long one in one round gets a short one in the next.
+  const int cluster = blockIdx.x / T::kCluster, clusters = gridDim.x / T::kCluster;
+  const auto tile_of = [=](int turn) { return turn * clusters + (turn & 1 ? clusters - 1 - cluster : cluster); };
   const Guard guard{&stop, p.status, kWaitLimitNs};
   if (threadIdx.x == 0) {
     for (int s = 0; s < T::kStages; ++s) {
@@ -553,7 +562,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     Tiles<T, GemmParams<kMats>> tiles{p};
     uint32_t it = 0;
     bool ok = true;
-    for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
+    for (int turn = 0, t = tile_of(0); ok && t < p.tiles; t = tile_of(++turn)) {
       int i, j, lo, hi;
       const GemmMat& g = tiles.at(t, &i, &j);
       steps_of(g, &lo, &hi);
@@ -594,7 +603,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     Tiles<T, GemmParams<kMats>> tiles{p};
     uint32_t it = 0, n = 0;
     bool ok = true;
-    for (int t = first_tile; ok && t < p.tiles; t += tile_step, ++n) {
+    for (int t = tile_of(0); ok && t < p.tiles; t = tile_of(++n)) {
       int i, j, lo, hi;
       const GemmMat& g = tiles.at(t, &i, &j);
       steps_of(g, &lo, &hi);
@@ -627,7 +636,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     const int parts = p.kind == kUpdate || p.terms == 3 ? 2 : 1;
     uint32_t e = 0;
     bool ok = true;
-    for (int t = first_tile; ok && t < p.tiles; t += tile_step) {
+    for (int turn = 0, t = tile_of(0); ok && t < p.tiles; t = tile_of(++turn)) {
       int i, j;
       const GemmMat& g = tiles.at(t, &i, &j);
       const int block = i * kPair + pair_rank;
@@ -658,9 +667,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     uint32_t n = 0, e = 0, left = 0;            // tiles, chunks, chunks whose slots this warp has released
     // a wait of this thread ran out; some thread's did (the same for all, known at the next barrier)
     bool lost = false, failed = false;
-    int known = -1, turn = 0;                   // the matrix whose m is `shift`
+    int known = -1, side = 0;                   // the matrix whose m is `shift`; the set of sums in use
     float shift = 0.0f;
-    for (int t = first_tile; !failed && t < p.tiles; t += tile_step, ++n) {
+    for (int t = tile_of(0); !failed && t < p.tiles; t = tile_of(++n)) {
       int i, j, lo, hi;
       const GemmMat& g = tiles.at(t, &i, &j);
       steps_of(g, &lo, &hi);
@@ -673,13 +682,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
 #pragma unroll 8
           for (int k = threadIdx.x - 128; k < count; k += 32 * kEpilogueWarps) sum += g.squares[k];
           sum = warp_sum(sum);
-          if (lane == 0) squares[turn][own] = sum;
+          if (lane == 0) squares[side][own] = sum;
           failed = named_or(1, 32 * kEpilogueWarps, lost);
           if (failed) break;
           sum = 0.0f;
 #pragma unroll
-          for (int k = 0; k < kEpilogueWarps; ++k) sum += squares[turn][k];
-          turn ^= 1;  // the next matrix's barrier comes before this set is written again
+          for (int k = 0; k < kEpilogueWarps; ++k) sum += squares[side][k];
+          side ^= 1;  // the next matrix's barrier comes before this set is written again
           shift = sum / (kScaleX * kScaleX) / static_cast<float>(min(g.m, min(g.n, g.k)));
           if (shift < kShiftFrom) shift = 0.0f;
         }
@@ -1213,7 +1222,8 @@ bool splits(const NsJob& j) { return std::min(j.rows, j.cols) <= 1408; }
 
 int parts_of(const NsJob& j) {
   const int64_t units = j.rows * ((j.cols + kUnit - 1) / kUnit);
-  return static_cast<int>(std::min<int64_t>(kMaxParts, (units + kPassWarps - 1) / kPassWarps));
+  // two units a warp: the blocks of a GPT-2 block's matrices (528) then run at once
+  return static_cast<int>(std::min<int64_t>(kMaxParts, (units + 2 * kPassWarps - 1) / (2 * kPassWarps)));
 }
 
 // A matrix's share of the workspace: X twice (read and written by turns) and A, P,
@@ -1448,10 +1458,9 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
     first.m = *momentum;
     if (int rc = launch_momentum(first, blocks, stream)) return rc;
   } else {
-    ns_squares<<<blocks, 32 * kPassWarps, 0, stream>>>(pass);
+    if (int rc = launch_after(ns_squares, blocks, 1, 32 * kPassWarps, 0, stream, pass)) return rc;
   }
-  ns_normalise<<<blocks, 32 * kPassWarps, 0, stream>>>(pass);
-  if (cudaGetLastError() != cudaSuccess) return FSDP_ECUDA;
+  if (int rc = launch_after(ns_normalise, blocks, 1, 32 * kPassWarps, 0, stream, pass)) return rc;
   p.count = count;
   p.terms = terms;
   p.status = dev.status;
