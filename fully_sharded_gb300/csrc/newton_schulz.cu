@@ -159,7 +159,7 @@ __device__ __forceinline__ void each_group(const PassMat& j, int part, F f) {
   }
 }
 
-// Sums of squares, one per block: a lane adds its groups of 8, then trees. fp32
+// Sums of squares, one per block (4096 x 11008 fp32: 30 us, 6.0 TB/s): a lane adds its groups of 8, then trees. fp32
 // throughout (a few hundred terms in sequence at most; fp64 runs at 1/64 of the rate).
 __global__ void __launch_bounds__(32 * kPassWarps) ns_squares(const __grid_constant__ PassParams p) {
   int part;
@@ -181,7 +181,8 @@ __device__ __forceinline__ float mean_of(float sum, const NsMomentum& m) {
 }
 
 // The momentum update of a unit's matrices (W = kWorld ranks; 0: any), and the sums
-// of squares of u. Bound by HBM: 2 W + 12 bytes an element.
+// of squares of u. Bound by HBM: 2 W + 12 bytes an element (a Llama block's seven matrices,
+// W = 8, 202 M elements: 0.82 ms, 6.9 TB/s).
 template <int kWorld>
 __global__ void __launch_bounds__(32 * kPassWarps) ns_momentum(const __grid_constant__ MomentumParams p) {
   int part;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(32 * kPassWarps) ns_momentum(const __grid_cons
   block_sum_to(sum, &j.partial[part]);
 }
 
-// X_0 as two parts.
+// X_0 as two parts. Bound by HBM: 8 bytes an element (4096 x 11008 fp32: 55 us, 6.5 TB/s).
 __global__ void __launch_bounds__(32 * kPassWarps) ns_normalise(const __grid_constant__ PassParams p) {
   int part;
   const PassMat j = pass_mat(p, &part);  // read ahead of the wait, as in ns_product
@@ -492,6 +493,22 @@ __device__ __forceinline__ void finish_rows(const GemmMat& g, const NsApply& ap,
   }
 }
 
+// One of the three products over all matrices of a launch; which tile by pair_time(),
+// block_time() and splits() below. What bounds it, by size (measured on GB300):
+//   - long sides from 2048 on: the tensor cores under the power cap. A step of 64 of a 256 x
+//     256 tile takes 0.36 us, 1.78 PFLOP/s over 76 pairs; a long run of such launches settles
+//     at 1.5 PFLOP/s, where cuBLAS settles at 1.55 to 1.60 on fp16 operands (1.69 on
+//     bf16: more mantissa bits switch). Rounds that are not full cost the rest: 136 tiles of
+//     a 4096-wide symmetric product are 1.8 rounds of 76.
+//   - around 1000: the ring of stages. 160 KB are in flight per SM and come back
+//     after 1.5 us, so a step of a 128 x 128 tile takes 0.33 us where its products take
+//     0.13; and about 3.5 us of each launch are its start and end (1 us from the
+//     previous kernel's end to the wait's return, 0.8 to the first stage, 0.9 for
+//     a chunk to leave, 0.5 to the exit).
+//   - few tiles: the same latencies; two blocks that share a tile (kSplit) pass 32 KB
+//     of sums to each other in 1.9 us and save half of the steps.
+// (The whole of 5 steps: 4096 x 11008 2.4 to 2.5 ms, 1.3 PFLOP/s of the work that symmetry
+// leaves; 768 x 2304, 768 x 768, 768 x 3072 and 3072 x 768 together 0.24 ms.)
 template <int kN, int kPair, int kSplit, int kMats>
 __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_constant__ GemmParams<kMats> p) {
   using T = Tile<kN, kPair, kSplit>;
@@ -854,8 +871,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
 // block goes through all its steps there, in one launch: X's two parts and those
 // of A (then of P, in the same place) as 128-byte-swizzled operand tiles, the
 // products in tensor memory, the short side's rows on its lanes. The three products
-// of a step follow one another, so it is bound by their latency (about 1 us each
-// with the passes between them). Tall matrices are transposed as they are read.
+// of a step follow one another, so it is bound by their latency, about 1 us each
+// with the passes between them (16 x 16: 13 us for 5 steps, 64 x 32 18, 128 x 128 42,
+// 100 x 300 69 us, whatever the number of matrices up to one for each SM). Tall
+// matrices are transposed as they are read.
 constexpr int kSmallSide = 128;
 constexpr int kSmallThreads = 256;
 constexpr int kSmallBytes = 220 * 1024;
@@ -1214,8 +1233,10 @@ bool is_small(const NsJob& j) {
   return SmallShape(static_cast<int>(j.rows), static_cast<int>(j.cols)).bytes() <= kSmallBytes;
 }
 
-// Matrices whose symmetric products are shared by two blocks a tile: those with so
-// few tiles (66 or fewer of 128 x 128) that two blocks for each still run at once. It
+// Matrices whose Gram products are shared by two blocks a tile: those with so few
+// tiles (66 or fewer of 128 x 128) that two blocks for each still run at once (5 steps of
+// 1024 x 4096: 267 -> 236 us, of 768 x 2304 and company 257 -> 239, of 512 x 512 114 -> 123:
+// there is no saving in a short inner dimension). It
 // goes by the matrix alone, not by its company, so that a matrix gives the same
 // bits in every call.
 bool splits(const NsJob& j) { return std::min(j.rows, j.cols) <= 1408; }
@@ -1411,8 +1432,8 @@ int run_small(const NsJob* const* jobs, int count, const NsPlan& plan, const NsM
 // of the measured cuBLAS rate), one of a 128 x 128 tile takes a block 0.33 (bound by
 // L2: 32 KB of operands for a quarter of the products); a tile's results leave in
 // 7.5 and 1.6, while the next tile's products run, the last one's after them.
-// Updates of a GPT-2 block's matrices (12 steps): pairs 292, single blocks
-// 268 us for all; of 4096 x 11008 (64 steps) pairs 268, single blocks 446 us each.
+// All of a GPT-2 block's matrices (updates of 12 steps): 267 us with pairs, 238 with single
+// blocks; 4096 x 4096 (64 steps) 1425 and 1657 us.
 double pair_time(int64_t tiles, int steps, int sms) {
   const double rounds = static_cast<double>((tiles + sms / 2 - 1) / (sms / 2));
   return rounds * std::max(0.36 * steps, 7.5) + 7.5;
@@ -1534,9 +1555,8 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
 int ns_plan(const fsdp_newton_schulz_t* h, NsPlan* plan) {
   if (h) {
     if (h->steps < 1 || h->steps > 32 || (h->terms != 0 && h->terms != 1 && h->terms != 3)) return FSDP_EINVAL;
-    if (!(h->eps > 0.0) || !std::isfinite(h->eps) || !(static_cast<float>(h->eps) > 0.0f) ||
-        !std::isfinite(static_cast<float>(h->eps)))
-      return FSDP_EINVAL;
+    const float eps = static_cast<float>(h->eps);
+    if (!(eps >= 0x1p-126f) || !std::isfinite(eps)) return FSDP_EINVAL;  // 1 / eps has to be finite
     plan->steps = h->steps;
     plan->terms = h->terms;
     plan->eps = static_cast<float>(h->eps);
@@ -1665,8 +1685,9 @@ extern "C" int fsdp_newton_schulz(const fsdp_matrix_t* matrices, int32_t n, cons
   if (int rc = make_jobs(matrices, n, true, &jobs)) return rc;
   if (jobs.empty()) return FSDP_OK;
   if (!workspace) return FSDP_EINVAL;
-  if (workspace_bytes < ns_workspace_bytes(jobs, plan)) return FSDP_EWORKSPACE;
-  const Strided ws{workspace, 1, workspace_bytes, workspace_bytes, 1};
+  const int64_t need = ns_workspace_bytes(jobs, plan);
+  if (workspace_bytes < need) return FSDP_EWORKSPACE;
+  const Strided ws{workspace, 1, need, need, 1};
   for (const NsJob& j : jobs)
     if (ws.overlaps({j.source, j.rows, j.cols, j.source_stride, size_of_dtype(j.dtype)}) ||
         ws.overlaps({j.out, j.rows, j.cols, j.out_stride, 2}))

@@ -7,9 +7,15 @@
 //
 // Both are bound by HBM (5 to 10 operations for 4 to 8 bytes moved per element at
 // bf16), so a row is read once: it stays in its threads' registers between the
-// sum over the row and the writes. A row belongs to one warp (short rows, several
-// to a block) or to one block; each thread holds up to kV groups of 8 elements.
-// Rows longer than that are read twice (norm_long_rows and its like).
+// sum over the row and the writes. A row belongs to a part of a warp, to one warp (short
+// rows, several to a block) or to one block; each thread holds up to kV groups of
+// 8 elements. Rows longer than that are read twice (norm_long_rows and its like).
+//
+// Measured on GB300 (fraction of the copy bandwidth of 6.79 TB/s): 16384 x 4096 bf16 with
+// the residual 82.9 us (95 %), backward with the residual's gradient 93.5 us (85 %);
+// 4097 x 11008 bf16 to 8 bits in groups of 128 43 us (47 %, bound by instructions: about
+// 25 an element, a conversion, two maxima and four products among them); one row of
+// 4096 8.5 us, of which the launch from Python is all but 3.
 #include "host_internal.h"
 #include "strided.h"
 #include "tensor_core.cuh"

@@ -605,7 +605,7 @@ typedef struct {
   int32_t terms;              /* 0, 1 or 3 */
   const double *coefficients; /* host: a, b, c of each step (3 * steps values); null: 3.4445,
                                  -4.7750, 2.0315 for every step */
-  double eps;                 /* finite, > 0 */
+  double eps;                 /* finite, at least 2^-126 */
 } fsdp_newton_schulz_t;
 
 typedef struct {
