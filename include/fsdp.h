@@ -297,7 +297,8 @@ int fsdp_shard_step_grouped_plan(const fsdp_unit_args_t *units, int32_t n_units,
 
 /* The current device's sticky status word, read after all work of the
  * device, on every stream, has finished (the call synchronizes the device). Bit 0 is
- * set when a bounded wait of the TMA form ran out (2 s on one mbarrier): the
+ * set when a bounded wait of the TMA form (or of the norm's backward pass, the
+ * orthogonalisation or the Muon step) ran out (2 s on one mbarrier): the
  * block that saw it stopped early, so the outputs of that launch are not
  * valid. This does not happen in a correct run. clear != 0 resets the word
  * after reading it. EINVAL: status_out NULL; ECUDA: the read failed. */
