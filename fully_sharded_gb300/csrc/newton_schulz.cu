@@ -44,6 +44,7 @@
 #include <cstdint>
 #include <cstring>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 namespace fsdp {
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
   __shared__ uint32_t tmem_slot;
   __shared__ int stop;
   __shared__ float squares[2][kEpilogueWarps];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
   const uint32_t slots = smem + T::kStages * T::kStageBytes, share = slots + kSlots * kSlotBytes;
   const int rank = T::kCluster == 2 ? static_cast<int>(block_rank()) : 0;
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     return !(col0 >= g.n || block * 128 >= g.m || (g.symmetric && col0 / 128 > block) || (kSplit == 2 && c != rank));
   };
 
-  if (warp == 0 && lane == 0) {  // producer: this block's rows of both operands
+  if (warp == 0) {  // producer: this block's rows of both operands
     Tiles<T, GemmParams<kMats>> tiles{p};
     uint32_t it = 0;
     bool ok = true;
@@ -586,27 +587,31 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
       const int blocks = (g.k + kTileK - 1) / kTileK;
       const int row0 = i * T::kM + pair_rank * 128, col0 = j * kN + pair_rank * T::kBRows;
       int term = lo / blocks, kb = lo - term * blocks;
+      const bool p_mn = g.p_mn, q_mn = g.q_mn;
       for (int step = lo; step < hi; ++step, ++it) {
         const CUtensorMap* mp = &g.p[term == 1 ? 1 : 0];
         const CUtensorMap* mq = &g.q[term == 2 ? 1 : 0];
         const int s = it % T::kStages;
-        ok = bar_wait(smem_addr(&empty_bar[s]), ((it / T::kStages) & 1u) ^ 1u, guard);
+        ok = bar_wait_warp(smem_addr(&empty_bar[s]), ((it / T::kStages) & 1u) ^ 1u, guard);
         if (!ok) break;
         // the first block's barrier counts the bytes of both
         const uint32_t own = smem_addr(&full_bar[s]), bar = kPair == 2 ? in_block(own, 0) : own;
         const uint32_t a = smem + s * T::kStageBytes, b = a + T::kABytes;
-        if (pair_rank == 0) bar_expect(own, T::kStageBytes * kPair);
         if (it == 0) await_inputs();
+        if (elect_one()) {
+          if (pair_rank == 0) bar_expect(own, T::kStageBytes * kPair);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int r = row0 + 64 * q;
-          tma_box<kPair>(a + q * 8192, mp, g.p_mn ? r : kb * kTileK, g.p_mn ? kb * kTileK : r, bar);
-        }
+          for (int q = 0; q < 2; ++q) {
+            const int r = row0 + 64 * q;
+            tma_box<kPair>(a + q * 8192, mp, p_mn ? r : kb * kTileK, p_mn ? kb * kTileK : r, bar);
+          }
 #pragma unroll
-        for (int q = 0; q < T::kBRows / 64; ++q) {
-          const int c = col0 + 64 * q;
-          tma_box<kPair>(b + q * 8192, mq, g.q_mn ? c : kb * kTileK, g.q_mn ? kb * kTileK : c, bar);
+          for (int q = 0; q < T::kBRows / 64; ++q) {
+            const int c = col0 + 64 * q;
+            tma_box<kPair>(b + q * 8192, mq, q_mn ? c : kb * kTileK, q_mn ? kb * kTileK : c, bar);
+          }
         }
+        __syncwarp();
         if (++kb == blocks) kb = 0, ++term;
       }
     }
@@ -616,7 +621,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
       const uint64_t* bar = pair_rank == 0 ? full_bar : empty_bar;
       bar_drain(smem_addr(&bar[last % T::kStages]), (last / T::kStages) & 1u, kWaitLimitNs);
     }
-  } else if (warp == 1 && lane == 0 && pair_rank == 0) {  // products, for both blocks of a pair
+  } else if (warp == 1 && pair_rank == 0) {  // products, for both blocks of a pair
     Tiles<T, GemmParams<kMats>> tiles{p};
     uint32_t it = 0, n = 0;
     bool ok = true;
@@ -625,7 +630,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
       const GemmMat& g = tiles.at(t, &i, &j);
       steps_of(g, &lo, &hi);
       const uint32_t buf = n & 1u, d = tmem + buf * kN;
-      ok = bar_wait(smem_addr(&free_bar[buf]), ((n >> 1) & 1u) ^ 1u, guard);
+      ok = bar_wait_warp(smem_addr(&free_bar[buf]), ((n >> 1) & 1u) ^ 1u, guard);
       if (!ok) break;
       fence_after();
       const uint32_t kind = product_kind(T::kM, kN, g.p_mn, g.q_mn);
@@ -634,21 +639,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
       const uint32_t a_block = g.p_mn ? 8192 : 0, b_block = g.q_mn ? 8192 : 0;
       for (int step = lo; step < hi; ++step, ++it) {
         const int s = it % T::kStages;
-        ok = bar_wait(smem_addr(&full_bar[s]), (it / T::kStages) & 1u, guard);
+        ok = bar_wait_warp(smem_addr(&full_bar[s]), (it / T::kStages) & 1u, guard);
         if (!ok) break;
         fence_after();
         const uint32_t a = smem + s * T::kStageBytes, b = a + T::kABytes;
+        const uint64_t da = operand(a, a_block, 1024), db = operand(b, b_block, 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int q = 0; q < kTileK / 16; ++q)
-          mma<kPair>(d, operand(a + q * a_step, a_block, 1024), operand(b + q * b_step, b_block, 1024), kind,
-                     step > lo || q > 0);
-        mma_commit<kPair>(smem_addr(&empty_bar[s]));
+          for (int q = 0; q < kTileK / 16; ++q)
+            mma<kPair>(d, da + (q * a_step >> 4), db + (q * b_step >> 4), kind, step > lo || q > 0);
+          mma_commit<kPair>(smem_addr(&empty_bar[s]));
+        }
+        __syncwarp();
       }
-      if (ok) mma_commit<kPair>(smem_addr(&done_bar[buf]));
+      if (ok && elect_one()) mma_commit<kPair>(smem_addr(&done_bar[buf]));
+      __syncwarp();
     }
     if (!ok && it > 0)  // products in flight end before the accumulators are freed
       bar_drain(smem_addr(&empty_bar[(it - 1) % T::kStages]), ((it - 1) / T::kStages) & 1u, kWaitLimitNs);
-  } else if (warp == 2 && lane == 0 && p.kind != kGram) {  // fetch of `in`, ahead of the epilogue
+  } else if (warp == 2 && p.kind != kGram) {  // fetch of `in`, ahead of the epilogue
     Tiles<T, GemmParams<kMats>> tiles{p};
     const int parts = p.kind == kUpdate || p.terms == 3 ? 2 : 1;
     uint32_t e = 0;
@@ -662,13 +671,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
         const int col0 = j * kN + c * kChunk;
         if (!has_chunk(g, block, col0, c)) continue;
         const uint32_t set = e % sets, bar = smem_addr(&in_bar[set]), to = slots + set * set_bytes;
-        ok = bar_wait(smem_addr(&out_bar[set]), ((e / sets) & 1u) ^ 1u, guard);
+        ok = bar_wait_warp(smem_addr(&out_bar[set]), ((e / sets) & 1u) ^ 1u, guard);
         if (!ok) break;
-        bar_expect(bar, parts * kSlotBytes);
         if (e == 0) await_inputs();
-        for (int part = 0; part < parts; ++part)
-          for (int b = 0; b < 2; ++b)
-            tma_box<1>(to + part * kSlotBytes + b * 8192, &in[part], col0, block * 128 + 64 * b, bar);
+        if (elect_one()) {
+          bar_expect(bar, parts * kSlotBytes);
+          for (int part = 0; part < parts; ++part)
+            for (int b = 0; b < 2; ++b)
+              tma_box<1>(to + part * kSlotBytes + b * 8192, &in[part], col0, block * 128 + 64 * b, bar);
+        }
+        __syncwarp();
         ++e;
       }
     }
@@ -935,7 +947,7 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
   const SmallMat g = p.mat[blockIdx.x];
   const SmallShape s(g.rows, g.cols);
   const bool wide = g.rows <= g.cols;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
   unsigned char* x = raw + (base - smem_addr(raw));
   unsigned char* a = x + 2 * s.part_x;
@@ -1058,16 +1070,17 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
   uint32_t phase = 0;
   // a wait of this thread ran out; some thread's did (the same for all, known at the next barrier)
   bool lost = false, failed = false;
-  // Makes what the threads wrote visible to the products, lets thread 0 issue them, and waits for them.
+  // Makes what the threads wrote visible to the products, lets warp 0 issue them, and waits for them.
   const auto run = [&](auto issue) {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     fence_before();
     failed = __syncthreads_or(lost);
     if (failed) return;
-    if (threadIdx.x == 0) {
+    if (warp == 0) {
       fence_after();
       issue();
-      mma_commit<1>(smem_addr(&done_bar));
+      if (elect_one()) mma_commit<1>(smem_addr(&done_bar));
+      __syncwarp();
     }
     lost = !bar_wait(smem_addr(&done_bar), phase & 1u, guard);
     ++phase;
@@ -1076,23 +1089,6 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
   const int row = (warp & 3) * 32 + lane;
   const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   const bool busy = (warp & 3) * 32 < s.side16;  // some lane of the warp has a row
-  // Calls f(column, results, hi parts, lo parts) for 8-column pieces [0, cols) of this thread's
-  // row of a region at `to`; the two warps of a lane quarter take 32 columns by turns.
-  const auto pieces = [&](unsigned char* to, int part, int col0, int cols, auto f) {
-    if (!busy) return;
-    for (int c = (warp >> 2) * 32; c < cols; c += 64) {
-      float v[32];
-      __syncwarp();
-      tmem_load32(lanes + c, v);
-      if (row >= s.side16) continue;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (c + 8 * q >= cols) break;
-        unsigned char* at = to + small_at(s.side16, row, col0 + c + 8 * q);
-        f(&v[8 * q], reinterpret_cast<uint4*>(at), reinterpret_cast<uint4*>(at + part));
-      }
-    }
-  };
   // old = hi + lo of a piece; stores `v` as two parts
   const auto sum_of = [](const uint4& hi, const uint4& lo, float* out) {
     const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
@@ -1117,61 +1113,72 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
     *hi = make_uint4(h[0], h[1], h[2], h[3]);
     *lo = make_uint4(l[0], l[1], l[2], l[3]);
   };
+  // Columns [col0, col0 + cols) of this thread's row of a region at `to` become alpha times
+  // the products' plus beta times (kOld) what is there; the two warps of a lane
+  // quarter take 32 columns by turns. All reads come before the first write.
+  const auto update = [&](auto with_old, unsigned char* to, int part, int col0, int cols, float alpha, float beta) {
+    constexpr bool kOld = decltype(with_old)::value;
+    if (!busy) return;
+    for (int c = (warp >> 2) * 32; c < cols; c += 64) {
+      const int n = row < s.side16 ? min(4, (cols - c) / 8) : 0;
+      unsigned char* at[4];
+      uint4 hi[4], lo[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        at[q] = to + small_at(s.side16, row, col0 + c + 8 * q);
+        if (kOld && q < n) {
+          hi[q] = *reinterpret_cast<const uint4*>(at[q]);
+          lo[q] = *reinterpret_cast<const uint4*>(at[q] + part);
+        }
+      }
+      float v[32];
+      __syncwarp();
+      tmem_load32(lanes + c, v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float old[8];
+        if (kOld) sum_of(hi[q], lo[q], old);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[8 * q + e] = kOld ? beta * old[e] + alpha * v[8 * q + e] : alpha * v[8 * q + e];
+        if (q < n) put(&v[8 * q], reinterpret_cast<uint4*>(at[q]), reinterpret_cast<uint4*>(at[q] + part));
+      }
+    }
+  };
+  const std::integral_constant<bool, true> added;
+  const std::integral_constant<bool, false> fresh;
   const uint32_t block = static_cast<uint32_t>(s.side16) * 128;
+  // One product over `deep` steps of 16 of the inner dimension, all terms: l and r are the hi
+  // parts' descriptors, l_lo and r_lo their lo parts' distances, `mn`: r's steps are
+  // 16 rows, else both operands' are 32 bytes within blocks of 64 columns.
+  const auto product = [&](uint64_t l, int l_lo, uint64_t r, int r_lo, int deep, uint32_t kind, bool mn) {
+    if (!elect_one()) return;
+    for (int t = 0; t < p.terms; ++t) {
+      const uint64_t lt = l + (t == 1 ? l_lo >> 4 : 0), rt = r + (t == 2 ? r_lo >> 4 : 0);
+#pragma unroll 4
+      for (int k = 0; k < deep; ++k) {
+        const uint32_t at = ((k >> 2) * block + (k & 3) * 32) >> 4;
+        mma<1>(tmem, lt + at, rt + (mn ? k * (2048 >> 4) : at), kind, t > 0 || k > 0);
+      }
+    }
+  };
   const uint32_t square = product_kind(128, s.side16, false, false);
+  const uint64_t x_rows = operand(x_addr, 0, 1024), a_rows = operand(a_addr, 0, 1024);
   for (int step = 0; step < p.steps && !failed; ++step) {
     const float ca = p.coef[3 * step], cb = p.coef[3 * step + 1], cc = p.coef[3 * step + 2];
-    run([&] {  // A = X X^T
-      for (int t = 0; t < p.terms; ++t) {
-        const uint32_t l = x_addr + (t == 1 ? s.part_x : 0), r = x_addr + (t == 2 ? s.part_x : 0);
-        for (int k = 0; k < (s.length + 15) / 16; ++k) {
-          const uint32_t at = (k >> 2) * block + (k & 3) * 32;
-          mma<1>(tmem, operand(l + at, 0, 1024), operand(r + at, 0, 1024), square, t > 0 || k > 0);
-        }
-      }
-    });
+    run([&] { product(x_rows, s.part_x, x_rows, s.part_x, (s.length + 15) / 16, square, false); });  // A = X X^T
     if (failed) break;
-    pieces(a, s.part_a, 0, s.side16, [&](float* v, uint4* hi, uint4* lo) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= kScaleA / (kScaleX * kScaleX);
-      put(v, hi, lo);
-    });
-    run([&] {  // A A
-      for (int t = 0; t < p.terms; ++t) {
-        const uint32_t l = a_addr + (t == 1 ? s.part_a : 0), r = a_addr + (t == 2 ? s.part_a : 0);
-        for (int k = 0; k < s.side16 / 16; ++k) {
-          const uint32_t at = (k >> 2) * block + (k & 3) * 32;
-          mma<1>(tmem, operand(l + at, 0, 1024), operand(r + at, 0, 1024), square, t > 0 || k > 0);
-        }
-      }
-    });
+    update(fresh, a, s.part_a, 0, s.side16, kScaleA / (kScaleX * kScaleX), 0.0f);
+    run([&] { product(a_rows, s.part_a, a_rows, s.part_a, s.side16 / 16, square, false); });  // A A
     if (failed) break;
-    pieces(a, s.part_a, 0, s.side16, [&](float* v, uint4* hi, uint4* lo) {
-      float old[8];
-      sum_of(*hi, *lo, old);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = cb * old[e] + cc / kScaleA * v[e];
-      put(v, hi, lo);
-    });
-    for (int col0 = 0; col0 < s.length && !failed; col0 += kSmallCols) {
+    update(added, a, s.part_a, 0, s.side16, cc / kScaleA, cb);
+    for (int col0 = 0; col0 < s.length && !failed; col0 += kSmallCols) {  // P X, columns from col0 on
       const int cols = min(kSmallCols, (s.length - col0 + 15) / 16 * 16);
-      run([&] {  // P X, columns from col0 on
-        const uint32_t kind = product_kind(128, cols, false, true);
-        for (int t = 0; t < p.terms; ++t) {
-          const uint32_t l = a_addr + (t == 1 ? s.part_a : 0), r = x_addr + (t == 2 ? s.part_x : 0) + (col0 >> 6) * block;
-          for (int k = 0; k < s.side16 / 16; ++k)
-            mma<1>(tmem, operand(l + (k >> 2) * block + (k & 3) * 32, 0, 1024), operand(r + k * 2048, block, 1024), kind,
-                   t > 0 || k > 0);
-        }
+      run([&] {
+        product(a_rows, s.part_a, operand(x_addr + (col0 >> 6) * block, block, 1024), s.part_x, s.side16 / 16,
+                product_kind(128, cols, false, true), true);
       });
       if (failed) break;
-      pieces(x, s.part_x, col0, cols, [&](float* v, uint4* hi, uint4* lo) {
-        float old[8];
-        sum_of(*hi, *lo, old);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = ca * old[e] + v[e] / kScaleA;
-        put(v, hi, lo);
-      });
+      update(added, x, s.part_x, col0, cols, 1.0f / kScaleA, ca);
     }
   }
   fence_before();

@@ -60,6 +60,20 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Gu
   }
 }
 
+// bar_wait by a whole warp, with the same answer for all its lanes: what follows stays
+// uniform, so that descriptors and addresses are formed in uniform registers, where
+// the tensor-core and TMA instructions take them (an issue loop in one lane's
+// divergent branch takes 60 to 100 cycles for each product).
+__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, const Guard& g) {
+  return __all_sync(0xffffffffu, bar_wait(bar, parity, g));
+}
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
+}
+
 // As bar_wait, for data that another block of the cluster wrote.
 __device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity, const Guard& g) {
   const uint64_t t0 = clock_ns();
