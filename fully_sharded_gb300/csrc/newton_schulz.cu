@@ -322,21 +322,16 @@ constexpr int kEpilogueWarps = 8;
 constexpr int kGemmThreads = 128 + 32 * kEpilogueWarps;  // producer, products, fetch of `in`, an idle warp, epilogue
 constexpr int kSlotBytes = 128 * kChunk * 2;              // one part of a chunk
 constexpr int kSlots = 4;
-constexpr int kShareBytes = 128 * kChunk * 4;             // a chunk's fp32 sums from the other block (kSplit = 2)
 
-// A tile: 128 rows per block of the pair (or single block) and kN columns. kSplit = 2:
-// the two blocks of a cluster share a tile, each takes half of the inner dimension,
-// sends the other the sums of the chunk that it does not finish, and finishes one.
-template <int kN, int kPair, int kSplit>
+// A tile: 128 rows per block of the pair (or single block) and kN columns.
+template <int kN, int kPair>
 struct Tile {
   static constexpr int kM = 128 * kPair;
-  static constexpr int kCluster = kPair * kSplit;
   static constexpr int kBRows = kN / kPair;  // a block's half of the second operand
   static constexpr int kABytes = 128 * kTileK * 2, kBBytes = kBRows * kTileK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kShare = kSplit == 2 ? kShareBytes : 0;
-  static constexpr int kStages = (230400 - 1024 - kSlots * kSlotBytes - kShare) / kStageBytes;
-  static constexpr int kSmemBytes = kStages * kStageBytes + kSlots * kSlotBytes + kShare + 1024;
+  static constexpr int kStages = (230400 - 1024 - kSlots * kSlotBytes) / kStageBytes;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kSlots * kSlotBytes + 1024;
   static constexpr int kTmemCols = 2 * kN;
 
   // symmetric results: tiles of tile row i with an element on or below the diagonal
@@ -494,40 +489,38 @@ __device__ __forceinline__ void finish_rows(const GemmMat& g, const NsApply& ap,
   }
 }
 
-// One of the three products over all matrices of a launch; which tile by pair_time(),
-// block_time() and splits() below. What bounds it, by size (measured on GB300):
+// One of the three products over all matrices of a launch; which tile by pair_time() and
+// block_time() below. What bounds it, by size (measured on GB300):
 //   - long sides from 2048 on: the tensor cores under the power cap. A step of 64 of a 256 x
-//     256 tile takes 0.36 us, 1.78 PFLOP/s over 76 pairs; a long run of such launches settles
-//     at 1.5 PFLOP/s, where cuBLAS settles at 1.55 to 1.60 on fp16 operands (1.69 on
+//     256 tile takes 0.33 us at first, 2.0 PFLOP/s over 76 pairs; a long run of such launches
+//     settles at 1.5 to 1.6 PFLOP/s, as cuBLAS does on fp16 operands (1.55 to 1.60; 1.69 on
 //     bf16: more mantissa bits switch). Rounds that are not full cost the rest: 136 tiles of
 //     a 4096-wide symmetric product are 1.8 rounds of 76.
-//   - around 1000: the ring of stages. 160 KB are in flight per SM and come back
-//     after 1.5 us, so a step of a 128 x 128 tile takes 0.33 us where its products take
-//     0.13; and about 3.5 us of each launch are its start and end (1 us from the
-//     previous kernel's end to the wait's return, 0.8 to the first stage, 0.9 for
-//     a chunk to leave, 0.5 to the exit).
-//   - few tiles: the same latencies; two blocks that share a tile (kSplit) pass 32 KB
-//     of sums to each other in 1.9 us and save half of the steps.
-// (The whole of 5 steps: 4096 x 11008 2.4 to 2.5 ms, 1.3 PFLOP/s of the work that symmetry
-// leaves; 768 x 2304, 768 x 768, 768 x 3072 and 3072 x 768 together 0.24 ms.)
-template <int kN, int kPair, int kSplit, int kMats>
+//   - around 1000: shared memory. A step of a 128 x 128 tile writes 32 KB of operands and
+//     the products read them once: 512 cycles at 128 bytes each, 0.27 us of the
+//     measured 0.28, where the products themselves take half of that. And about 4 us of
+//     each launch are its start and end (1 us from the previous kernel's end to the
+//     wait's return, 0.8 to the first stage, 0.9 for a chunk to leave, 0.5 to the exit).
+// (The whole of 5 steps: 4096 x 11008 2.3 ms, 1.35 PFLOP/s of the work that symmetry leaves;
+// 768 x 2304, 768 x 768, 768 x 3072 and 3072 x 768 together 0.22 ms; 512 x 512 0.10 ms.)
+// Halving the inner dimension between two blocks of a cluster where tiles are few was
+// slower below 768 x 3072 (512 x 512 110 us) and 2 to 6 % faster above: not kept.
+template <int kN, int kPair, int kMats>
 __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_constant__ GemmParams<kMats> p) {
-  using T = Tile<kN, kPair, kSplit>;
+  using T = Tile<kN, kPair>;
   extern __shared__ unsigned char raw[];
   __shared__ __align__(8) uint64_t full_bar[T::kStages], empty_bar[T::kStages], done_bar[2], free_bar[2];
   __shared__ __align__(8) uint64_t in_bar[2], out_bar[2];     // a set of slots: `in` has come; the result has left
-  __shared__ __align__(8) uint64_t shared_bar, taken_bar;     // kSplit: sums have come from, were taken by the other block
   __shared__ uint32_t tmem_slot;
   __shared__ int stop;
   __shared__ float squares[2][kEpilogueWarps];
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
-  const uint32_t slots = smem + T::kStages * T::kStageBytes, share = slots + kSlots * kSlotBytes;
-  const int rank = T::kCluster == 2 ? static_cast<int>(block_rank()) : 0;
-  const int pair_rank = kPair == 2 ? rank : 0;
+  const uint32_t slots = smem + T::kStages * T::kStageBytes;
+  const int rank = kPair == 2 ? static_cast<int>(block_rank()) : 0;
   // Tiles go round the clusters forwards, then backwards, and so on: they are sorted by
   // length, so who had a long one in one round gets a short one in the next.
-  const int cluster = blockIdx.x / T::kCluster, clusters = gridDim.x / T::kCluster;
+  const int cluster = blockIdx.x / kPair, clusters = gridDim.x / kPair;
   const auto tile_of = [=](int turn) { return turn * clusters + (turn & 1 ? clusters - 1 - cluster : cluster); };
   const Guard guard{&stop, p.status, kWaitLimitNs};
   if (threadIdx.x == 0) {
@@ -541,8 +534,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
       bar_init(smem_addr(&in_bar[b]), 1);
       bar_init(smem_addr(&out_bar[b]), kEpilogueWarps);
     }
-    bar_init(smem_addr(&shared_bar), 1);
-    bar_init(smem_addr(&taken_bar), kEpilogueWarps);
     stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -553,7 +544,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
   }
   fence_before();
   __syncthreads();
-  if constexpr (T::kCluster == 2) cluster_sync();
+  if constexpr (kPair == 2) cluster_sync();
   fence_after();
   const uint32_t tmem = tmem_slot;
   // The previous kernel's results: each role waits for them right before its first
@@ -562,18 +553,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
   asm volatile("griddepcontrol.launch_dependents;");
   const auto await_inputs = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
 
-  // this block's steps of the inner dimension, over all terms: [lo, hi)
-  const auto steps_of = [&](const GemmMat& g, int* lo, int* hi) {
-    const int all = (g.k + kTileK - 1) / kTileK * p.terms;
-    *lo = kSplit == 2 ? all * rank / 2 : 0;
-    *hi = kSplit == 2 ? all * (rank + 1) / 2 : all;
-  };
   // sets of slots: a chunk needs hi and lo, or a part and its mirror image, or all four
   const int sets = p.terms == 3 && p.kind != kUpdate ? 1 : 2;
   const uint32_t set_bytes = sets == 1 ? kSlots * kSlotBytes : 2 * kSlotBytes;
   // whether this block finishes the chunk of a tile
-  const auto has_chunk = [&](const GemmMat& g, int block, int col0, int c) {
-    return !(col0 >= g.n || block * 128 >= g.m || (g.symmetric && col0 / 128 > block) || (kSplit == 2 && c != rank));
+  const auto has_chunk = [&](const GemmMat& g, int block, int col0) {
+    return !(col0 >= g.n || block * 128 >= g.m || (g.symmetric && col0 / 128 > block));
   };
 
   if (warp == 0) {  // producer: this block's rows of both operands
@@ -581,14 +566,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     uint32_t it = 0;
     bool ok = true;
     for (int turn = 0, t = tile_of(0); ok && t < p.tiles; t = tile_of(++turn)) {
-      int i, j, lo, hi;
+      int i, j;
       const GemmMat& g = tiles.at(t, &i, &j);
-      steps_of(g, &lo, &hi);
       const int blocks = (g.k + kTileK - 1) / kTileK;
-      const int row0 = i * T::kM + pair_rank * 128, col0 = j * kN + pair_rank * T::kBRows;
-      int term = lo / blocks, kb = lo - term * blocks;
+      const int row0 = i * T::kM + rank * 128, col0 = j * kN + rank * T::kBRows;
+      int term = 0, kb = 0;
       const bool p_mn = g.p_mn, q_mn = g.q_mn;
-      for (int step = lo; step < hi; ++step, ++it) {
+      for (int step = 0; step < blocks * p.terms; ++step, ++it) {
         const CUtensorMap* mp = &g.p[term == 1 ? 1 : 0];
         const CUtensorMap* mq = &g.q[term == 2 ? 1 : 0];
         const int s = it % T::kStages;
@@ -599,7 +583,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
         const uint32_t a = smem + s * T::kStageBytes, b = a + T::kABytes;
         if (it == 0) await_inputs();
         if (elect_one()) {
-          if (pair_rank == 0) bar_expect(own, T::kStageBytes * kPair);
+          if (rank == 0) bar_expect(own, T::kStageBytes * kPair);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const int r = row0 + 64 * q;
@@ -618,17 +602,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     // every copy lands (its stage is used and released) before the block ends
     for (uint32_t back = 1; back <= T::kStages && back <= it; ++back) {
       const uint32_t last = it - back;
-      const uint64_t* bar = pair_rank == 0 ? full_bar : empty_bar;
+      const uint64_t* bar = rank == 0 ? full_bar : empty_bar;
       bar_drain(smem_addr(&bar[last % T::kStages]), (last / T::kStages) & 1u, kWaitLimitNs);
     }
-  } else if (warp == 1 && pair_rank == 0) {  // products, for both blocks of a pair
+  } else if (warp == 1 && rank == 0) {  // products, for both blocks of a pair
     Tiles<T, GemmParams<kMats>> tiles{p};
     uint32_t it = 0, n = 0;
     bool ok = true;
     for (int t = tile_of(0); ok && t < p.tiles; t = tile_of(++n)) {
-      int i, j, lo, hi;
+      int i, j;
       const GemmMat& g = tiles.at(t, &i, &j);
-      steps_of(g, &lo, &hi);
+      const int steps = (g.k + kTileK - 1) / kTileK * p.terms;
       const uint32_t buf = n & 1u, d = tmem + buf * kN;
       ok = bar_wait_warp(smem_addr(&free_bar[buf]), ((n >> 1) & 1u) ^ 1u, guard);
       if (!ok) break;
@@ -637,7 +621,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
       // bytes from one 16-deep product's operand to the next, and between blocks of 64 rows
       const uint32_t a_step = g.p_mn ? 2048 : 32, b_step = g.q_mn ? 2048 : 32;
       const uint32_t a_block = g.p_mn ? 8192 : 0, b_block = g.q_mn ? 8192 : 0;
-      for (int step = lo; step < hi; ++step, ++it) {
+      for (int step = 0; step < steps; ++step, ++it) {
         const int s = it % T::kStages;
         ok = bar_wait_warp(smem_addr(&full_bar[s]), (it / T::kStages) & 1u, guard);
         if (!ok) break;
@@ -647,7 +631,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
         if (elect_one()) {
 #pragma unroll
           for (int q = 0; q < kTileK / 16; ++q)
-            mma<kPair>(d, da + (q * a_step >> 4), db + (q * b_step >> 4), kind, step > lo || q > 0);
+            mma<kPair>(d, da + (q * a_step >> 4), db + (q * b_step >> 4), kind, step > 0 || q > 0);
           mma_commit<kPair>(smem_addr(&empty_bar[s]));
         }
         __syncwarp();
@@ -665,11 +649,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     for (int turn = 0, t = tile_of(0); ok && t < p.tiles; t = tile_of(++turn)) {
       int i, j;
       const GemmMat& g = tiles.at(t, &i, &j);
-      const int block = i * kPair + pair_rank;
+      const int block = i * kPair + rank;
       const CUtensorMap* in = g.in_q ? g.q : g.p;
       for (int c = 0; c < kN / kChunk; ++c) {
         const int col0 = j * kN + c * kChunk;
-        if (!has_chunk(g, block, col0, c)) continue;
+        if (!has_chunk(g, block, col0)) continue;
         const uint32_t set = e % sets, bar = smem_addr(&in_bar[set]), to = slots + set * set_bytes;
         ok = bar_wait_warp(smem_addr(&out_bar[set]), ((e / sets) & 1u) ^ 1u, guard);
         if (!ok) break;
@@ -691,7 +675,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     const int own = warp - 4, quarter = own & 3, half = own >> 2;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const bool leader = own == 0 && lane == 0;
     await_inputs();
     uint32_t n = 0, e = 0, left = 0;            // tiles, chunks, chunks whose slots this warp has released
     // a wait of this thread ran out; some thread's did (the same for all, known at the next barrier)
@@ -699,9 +682,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     int known = -1, side = 0;                   // the matrix whose m is `shift`; the set of sums in use
     float shift = 0.0f;
     for (int t = tile_of(0); !failed && t < p.tiles; t = tile_of(++n)) {
-      int i, j, lo, hi;
+      int i, j;
       const GemmMat& g = tiles.at(t, &i, &j);
-      steps_of(g, &lo, &hi);
       if (known != tiles.mat) {  // its m, from all blocks' sums in a fixed order
         known = tiles.mat;
         shift = 0.0f;
@@ -724,44 +706,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
       }
       const float alpha = p.kind == kGram ? kScaleA / (kScaleX * kScaleX) : p.kind == kPoly ? p.c / kScaleA : 1.0f / kScaleA;
       const float beta = p.kind == kPoly ? p.b + 2.0f * p.c * shift : p.a + p.b * shift + p.c * shift * shift;
-      const int block = i * kPair + pair_rank;  // in rows of 128, as col0 / 128 in columns
+      const int block = i * kPair + rank;  // in rows of 128, as col0 / 128 in columns
       const uint32_t buf = n & 1u;
       lost |= !bar_wait(smem_addr(&done_bar[buf]), (n >> 1) & 1u, guard);
       fence_after();
-      const auto sums = [&](int c, float (&v)[32]) {
-        __syncwarp();
-        tmem_load32(lanes + buf * kN + c * kChunk + half * 32, v);
-        if (kSplit == 2 && lo == hi) {  // no step of this tile was this block's
-#pragma unroll
-          for (int q = 0; q < 32; ++q) v[q] = 0.0f;
-        }
-      };
-      if constexpr (kSplit == 2) {  // the other block's chunk
-        float v[32];
-        sums(1 - rank, v);
-        lost |= !bar_wait_cluster(smem_addr(&taken_bar), (n & 1u) ^ 1u, guard);
-        if (leader) bar_expect(smem_addr(&shared_bar), kShareBytes);  // what comes the other way
-        const uint32_t to = in_block(share, 1 - rank), bar = in_block(smem_addr(&shared_bar), 1 - rank);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) store_async(to + ((half * 8 + q) * 128 + row) * 16, &v[4 * q], bar);
-      }
-      bool any = false;
       for (int c = 0; c < kN / kChunk; ++c) {
         const int col0 = j * kN + c * kChunk;
-        if (!has_chunk(g, block, col0, c)) continue;
-        any = true;
+        if (!has_chunk(g, block, col0)) continue;
         const uint32_t set = e % sets, base = slots + set * set_bytes;
         float v[32];
-        sums(c, v);
-        if constexpr (kSplit == 2) {
-          lost |= !bar_wait_cluster(smem_addr(&shared_bar), n & 1u, guard);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint4 w = shared_load(share + ((half * 8 + q) * 128 + row) * 16);
-            v[4 * q] += __uint_as_float(w.x), v[4 * q + 1] += __uint_as_float(w.y);
-            v[4 * q + 2] += __uint_as_float(w.z), v[4 * q + 3] += __uint_as_float(w.w);
-          }
-        }
+        __syncwarp();
+        tmem_load32(lanes + buf * kN + c * kChunk + half * 32, v);
 #pragma unroll
         for (int q = 0; q < 32; ++q) v[q] *= alpha;
         if (p.kind == kGram) {
@@ -850,14 +805,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
         }
         ++e;
       }
-      if (kSplit == 2 && !any && !failed) {  // nothing to finish: what came is let go
-        lost |= !bar_wait_cluster(smem_addr(&shared_bar), n & 1u, guard);
-        failed = named_or(1, 32 * kEpilogueWarps, lost);
-      }
-      if constexpr (kSplit == 2) {
-        __syncwarp();
-        if (lane == 0) bar_arrive_cluster(in_block(smem_addr(&taken_bar), 1 - rank));
-      }
       fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -872,7 +819,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
   __syncwarp();
   fence_before();
   __syncthreads();
-  if constexpr (T::kCluster == 2) cluster_sync();  // neither block leaves while the other may signal it
+  if constexpr (kPair == 2) cluster_sync();  // neither block leaves while the other may signal it
   fence_after();
   if (warp == 1) tmem_free<kPair>(tmem, T::kTmemCols);
 }
@@ -884,7 +831,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
 // of A (then of P, in the same place) as 128-byte-swizzled operand tiles, the
 // products in tensor memory, the short side's rows on its lanes. The three products
 // of a step follow one another, so it is bound by their latency, about 1 us each
-// with the passes between them (16 x 16: 13 us for 5 steps, 64 x 32 18, 128 x 128 42,
+// with the passes between them (16 x 16: 15 us for 5 steps, 64 x 32 18, 128 x 128 42,
 // 100 x 300 69 us, whatever the number of matrices up to one for each SM). Tall
 // matrices are transposed as they are read.
 constexpr int kSmallSide = 128;
@@ -1136,11 +1083,12 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
       tmem_load32(lanes + c, v);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
+        if (q >= n) continue;
         float old[8];
         if (kOld) sum_of(hi[q], lo[q], old);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[8 * q + e] = kOld ? beta * old[e] + alpha * v[8 * q + e] : alpha * v[8 * q + e];
-        if (q < n) put(&v[8 * q], reinterpret_cast<uint4*>(at[q]), reinterpret_cast<uint4*>(at[q] + part));
+        put(&v[8 * q], reinterpret_cast<uint4*>(at[q]), reinterpret_cast<uint4*>(at[q] + part));
       }
     }
   };
@@ -1239,14 +1187,6 @@ bool is_small(const NsJob& j) {
   if (std::min(j.rows, j.cols) > kSmallSide || std::max(j.rows, j.cols) > kSmallBytes) return false;
   return SmallShape(static_cast<int>(j.rows), static_cast<int>(j.cols)).bytes() <= kSmallBytes;
 }
-
-// Matrices whose Gram products are shared by two blocks a tile: those with so few
-// tiles (66 or fewer of 128 x 128) that two blocks for each still run at once (5 steps of
-// 1024 x 4096: 267 -> 236 us, of 768 x 2304 and company 257 -> 239, of 512 x 512 114 -> 123:
-// there is no saving in a short inner dimension). It
-// goes by the matrix alone, not by its company, so that a matrix gives the same
-// bits in every call.
-bool splits(const NsJob& j) { return std::min(j.rows, j.cols) <= 1408; }
 
 int parts_of(const NsJob& j) {
   const int64_t units = j.rows * ((j.cols + kUnit - 1) / kUnit);
@@ -1349,25 +1289,25 @@ int launch_after(K kernel, int grid, int cluster, int threads, int smem, cudaStr
 }
 
 // How many clusters of the kernel run at once (looked up once per device).
-template <int kN, int kPair, int kSplit, int kMats>
+template <int kN, int kPair, int kMats>
 int resident_clusters(const Device& dev) {
-  using T = Tile<kN, kPair, kSplit>;
+  using T = Tile<kN, kPair>;
   static std::atomic<int> cached[64];
   if (dev.id >= 64) return 0;
   int n = cached[dev.id].load(std::memory_order_acquire);
   if (n) return n;
-  const auto kernel = ns_product<kN, kPair, kSplit, kMats>;
+  const auto kernel = ns_product<kN, kPair, kMats>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess) return 0;
-  if (T::kCluster == 1) {
+  if (kPair == 1) {
     n = dev.sms;
   } else {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(dev.sms / T::kCluster * T::kCluster);
+    cfg.gridDim = dim3(dev.sms / kPair * kPair);
     cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = T::kSmemBytes;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = T::kCluster;
+    attr[0].val.clusterDim.x = kPair;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -1377,9 +1317,9 @@ int resident_clusters(const Device& dev) {
   return n;
 }
 
-template <int kN, int kPair, int kSplit, int kMats>
+template <int kN, int kPair, int kMats>
 int launch_product(GemmParams<kMats>& p, const Device& dev, cudaStream_t stream) {
-  using T = Tile<kN, kPair, kSplit>;
+  using T = Tile<kN, kPair>;
   p.tiles = 0;
   for (int i = 0; i < p.count; ++i) {
     GemmMat& g = p.mat[i];
@@ -1392,10 +1332,10 @@ int launch_product(GemmParams<kMats>& p, const Device& dev, cudaStream_t stream)
     }
     p.tiles += g.tiles;
   }
-  const int room = resident_clusters<kN, kPair, kSplit, kMats>(dev);
+  const int room = resident_clusters<kN, kPair, kMats>(dev);
   if (room < 1) return FSDP_ECUDA;
-  return launch_after(ns_product<kN, kPair, kSplit, kMats>, std::min(p.tiles, room) * T::kCluster, T::kCluster,
-                      kGemmThreads, T::kSmemBytes, stream, p);
+  return launch_after(ns_product<kN, kPair, kMats>, std::min(p.tiles, room) * kPair, kPair, kGemmThreads, T::kSmemBytes,
+                      stream, p);
 }
 
 int launch_momentum(const MomentumParams& p, int blocks, cudaStream_t stream) {
@@ -1435,25 +1375,25 @@ int run_small(const NsJob* const* jobs, int count, const NsPlan& plan, const NsM
 }
 
 // Estimated times, in microseconds, of a launch of `tiles` tiles of `steps` steps of 64
-// of the inner dimension. Measured on GB300: a step of a 256 x 256 tile takes a pair 0.36 (93 %
-// of the measured cuBLAS rate), one of a 128 x 128 tile takes a block 0.33 (bound by
-// L2: 32 KB of operands for a quarter of the products); a tile's results leave in
-// 7.5 and 1.6, while the next tile's products run, the last one's after them.
-// All of a GPT-2 block's matrices (updates of 12 steps): 267 us with pairs, 238 with single
-// blocks; 4096 x 4096 (64 steps) 1425 and 1657 us.
+// of the inner dimension. Measured on GB300: a step of a 256 x 256 tile takes a pair 0.33 to
+// 0.36, one of a 128 x 128 tile takes a block 0.28; a tile's results leave in 9 and 2.5
+// beside the next tile's products, and the last one's in 11 and 2.5 after them.
+// All steps of a GPT-2 block's matrices with pairs for the updates (12 steps each) 253 us,
+// with single blocks 217; of 4096 x 4096 (64 steps) 1008 with pairs, 1233 with single blocks for the
+// updates.
 double pair_time(int64_t tiles, int steps, int sms) {
   const double rounds = static_cast<double>((tiles + sms / 2 - 1) / (sms / 2));
-  return rounds * std::max(0.36 * steps, 7.5) + 7.5;
+  return rounds * std::max(0.34 * steps, 9.0) + 11.0;
 }
 double block_time(int64_t tiles, int steps, int sms) {
   const double rounds = static_cast<double>((tiles + sms - 1) / sms);
-  return rounds * std::max(0.33 * steps, 1.6) + 1.6;
+  return rounds * std::max(0.28 * steps, 2.5) + 2.5;
 }
 
 // One launch's matrices through all steps.
 template <int kMats>
-int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms, bool split,
-              const NsMomentum* momentum, const NsApply* apply, unsigned char* workspace, const Device& dev, cudaStream_t stream) {
+int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms, const NsMomentum* momentum,
+              const NsApply* apply, unsigned char* workspace, const Device& dev, cudaStream_t stream) {
   static thread_local MomentumParams first;
   PassParams& pass = first.pass;
   static thread_local GemmParams<kMats> p;
@@ -1545,12 +1485,11 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
       p.a = plan.coef[3 * s];
       p.b = plan.coef[3 * s + 1];
       p.c = plan.coef[3 * s + 2];
-      // pairs of blocks on 256 x 256 tiles, or single ones on 128 x 128 (the same sums in the
-      // same order), whichever is estimated faster; or two blocks a tile (see splits())
+      // pairs of blocks on 256 x 256 tiles, or single ones on 128 x 128, whichever is estimated
+      // faster: the sums and their order are the same, so that a matrix gives the same bits in
+      // any company
       const bool pairs = pair_time(large_tiles, steps, dev.sms) < block_time(small_tiles, steps, dev.sms);
-      const int rc = split && kind == kGram ? launch_product<128, 1, 2>(p, dev, stream)
-                     : pairs                ? launch_product<256, 2, 1>(p, dev, stream)
-                                            : launch_product<128, 1, 1>(p, dev, stream);
+      const int rc = pairs ? launch_product<256, 2>(p, dev, stream) : launch_product<128, 1>(p, dev, stream);
       if (rc != FSDP_OK) return rc;
     }
   }
@@ -1616,12 +1555,10 @@ int ns_run(const std::vector<NsJob>& jobs, const NsPlan& plan, const NsMomentum*
     const int count = static_cast<int>(std::min<size_t>(kSmallMats, small.size() - at));
     if (int rc = run_small(&small[at], count, plan, momentum, apply, dev, stream)) return rc;
   }
-  for (int kind = 0; kind < 4; ++kind) {
-    const int terms = kind & 1 ? 3 : 1;
-    const bool split = kind & 2;
+  for (int terms : {1, 3}) {
     std::vector<const NsJob*> group;
     for (const NsJob& j : jobs)
-      if (!is_small(j) && terms_of(j, plan) == terms && splits(j) == split) group.push_back(&j);
+      if (!is_small(j) && terms_of(j, plan) == terms) group.push_back(&j);
     // the tiles that take longest first, so that the short ones fill up the end
     std::stable_sort(group.begin(), group.end(), [](const NsJob* a, const NsJob* b) {
       return std::max(a->rows, a->cols) > std::max(b->rows, b->cols);
@@ -1629,8 +1566,8 @@ int ns_run(const std::vector<NsJob>& jobs, const NsPlan& plan, const NsMomentum*
     for (size_t at = 0; at < group.size(); at += kMaxMats) {
       const int count = static_cast<int>(std::min<size_t>(kMaxMats, group.size() - at));
       const int rc = count <= 8
-                         ? run_group<8>(&group[at], count, plan, terms, split, momentum, apply, base, dev, stream)
-                         : run_group<kMaxMats>(&group[at], count, plan, terms, split, momentum, apply, base, dev, stream);
+                         ? run_group<8>(&group[at], count, plan, terms, momentum, apply, base, dev, stream)
+                         : run_group<kMaxMats>(&group[at], count, plan, terms, momentum, apply, base, dev, stream);
       if (rc != FSDP_OK) return rc;
       for (int i = 0; i < count; ++i) base += carve(*group[at + i], plan, nullptr, nullptr);
     }

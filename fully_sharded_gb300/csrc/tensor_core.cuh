@@ -74,27 +74,6 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
-// As bar_wait, for data that another block of the cluster wrote.
-__device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity, const Guard& g) {
-  const uint64_t t0 = clock_ns();
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, "
-        "p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (*g.stop) return false;
-    if (clock_ns() - t0 > g.limit_ns) {
-      *g.stop = 1;
-      atomicOr(g.status, 1u);
-      return false;
-    }
-  }
-}
-
 // A wait for copies or products already issued, after a stop too (bounded again).
 __device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = clock_ns();
@@ -169,14 +148,6 @@ __device__ __forceinline__ bool named_or(int id, int threads, bool flag) {
       : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(flag))
       : "memory");
   return any != 0;
-}
-// 16 bytes into another block's shared memory, counted there by that block's barrier `bar`.
-__device__ __forceinline__ void store_async(uint32_t addr, const float* v, uint32_t bar) {
-  asm volatile(
-      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
-      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
-      "r"(bar)
-      : "memory");
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
