@@ -404,7 +404,8 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kWi
       const int groups = kQuant == 1 ? 1 : (all + p.a.group - 1) >> p.group_bits;
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
-        if constexpr (kQuant == 2) most = group_max(top[k], p.a.group / 8);
+        // a row of 8 or 16 lanes can be shorter than its group: the lanes after it are another row's
+        if constexpr (kQuant == 2) most = group_max(top[k], min(p.a.group / 8, r.n));
         const float scale = scale_of(most * rstd);
         const int j = place<kMap>(r, k, 0);
         if (kQuant == 1 ? (k == 0 && r.t == 0 && cols > 0) : (j < cols && (j & (p.a.group - 1)) == 0))

@@ -112,6 +112,38 @@ def test_forward_8bit(rows, cols, group, dtype):
     assert untouched(whole, y)
 
 
+@pytest.mark.parametrize("rows,cols", [(600, 8), (600, 40), (521, 64), (513, 65), (1100, 100), (600, 128), (515, 129), (530, 769), (600, 1024),
+                                       (1100, 2000), (700, 4104)])
+@pytest.mark.parametrize("group", [0, 32, 64, 128, 256])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_forward_8bit_of_many_rows(rows, cols, group, dtype):
+    """Rows that share a warp or a block keep their own scales: each is of another size than its neighbours."""
+    gen = torch.Generator(device="cuda").manual_seed(rows + cols + group)
+    x = rand(gen, rows, cols, dtype=dtype)
+    x[:, 0] = 0.5
+    x[1::3] = 0  # rows of zeros, whose scale is the smallest
+    x[2::3, 1:] = 0  # and rows of a single value, whose scale is the largest
+    gain = rand(gen, cols, dtype=F32) + 2
+    whole, y = guarded(rows, cols, E4M3)
+    scales = torch.empty(rows, -(-cols // group) if group else 1, device="cuda")
+    fs.fsdp_rmsnorm(x, gain, y, scales=scales, group=group)
+    check_8bit(y, scales, want_forward(x, None, gain, 1e-6)[2], group)
+    assert untouched(whole, y)
+
+
+@pytest.mark.parametrize("rows,cols", [(513, 65), (600, 100), (1000, 128), (700, 129)])
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_forward_and_backward_of_many_short_rows(rows, cols, dtype):
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    x, residual, gain = rand(gen, rows, cols, dtype=dtype), rand(gen, rows, cols, dtype=dtype), rand(gen, cols, dtype=F32)
+    whole, y = guarded(rows, cols, dtype)
+    h = torch.empty_like(x)
+    fs.fsdp_rmsnorm(x, gain, y, residual=residual, h_out=h)
+    check_y(y, want_forward(x, residual, gain, 1e-6)[2], cols)
+    assert torch.equal(h, (x.float() + residual.float()).to(dtype)) and untouched(whole, y)
+    check_backward(rand(gen, rows, cols, dtype=dtype), h, gain, residual)
+
+
 @pytest.mark.parametrize("cols,stride,offset", [(768, 1024, 0), (768, 769, 1), (100, 104, 3), (4096, 4104, 4), (1000, 1001, 0)])
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 def test_forward_strides_and_offsets(cols, stride, offset, dtype):
