@@ -24,6 +24,13 @@
 // P' is several times smaller than P, and so is the part of X' that comes from rounded
 // operands (error of a 768 x 2304 matrix 1.5e-3 -> 0.5e-3 of its norm).
 //
+// Long Gram products are cut into segments. The tensor cores' sums are cut off, not
+// rounded, at each addition, so a sum's error grows with the number of steps (measured:
+// 7e-9 of the result per element of the long side and term; 12 % at 16.8 M). Where a
+// product has more than 256 steps of 64, blocks take segments of it, and a pass adds
+// the segments' fp32 results in order (1 x 16.8 M: 6e-5, and 757 -> 26 ms; 300 x 262144: 6e-5,
+// 5.7 -> 1.6 ms; 50257 x 768 0.8 ms).
+//
 // Each of the three products is one launch over all matrices of the call: a
 // persistent grid of tiles; in each block a producer lane (TMA), a product lane
 // (tcgen05, two accumulators in tensor memory), a lane that fetches what the result
@@ -297,6 +304,10 @@ struct GemmMat {
   const float* squares;    // sums of squares of X over 32 x 32 blocks (null: X_0, no shift)
   float* new_squares;      // those of the next X
   int32_t squares_count;
+  int32_t splits, seg_blocks;  // a long Gram product's segments (0: it is whole) and their length in steps of 64
+  float* partial;              // their results, each a square of `square_of(n)` rows
+  __half* joined[2];           // where their sum goes: hi, lo (null: not kept)
+  int64_t joined_ld;
   uint16_t* out;
   int64_t out_stride;
   int64_t flat;
@@ -341,20 +352,27 @@ struct Tile {
   }
 };
 
+__host__ __device__ constexpr int square_of(int side) { return (side + 31) / 32 * 32; }
+
 // Tile t of a launch: its matrix and place. Calls come with growing t.
-template <typename T, typename P>
+template <typename T, typename P, bool kLong = false>
 struct Tiles {
   const P& p;
-  int mat = 0, first = 0;
+  int mat = 0, first = 0, split = 0;
   int row = 0, base = 0;  // symmetric: the current row of tiles and its first tile
 
   __device__ __forceinline__ const GemmMat& at(int t, int* i, int* j) {
     while (t - first >= p.mat[mat].tiles) {
       first += p.mat[mat++].tiles;
-      row = base = 0;
+      row = base = split = 0;
     }
     const GemmMat& g = p.mat[mat];
-    const int l = t - first;
+    int l = t - first;
+    if constexpr (kLong) {  // one segment's tiles after another's
+      const int each = g.tiles / g.splits, s = l / each;
+      if (s != split) split = s, row = base = 0;
+      l -= s * each;
+    }
     if (!g.symmetric) {
       // along the short side first: the tiles at work share the long operand's rows or
       // columns and the whole of the short one, which stays in L2
@@ -489,7 +507,8 @@ __device__ __forceinline__ void finish_rows(const GemmMat& g, const NsApply& ap,
   }
 }
 
-// One of the three products over all matrices of a launch; which tile by pair_time() and
+// One of the three products over all matrices of a launch (kLong: segments of the long Gram
+// products, left as fp32 for ns_join); which tile by pair_time() and
 // block_time() below. What bounds it, by size (measured on GB300):
 //   - long sides from 2048 on: the tensor cores under the power cap. A step of 64 of a 256 x
 //     256 tile takes 0.33 us at first, 2.0 PFLOP/s over 76 pairs; a long run of such launches
@@ -505,7 +524,7 @@ __device__ __forceinline__ void finish_rows(const GemmMat& g, const NsApply& ap,
 // 768 x 2304, 768 x 768, 768 x 3072 and 3072 x 768 together 0.22 ms; 512 x 512 0.10 ms.)
 // Halving the inner dimension between two blocks of a cluster where tiles are few was
 // slower below 768 x 3072 (512 x 512 110 us) and 2 to 6 % faster above: not kept.
-template <int kN, int kPair, int kMats>
+template <int kN, int kPair, int kMats, bool kLong>
 __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_constant__ GemmParams<kMats> p) {
   using T = Tile<kN, kPair>;
   extern __shared__ unsigned char raw[];
@@ -556,19 +575,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
   // sets of slots: a chunk needs hi and lo, or a part and its mirror image, or all four
   const int sets = p.terms == 3 && p.kind != kUpdate ? 1 : 2;
   const uint32_t set_bytes = sets == 1 ? kSlots * kSlotBytes : 2 * kSlotBytes;
+  // steps of a tile's inner dimension from step `from` on
+  const auto inner = [&](const GemmMat& g, int split, int* from) {
+    const int blocks = (g.k + kTileK - 1) / kTileK;
+    *from = kLong ? split * g.seg_blocks : 0;
+    return kLong ? min(g.seg_blocks, blocks - *from) : blocks;
+  };
   // whether this block finishes the chunk of a tile
   const auto has_chunk = [&](const GemmMat& g, int block, int col0) {
     return !(col0 >= g.n || block * 128 >= g.m || (g.symmetric && col0 / 128 > block));
   };
 
   if (warp == 0) {  // producer: this block's rows of both operands
-    Tiles<T, GemmParams<kMats>> tiles{p};
+    Tiles<T, GemmParams<kMats>, kLong> tiles{p};
     uint32_t it = 0;
     bool ok = true;
     for (int turn = 0, t = tile_of(0); ok && t < p.tiles; t = tile_of(++turn)) {
       int i, j;
       const GemmMat& g = tiles.at(t, &i, &j);
-      const int blocks = (g.k + kTileK - 1) / kTileK;
+      int from;
+      const int blocks = inner(g, tiles.split, &from);
       const int row0 = i * T::kM + rank * 128, col0 = j * kN + rank * T::kBRows;
       int term = 0, kb = 0;
       const bool p_mn = g.p_mn, q_mn = g.q_mn;
@@ -587,12 +613,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const int r = row0 + 64 * q;
-            tma_box<kPair>(a + q * 8192, mp, p_mn ? r : kb * kTileK, p_mn ? kb * kTileK : r, bar);
+            tma_box<kPair>(a + q * 8192, mp, p_mn ? r : (from + kb) * kTileK, p_mn ? (from + kb) * kTileK : r, bar);
           }
 #pragma unroll
           for (int q = 0; q < T::kBRows / 64; ++q) {
             const int c = col0 + 64 * q;
-            tma_box<kPair>(b + q * 8192, mq, q_mn ? c : kb * kTileK, q_mn ? kb * kTileK : c, bar);
+            tma_box<kPair>(b + q * 8192, mq, q_mn ? c : (from + kb) * kTileK, q_mn ? (from + kb) * kTileK : c, bar);
           }
         }
         __syncwarp();
@@ -606,13 +632,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
       bar_drain(smem_addr(&bar[last % T::kStages]), (last / T::kStages) & 1u, kWaitLimitNs);
     }
   } else if (warp == 1 && rank == 0) {  // products, for both blocks of a pair
-    Tiles<T, GemmParams<kMats>> tiles{p};
+    Tiles<T, GemmParams<kMats>, kLong> tiles{p};
     uint32_t it = 0, n = 0;
     bool ok = true;
     for (int t = tile_of(0); ok && t < p.tiles; t = tile_of(++n)) {
       int i, j;
       const GemmMat& g = tiles.at(t, &i, &j);
-      const int steps = (g.k + kTileK - 1) / kTileK * p.terms;
+      int from;
+      const int steps = inner(g, tiles.split, &from) * p.terms;
       const uint32_t buf = n & 1u, d = tmem + buf * kN;
       ok = bar_wait_warp(smem_addr(&free_bar[buf]), ((n >> 1) & 1u) ^ 1u, guard);
       if (!ok) break;
@@ -642,7 +669,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     if (!ok && it > 0)  // products in flight end before the accumulators are freed
       bar_drain(smem_addr(&empty_bar[(it - 1) % T::kStages]), ((it - 1) / T::kStages) & 1u, kWaitLimitNs);
   } else if (warp == 2 && p.kind != kGram) {  // fetch of `in`, ahead of the epilogue
-    Tiles<T, GemmParams<kMats>> tiles{p};
+    Tiles<T, GemmParams<kMats>, kLong> tiles{p};
     const int parts = p.kind == kUpdate || p.terms == 3 ? 2 : 1;
     uint32_t e = 0;
     bool ok = true;
@@ -671,7 +698,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     for (uint32_t back = 1; back <= static_cast<uint32_t>(sets) && back <= e; ++back)
       bar_drain(smem_addr(&in_bar[(e - back) % sets]), ((e - back) / sets) & 1u, kWaitLimitNs);
   } else if (warp >= 4) {  // epilogue: this block's 128 rows
-    Tiles<T, GemmParams<kMats>> tiles{p};
+    Tiles<T, GemmParams<kMats>, kLong> tiles{p};
     const int own = warp - 4, quarter = own & 3, half = own >> 2;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -684,7 +711,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     for (int t = tile_of(0); !failed && t < p.tiles; t = tile_of(++n)) {
       int i, j;
       const GemmMat& g = tiles.at(t, &i, &j);
-      if (known != tiles.mat) {  // its m, from all blocks' sums in a fixed order
+      if (!kLong && known != tiles.mat) {  // its m, from all blocks' sums in a fixed order
         known = tiles.mat;
         shift = 0.0f;
         if (g.squares) {
@@ -710,7 +737,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
       const uint32_t buf = n & 1u;
       lost |= !bar_wait(smem_addr(&done_bar[buf]), (n >> 1) & 1u, guard);
       fence_after();
-      for (int c = 0; c < kN / kChunk; ++c) {
+      if constexpr (kLong) {
+        failed = named_or(1, 32 * kEpilogueWarps, lost);
+        const int64_t ld = square_of(g.n);
+        for (int c = 0; c < kN / kChunk && !failed; ++c) {
+          const int col0 = j * kN + c * kChunk + half * 32, row0 = block * 128 + quarter * 32;
+          if (col0 >= ld || row0 >= ld) continue;  // the same for the warp
+          float v[32];
+          __syncwarp();
+          tmem_load32(lanes + buf * kN + c * kChunk + half * 32, v);
+          float4* to = reinterpret_cast<float4*>(g.partial + (tiles.split * ld + row0 + lane) * ld + col0);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) to[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+      }
+      for (int c = 0; !kLong && c < kN / kChunk; ++c) {
         const int col0 = j * kN + c * kChunk;
         if (!has_chunk(g, block, col0)) continue;
         const uint32_t set = e % sets, base = slots + set * set_bytes;
@@ -824,6 +865,72 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
   if (warp == 1) tmem_free<kPair>(tmem, T::kTmemCols);
 }
 
+// The sum of the segments of the long Gram products: A (shifted, as two parts) from the fp32
+// results, a block of 32 x 32 on or below the diagonal and its mirror image per block of
+// threads. Bound by reading 4 bytes per element and segment.
+template <int kMats>
+__global__ void __launch_bounds__(32 * kEpilogueWarps) ns_join(const __grid_constant__ GemmParams<kMats> p) {
+  __shared__ uint32_t mirror[32][33];
+  __shared__ float squares[kEpilogueWarps];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int i = 0, b = blockIdx.x;
+  for (;; ++i) {
+    const int wide = square_of(p.mat[i].n) / 32, blocks = p.mat[i].splits ? wide * (wide + 1) / 2 : 0;
+    if (b < blocks) break;
+    b -= blocks;
+  }
+  const GemmMat& g = p.mat[i];
+  int bi = static_cast<int>((sqrtf(8.0f * b + 1.0f) - 1.0f) * 0.5f);
+  while (bi * (bi + 1) / 2 > b) --bi;
+  while ((bi + 1) * (bi + 2) / 2 <= b) ++bi;
+  const int bj = b - bi * (bi + 1) / 2, splits = g.splits, n = g.n;
+  const int64_t ld = square_of(n), next = ld * ld;
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float shift = 0.0f;
+  if (g.squares) {  // m, in the order of ns_product
+    float sum = 0.0f;
+    const int count = g.squares_count;
+#pragma unroll 8
+    for (int k = threadIdx.x; k < count; k += 32 * kEpilogueWarps) sum += g.squares[k];
+    sum = warp_sum(sum);
+    if (lane == 0) squares[warp] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kEpilogueWarps; ++k) sum += squares[k];
+    shift = sum / (kScaleX * kScaleX) / static_cast<float>(n);
+    if (shift < kShiftFrom) shift = 0.0f;
+  }
+  constexpr int kRows = 32 / kEpilogueWarps;
+  const float* from = g.partial + (bi * 32 + warp) * ld + bj * 32 + lane;
+  float v[kRows] = {};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s, from += next)
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) v[k] += from[k * kEpilogueWarps * ld];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int r = bi * 32 + warp + k * kEpilogueWarps, c = bj * 32 + lane;
+    v[k] = v[k] * (kScaleA / (kScaleX * kScaleX)) - (r == c ? shift * kScaleA : 0.0f);
+    const __half hi = __float2half_rn(v[k]), lo = __float2half_rn(v[k] - __half2float(hi));
+    mirror[warp + k * kEpilogueWarps][lane] = __half_as_ushort(hi) | static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
+    if (r >= n || c >= n) continue;
+    g.joined[0][r * g.joined_ld + c] = hi;
+    if (g.joined[1]) g.joined[1][r * g.joined_ld + c] = lo;
+  }
+  if (bi == bj) return;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int r = bj * 32 + warp + k * kEpilogueWarps, c = bi * 32 + lane;
+    if (r >= n || c >= n) continue;
+    const uint32_t two = mirror[lane][warp + k * kEpilogueWarps];
+    g.joined[0][r * g.joined_ld + c] = __ushort_as_half(static_cast<unsigned short>(two));
+    if (g.joined[1]) g.joined[1][r * g.joined_ld + c] = __ushort_as_half(static_cast<unsigned short>(two >> 16));
+  }
+}
+
 // ----------------------------------------------------------- small matrices
 
 // A matrix with a short side of at most 128 that fits the shared memory of one
@@ -912,7 +1019,7 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
   asm volatile("griddepcontrol.launch_dependents;");
   const int count = g.rows * g.cols;
   float squares = 0.0f;
-  if (p.applies) {  // u, written to where it is read again below by the same thread
+  if (p.applies) {  // u, written to where this block reads it again after the barrier below
     const NsMomentum& m = p.momentum;
     float* u = static_cast<float*>(const_cast<void*>(g.source));
     int64_t at = g.flat + threadIdx.x, rank = at / m.shard;
@@ -1194,11 +1301,25 @@ int parts_of(const NsJob& j) {
   return static_cast<int>(std::min<int64_t>(kMaxParts, (units + 2 * kPassWarps - 1) / (2 * kPassWarps)));
 }
 
+// The segments of a Gram product of more than 256 steps: at most 256 steps each, and as many as
+// give each of 152 SMs a tile, but for segments of less than 32 blocks of 64. (By the matrix alone, so that it gives
+// the same bits in any company.)
+struct Segments {
+  int splits = 0, blocks = 0;
+};
+Segments segments_of(const NsJob& j, int terms) {
+  const int64_t blocks = (std::max(j.rows, j.cols) + kTileK - 1) / kTileK;
+  if (blocks * terms <= 256) return {};
+  const int64_t rows = (std::min(j.rows, j.cols) + 127) / 128, tiles = rows * (rows + 1) / 2;
+  const int64_t each = std::min<int64_t>(256 / terms, std::max<int64_t>(32, (blocks * tiles + 151) / 152));
+  return {static_cast<int>((blocks + each - 1) / each), static_cast<int>(each)};
+}
+
 // A matrix's share of the workspace: X twice (read and written by turns) and A, P,
 // each as hi and, where it is used, lo part, rows a multiple of 128 bytes apart.
 struct Buffers {
   __half *x[2][2], *a[2], *poly[2];
-  float *partial, *squares[2];
+  float *partial, *squares[2], *segments;
   int64_t ld_x, ld_a;
   int64_t squares_count;
 };
@@ -1226,6 +1347,8 @@ int64_t carve(const NsJob& j, const NsPlan& plan, unsigned char* base, Buffers* 
   b.partial = reinterpret_cast<float*>(take(kMaxParts * 4));
   b.squares_count = (j.rows + 127) / 128 * 4 * (b.ld_x / 32);
   for (int k = 0; k < 2; ++k) b.squares[k] = reinterpret_cast<float*>(take(b.squares_count * 4));
+  const int64_t square = square_of(static_cast<int>(side));
+  b.segments = reinterpret_cast<float*>(take(segments_of(j, terms).splits * square * square * 4));
   if (out) *out = b;
   return at;
 }
@@ -1289,14 +1412,14 @@ int launch_after(K kernel, int grid, int cluster, int threads, int smem, cudaStr
 }
 
 // How many clusters of the kernel run at once (looked up once per device).
-template <int kN, int kPair, int kMats>
+template <int kN, int kPair, int kMats, bool kLong>
 int resident_clusters(const Device& dev) {
   using T = Tile<kN, kPair>;
   static std::atomic<int> cached[64];
   if (dev.id >= 64) return 0;
   int n = cached[dev.id].load(std::memory_order_acquire);
   if (n) return n;
-  const auto kernel = ns_product<kN, kPair, kMats>;
+  const auto kernel = ns_product<kN, kPair, kMats, kLong>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess) return 0;
   if (kPair == 1) {
     n = dev.sms;
@@ -1317,7 +1440,7 @@ int resident_clusters(const Device& dev) {
   return n;
 }
 
-template <int kN, int kPair, int kMats>
+template <int kN, int kPair, bool kLong = false, int kMats>
 int launch_product(GemmParams<kMats>& p, const Device& dev, cudaStream_t stream) {
   using T = Tile<kN, kPair>;
   p.tiles = 0;
@@ -1330,11 +1453,14 @@ int launch_product(GemmParams<kMats>& p, const Device& dev, cudaStream_t stream)
       g.tiles = 0;
       for (int r = 0; r < rows; ++r) g.tiles += T::below(r, g.col_tiles);
     }
+    if (kLong) g.tiles *= g.splits;
+    if (!kLong && g.splits) g.tiles = 0;
     p.tiles += g.tiles;
   }
-  const int room = resident_clusters<kN, kPair, kMats>(dev);
+  if (p.tiles == 0) return FSDP_OK;
+  const int room = resident_clusters<kN, kPair, kMats, kLong>(dev);
   if (room < 1) return FSDP_ECUDA;
-  return launch_after(ns_product<kN, kPair, kMats>, std::min(p.tiles, room) * kPair, kPair, kGemmThreads, T::kSmemBytes,
+  return launch_after(ns_product<kN, kPair, kMats, kLong>, std::min(p.tiles, room) * kPair, kPair, kGemmThreads, T::kSmemBytes,
                       stream, p);
 }
 
@@ -1438,7 +1564,7 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
     const int now = s & 1, next = now ^ 1;
     for (int kind = kGram; kind <= kUpdate; ++kind) {
       int64_t large_tiles = 0, small_tiles = 0;
-      int steps = 0;
+      int steps = 0, join_blocks = 0;
       for (int i = 0; i < count; ++i) {
         const NsJob& j = *jobs[i];
         const Buffers& b = buffers[i];
@@ -1453,12 +1579,25 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
         g.squares = s > 0 ? b.squares[now] : nullptr;
         g.new_squares = b.squares[next];
         g.squares_count = static_cast<int32_t>(b.squares_count);
+        g.splits = 0;
         if (kind == kGram) {
           use(g.p, q.x[now]);
           use(g.q, q.x[now]);
           use(g.result, q.a);
           g.k = static_cast<int32_t>(std::max(j.rows, j.cols));
           g.p_mn = g.q_mn = !wide;
+          const Segments cut = segments_of(j, terms);
+          g.splits = cut.splits;
+          g.seg_blocks = cut.blocks;
+          g.partial = b.segments;
+          g.joined[0] = b.a[0];
+          g.joined[1] = b.a[1];
+          g.joined_ld = b.ld_a;
+          if (g.splits) {
+            const int square = square_of(side) / 32;
+            join_blocks += square * (square + 1) / 2;
+            continue;
+          }
         } else if (kind == kPoly) {
           use(g.p, q.a);
           use(g.q, q.a);
@@ -1485,6 +1624,10 @@ int run_group(const NsJob* const* jobs, int count, const NsPlan& plan, int terms
       p.a = plan.coef[3 * s];
       p.b = plan.coef[3 * s + 1];
       p.c = plan.coef[3 * s + 2];
+      if (join_blocks) {
+        if (int rc = launch_product<128, 1, true>(p, dev, stream)) return rc;
+        if (int rc = launch_after(ns_join<kMats>, join_blocks, 1, 32 * kEpilogueWarps, 0, stream, p)) return rc;
+      }
       // pairs of blocks on 256 x 256 tiles, or single ones on 128 x 128, whichever is estimated
       // faster: the sums and their order are the same, so that a matrix gives the same bits in
       // any company

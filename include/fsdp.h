@@ -600,7 +600,9 @@ int fsdp_rmsnorm_backward_workspace(int64_t rows, int64_t cols, int64_t *bytes_o
  * scaled by powers of two; the error is below 0.3 % of the result's norm,
  * typically 0.03 to 0.1 %); 3: as two such parts each, three products (about 1e-5); 0: 3 where the
  * short side is below 256 and 1 otherwise. Between steps X is held as two fp16
- * parts, 22 bits; accumulation is fp32. */
+ * parts, 22 bits; accumulation is fp32, in segments of at most 16384 elements
+ * along a long side (1e-4 at the longest). |G|^2 is an fp32 sum: |G| has to be below 1e19, and
+ * with an eps below 1e-18 above that. */
 typedef struct {
   int32_t steps;              /* 1 .. 32 */
   int32_t terms;              /* 0, 1 or 3 */

@@ -75,6 +75,31 @@ def test_one_matrix(rows, cols, dtype):
     check(run([g])[0], reference(g), terms_of((rows, cols)))
 
 
+LONG = [(1, 5440), (1, 5441), (140, 6000), (6000, 140), (255, 20000), (33, 100003), (300, 16385), (16400, 300), (1100, 17000),
+        (1 << 20, 8), (7, 262147)]
+
+
+@pytest.mark.parametrize("rows,cols", LONG)
+def test_long_inner_dimension(rows, cols):
+    """Products cut into segments: the same precision whatever the length."""
+    g = gauss(rows + cols, rows, cols)
+    check(run([g])[0], reference(g), terms_of((rows, cols)))
+
+
+def test_long_inner_dimension_of_one_sign():
+    g = 1 + 0.1 * gauss(8, 1, 1 << 22)
+    check(run([g])[0], reference(g), 3)
+
+
+def test_long_and_short_together():
+    sources = [gauss(i, r, c) for i, (r, c) in enumerate(LONG[:9] + [(300, 400), (140, 600), (16, 20)])]
+    for hyper in (None, fs.NewtonSchulz(terms=3)):
+        outs = run(sources, hyper=hyper)
+        for g, out in zip(sources, outs):
+            check(out, reference(g), 3 if hyper else terms_of(g.shape))
+            assert torch.equal(out, run([g], hyper=hyper)[0])
+
+
 @pytest.mark.parametrize("rows,cols", [(40, 56), (200, 600), (512, 700), (900, 300)])
 @pytest.mark.parametrize("terms", [1, 3])
 def test_terms(rows, cols, terms):
