@@ -26,10 +26,10 @@
 //
 // Long Gram products are cut into segments. The tensor cores' sums are cut off, not
 // rounded, at each addition, so a sum's error grows with the number of steps (measured:
-// 7e-9 of the result per element of the long side and term; 12 % at 16.8 M). Where a
-// product has more than 256 steps of 64, blocks take segments of it, and a pass adds
-// the segments' fp32 results in order (1 x 16.8 M: 6e-5, and 757 -> 26 ms; 300 x 262144: 6e-5,
-// 5.7 -> 1.6 ms; 50257 x 768 0.8 ms).
+// 7e-9 of the result per element of the long side; 12 % at 16.8 M). Where a
+// product has more than 256 steps of 64, or few tiles and many steps, blocks take segments of
+// it, and a pass adds the segments' fp32 results in order (1 x 16.8 M: 6e-5, and 757 -> 26 ms;
+// 300 x 262144: 6e-5, 5.7 -> 1.6 ms; 50257 x 768 0.8 ms).
 //
 // Each of the three products is one launch over all matrices of the call: a
 // persistent grid of tiles; in each block a producer lane (TMA), a product lane
@@ -1301,17 +1301,23 @@ int parts_of(const NsJob& j) {
   return static_cast<int>(std::min<int64_t>(kMaxParts, (units + 2 * kPassWarps - 1) / (2 * kPassWarps)));
 }
 
-// The segments of a Gram product of more than 256 steps: at most 256 steps each, and as many as
-// give each of 152 SMs a tile, but for segments of less than 32 blocks of 64. (By the matrix alone, so that it gives
-// the same bits in any company.)
+// The segments of a matrix's Gram product. Products of more than 256 steps are cut for their
+// sums' sake. Others are cut where that saves one block a long wait: into segments of 24 steps or
+// more, as many as give each of 152 SMs a tile, if at least 12 us of steps go (the second launch costs
+// half of that; 31 x 5000 289 -> 112 us, 300 x 5000 169 -> 157, 1024 x 8192 328 -> 279; but twelve of
+// 300 x 5000 471 -> 496; with
+// 9 us 768 x 4096 would be cut, 192 -> 195 us alone and 575 -> 697 for eight of them). By the
+// matrix alone, so that it gives the same bits in any company.
 struct Segments {
   int splits = 0, blocks = 0;
 };
 Segments segments_of(const NsJob& j, int terms) {
-  const int64_t blocks = (std::max(j.rows, j.cols) + kTileK - 1) / kTileK;
-  if (blocks * terms <= 256) return {};
+  constexpr int kMostSteps = 256, kLeastSteps = 24, kSms = 152;
+  const int64_t blocks = (std::max(j.rows, j.cols) + kTileK - 1) / kTileK, steps = blocks * terms;
   const int64_t rows = (std::min(j.rows, j.cols) + 127) / 128, tiles = rows * (rows + 1) / 2;
-  const int64_t each = std::min<int64_t>(256 / terms, std::max<int64_t>(32, (blocks * tiles + 151) / 152));
+  const int64_t splits = std::max<int64_t>({(steps + kMostSteps - 1) / kMostSteps, std::min(kSms / tiles, steps / kLeastSteps), 1});
+  const int64_t each = (blocks + splits - 1) / splits;
+  if (steps <= kMostSteps && 0.28 * static_cast<double>(steps - each * terms) < 12.0) return {};
   return {static_cast<int>((blocks + each - 1) / each), static_cast<int>(each)};
 }
 
