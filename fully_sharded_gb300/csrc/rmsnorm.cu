@@ -48,10 +48,14 @@ constexpr int kLongThreads = 256;     // rows beyond the registers
 //     of a row are partly outside, where a load's surplus is dropped (it lies in
 //     a 16-byte piece that holds an element of the row) and stores go one by one.
 //     (43633 x 769 bf16 with the residual, 268 MB: 224 us strided, see below.)
-//   kGroups: 8 consecutive elements one by one (other rows, 8-bit groups).
+//   kGroups: 8 consecutive elements from any place, put together from the aligned vectors
+//     that hold them (8-bit outputs of other rows: 33520 x 1001 bf16 with the residual, groups
+//     of 128: 72 us, 139 one by one; 8194 x 4095 with one scale a row 74 us, 277 strided).
+//   kSingles: the same one by one, for rows that a warp holds: all of it would wait for the
+//     last, partial group, which goes one by one anyway (260111 x 129: 121 us, 170 by vectors).
 //   kStrided: element by element across the row's threads, so that a warp's
-//     accesses stay contiguous (other rows, no groups).
-enum RowMap { kVector, kShifted, kGroups, kStrided };
+//     accesses stay contiguous (other rows).
+enum RowMap { kVector, kShifted, kGroups, kSingles, kStrided };
 template <RowMap kMap>
 constexpr bool kByVectors = kMap == kVector || kMap == kShifted;
 
@@ -119,6 +123,58 @@ __device__ __forceinline__ void store_vec(uint8_t* p, const float* v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(two[0] | two[1] << 16, two[2] | two[3] << 16);
 }
 
+// The same to a place of any alignment: the aligned 4 bytes among them as one store, the rest around it.
+__device__ __forceinline__ void store8_anywhere(uint8_t* p, const float* v) {
+  uint32_t two[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    two[e] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * e], v[2 * e + 1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t lo = two[0] | two[1] << 16, hi = two[2] | two[3] << 16;
+  const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 3u);
+  if (s == 0) {
+    reinterpret_cast<uint32_t*>(p)[0] = lo;
+    reinterpret_cast<uint32_t*>(p)[1] = hi;
+  } else if (s == 2) {
+    *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(lo);
+    *reinterpret_cast<uint32_t*>(p + 2) = __funnelshift_r(lo, hi, 16);
+    *reinterpret_cast<uint16_t*>(p + 6) = static_cast<uint16_t>(hi >> 16);
+  } else if (s == 1) {
+    p[0] = static_cast<uint8_t>(lo);
+    *reinterpret_cast<uint16_t*>(p + 1) = static_cast<uint16_t>(lo >> 8);
+    *reinterpret_cast<uint32_t*>(p + 3) = __funnelshift_r(lo, hi, 24);
+    p[7] = static_cast<uint8_t>(hi >> 24);
+  } else {
+    p[0] = static_cast<uint8_t>(lo);
+    *reinterpret_cast<uint32_t*>(p + 1) = __funnelshift_r(lo, hi, 8);
+    *reinterpret_cast<uint16_t*>(p + 5) = static_cast<uint16_t>(hi >> 8);
+    p[7] = static_cast<uint8_t>(hi >> 24);
+  }
+}
+
+__device__ __forceinline__ void store8_anywhere(__nv_bfloat16* p, const float* v) {
+  const uint32_t w[4] = {pack(v[0], v[1]), pack(v[2], v[3]), pack(v[4], v[5]), pack(v[6], v[7])};
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  if ((at & 15u) == 0) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if ((at & 3u) == 0) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) reinterpret_cast<uint32_t*>(p)[e] = w[e];
+  } else {
+    *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+#pragma unroll
+    for (int e = 0; e < 3; ++e) reinterpret_cast<uint32_t*>(p + 1)[e] = __funnelshift_r(w[e], w[e + 1], 16);
+    *reinterpret_cast<uint16_t*>(p + 7) = static_cast<uint16_t>(w[3] >> 16);
+  }
+}
+__device__ __forceinline__ void store8_anywhere(float* p, const float* v) {
+  if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+    store_vec(p, v);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p[e] = v[e];
+}
+
 __device__ __forceinline__ float load_gain(const void* gain, int32_t dtype, int64_t j) {
   return dtype == FSDP_DTYPE_F32 ? load1(static_cast<const float*>(gain) + j)
                                  : load1(static_cast<const __nv_bfloat16*>(gain) + j);
@@ -136,6 +192,45 @@ __device__ __forceinline__ int place(const RowThreads& r, int v, int e) {
   return kMap == kShifted ? j - r.phase : j;
 }
 
+// kWords 4-byte words from any 2-byte boundary, out of aligned vectors that each hold some of
+// the first `bytes` bytes (what follows them is not defined).
+template <int kWords>
+__device__ __forceinline__ void load_words(const void* p, uint32_t (&out)[kWords], int bytes = 4 * kWords) {
+  constexpr int kVecs = kWords / 4 + 1;
+  const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p) - s);
+  uint32_t w[4 * kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const uint4 t = bytes > 0 && 16 * i < static_cast<int>(s) + bytes ? q[i] : make_uint4(0, 0, 0, 0);
+    w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
+  }
+#pragma unroll
+  for (int i = 0; i + 2 < 4 * kVecs; ++i) w[i] = s & 8u ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i + 1 < 4 * kVecs; ++i) w[i] = s & 4u ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], (s & 2u) * 8u);
+}
+
+// 8 consecutive elements from any place, by aligned vectors; zeros from `count` on.
+template <typename T>
+__device__ __forceinline__ void load8_anywhere(const T* p, int count, float (&v)[8]) {
+  uint32_t w[2 * sizeof(T)];
+  load_words(p, w, min(count, 8) * static_cast<int>(sizeof(T)));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (sizeof(T) == 4)
+      v[e] = __uint_as_float(w[e]);
+    else
+      v[e] = __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+  }
+  if (count < 8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < count ? v[e] : 0.0f;
+  }
+}
+
 // A thread's kV groups of a row, as loaded.
 template <RowMap kMap, int kV, typename T>
 struct RowLoad {
@@ -149,6 +244,8 @@ struct RowLoad {
         raw[k].load(p + j, there && j < cols, there && j < cols);
       } else if constexpr (kMap == kShifted) {
         raw[k].load(p + j, there && j + 4 > 0 && j < cols, there && j + 8 > 0 && j + 4 < cols);
+      } else if constexpr (kMap == kGroups) {
+        load8_anywhere(p + j, there ? cols - j : 0, v[k]);
       } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -188,6 +285,8 @@ __device__ __forceinline__ void store_group(T* p, const RowThreads& r, int v, in
     if (j < cols) store_vec(p + j, in);
   } else if (kMap == kShifted && j >= 0 && j + 8 <= cols) {
     store_vec(p + j, in);
+  } else if (kMap == kGroups && j + 8 <= cols) {
+    store8_anywhere(p + j, in);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -207,33 +306,13 @@ __device__ __forceinline__ void store_each(float* p, const RowThreads& r, int v,
   }
 }
 
-// kWords 4-byte words from any 2-byte boundary, out of aligned vectors that each hold some of them.
-template <int kWords>
-__device__ __forceinline__ void load_words(const void* p, uint32_t (&out)[kWords]) {
-  constexpr int kVecs = kWords / 4 + 1;
-  const uint32_t s = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p) & 15u);
-  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p) - s);
-  uint32_t w[4 * kVecs];
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const uint4 t = 16 * i < static_cast<int>(s) + 4 * kWords ? q[i] : make_uint4(0, 0, 0, 0);
-    w[4 * i] = t.x, w[4 * i + 1] = t.y, w[4 * i + 2] = t.z, w[4 * i + 3] = t.w;
-  }
-#pragma unroll
-  for (int i = 0; i + 2 < 4 * kVecs; ++i) w[i] = s & 8u ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i + 1 < 4 * kVecs; ++i) w[i] = s & 4u ? w[i + 1] : w[i];
-#pragma unroll
-  for (int i = 0; i < kWords; ++i) out[i] = __funnelshift_r(w[i], w[i + 1], (s & 2u) * 8u);
-}
-
 // The gains of group v (zeros past the end); `vectors`: the gain starts on a
-// 16-byte boundary and the map is kVector.
+// 16-byte boundary.
 template <RowMap kMap>
 __device__ __forceinline__ void gain_group(const void* gain, int32_t dtype, bool vectors, const RowThreads& r, int v,
                                            int cols, float* out) {
   const int j = place<kMap>(r, v, 0);
-  if (kMap == kVector && vectors) {
+  if ((kMap == kVector || (kMap == kGroups && j + 8 <= cols)) && vectors) {
     if (dtype == FSDP_DTYPE_F32) {
       Raw8<float> raw;
       raw.a = raw.b = make_float4(0, 0, 0, 0);
@@ -248,6 +327,16 @@ __device__ __forceinline__ void gain_group(const void* gain, int32_t dtype, bool
       if (j < cols) raw.a = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(gain) + j);
       raw.to(out);
     }
+    return;
+  }
+  if constexpr (kMap == kGroups) {
+    float g[8];
+    if (dtype == FSDP_DTYPE_F32)
+      load8_anywhere(static_cast<const float*>(gain) + j, cols - j, g);
+    else
+      load8_anywhere(static_cast<const __nv_bfloat16*>(gain) + j, cols - j, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] = g[e];
     return;
   }
   if (kMap == kShifted && j >= 0 && j + 8 <= cols) {
@@ -309,6 +398,8 @@ struct NormParams {
   float *scales, *rstd;
   int32_t threads;  // of a row
   int32_t group_bits;  // log2 of the group
+  // that share a group's maximum: no more than the row's (of 8 or 16 lanes), the next ones are another row's
+  int32_t group_lanes;
   bool gain_vectors;
 };
 
@@ -404,8 +495,7 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kWi
       const int groups = kQuant == 1 ? 1 : (all + p.a.group - 1) >> p.group_bits;
 #pragma unroll
       for (int k = 0; k < kV; ++k) {
-        // a row of 8 or 16 lanes can be shorter than its group: the lanes after it are another row's
-        if constexpr (kQuant == 2) most = group_max(top[k], min(p.a.group / 8, r.n));
+        if constexpr (kQuant == 2) most = group_max(top[k], p.group_lanes);
         const float scale = scale_of(most * rstd);
         const int j = place<kMap>(r, k, 0);
         if (kQuant == 1 ? (k == 0 && r.t == 0 && cols > 0) : (j < cols && (j & (p.a.group - 1)) == 0))
@@ -846,17 +936,22 @@ int run_forward_as(const NormParams& p, const Spread& s, RowMap map, int grid, c
            : quant == 1 ? run_forward<T, kResidual, 1, kVector>(p, s, grid, st)
                         : run_forward<T, kResidual, 2, kVector>(p, s, grid, st);
   if (map == kShifted) return run_forward<T, kResidual, 0, kShifted>(p, s, grid, st);
+  if (map == kSingles)  // a group of 8 per lane
+    return launch_rows(quant == 1 ? norm_rows<T, kResidual, 1, kSingles, 1> : norm_rows<T, kResidual, 2, kSingles, 1>, grid,
+                       s.threads * s.per_block, 0, st, p);
   return quant == 0   ? run_forward<T, kResidual, 0, kStrided>(p, s, grid, st)
-         : quant == 1 ? run_forward<T, kResidual, 1, kStrided>(p, s, grid, st)
+         : quant == 1 ? run_forward<T, kResidual, 1, kGroups>(p, s, grid, st)
                       : run_forward<T, kResidual, 2, kGroups>(p, s, grid, st);
 }
 
 template <typename T>
 int forward(NormParams p, RowMap map, cudaStream_t st) {
   const bool quant = p.a.y_dtype == FSDP_DTYPE_E4M3;
-  if (quant && map == kShifted) map = kStrided;  // y's rows have a distance of their own
+  // 8 bits: y's rows have a distance of their own
+  if (quant && map != kVector) map = p.a.cols <= 256 ? kSingles : kGroups;
   const Spread s = forward_spread(p.a.rows, covered(p.a.cols, map));
   p.threads = s.threads;
+  p.group_lanes = std::min(p.a.group / 8, s.threads);
   // as many blocks as run at once where a block works ahead, else one for each row
   int64_t most = 1 << 20;
   if (s.v > 1 && map == kVector && !p.residual)
@@ -981,7 +1076,7 @@ extern "C" int fsdp_rmsnorm(const fsdp_rmsnorm_t* a, const void* x, const void* 
   }
   int group_bits = 0;
   while (a->group >> (group_bits + 1)) ++group_bits;
-  const NormParams p{*a, x, residual, gain, h_out, y, scales, rstd, 0, group_bits,
+  const NormParams p{*a, x, residual, gain, h_out, y, scales, rstd, 0, group_bits, 0,
                      reinterpret_cast<uintptr_t>(gain) % 16 == 0};
   RowMap map = map_of({{x, a->x_stride}, {residual, a->residual_stride}, {h_out, a->h_stride}, {e4m3 ? nullptr : y, a->y_stride}},
                    a->rows, a->cols, es);
