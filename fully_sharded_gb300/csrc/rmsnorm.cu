@@ -17,6 +17,7 @@
 // 25 an element, a conversion, two maxima and four products among them); one row of
 // 4096 8.5 us, of which the launch from Python is all but 3.
 #include "host_internal.h"
+#include "row_map.h"
 #include "strided.h"
 #include "tensor_core.cuh"
 
@@ -37,25 +38,6 @@ constexpr int kMaxV = 4;              // groups of 8 elements per thread
 constexpr int kMaxThreads = 512;      // of a row held in registers
 constexpr int kLongThreads = 256;     // rows beyond the registers
 
-// Where a thread's 8 kV elements of a row lie.
-//   kVector: groups of 8 consecutive elements, read and written as vectors: cols is a
-//     multiple of 8 and every row of every array starts on a 16-byte boundary. (A group
-//     is whole or absent: one predicate and no branch around a load, so that all of
-//     a thread's loads are in flight together.)
-//   kShifted: the same groups moved back by the row's own distance from a 16-byte
-//     boundary (`phase` elements, the same for all arrays), so that rows of any
-//     length are read and written as aligned vectors too; the first and the last group
-//     of a row are partly outside, where a load's surplus is dropped (it lies in
-//     a 16-byte piece that holds an element of the row) and stores go one by one.
-//     (43633 x 769 bf16 with the residual, 268 MB: 224 us strided, see below.)
-//   kGroups: 8 consecutive elements from any place, put together from the aligned vectors
-//     that hold them (8-bit outputs of other rows: 33520 x 1001 bf16 with the residual, groups
-//     of 128: 72 us, 139 one by one; 8194 x 4095 with one scale a row 74 us, 277 strided).
-//   kSingles: the same one by one, for rows that a warp holds: all of it would wait for the
-//     last, partial group, which goes one by one anyway (260111 x 129: 121 us, 170 by vectors).
-//   kStrided: element by element across the row's threads, so that a warp's
-//     accesses stay contiguous (other rows).
-enum RowMap { kVector, kShifted, kGroups, kSingles, kStrided };
 template <RowMap kMap>
 constexpr bool kByVectors = kMap == kVector || kMap == kShifted;
 
@@ -184,19 +166,6 @@ __device__ __forceinline__ float load_gain(const void* gain, int32_t dtype, int6
   return dtype == FSDP_DTYPE_F32 ? load1(static_cast<const float*>(gain) + j)
                                  : load1(static_cast<const __nv_bfloat16*>(gain) + j);
 }
-// The row's threads: `t` of `n` (n up to 32: part of a warp or a warp; else the block).
-struct RowThreads {
-  int t, n;
-  int phase;  // kShifted: elements from the last 16-byte boundary to the row's first
-};
-
-// First element of group v, or element (v, e) in the strided map.
-template <RowMap kMap>
-__device__ __forceinline__ int place(const RowThreads& r, int v, int e) {
-  const int j = kMap == kStrided ? (v * 8 + e) * r.n + r.t : (v * r.n + r.t) * 8 + e;
-  return kMap == kShifted ? j - r.phase : j;
-}
-
 // kWords 4-byte words from any 2-byte boundary, out of aligned vectors that each hold some of
 // the first `bytes` bytes (what follows them is not defined).
 template <int kWords>
@@ -245,10 +214,9 @@ struct RowLoad {
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
       const int j = place<kMap>(r, k, 0);
-      if constexpr (kMap == kVector) {
-        raw[k].load(p + j, there && j < cols, there && j < cols);
-      } else if constexpr (kMap == kShifted) {
-        raw[k].load(p + j, there && j + 4 > 0 && j < cols, there && j + 8 > 0 && j + 4 < cols);
+      if constexpr (kByVectors<kMap>) {
+        const bool first = there && holds_some<kMap>(j, 4, cols);
+        raw[k].load(p + j, first, kMap == kVector ? first : there && holds_some<kMap>(j + 4, 4, cols));
       } else if constexpr (kMap == kGroups) {
         load8_anywhere(p + j, there ? cols - j : 0, v[k]);
       } else {
