@@ -556,6 +556,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
     stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  // Held while this grid waits for the previous one, which is safe: with its 225 KB a block shares its SM
+  // with no other block that has tensor memory, and the next launch starts after this barrier.
   if (warp == 1) tmem_alloc<kPair>(smem_addr(&tmem_slot), T::kTmemCols);
   if (warp == 2 && lane < 3) {  // the first matrix's maps
     const GemmMat& g = p.mat[0];
@@ -1012,11 +1014,13 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
     stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0) tmem_alloc<1>(smem_addr(&tmem_slot), kSmallCols);
   for (int i = threadIdx.x * 16; i < 2 * s.part_x; i += kSmallThreads * 16)
     *reinterpret_cast<uint4*>(x + i) = make_uint4(0, 0, 0, 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
+  // Tensor memory is held by no block that still waits for another grid (several of these blocks
+  // share an SM), and the next launch starts when every block here has its columns: who queues
+  // for columns queues behind blocks that run to their end.
+  if (warp == 0) tmem_alloc<1>(smem_addr(&tmem_slot), kSmallCols);
   const int count = g.rows * g.cols;
   float squares = 0.0f;
   if (p.applies) {  // u, written to where this block reads it again after the barrier below
@@ -1066,7 +1070,8 @@ __global__ void __launch_bounds__(kSmallThreads) ns_small(const __grid_constant_
     return Piece{row, col, min(8, s.length - col), small_at(s.side16, row, col)};
   };
   const int64_t along = wide ? 1 : g.source_stride, across = wide ? g.source_stride : 1;
-  __syncthreads();  // the zeros, and u, are written
+  __syncthreads();  // the zeros, and u, are written, and the columns are held
+  asm volatile("griddepcontrol.launch_dependents;");
   // The source is read once: its fp32 bits wait where the element's two parts will be,
   // until the norm is known.
   for (int t = threadIdx.x; t < all; t += kSmallThreads) {
