@@ -642,6 +642,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_product(const __grid_const
       const GemmMat& g = tiles.at(t, &i, &j);
       int from;
       const int steps = inner(g, tiles.split, &from) * p.terms;
+      if (n == 0) await_inputs();  // the limit of the waits below does not run while earlier kernels do
       const uint32_t buf = n & 1u, d = tmem + buf * kN;
       ok = bar_wait_warp(smem_addr(&free_bar[buf]), ((n >> 1) & 1u) ^ 1u, guard);
       if (!ok) break;

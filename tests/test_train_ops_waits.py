@@ -35,3 +35,18 @@ def test_products_release_the_next_launch_with_their_tensor_memory_in_hand():
     body = kernel("ns_product")
     (alloc,), (release,) = places(body, "tmem_alloc"), places(body, "griddepcontrol.launch_dependents")
     assert any(alloc < b < release for b in places(body, "__syncthreads()"))
+
+
+def test_no_bounded_wait_of_the_products_begins_before_the_previous_grids_end():
+    """Each role waits for the previous grid before its first wait that depends on it: the 2 s limit
+    would otherwise run while earlier kernels of the stream do, and the launch be given up in a correct run."""
+    body = kernel("ns_product")
+    starts = [body.index(role) for role in ("if (warp == 0)", "else if (warp == 1 && rank == 0)", "else if (warp == 2", "else if (warp >= 4)")]
+    for begin, end in zip(starts, starts[1:] + [len(body)]):
+        role = body[begin:end]
+        awaited = places(role, "await_inputs()")
+        assert len(awaited) == 1
+        # barriers that only the block's own progress arms are free at first and may be passed before
+        depends = [p for bar in ("full_bar", "in_bar", "done_bar") for w in ("bar_wait(", "bar_wait_warp(")
+                   for p in places(role, w + "smem_addr(&" + bar)]
+        assert all(awaited[0] < p for p in depends)
