@@ -494,6 +494,20 @@ __device__ __forceinline__ float long_reduce(float v, float* shared) {
   return row_reduce<kMax>(v, RowThreads{static_cast<int>(threadIdx.x), kLongThreads, 0}, shared);
 }
 
+// A thread's sum over a long row: what each addition rounds off is kept beside it (Knuth's two-sum), so that the
+// error does not grow with the row (2^24 equal values in fp32: a plain running sum is off by up to
+// 6e-4 of itself, this one by 2e-8).
+struct LongSum {
+  float sum = 0.0f, rest = 0.0f;
+  __device__ __forceinline__ void add(float v) {
+    const float next = sum + v, added = next - sum;
+    rest += (sum - (next - added)) + (v - added);
+    sum = next;
+  }
+  // past an infinity or a NaN, `rest` is a NaN and says nothing
+  __device__ __forceinline__ float value() const { return isfinite(rest) ? sum + rest : sum; }
+};
+
 // Calls f(j, count) for the thread's groups of 8 elements of a long row; all threads of the
 // block make the same number of calls (count, up to 8, may be 0 or less).
 template <typename F>
@@ -544,14 +558,15 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_rows(const __grid_cons
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += w[e];
     };
-    float sum = 0.0f;
+    LongSum squares;
     each_long_group(cols, [&](int64_t j, int count) {
-      float v[8];
+      float v[8], sum = 0.0f;
       values(j, count, v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum += v[e] * v[e];
+      squares.add(sum);
     });
-    const float rstd = rsqrtf(long_reduce<false>(sum, shared) / static_cast<float>(cols) + static_cast<float>(p.a.eps));
+    const float rstd = rsqrtf(long_reduce<false>(squares.value(), shared) / static_cast<float>(cols) + static_cast<float>(p.a.eps));
     if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
     // y before it is rounded, and h on its way
     const auto normed = [&](int64_t j, int count, bool last, float (&v)[8]) {
@@ -815,9 +830,9 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_rows_backward(const __
     const T* dh = p.dh ? static_cast<const T*>(p.dh) + row * p.a.dh_stride : nullptr;
     T* dx = static_cast<T*>(p.dx) + row * p.a.dx_stride;
     const float r = p.rstd[row];
-    float sum = 0.0f;
+    LongSum products;
     each_long_group(cols, [&](int64_t j, int count) {
-      float u[8], n[8], g[8], acc[8] = {};
+      float u[8], n[8], g[8], acc[8] = {}, sum = 0.0f;
       load8_anywhere(dy + j, count, u);
       load8_anywhere(h + j, count, n);
       load8_gain(p.gain, p.a.gain_dtype, j, count, g);
@@ -828,9 +843,10 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_rows_backward(const __
         sum += t * g[e];
         acc[e] += t;
       }
+      products.add(sum);
       store8_upto(mine + j, count, acc);
     });
-    const float mean = long_reduce<false>(sum, shared) / static_cast<float>(cols);
+    const float mean = long_reduce<false>(products.value(), shared) / static_cast<float>(cols);
     each_long_group(cols, [&](int64_t j, int count) {
       float u[8], n[8], g[8], d[8] = {};
       load8_anywhere(dy + j, count, u);
