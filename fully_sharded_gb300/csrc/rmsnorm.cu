@@ -13,7 +13,7 @@
 //
 // Measured on GB300 (fraction of the copy bandwidth of 6.79 TB/s): 16384 x 4096 bf16 with
 // the residual 82.9 us (95 %), backward with the residual's gradient 93.5 us (85 %);
-// 4097 x 11008 bf16 to 8 bits in groups of 128 43 us (47 %, bound by instructions: about
+// 4097 x 11008 bf16 to 8 bits in groups of 128 45 us (45 %, bound by instructions: about
 // 25 an element, a conversion, two maxima and four products among them); one row of
 // 4096 8.5 us, of which the launch from Python is all but 3.
 #include "host_internal.h"
@@ -333,22 +333,29 @@ __device__ __forceinline__ void gain_group(const void* gain, int32_t dtype, bool
   }
 }
 
+// The larger one, or a NaN if either is one: the maximum of a group with a NaN is a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 template <bool kMax>
 __device__ __forceinline__ float warp_reduce(float v, int lanes = 32) {
   for (int o = lanes / 2; o > 0; o >>= 1) {
     const float w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = kMax ? fmaxf(v, w) : v + w;
+    v = kMax ? max_nan(v, w) : v + w;
   }
   return v;
 }
 
 // Over aligned groups of 4, 8, 16 or 32 lanes.
 __device__ __forceinline__ float group_max(float v, int lanes) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-  if (lanes > 4) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-  if (lanes > 8) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-  if (lanes > 16) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+  v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 1));
+  v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 2));
+  if (lanes > 4) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  if (lanes > 8) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  if (lanes > 16) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 16));
   return v;
 }
 
@@ -377,7 +384,7 @@ struct NormParams {
 };
 
 // The scale of a group whose largest |y| is `top`.
-__device__ __forceinline__ float scale_of(float top) { return fmaxf(top * (1.0f / 448.0f), 0x1p-126f); }
+__device__ __forceinline__ float scale_of(float top) { return max_nan(top * (1.0f / 448.0f), 0x1p-126f); }
 
 // Threads of a row at most, and blocks of them that an SM's registers are to hold:
 // more rows in flight while others wait at their reductions. kWide: rows that need
@@ -458,8 +465,8 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kWi
       for (int k = 0; k < kV; ++k) {
         top[k] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top[k] = fmaxf(top[k], fabsf(v[k][e]));
-        most = fmaxf(most, top[k]);
+        for (int e = 0; e < 8; ++e) top[k] = max_nan(top[k], fabsf(v[k][e]));
+        most = max_nan(most, top[k]);
       }
       if constexpr (kQuant == 1) {
         most = row_reduce<true>(most, r, shared[2]);
@@ -592,7 +599,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_rows(const __grid_cons
           float v[8];
           normed(j, count, false, v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) all = fmaxf(all, fabsf(v[e]));
+          for (int e = 0; e < 8; ++e) all = max_nan(all, fabsf(v[e]));
         });
         all = long_reduce<true>(all, shared);
         if (threadIdx.x == 0) p.scales[row] = scale_of(all);
@@ -604,7 +611,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_long_rows(const __grid_cons
         normed(j, count, true, v);
         if constexpr (kQuant == 2) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+          for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(v[e]));
           all = warp_reduce<true>(top, p.a.group / 8);
         }
         const float scale = scale_of(all), inverse = __frcp_rn(scale);

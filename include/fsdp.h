@@ -540,7 +540,8 @@ int fsdp_account(double P, double U, int32_t N, int32_t F, int32_t prefetch,
  *   scale = max(max|y| / 448, 2^-126),   y_out = round(y (1 / scale))
  * to the nearest even e4m3 value, at most 448; scales is fp32 [rows][ceil(cols / group)],
  * contiguous. Other y types: scales null and group 0. A row with an infinity or a NaN
- * gives what the formulas give.
+ * gives what the formulas give; the maximum over a NaN is a NaN, so a group with one
+ * (an infinity times rstd = 0 included) has the scale NaN and NaN for all its values.
  * In place: h_out may be x or residual, and y may be x (same address, stride
  * and type), as long as the outputs are distinct; column slices of one
  * buffer (equal strides, disjoint columns) may be mixed freely.
