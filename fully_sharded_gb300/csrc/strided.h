@@ -22,9 +22,8 @@ struct Strided {
 
   bool ok() const {
     if (!p || reinterpret_cast<uintptr_t>(p) % size != 0) return false;
-    if (rows > 1 && stride < cols) return false;
-    // the span fits the address arithmetic
-    return stride >= 0 && (rows < 2 || stride <= INT64_MAX / 8 / rows);
+    // the span fits the address arithmetic; a single row's stride is not used
+    return rows < 2 || (stride >= cols && stride <= INT64_MAX / 8 / rows);
   }
   int64_t pitch() const { return rows > 1 ? stride * size : 0; }
   uintptr_t lo() const { return reinterpret_cast<uintptr_t>(p); }

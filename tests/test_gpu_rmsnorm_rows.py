@@ -35,3 +35,32 @@ def test_part_of_a_warp_without_rows(rows, cols, stride, dtype):
     check_y(y, want_forward(x, None, gain, 1e-6)[2], cols)
     check_backward(dy, h, gain, residual, dx=dx)
     assert untouched(whole_dx, dx)
+
+
+@pytest.mark.parametrize("cols", [768, 101, 20001])
+@pytest.mark.parametrize("stride", [0, -1, -(1 << 40), 1 << 62])
+def test_the_stride_of_a_single_row_does_not_matter(cols, stride):
+    import ctypes
+
+    gen = torch.Generator(device="cuda").manual_seed(cols)
+    x, dy, dh, gain = (rand(gen, *s) for s in ((1, cols), (1, cols), (1, cols), (cols,)))
+    y, h, dx, rstd, dgain = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x), torch.empty(1, device="cuda"), torch.empty_like(gain)
+    stream = torch.cuda.current_stream().cuda_stream
+    a = fs.RmsNormArgs(1, cols, stride, stride, stride, stride, 0, 0, 0, 0, 1e-6)
+    assert fs._lib.fsdp_rmsnorm(ctypes.byref(a), x.data_ptr(), dh.data_ptr(), gain.data_ptr(), h.data_ptr(), y.data_ptr(), None,
+                                rstd.data_ptr(), stream) == fs.FSDP_OK
+    check_y(y, want_forward(x, dh, gain, 1e-6)[2], cols)
+    b = fs.RmsNormBackwardArgs(1, cols, stride, stride, stride, stride, 0, 0)
+    workspace = torch.empty(fs.fsdp_rmsnorm_backward_workspace(1, cols), dtype=torch.uint8, device="cuda")
+    assert fs._lib.fsdp_rmsnorm_backward(ctypes.byref(b), dy.data_ptr(), h.data_ptr(), gain.data_ptr(), rstd.data_ptr(), dh.data_ptr(),
+                                         dx.data_ptr(), dgain.data_ptr(), workspace.data_ptr(), workspace.numel(), stream) == fs.FSDP_OK
+    plain, plain_gain = torch.empty_like(dx), torch.empty_like(gain)
+    fs.fsdp_rmsnorm_backward(dy, h, gain, rstd, plain, plain_gain, workspace, dh=dh)
+    assert torch.equal(dx, plain) and torch.equal(dgain, plain_gain)
+    out, again = torch.empty(1, cols, dtype=BF16, device="cuda"), torch.empty(1, cols, dtype=BF16, device="cuda")
+    batch = fs.NewtonSchulzBatch([x], [out])
+    batch.array[0].source_stride = batch.array[0].out_stride = stride
+    room = torch.empty(fs.fsdp_newton_schulz_workspace(batch), dtype=torch.uint8, device="cuda")
+    fs.fsdp_newton_schulz(batch, room)
+    fs.fsdp_newton_schulz(fs.NewtonSchulzBatch([x], [again]), room)
+    assert torch.equal(out, again)
