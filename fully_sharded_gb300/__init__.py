@@ -578,13 +578,13 @@ def _torch():
 _torch_module = None
 
 
-def _cuda_stream(stream):
-    """The stream's handle; None: the current stream (of a caller that holds CUDA tensors)."""
+def _cuda_stream(stream, device: int | None = None):
+    """The stream's handle; None: the current stream (of `device`, or of the current one)."""
     if stream is None:
         torch = _torch()
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 2.8 us less than the Stream object
         if raw is not None:
-            return raw(torch.cuda.current_device())
+            return raw(torch.cuda.current_device() if device is None else device)
         return torch.cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
@@ -599,10 +599,27 @@ def _float_dtype(t, what: str) -> int:
     raise ValueError("%s: expected float32 or bfloat16, got %s" % (what, dtype))
 
 
-def _matrix(t, what: str, shape, dtype=None):
-    """(address, row stride) of a CUDA matrix of the given shape whose rows are contiguous."""
+def _device(t, what: str) -> int:
     if not t.is_cuda:
         raise ValueError("%s: expected a CUDA tensor, got one on %s" % (what, t.device))
+    return t.get_device()
+
+
+def _current_device(device: int, what: str):
+    """Kernels are launched on the current device: the tensors have to lie there."""
+    current = _torch().cuda.current_device()
+    if device != current:
+        raise ValueError("%s: on cuda:%d, but the current device is cuda:%d" % (what, device, current))
+
+
+def _same_device(t, what: str, device: int):
+    if t.get_device() != device:  # -1: not a CUDA tensor
+        raise ValueError("%s: expected a CUDA tensor on cuda:%d, got one on %s" % (what, device, t.device))
+
+
+def _matrix(t, what: str, shape, device: int, dtype=None):
+    """(address, row stride) of a matrix of the given shape on `device` whose rows are contiguous."""
+    _same_device(t, what, device)
     if t.shape != shape:
         raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
     if dtype is not None and t.dtype is not dtype:
@@ -614,17 +631,20 @@ def _matrix(t, what: str, shape, dtype=None):
     return t.data_ptr(), (row if rows > 1 else cols)
 
 
-def _vector(t, what: str, n: int, dtype=None):
-    if not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+def _vector(t, what: str, n: int, device: int, dtype=None):
+    _same_device(t, what, device)
+    if not t.is_contiguous() or t.numel() != n:
         raise ValueError("%s: expected a contiguous CUDA tensor of %d elements" % (what, n))
     if dtype is not None and t.dtype != dtype:
         raise ValueError("%s: expected %s, got %s" % (what, dtype, t.dtype))
     return t.data_ptr()
 
 
-def _workspace(t):
+def _workspace(t, device: int | None):
     if t is None:
         return None, 0
+    if device is not None:
+        _same_device(t, "workspace", device)
     return _dptr(t), t.numel() * t.element_size()
 
 
@@ -645,30 +665,32 @@ def fsdp_rmsnorm(x, gain, y, residual=None, h_out=None, scales=None, rstd=None, 
     rows, cols = shape
     dtype, y_dtype = x.dtype, y.dtype
     code = _float_dtype(x, "x")
-    xp, x_stride = _matrix(x, "x", shape)
+    device = _device(x, "x")
+    _current_device(device, "x")
+    xp, x_stride = _matrix(x, "x", shape, device)
     rp = hp = sp = None
     r_stride = h_stride = cols
     if residual is not None:
-        rp, r_stride = _matrix(residual, "residual", shape, dtype)
+        rp, r_stride = _matrix(residual, "residual", shape, device, dtype)
     if h_out is not None:
-        hp, h_stride = _matrix(h_out, "h_out", shape, dtype)
+        hp, h_stride = _matrix(h_out, "h_out", shape, device, dtype)
     y_code = code
     if y_dtype == torch.float8_e4m3fn:
         y_code = FSDP_DTYPE_E4M3
         if scales is None:
             raise ValueError("scales: needed for an 8-bit y")
-        sp = _vector(scales, "scales", rows * (-(-cols // group) if group > 0 else 1), torch.float32)
+        sp = _vector(scales, "scales", rows * (-(-cols // group) if group > 0 else 1), device, torch.float32)
     else:
         if y_dtype != dtype:
             raise ValueError("y: expected %s or torch.float8_e4m3fn, got %s" % (dtype, y_dtype))
         if scales is not None:
             raise ValueError("scales: only for an 8-bit y")
-    yp, y_stride = _matrix(y, "y", shape)
-    dp = _vector(rstd, "rstd", rows, torch.float32) if rstd is not None else None
+    yp, y_stride = _matrix(y, "y", shape, device)
+    dp = _vector(rstd, "rstd", rows, device, torch.float32) if rstd is not None else None
     a = RmsNormArgs(rows, cols, x_stride, r_stride, h_stride, y_stride, code, _float_dtype(gain, "gain"), y_code, group,
                     eps)
-    _check("fsdp_rmsnorm", _lib.fsdp_rmsnorm(ctypes.byref(a), xp, rp, _vector(gain, "gain", cols), hp, yp, sp, dp,
-                                             _cuda_stream(stream)))
+    _check("fsdp_rmsnorm", _lib.fsdp_rmsnorm(ctypes.byref(a), xp, rp, _vector(gain, "gain", cols, device), hp, yp, sp, dp,
+                                             _cuda_stream(stream, device)))
 
 
 def fsdp_rmsnorm_backward_workspace(rows: int, cols: int) -> int:
@@ -685,16 +707,18 @@ def fsdp_rmsnorm_backward(dy, h, gain, rstd, dx, dgain, workspace, dh=None, stre
     shape = _shape2(h, "h")
     rows, cols = shape
     dtype = h.dtype
-    hp, h_stride = _matrix(h, "h", shape)
-    yp, dy_stride = _matrix(dy, "dy", shape, dtype)
-    xp, dx_stride = _matrix(dx, "dx", shape, dtype)
-    dhp, dh_stride = _matrix(dh, "dh", shape, dtype) if dh is not None else (None, cols)
+    device = _device(h, "h")
+    _current_device(device, "h")
+    hp, h_stride = _matrix(h, "h", shape, device)
+    yp, dy_stride = _matrix(dy, "dy", shape, device, dtype)
+    xp, dx_stride = _matrix(dx, "dx", shape, device, dtype)
+    dhp, dh_stride = _matrix(dh, "dh", shape, device, dtype) if dh is not None else (None, cols)
     a = RmsNormBackwardArgs(rows, cols, dy_stride, h_stride, dh_stride, dx_stride, _float_dtype(h, "h"),
                             _float_dtype(gain, "gain"))
-    ws, ws_bytes = _workspace(workspace)
+    ws, ws_bytes = _workspace(workspace, device)
     _check("fsdp_rmsnorm_backward", _lib.fsdp_rmsnorm_backward(
-        ctypes.byref(a), yp, hp, _vector(gain, "gain", cols), _vector(rstd, "rstd", rows, _torch().float32), dhp, xp,
-        _vector(dgain, "dgain", cols, gain.dtype), ws, ws_bytes, _cuda_stream(stream)))
+        ctypes.byref(a), yp, hp, _vector(gain, "gain", cols, device), _vector(rstd, "rstd", rows, device, _torch().float32),
+        dhp, xp, _vector(dgain, "dgain", cols, device, gain.dtype), ws, ws_bytes, _cuda_stream(stream, device)))
 
 
 class NewtonSchulzBatch:
@@ -707,12 +731,13 @@ class NewtonSchulzBatch:
         self._keep = (list(sources), list(outs))
         self.n = len(sources)
         self.array = (MatrixArgs * max(1, self.n))()
+        self.device = _device(sources[0], "source") if self.n else None
         for a, source, out in zip(self.array, sources, outs):
             shape = _shape2(source, "source")
             a.rows, a.cols = shape
             a.dtype = _float_dtype(source, "source")
-            a.source, a.source_stride = _matrix(source, "source", shape)
-            a.out, a.out_stride = _matrix(out, "out", shape, _torch().bfloat16)
+            a.source, a.source_stride = _matrix(source, "source", shape, self.device)
+            a.out, a.out_stride = _matrix(out, "out", shape, self.device, _torch().bfloat16)
 
 
 def _byref_or_none(x):
@@ -729,7 +754,9 @@ def fsdp_newton_schulz_workspace(batch: NewtonSchulzBatch, newton_schulz: Newton
 
 def fsdp_newton_schulz(batch: NewtonSchulzBatch, workspace, newton_schulz: NewtonSchulz | None = None, stream=None):
     """Orthogonalises every matrix of the batch into its out by Newton-Schulz products."""
-    ws, ws_bytes = _workspace(workspace)
+    if batch.device is not None:
+        _current_device(batch.device, "batch")
+    ws, ws_bytes = _workspace(workspace, batch.device)
     _check("fsdp_newton_schulz", _lib.fsdp_newton_schulz(batch.array, batch.n, _byref_or_none(newton_schulz), ws,
                                                          ws_bytes, _cuda_stream(stream)))
 
@@ -750,6 +777,15 @@ class MuonUnit:
             for x in xs:
                 if x is not None and not isinstance(x, int) and x.numel() != n:
                     raise ValueError("%s: expected %d elements, got %d" % (what, n, x.numel()))
+        self.device = None  # of the tensors among the arguments (addresses have none)
+        for what, xs in (("grads", grads), ("master", master), ("exp_avg", exp_avg), ("exp_avg_sq", exp_avg_sq),
+                         ("full_out", [full_out])):
+            for x in xs:
+                if x is None or isinstance(x, int):
+                    continue
+                if self.device is None:
+                    self.device = _device(x, what)
+                _same_device(x, what, self.device)
         self._tensors = (MuonTensor * max(1, len(tensors)))(*tensors)
         arrays = dict(grads=_parray(grads, 2), master=_parray(master, 4), exp_avg=_parray(exp_avg, 4),
                       exp_avg_sq=_parray(exp_avg_sq, 4))
@@ -772,6 +808,8 @@ def fsdp_muon_workspace(unit: MuonUnit, muon: Muon | None = None) -> int:
 def fsdp_muon_step(unit: MuonUnit, muon: Muon, workspace, stream=None):
     """The Muon step of one unit on all its ranks: reduce-scatter and momentum, every matrix's update
     orthogonalised and applied, the other tensors by Adam, the bf16 cast and the gather."""
-    ws, ws_bytes = _workspace(workspace)
+    if unit.device is not None:
+        _current_device(unit.device, "unit")
+    ws, ws_bytes = _workspace(workspace, unit.device)
     _check("fsdp_muon_step", _lib.fsdp_muon_step(ctypes.byref(unit.args), ctypes.byref(muon), ws, ws_bytes,
                                                  _cuda_stream(stream)))
