@@ -480,6 +480,7 @@ __global__ void __launch_bounds__(forward_threads(kV, kWide), forward_blocks(kWi
         const int j = place<kMap>(r, k, 0);
         if (kQuant == 1 ? (k == 0 && r.t == 0 && cols > 0) : (j < cols && (j & (p.a.group - 1)) == 0))
           p.scales[row * groups + (kQuant == 1 ? 0 : j >> p.group_bits)] = scale;
+        // y / scale as h gain (rstd / scale): three roundings, as y (1 / scale) has, and a product an element less
         float inverse = __frcp_rn(scale), q[8];
         if (rstd * inverse <= 0x1p127f) {
           inverse *= rstd;

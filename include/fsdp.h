@@ -538,15 +538,18 @@ int fsdp_account(double P, double U, int32_t N, int32_t F, int32_t prefetch,
  * E4M3: each row is cut into groups of `group` consecutive elements (32, 64, 128
  * or 256; 0: the whole row; the last group may be short), and
  *   scale = max(max|y| / 448, 2^-126),   y_out = round(y (1 / scale))
- * to the nearest even e4m3 value, at most 448; scales is fp32 [rows][ceil(cols / group)],
- * contiguous. Other y types: scales null and group 0. A row with an infinity or a NaN
- * gives what the formulas give; the maximum over a NaN is a NaN, so a group with one
- * (an infinity times rstd = 0 included) has the scale NaN and NaN for all its values.
+ * to the nearest even e4m3 value, at most 448, formed in fp32 (rstd and 1 / scale may be
+ * multiplied first). A value on the boundary between two e4m3 values, or within a few
+ * fp32 roundings of it, may go to either: with bf16 inputs about 0.04 % of the values lie
+ * exactly on one. scales is fp32 [rows][ceil(cols / group)], contiguous. Other y types:
+ * scales null and group 0. A row with an infinity or a NaN gives what the formulas give; the
+ * maximum over a NaN is a NaN, so a group with one (an infinity times rstd = 0 included)
+ * has the scale NaN and NaN for all its values.
  * In place: h_out may be x or residual, and y may be x (same address, stride
  * and type), as long as the outputs are distinct; column slices of one
  * buffer (equal strides, disjoint columns) may be mixed freely.
  * rows = 0 launches nothing. EINVAL: cols < 1 or > 2^30, rows < 0, a stride below cols, a
- * type, group or eps (finite, > 0) outside the above, a missing pointer, one not
+ * type, group or eps (finite, a float above 0) outside the above, a missing pointer, one not
  * aligned to its elements. EALIAS: other overlaps. */
 typedef struct {
   int64_t rows;
