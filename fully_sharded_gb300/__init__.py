@@ -612,14 +612,14 @@ def _current_device(device: int, what: str):
         raise ValueError("%s: on cuda:%d, but the current device is cuda:%d" % (what, device, current))
 
 
-def _same_device(t, what: str, device: int):
-    if t.get_device() != device:  # -1: not a CUDA tensor
-        raise ValueError("%s: expected a CUDA tensor on cuda:%d, got one on %s" % (what, device, t.device))
+def _elsewhere(t, what: str, device: int) -> ValueError:
+    return ValueError("%s: expected a CUDA tensor on cuda:%d, got one on %s" % (what, device, t.device))
 
 
 def _matrix(t, what: str, shape, device: int, dtype=None):
     """(address, row stride) of a matrix of the given shape on `device` whose rows are contiguous."""
-    _same_device(t, what, device)
+    if t.get_device() != device:  # -1: not a CUDA tensor
+        raise _elsewhere(t, what, device)
     if t.shape != shape:
         raise ValueError("%s: expected shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
     if dtype is not None and t.dtype is not dtype:
@@ -632,7 +632,8 @@ def _matrix(t, what: str, shape, device: int, dtype=None):
 
 
 def _vector(t, what: str, n: int, device: int, dtype=None):
-    _same_device(t, what, device)
+    if t.get_device() != device:
+        raise _elsewhere(t, what, device)
     if not t.is_contiguous() or t.numel() != n:
         raise ValueError("%s: expected a contiguous CUDA tensor of %d elements" % (what, n))
     if dtype is not None and t.dtype != dtype:
@@ -643,8 +644,8 @@ def _vector(t, what: str, n: int, device: int, dtype=None):
 def _workspace(t, device: int | None):
     if t is None:
         return None, 0
-    if device is not None:
-        _same_device(t, "workspace", device)
+    if device is not None and t.get_device() != device:
+        raise _elsewhere(t, "workspace", device)
     return _dptr(t), t.numel() * t.element_size()
 
 
@@ -785,7 +786,8 @@ class MuonUnit:
                     continue
                 if self.device is None:
                     self.device = _device(x, what)
-                _same_device(x, what, self.device)
+                if x.get_device() != self.device:
+                    raise _elsewhere(x, what, self.device)
         self._tensors = (MuonTensor * max(1, len(tensors)))(*tensors)
         arrays = dict(grads=_parray(grads, 2), master=_parray(master, 4), exp_avg=_parray(exp_avg, 4),
                       exp_avg_sq=_parray(exp_avg_sq, 4))
