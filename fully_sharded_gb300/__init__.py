@@ -31,6 +31,8 @@ __all__ = [
     "fsdp_rmsnorm", "fsdp_rmsnorm_backward", "fsdp_rmsnorm_backward_workspace",
     "NewtonSchulz", "NewtonSchulzBatch", "fsdp_newton_schulz", "fsdp_newton_schulz_workspace",
     "Muon", "MuonTensor", "MuonUnit", "fsdp_muon_step", "fsdp_muon_workspace",
+    "fsdp_embedding", "fsdp_embedding_backward", "fsdp_embedding_backward_workspace", "fsdp_dropout",
+    "fsdp_cross_entropy", "fsdp_cross_entropy_workspace",
 ]
 
 FSDP_OK = 0
@@ -43,9 +45,12 @@ NOALLOC_STAGING_BYTES = 64 << 20  # FSDP_NOALLOC_STAGING_BYTES of include/fsdp.h
 FSDP_DTYPE_F32 = 0
 FSDP_DTYPE_BF16 = 1
 FSDP_DTYPE_E4M3 = 2
+FSDP_DTYPE_I32 = 3
+FSDP_DTYPE_I64 = 4
 MAX_WORLD = 64
 
 _c_i32, _c_i64, _c_dbl, _c_p = ctypes.c_int32, ctypes.c_int64, ctypes.c_double, ctypes.c_void_p
+_c_u64 = ctypes.c_uint64
 
 
 class Layout(ctypes.Structure):
@@ -146,6 +151,29 @@ class MuonUnitArgs(ctypes.Structure):
                 ("master", _c_p), ("exp_avg", _c_p), ("exp_avg_sq", _c_p), ("full_out", _c_p)]
 
 
+class EmbeddingArgs(ctypes.Structure):
+    _fields_ = [("rows", _c_i64), ("cols", _c_i64), ("vocab", _c_i64), ("table_stride", _c_i64),
+                ("addend_stride", _c_i64), ("out_stride", _c_i64), ("dtype", _c_i32), ("token_dtype", _c_i32),
+                ("scale", _c_dbl)]
+
+
+class EmbeddingBackwardArgs(ctypes.Structure):
+    _fields_ = [("rows", _c_i64), ("cols", _c_i64), ("vocab", _c_i64), ("dout_stride", _c_i64),
+                ("dtable_stride", _c_i64), ("dtype", _c_i32), ("table_dtype", _c_i32), ("token_dtype", _c_i32),
+                ("accumulate", _c_i32), ("scale", _c_dbl)]
+
+
+class DropoutArgs(ctypes.Structure):
+    _fields_ = [("rows", _c_i64), ("cols", _c_i64), ("x_stride", _c_i64), ("residual_stride", _c_i64),
+                ("out_stride", _c_i64), ("seed", _c_u64), ("offset", _c_u64), ("dtype", _c_i32), ("p", _c_dbl)]
+
+
+class CrossEntropyArgs(ctypes.Structure):
+    _fields_ = [("rows", _c_i64), ("cols", _c_i64), ("vocab", _c_i64), ("hidden_stride", _c_i64),
+                ("weight_stride", _c_i64), ("dhidden_stride", _c_i64), ("dweight_stride", _c_i64), ("piece", _c_i64),
+                ("target_dtype", _c_i32), ("scale", _c_dbl)]
+
+
 class ZeroAccount(ctypes.Structure):
     _fields_ = [(n, _c_dbl) for n in ("weights_bytes", "grads_bytes", "optimizer_bytes", "total_bytes",
                                       "reduction_vs_ddp", "comm_elems")]
@@ -219,6 +247,12 @@ def _load():
                                          ctypes.POINTER(_c_i64)],
         "fsdp_muon_step": [ctypes.POINTER(MuonUnitArgs), ctypes.POINTER(Muon), P, _c_i64, P],
         "fsdp_muon_workspace": [ctypes.POINTER(MuonUnitArgs), ctypes.POINTER(Muon), ctypes.POINTER(_c_i64)],
+        "fsdp_embedding": [ctypes.POINTER(EmbeddingArgs), P, P, P, P, P],
+        "fsdp_embedding_backward": [ctypes.POINTER(EmbeddingBackwardArgs), P, P, P, P, _c_i64, P],
+        "fsdp_embedding_backward_workspace": [_c_i64, _c_i64, _c_i64, ctypes.POINTER(_c_i64)],
+        "fsdp_dropout": [ctypes.POINTER(DropoutArgs), P, P, P, P, P],
+        "fsdp_cross_entropy": [ctypes.POINTER(CrossEntropyArgs), P, P, P, P, P, P, P, P, P, _c_i64, P],
+        "fsdp_cross_entropy_workspace": [ctypes.POINTER(CrossEntropyArgs), _c_i32, ctypes.POINTER(_c_i64)],
     }
     for name, args in sigs.items():
         fn = getattr(lib, name)
@@ -815,3 +849,127 @@ def fsdp_muon_step(unit: MuonUnit, muon: Muon, workspace, stream=None):
     ws, ws_bytes = _workspace(workspace, unit.device)
     _check("fsdp_muon_step", _lib.fsdp_muon_step(ctypes.byref(unit.args), ctypes.byref(muon), ws, ws_bytes,
                                                  _cuda_stream(stream)))
+
+
+# -------------------------- operators at a model's ends and between its blocks
+
+def _index(t, what: str, n: int, device: int):
+    """(address, type code) of a contiguous vector of n 32- or 64-bit indexes on `device`."""
+    torch = _torch()
+    if t.dtype is torch.int64:
+        return _vector(t, what, n, device), FSDP_DTYPE_I64
+    if t.dtype is torch.int32:
+        return _vector(t, what, n, device), FSDP_DTYPE_I32
+    raise ValueError("%s: expected int32 or int64, got %s" % (what, t.dtype))
+
+
+def fsdp_embedding(tokens, table, out, scale: float = 1.0, addend=None, stream=None):
+    """out[r] = scale * table[tokens[r]] + addend[r]: tokens int32 or int64; table, addend and out float32 or
+    bfloat16; a negative token takes zeros for its row. out may be addend."""
+    shape = _shape2(out, "out")
+    rows, cols = shape
+    vocab, width = _shape2(table, "table")
+    if width != cols:
+        raise ValueError("table: expected rows of %d elements, got %d" % (cols, width))
+    code = _float_dtype(out, "out")
+    device = _device(out, "out")
+    _current_device(device, "out")
+    op, out_stride = _matrix(out, "out", shape, device)
+    wp, table_stride = _matrix(table, "table", table.shape, device, out.dtype)
+    ap, addend_stride = _matrix(addend, "addend", shape, device, out.dtype) if addend is not None else (None, cols)
+    tp, token_code = _index(tokens, "tokens", rows, device)
+    a = EmbeddingArgs(rows, cols, vocab, table_stride, addend_stride, out_stride, code, token_code, scale)
+    _check("fsdp_embedding", _lib.fsdp_embedding(ctypes.byref(a), tp, wp, ap, op, _cuda_stream(stream, device)))
+
+
+def fsdp_embedding_backward_workspace(rows: int, cols: int, vocab: int) -> int:
+    """Bytes of workspace that fsdp_embedding_backward needs (host only)."""
+    n = _c_i64(0)
+    _check("fsdp_embedding_backward_workspace",
+           _lib.fsdp_embedding_backward_workspace(rows, cols, vocab, ctypes.byref(n)))
+    return n.value
+
+
+def fsdp_embedding_backward(tokens, dout, dtable, workspace, scale: float = 1.0, accumulate: bool = False, stream=None):
+    """Gradient of fsdp_embedding's table: dtable[v] = scale * the sum of dout's rows whose token is v, in a fixed
+    order; accumulate: added to dtable, whose other rows stay (a tied table). dtable may be a view into a
+    rank's gradient row."""
+    shape = _shape2(dout, "dout")
+    rows, cols = shape
+    vocab, width = _shape2(dtable, "dtable")
+    if width != cols:
+        raise ValueError("dtable: expected rows of %d elements, got %d" % (cols, width))
+    device = _device(dout, "dout")
+    _current_device(device, "dout")
+    dp, dout_stride = _matrix(dout, "dout", shape, device)
+    wp, dtable_stride = _matrix(dtable, "dtable", dtable.shape, device)
+    tp, token_code = _index(tokens, "tokens", rows, device)
+    a = EmbeddingBackwardArgs(rows, cols, vocab, dout_stride, dtable_stride, _float_dtype(dout, "dout"),
+                              _float_dtype(dtable, "dtable"), token_code, 1 if accumulate else 0, scale)
+    ws, ws_bytes = _workspace(workspace, device)
+    _check("fsdp_embedding_backward", _lib.fsdp_embedding_backward(ctypes.byref(a), tp, dp, wp, ws, ws_bytes,
+                                                                   _cuda_stream(stream, device)))
+
+
+def fsdp_dropout(x, out, p: float, seed: int, offset: int = 0, residual=None, counter=None, stream=None):
+    """out = residual + dropout(x): each element is dropped with probability p (in steps of 2^-16), the others are
+    divided by what stays. The draws follow from seed, offset (0 .. 2^64 - 1) and an element's place; the gradient is
+    the same call on out's gradient without a residual. counter: an int64 CUDA tensor of one element that is
+    added to offset when the kernel runs (for captured graphs). out may be x or residual."""
+    shape = _shape2(x, "x")
+    rows, cols = shape
+    dtype = x.dtype
+    code = _float_dtype(x, "x")
+    device = _device(x, "x")
+    _current_device(device, "x")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError("seed and offset: expected 64-bit unsigned values, got %d and %d" % (seed, offset))
+    xp, x_stride = _matrix(x, "x", shape, device)
+    op, out_stride = _matrix(out, "out", shape, device, dtype)
+    rp, r_stride = _matrix(residual, "residual", shape, device, dtype) if residual is not None else (None, cols)
+    cp = _vector(counter, "counter", 1, device, _torch().int64) if counter is not None else None
+    a = DropoutArgs(rows, cols, x_stride, r_stride, out_stride, seed, offset, code, p)
+    _check("fsdp_dropout", _lib.fsdp_dropout(ctypes.byref(a), xp, rp, cp, op, _cuda_stream(stream, device)))
+
+
+def fsdp_cross_entropy_workspace(rows: int, cols: int, vocab: int, gradients: bool = True, piece: int = 0) -> int:
+    """Bytes of workspace that fsdp_cross_entropy needs (host only)."""
+    n = _c_i64(0)
+    a = CrossEntropyArgs(rows, cols, vocab, cols, cols, cols, cols, piece, FSDP_DTYPE_I64, 1.0)
+    _check("fsdp_cross_entropy_workspace",
+           _lib.fsdp_cross_entropy_workspace(ctypes.byref(a), 1 if gradients else 0, ctypes.byref(n)))
+    return n.value
+
+
+def fsdp_cross_entropy(hidden, weight, targets, loss, workspace, lse=None, dhidden=None, dweight=None,
+                       scale: float = 1.0, dloss=None, piece: int = 0, stream=None):
+    """Softmax cross entropy of hidden @ weight.T against targets: loss (and lse) fp32 [rows]; with dhidden and dweight
+    also the gradients of scale * sum(dloss * loss) (dloss None: ones). hidden, weight and their gradients are
+    bfloat16; a row with a negative target has loss 0 and no part in the gradients. The logits are
+    never stored; `piece` rows are worked on at a time (0: chosen; as given to the workspace's size)."""
+    torch = _torch()
+    shape = _shape2(hidden, "hidden")
+    rows, cols = shape
+    vocab, width = _shape2(weight, "weight")
+    if width != cols:
+        raise ValueError("weight: expected rows of %d elements, got %d" % (cols, width))
+    if (dhidden is None) != (dweight is None):
+        raise ValueError("dhidden and dweight: expected both or neither")
+    bf16, f32 = torch.bfloat16, torch.float32
+    device = _device(hidden, "hidden")
+    _current_device(device, "hidden")
+    hp, hidden_stride = _matrix(hidden, "hidden", shape, device, bf16)
+    wp, weight_stride = _matrix(weight, "weight", weight.shape, device, bf16)
+    tp, target_code = _index(targets, "targets", rows, device)
+    lp = _vector(loss, "loss", rows, device, f32)
+    sp = _vector(lse, "lse", rows, device, f32) if lse is not None else None
+    gp = _vector(dloss, "dloss", rows, device, f32) if dloss is not None else None
+    dhp = dwp = None
+    dh_stride = dw_stride = cols
+    if dhidden is not None:
+        dhp, dh_stride = _matrix(dhidden, "dhidden", shape, device, bf16)
+        dwp, dw_stride = _matrix(dweight, "dweight", weight.shape, device, bf16)
+    a = CrossEntropyArgs(rows, cols, vocab, hidden_stride, weight_stride, dh_stride, dw_stride, piece, target_code, scale)
+    ws, ws_bytes = _workspace(workspace, device)
+    _check("fsdp_cross_entropy", _lib.fsdp_cross_entropy(ctypes.byref(a), hp, wp, tp, gp, lp, sp, dhp, dwp, ws, ws_bytes,
+                                                         _cuda_stream(stream, device)))

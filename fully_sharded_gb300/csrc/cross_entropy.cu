@@ -1,0 +1,870 @@
+// Softmax cross entropy of a projection onto a vocabulary, with its gradients
+// (fsdp_cross_entropy).
+//
+//   x = H W^T,  lse_r = log sum_v exp(x_rv),  loss_r = lse_r - x_rt
+//   dH = G W,  dW = G^T H,  G_rv = g_r (exp(x_rv - lse_r) - [v = t_r])
+//
+// The logits x exist only as tiles in tensor memory and registers. What is kept of a
+// piece of rows is E = exp(x) in bf16, which the gradients' products read as it
+// is: with s_r = g_r exp(-lse_r),
+//   dH_r = s_r sum_v E_rv W_v,   dW_v = sum_r E_rv (s_r H_r),
+// so that normalising takes a factor per row (in the epilogue of the first product, in a scaled
+// copy of H for the second) and no pass over E, and the targets' -1 is one element of each
+// row: E_rt = exp(lse_r) expm1(x_rt - lse_r). bf16's exponents hold exp(x) for |x| up to 87; a row
+// with |lse| or the largest logit of some 128 columns beyond 60 (or not finite) goes by the
+// general form instead: its E is kept relative to each such span's own maximum and
+// rescaled to exp(x - lse) once lse is known.
+//
+// Launches for each piece: the scores (product and statistics), the rows (lse, loss,
+// targets, scaled H), the gradients' two products together.
+#include "host_internal.h"
+#include "launch.h"
+#include "strided.h"
+#include "tensor_core.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+namespace fsdp {
+namespace {
+
+using namespace tc;
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+constexpr float kPlainRange = 60.0f;              // of the logits of a row whose E is exp(x) itself
+
+constexpr int kTileK = 64;
+constexpr int kN = 256;                           // columns of a tile
+constexpr int kSpan = 128;                        // columns of a tile that one thread holds; of one statistic
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpilogueWarps;  // producer, products, two idle warps, epilogue
+constexpr int kBoxBytes = 32 * 64 * 2;            // what a warp sends at once: 32 rows of 64 columns
+constexpr int kOutBytes = kEpilogueWarps * 2 * kBoxBytes;
+// Registers after the start: 384 threads come with 168 each.
+constexpr int kLeanRegisters = 56, kEpilogueRegisters = 224;
+static_assert(128 * kLeanRegisters + 32 * kEpilogueWarps * kEpilogueRegisters <= kThreads * 168, "register split");
+
+// A tile: 128 rows per block of the pair (or single block) and 256 columns.
+template <int kPair>
+struct Tile {
+  static constexpr int kM = 128 * kPair;
+  static constexpr int kBRows = kN / kPair;  // a block's part of the second operand
+  static constexpr int kABytes = 128 * kTileK * 2, kBBytes = kBRows * kTileK * 2;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = (230400 - 1024 - kOutBytes) / kStageBytes;
+  static constexpr int kSmemBytes = kStages * kStageBytes + kOutBytes + 1024;
+  static constexpr int kTmemCols = 2 * kN;
+};
+
+enum Result : int32_t {
+  kScores,   // E and the statistics of a piece's logits
+  kRows,     // bf16 rows, times a factor per row
+  kPartial,  // fp32, a part of the inner dimension: joined later
+  kAdd,      // fp32 sum over the pieces: written by the first, added to by the others
+  kLast,     // bf16 rows of that sum and the last piece's
+};
+
+// C[m, n] = sum_k A[m, k] B[n, k].
+struct Product {
+  CUtensorMap a, b, out;   // boxes of 64 x 64 of the operands; of 32 x 64 of the result
+  int32_t m, n, k;
+  int32_t row_tiles, col_tiles, tiles;
+  int32_t splits, split_steps;  // parts of the inner dimension, and their length in steps of 64
+  uint8_t a_mn, b_mn;      // the operand's row index (of C's rows, columns) is the contiguous one
+  uint8_t rows_first;      // order of the tiles
+  uint8_t first;           // kAdd: the first piece
+  int32_t result;
+  uint16_t* rows;          // kRows, kLast: where the bf16 rows go if `out` cannot describe them, else null
+  int64_t rows_stride;
+  const float* factor;     // kRows: of each row (null: 1)
+  float* wide;             // kPartial, kAdd, kLast: fp32, a row `wide_stride` from the next
+  int64_t wide_stride;
+};
+
+struct Params {
+  Product product[2];
+  int32_t count, tiles;
+  int32_t segment;         // steps of 64 that are summed in tensor memory
+  int32_t index_bits;      // of the targets: 32 or 64
+  bool keep;               // E is kept
+  const void* targets;
+  float2* stats;           // [row][span]: largest logit, sum of exp(x - reference)
+  int64_t spans;
+  float* target_score;
+  unsigned int* status;
+};
+
+__device__ __forceinline__ int64_t index_at(const void* p, int bits, int64_t i) {
+  return bits == 64 ? static_cast<const int64_t*>(p)[i] : static_cast<const int32_t*>(p)[i];
+}
+
+// The reference of a span's exponentials: none where exp(x) itself can be kept.
+__device__ __forceinline__ float reference_of(float most) {
+  return !(fabsf(most) > kPlainRange) || most == -INFINITY ? 0.0f : most;
+}
+
+constexpr float kLog2e = 1.44269504088896341f;
+
+__device__ __forceinline__ void shared_store(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint16_t shared_load_half(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// bf16, bf16 -> fp32.
+__device__ __forceinline__ uint32_t bf16_kind(int m, int n, bool a_mn, bool b_mn) {
+  return product_kind(m, n, a_mn, b_mn) | (1u << 7) | (1u << 10);
+}
+
+struct Place {
+  int product, split, i, j;
+};
+
+__device__ __forceinline__ Place place_of(const Params& p, int t) {
+  Place q{0, 0, 0, 0};
+  if (p.count > 1 && t >= p.product[0].tiles) {
+    q.product = 1;
+    t -= p.product[0].tiles;
+  }
+  const Product& g = p.product[q.product];
+  const int each = g.row_tiles * g.col_tiles;
+  q.split = t / each;
+  t -= q.split * each;
+  if (g.rows_first) {
+    q.j = t / g.row_tiles;
+    q.i = t - q.j * g.row_tiles;
+  } else {
+    q.i = t / g.col_tiles;
+    q.j = t - q.i * g.col_tiles;
+  }
+  return q;
+}
+
+// Sends 64 columns of the warp's 32 rows (a lane's own row in v, as bf16), from (row0, col0) on.
+template <typename F>
+__device__ __forceinline__ void send_rows(const Product& g, uint32_t box, int row0, int col0, int lane, F value) {
+  if (lane == 0) bulk_wait_read<1>();  // the box before the last has left its place
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 two = __floats2bfloat162_rn(value(8 * q + 2 * k), value(8 * q + 2 * k + 1));
+      w[k] = *reinterpret_cast<const uint32_t*>(&two);
+    }
+    shared_store(box + lane * 128 + ((q ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+  }
+  if (!g.rows) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) tma_store(&g.out, col0, row0, box);
+  } else {  // rows off 16-byte alignment, element by element
+    __syncwarp();
+    const int rows = min(32, g.m - row0);
+    for (int r = 0; r < rows; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = 32 * h + lane;
+        if (col0 + c >= g.n) continue;
+        g.rows[(row0 + r) * g.rows_stride + col0 + c] =
+            shared_load_half(box + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2);
+      }
+    __syncwarp();
+  }
+  if (lane == 0) bulk_commit();
+}
+
+template <int kPair, bool kIsScores>
+__global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant__ Params p) {
+  using T = Tile<kPair>;
+  extern __shared__ unsigned char raw[];
+  __shared__ __align__(8) uint64_t full_bar[T::kStages], empty_bar[T::kStages], done_bar[2], free_bar[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int stop;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+  const uint32_t smem = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t boxes = smem + T::kStages * T::kStageBytes;
+  const int rank = kPair == 2 ? static_cast<int>(block_rank()) : 0;
+  const int cluster = blockIdx.x / kPair, clusters = gridDim.x / kPair;
+  const Guard guard{&stop, p.status, kWaitLimitNs};
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < T::kStages; ++s) {
+      bar_init(smem_addr(&full_bar[s]), 1);
+      bar_init(smem_addr(&empty_bar[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      bar_init(smem_addr(&done_bar[b]), 1);
+      bar_init(smem_addr(&free_bar[b]), kEpilogueWarps * kPair);
+    }
+    stop = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // Held while this grid waits for the previous one, which is safe: with its 220 KB a block shares its SM
+  // with no other block that has tensor memory, and the next launch starts after this barrier.
+  if (warp == 1) tmem_alloc<kPair>(smem_addr(&tmem_slot), T::kTmemCols);
+  fence_before();
+  __syncthreads();
+  if constexpr (kPair == 2) cluster_sync();
+  fence_after();
+  const uint32_t tmem = tmem_slot;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const auto await_inputs = [] { asm volatile("griddepcontrol.wait;" ::: "memory"); };
+  // steps of a tile's inner dimension, from step `from` on
+  const auto inner = [](const Product& g, int split, int* from) {
+    *from = split * g.split_steps;
+    return min(g.split_steps, (g.k + kTileK - 1) / kTileK - *from);
+  };
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeanRegisters));
+    if (warp == 0) {  // producer: this block's rows of both operands
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = cluster; ok && t < p.tiles; t += clusters) {
+        const Place at = place_of(p, t);
+        const Product& g = p.product[at.product];
+        int from;
+        const int steps = inner(g, at.split, &from);
+        const int row0 = at.i * T::kM + rank * 128, col0 = at.j * kN + rank * T::kBRows;
+        const bool a_mn = g.a_mn, b_mn = g.b_mn;
+        for (int step = 0; step < steps; ++step, ++it) {
+          const int s = it % T::kStages;
+          ok = bar_wait_warp(smem_addr(&empty_bar[s]), ((it / T::kStages) & 1u) ^ 1u, guard);
+          if (!ok) break;
+          // the first block's barrier counts the bytes of both
+          const uint32_t own = smem_addr(&full_bar[s]), bar = kPair == 2 ? in_block(own, 0) : own;
+          const uint32_t a = smem + s * T::kStageBytes, b = a + T::kABytes;
+          const int k0 = (from + step) * kTileK;
+          if (it == 0) await_inputs();
+          if (elect_one()) {
+            if (rank == 0) bar_expect(own, T::kStageBytes * kPair);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int r = row0 + 64 * q;
+              tma_box<kPair>(a + q * 8192, &g.a, a_mn ? r : k0, a_mn ? k0 : r, bar);
+            }
+#pragma unroll
+            for (int q = 0; q < T::kBRows / 64; ++q) {
+              const int c = col0 + 64 * q;
+              tma_box<kPair>(b + q * 8192, &g.b, b_mn ? c : k0, b_mn ? k0 : c, bar);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      // every copy lands (its stage is used and released) before the block ends
+      for (uint32_t back = 1; back <= T::kStages && back <= it; ++back) {
+        const uint32_t last = it - back;
+        const uint64_t* bar = rank == 0 ? full_bar : empty_bar;
+        bar_drain(smem_addr(&bar[last % T::kStages]), (last / T::kStages) & 1u, kWaitLimitNs);
+      }
+    } else if (warp == 1 && rank == 0) {  // products, for both blocks of a pair
+      uint32_t it = 0, n = 0;             // steps; segments
+      bool ok = true;
+      for (int t = cluster; ok && t < p.tiles; t += clusters) {
+        const Place at = place_of(p, t);
+        const Product& g = p.product[at.product];
+        int from;
+        const int steps = inner(g, at.split, &from);
+        if (it == 0) await_inputs();  // the limit of the waits below does not run while earlier kernels do
+        const uint32_t kind = bf16_kind(T::kM, kN, g.a_mn, g.b_mn);
+        // bytes from one 16-deep product's operand to the next, and between blocks of 64 rows
+        const uint32_t a_step = g.a_mn ? 2048 : 32, b_step = g.b_mn ? 2048 : 32;
+        const uint32_t a_block = g.a_mn ? 8192 : 0, b_block = g.b_mn ? 8192 : 0;
+        for (int step0 = 0; ok && step0 < steps; step0 += p.segment, ++n) {
+          const uint32_t buf = n & 1u, d = tmem + buf * kN;
+          ok = bar_wait_warp(smem_addr(&free_bar[buf]), ((n >> 1) & 1u) ^ 1u, guard);
+          if (!ok) break;
+          fence_after();
+          const int count = min(p.segment, steps - step0);
+          for (int step = 0; step < count; ++step, ++it) {
+            const int s = it % T::kStages;
+            ok = bar_wait_warp(smem_addr(&full_bar[s]), (it / T::kStages) & 1u, guard);
+            if (!ok) break;
+            fence_after();
+            const uint32_t a = smem + s * T::kStageBytes, b = a + T::kABytes;
+            const uint64_t da = operand(a, a_block, 1024), db = operand(b, b_block, 1024);
+            if (elect_one()) {
+#pragma unroll
+              for (int q = 0; q < kTileK / 16; ++q)
+                mma<kPair>(d, da + (q * a_step >> 4), db + (q * b_step >> 4), kind, step > 0 || q > 0);
+              mma_commit<kPair>(smem_addr(&empty_bar[s]));
+            }
+            __syncwarp();
+          }
+          if (ok && elect_one()) mma_commit<kPair>(smem_addr(&done_bar[buf]));
+          __syncwarp();
+        }
+      }
+      if (!ok && it > 0)  // products in flight end before the accumulators are freed
+        bar_drain(smem_addr(&empty_bar[(it - 1) % T::kStages]), ((it - 1) / T::kStages) & 1u, kWaitLimitNs);
+    }
+  } else {  // epilogue: this block's 128 rows, 128 columns of one row in each thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegisters));
+    const int own = warp - 4, quarter = own & 3, half = own >> 2;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kSpan;
+    const uint32_t box = boxes + own * 2 * kBoxBytes;
+    uint32_t n = 0, sent = 0;
+    bool ok = true;
+    await_inputs();
+    for (int t = cluster; ok && t < p.tiles; t += clusters) {
+      const Place at = place_of(p, t);
+      const Product& g = p.product[at.product];
+      int from;
+      const int steps = inner(g, at.split, &from);
+      float x[kSpan];
+#pragma unroll
+      for (int c = 0; c < kSpan; ++c) x[c] = 0.0f;
+      for (int step0 = 0; ok && step0 < steps; step0 += p.segment, ++n) {
+        const uint32_t buf = n & 1u;
+        ok = bar_wait_warp(smem_addr(&done_bar[buf]), (n >> 1) & 1u, guard);
+        if (!ok) break;
+        fence_after();
+#pragma unroll
+        for (int c = 0; c < kSpan; c += 32) {
+          float v[32];
+          tmem_load32(lanes + buf * kN + c, v);
+#pragma unroll
+          for (int q = 0; q < 32; ++q) x[c + q] += v[q];
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kPair == 2)
+            bar_arrive_cluster(in_block(smem_addr(&free_bar[buf]), 0));
+          else
+            bar_arrive(smem_addr(&free_bar[buf]));
+        }
+      }
+      if (!ok) break;
+      const int row0 = (at.i * kPair + rank) * 128 + quarter * 32, row = row0 + lane;
+      const int col0 = at.j * kN + half * kSpan;
+      if (row0 >= g.m || col0 >= g.n) continue;  // the same for the warp
+      if constexpr (kIsScores) {
+        if (col0 + kSpan > g.n)
+#pragma unroll
+          for (int c = 0; c < kSpan; ++c)
+            if (col0 + c >= g.n) x[c] = -INFINITY;
+        if (row < g.m) {
+          const int64_t target = index_at(p.targets, p.index_bits, row) - col0;
+          if (target >= 0 && target < kSpan) {
+            float score = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kSpan; ++c) score += c == static_cast<int>(target) ? x[c] : 0.0f;  // x stays in registers
+            p.target_score[row] = score;
+          }
+        }
+        float most = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kSpan; ++c) most = fmaxf(most, x[c]);
+        const float shift = reference_of(most) * kLog2e;
+        float sum[4] = {};
+#pragma unroll
+        for (int c = 0; c < kSpan; ++c) {
+          x[c] = exp2f(fmaf(x[c], kLog2e, -shift));
+          sum[c & 3] += x[c];
+        }
+        if (row < g.m) p.stats[row * p.spans + col0 / kSpan] = make_float2(most, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+        if (!p.keep) continue;
+#pragma unroll
+        for (int c = 0; c < kSpan; c += 64) {
+          if (col0 + c >= g.n) continue;
+          send_rows(g, box + (sent++ & 1) * kBoxBytes, row0, col0 + c, lane, [&](int q) { return x[c + q]; });
+        }
+      } else {
+        if (g.result != kRows) {
+          float* wide = g.wide + (static_cast<int64_t>(at.split) * g.m + row) * g.wide_stride + col0;
+          const bool add = g.result == kLast || (g.result == kAdd && !g.first);
+          // a row holds whole groups of 8 elements
+          if (row < g.m) {
+#pragma unroll
+            for (int c = 0; c < kSpan; c += 4) {
+              if (col0 + c >= g.wide_stride) continue;
+              float4* to = reinterpret_cast<float4*>(wide + c);
+              if (add) {
+                const float4 old = *to;
+                x[c] += old.x, x[c + 1] += old.y, x[c + 2] += old.z, x[c + 3] += old.w;
+              }
+              if (g.result != kLast) *to = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+            }
+          }
+          if (g.result != kLast) continue;
+          __syncwarp();
+        }
+        const float factor = g.factor && row < g.m ? g.factor[row] : 1.0f;
+#pragma unroll
+        for (int c = 0; c < kSpan; c += 64) {
+          if (col0 + c >= g.n) continue;
+          send_rows(g, box + (sent++ & 1) * kBoxBytes, row0, col0 + c, lane,
+                    [&](int q) { return factor == 0.0f ? 0.0f : x[c + q] * factor; });
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if constexpr (kPair == 2) cluster_sync();  // neither block leaves while the other may signal it
+  fence_after();
+  if (warp == 1) tmem_free<kPair>(tmem, T::kTmemCols);
+}
+
+// ------------------------------------------------------------------ the rows
+
+constexpr int kRowWarps = 8;
+
+struct RowParams {
+  const float2* stats;
+  int64_t spans;
+  const float* target_score;
+  const void* targets;
+  int32_t index_bits, rows, cols, vocab;
+  bool keep;
+  float scale;
+  const float* dloss;
+  float *loss, *lse;
+  float* factor;           // s_r
+  uint16_t* e;
+  int64_t e_stride;
+  const uint16_t* hidden;
+  int64_t hidden_stride;
+  uint16_t* scaled;        // s_r H_r
+  int64_t scaled_stride;
+};
+
+__device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+
+__device__ __forceinline__ float warp_sum(float v) {
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// A warp per row of the piece: its lse and loss from the spans' statistics; for the
+// gradients its factor, its target's element of E and its scaled row of H.
+__global__ void __launch_bounds__(32 * kRowWarps) ce_rows(const __grid_constant__ RowParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x % 32;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + threadIdx.x / 32;
+  if (row >= p.rows) return;
+  const float2* stats = p.stats + row * p.spans;
+  float most = -INFINITY, far = 0.0f, sum = 0.0f;
+  for (int64_t i = lane; i < p.spans; i += 32) {
+    const float2 s = stats[i];
+    most = fmaxf(most, s.x);
+    far = fmaxf(far, fabsf(s.x));
+    sum += s.y;
+  }
+  most = warp_max(most);
+  far = warp_max(far);
+  float lse;
+  if (!(far > kPlainRange)) {
+    lse = logf(warp_sum(sum));
+  } else {
+    sum = 0.0f;
+    for (int64_t i = lane; i < p.spans; i += 32) {
+      const float2 s = stats[i];
+      sum += s.y == 0.0f ? 0.0f : s.y * expf(reference_of(s.x) - most);
+    }
+    lse = most + logf(warp_sum(sum));
+  }
+  const int64_t target = index_at(p.targets, p.index_bits, row);
+  const bool there = target >= 0;
+  const float score = there && target < p.vocab ? p.target_score[row] : NAN;
+  if (lane == 0) {
+    p.loss[row] = there ? lse - score : 0.0f;
+    if (p.lse) p.lse[row] = lse;
+  }
+  if (!p.keep) return;
+  const float g = there ? (target < p.vocab ? p.scale * (p.dloss ? p.dloss[row] : 1.0f) : NAN) : 0.0f;
+  uint16_t* e = p.e + row * p.e_stride;
+  const bool plain = !(far > kPlainRange) && fabsf(lse) <= kPlainRange;
+  // The target's element is the largest of the row's: its rounding to bf16 goes into the row's factor
+  // (relative to which the others, rounded too, are then off by one more rounding).
+  float factor = g;
+  const bool has = there && target < p.vocab;
+  const float exact = has ? (plain ? expf(lse) : 1.0f) * expm1f(score - lse) : 0.0f;
+  const uint16_t rounded = bf16_bits(exact);
+  if (plain) factor *= expf(-lse);
+  if (bf16_value(rounded) != 0.0f) factor *= exact / bf16_value(rounded);
+  if (plain) {
+    if (lane == 0 && has) e[target] = rounded;
+  } else {
+    for (int64_t v = lane; v < p.vocab; v += 32) {
+      const float kept = bf16_value(e[v]);  // zeros stay: their span's factor may not be finite
+      const float own = kept == 0.0f && lse == lse ? 0.0f : kept * expf(reference_of(stats[v / kSpan].x) - lse);
+      e[v] = !there ? uint16_t(0) : v == target ? rounded : bf16_bits(own);
+    }
+  }
+  if (lane == 0) p.factor[row] = factor;
+  const uint16_t* h = p.hidden + row * p.hidden_stride;
+  uint16_t* scaled = p.scaled + row * p.scaled_stride;
+  for (int c = lane; c < p.cols; c += 32) scaled[c] = factor == 0.0f ? uint16_t(0) : bf16_bits(bf16_value(h[c]) * factor);
+}
+
+// ------------------------------------------------- copies and joined results
+
+struct CopyParams {
+  const uint16_t* from;
+  int64_t from_stride;
+  uint16_t* to;
+  int64_t to_stride;
+  int64_t rows, cols;
+};
+
+// Rows off 16-byte alignment into rows that tensor maps can describe.
+__global__ void __launch_bounds__(256) ce_copy(const __grid_constant__ CopyParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x % 32;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; r < p.rows; r += static_cast<int64_t>(gridDim.x) * 8)
+    for (int64_t c = lane; c < p.cols; c += 32) p.to[r * p.to_stride + c] = p.from[r * p.from_stride + c];
+}
+
+struct JoinParams {
+  const float* wide;
+  int64_t wide_stride;
+  int32_t splits;
+  int64_t rows, cols;
+  const float* factor;
+  uint16_t* out;
+  int64_t out_stride;
+};
+
+// The sum of a product's parts, times the row's factor.
+__global__ void __launch_bounds__(256) ce_join(const __grid_constant__ JoinParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t per_row = (p.cols + 255) / 256;
+  const int64_t row = blockIdx.x / per_row, col = (blockIdx.x - row * per_row) * 256 + threadIdx.x;
+  if (col >= p.cols) return;
+  float sum = 0.0f;
+  for (int s = 0; s < p.splits; ++s) sum += p.wide[(s * p.rows + row) * p.wide_stride + col];
+  const float factor = p.factor[row];
+  p.out[row * p.out_stride + col] = bf16_bits(factor == 0.0f ? 0.0f : sum * factor);
+}
+
+// ---------------------------------------------------------------------- host
+
+constexpr int64_t kMaxCols = int64_t(1) << 24, kMaxVocab = int64_t(1) << 30, kMaxRows = int64_t(1) << 40;
+constexpr int64_t kPieceBytes = int64_t(1) << 30;  // of E
+constexpr int64_t kMaxPiece = 1 << 20;
+
+int64_t round_to(int64_t n, int64_t k) { return (n + k - 1) / k * k; }
+
+// The sizes of a call and its workspace.
+struct Plan {
+  int64_t piece, pieces;   // rows of a piece
+  int64_t spans, e_stride, h_stride;
+  int pair, splits, split_steps;
+  int64_t stats, target_score, factor, e, scaled, hidden, weight, sum, partial, bytes;  // offsets
+};
+
+int make_plan(const fsdp_cross_entropy_t& a, bool gradients, Plan* out) {
+  if (a.rows < 0 || a.rows > kMaxRows || a.cols < 1 || a.cols > kMaxCols || a.vocab < 1 || a.vocab > kMaxVocab ||
+      a.piece < 0)
+    return FSDP_EINVAL;
+  Plan p{};
+  p.spans = (a.vocab + kSpan - 1) / kSpan;
+  p.e_stride = round_to(a.vocab, 64);
+  p.h_stride = round_to(a.cols, 8);
+  int64_t piece = a.piece;
+  if (!piece) piece = std::max<int64_t>(256, kPieceBytes / (p.e_stride * 2) / 256 * 256);
+  p.piece = std::max<int64_t>(1, std::min({piece, a.rows, kMaxPiece}));
+  p.pieces = (a.rows + p.piece - 1) / p.piece;
+  p.pair = p.piece <= 128 ? 1 : 2;
+  const int clusters = 152 / p.pair;
+  const int64_t tiles = ((p.piece + 128 * p.pair - 1) / (128 * p.pair)) * ((a.cols + kN - 1) / kN);
+  const int64_t steps = (a.vocab + kTileK - 1) / kTileK;
+  p.splits = static_cast<int>(std::max<int64_t>(1, std::min(clusters / tiles, steps / 8)));
+  p.split_steps = static_cast<int>((steps + p.splits - 1) / p.splits);
+  p.splits = static_cast<int>((steps + p.split_steps - 1) / p.split_steps);
+  int64_t at = 256;  // the caller's pointer may have any alignment
+  const auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += round_to(bytes, 256);
+    return here;
+  };
+  p.stats = take(p.piece * p.spans * 8);
+  p.target_score = take(p.piece * 4);
+  p.hidden = take(p.piece * p.h_stride * 2);
+  p.weight = take(a.vocab * p.h_stride * 2);
+  if (gradients) {
+    p.factor = take(p.piece * 4);
+    p.e = take(p.piece * p.e_stride * 2);
+    p.scaled = take(p.piece * p.h_stride * 2);
+    if (p.pieces > 1) p.sum = take(a.vocab * p.h_stride * 4);
+    if (p.splits > 1) p.partial = take(p.splits * p.piece * p.h_stride * 4);
+  }
+  p.bytes = at;
+  *out = p;
+  return FSDP_OK;
+}
+
+// Whether a tensor map can describe these bf16 rows.
+bool mappable(const void* p, int64_t rows, int64_t stride) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows < 2 || stride % 8 == 0);
+}
+
+bool bf16_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t stride, int box_rows) {
+  if (rows < 2) stride = round_to(cols, 8);  // not used
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows, cols, stride, box_rows);
+}
+
+// How many clusters of the kernel run at once (looked up once per device).
+template <int kPair, bool kIsScores>
+int resident_clusters(const Device& dev) {
+  using T = Tile<kPair>;
+  static std::atomic<int> cached[64];
+  if (dev.id >= 64) return 0;
+  int n = cached[dev.id].load(std::memory_order_acquire);
+  if (n) return n;
+  const auto kernel = ce_product<kPair, kIsScores>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmemBytes) != cudaSuccess) return 0;
+  if (kPair == 1) {
+    n = dev.sms;
+  } else {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(dev.sms / kPair * kPair);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = T::kSmemBytes;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kPair;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 0;
+  }
+  cached[dev.id].store(n, std::memory_order_release);
+  return n;
+}
+
+template <int kPair, bool kIsScores>
+int launch_products(Params& p, const Device& dev, cudaStream_t stream) {
+  using T = Tile<kPair>;
+  p.tiles = 0;
+  for (int i = 0; i < p.count; ++i) {
+    Product& g = p.product[i];
+    g.row_tiles = (g.m + T::kM - 1) / T::kM;
+    g.col_tiles = (g.n + kN - 1) / kN;
+    g.tiles = g.row_tiles * g.col_tiles * g.splits;
+    p.tiles += g.tiles;
+  }
+  const int room = resident_clusters<kPair, kIsScores>(dev);
+  if (room < 1) return FSDP_ECUDA;
+  return launch_after(ce_product<kPair, kIsScores>, std::min(p.tiles, room) * kPair, kPair, kThreads, T::kSmemBytes, stream, p);
+}
+
+int steps_of(int64_t k) { return static_cast<int>((k + kTileK - 1) / kTileK); }
+
+int copy_rows(const uint16_t* from, int64_t from_stride, uint16_t* to, int64_t to_stride, int64_t rows, int64_t cols,
+              cudaStream_t st) {
+  const CopyParams p{from, from_stride, to, to_stride, rows, cols};
+  return launch_after(ce_copy, static_cast<int>(std::min<int64_t>((rows + 7) / 8, 152 * 8)), 1, 256, 0, st, p);
+}
+
+struct Call {
+  const uint16_t *hidden, *weight;
+  const void* targets;
+  const float* dloss;
+  float *loss, *lse;
+  uint16_t *dhidden, *dweight;
+};
+
+int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* workspace, cudaStream_t st) {
+  Device dev;
+  if (int rc = device_facts(&dev)) return rc;
+  if (!encoder()) return FSDP_ECUDA;
+  auto* base = reinterpret_cast<unsigned char*>(round_to(reinterpret_cast<intptr_t>(workspace), 256) - 256);
+  const auto at = [&](int64_t offset) { return base + offset; };
+  const bool gradients = c.dhidden != nullptr;
+  const int index_bytes = a.target_dtype == FSDP_DTYPE_I64 ? 8 : 4;
+  const uint16_t* weight = c.weight;
+  int64_t weight_stride = a.weight_stride;
+  if (!mappable(weight, a.vocab, weight_stride)) {
+    auto* copy = reinterpret_cast<uint16_t*>(at(plan.weight));
+    if (int rc = copy_rows(weight, weight_stride, copy, plan.h_stride, a.vocab, a.cols, st)) return rc;
+    weight = copy;
+    weight_stride = plan.h_stride;
+  }
+  Params scores{}, products{};
+  RowParams rows{};
+  scores.count = 1;
+  scores.segment = 16;
+  products.segment = 64;
+  scores.status = products.status = dev.status;
+  scores.index_bits = rows.index_bits = 8 * index_bytes;
+  scores.keep = rows.keep = gradients;
+  scores.stats = reinterpret_cast<float2*>(at(plan.stats));
+  rows.stats = scores.stats;
+  scores.spans = rows.spans = plan.spans;
+  scores.target_score = reinterpret_cast<float*>(at(plan.target_score));
+  rows.target_score = scores.target_score;
+  rows.cols = static_cast<int32_t>(a.cols);
+  rows.vocab = static_cast<int32_t>(a.vocab);
+  rows.scale = static_cast<float>(a.scale);
+  if (gradients) {
+    rows.factor = reinterpret_cast<float*>(at(plan.factor));
+    rows.e = reinterpret_cast<uint16_t*>(at(plan.e));
+    rows.e_stride = plan.e_stride;
+    rows.scaled = reinterpret_cast<uint16_t*>(at(plan.scaled));
+    rows.scaled_stride = plan.h_stride;
+  }
+  rows.hidden_stride = a.hidden_stride;
+
+  for (int64_t r0 = 0; r0 < a.rows; r0 += plan.piece) {
+    const int64_t n = std::min(plan.piece, a.rows - r0);
+    const uint16_t* hidden = c.hidden + r0 * a.hidden_stride;
+    int64_t hidden_stride = a.hidden_stride;
+    rows.hidden = hidden;
+    if (!mappable(hidden, n, hidden_stride)) {
+      auto* copy = reinterpret_cast<uint16_t*>(at(plan.hidden));
+      if (int rc = copy_rows(hidden, hidden_stride, copy, plan.h_stride, n, a.cols, st)) return rc;
+      hidden = copy;
+      hidden_stride = plan.h_stride;
+    }
+    scores.targets = static_cast<const unsigned char*>(c.targets) + r0 * index_bytes;
+    rows.targets = scores.targets;
+    rows.rows = static_cast<int32_t>(n);
+    rows.dloss = c.dloss ? c.dloss + r0 : nullptr;
+    rows.loss = c.loss + r0;
+    rows.lse = c.lse ? c.lse + r0 : nullptr;
+
+    Product& s = scores.product[0];
+    s = Product{};
+    s.m = static_cast<int32_t>(n);
+    s.n = static_cast<int32_t>(a.vocab);
+    s.k = static_cast<int32_t>(a.cols);
+    s.splits = 1;
+    s.split_steps = steps_of(s.k);
+    s.rows_first = 1;
+    s.result = kScores;
+    bool ok = bf16_map(&s.a, hidden, n, a.cols, hidden_stride, 64) && bf16_map(&s.b, weight, a.vocab, a.cols, weight_stride, 64);
+    if (gradients) ok = ok && bf16_map(&s.out, rows.e, n, a.vocab, plan.e_stride, 32);
+    if (!ok) return FSDP_ECUDA;
+    if (int rc = plan.pair == 2 ? launch_products<2, true>(scores, dev, st) : launch_products<1, true>(scores, dev, st))
+      return rc;
+    if (int rc = launch_after(ce_rows, static_cast<int>((n + kRowWarps - 1) / kRowWarps), 1, 32 * kRowWarps, 0, st, rows))
+      return rc;
+    if (!gradients) continue;
+
+    products.count = 2;
+    uint16_t* dhidden = c.dhidden + r0 * a.dhidden_stride;
+    Product& dh = products.product[0];
+    dh = Product{};
+    dh.m = s.m;
+    dh.n = s.k;
+    dh.k = s.n;
+    dh.b_mn = 1;
+    dh.splits = plan.splits;
+    dh.split_steps = plan.split_steps;
+    dh.result = plan.splits > 1 ? kPartial : kRows;
+    dh.factor = rows.factor;
+    dh.wide = reinterpret_cast<float*>(at(plan.partial));
+    dh.wide_stride = plan.h_stride;
+    ok = bf16_map(&dh.a, rows.e, n, a.vocab, plan.e_stride, 64) && bf16_map(&dh.b, weight, a.vocab, a.cols, weight_stride, 64);
+    if (mappable(dhidden, n, a.dhidden_stride)) {
+      ok = ok && bf16_map(&dh.out, dhidden, n, a.cols, a.dhidden_stride, 32);
+    } else {
+      dh.rows = dhidden;
+      dh.rows_stride = a.dhidden_stride;
+    }
+    Product& dw = products.product[1];
+    dw = Product{};
+    dw.m = s.n;
+    dw.n = s.k;
+    dw.k = s.m;
+    dw.a_mn = dw.b_mn = 1;
+    dw.splits = 1;
+    dw.split_steps = steps_of(n);
+    dw.first = r0 == 0;
+    dw.result = plan.pieces == 1 ? kRows : r0 + n < a.rows ? kAdd : kLast;
+    dw.wide = reinterpret_cast<float*>(at(plan.sum));
+    dw.wide_stride = plan.h_stride;
+    dw.a = dh.a;
+    ok = ok && bf16_map(&dw.b, rows.scaled, n, a.cols, plan.h_stride, 64);
+    if (mappable(c.dweight, a.vocab, a.dweight_stride)) {
+      ok = ok && bf16_map(&dw.out, c.dweight, a.vocab, a.cols, a.dweight_stride, 32);
+    } else {
+      dw.rows = c.dweight;
+      dw.rows_stride = a.dweight_stride;
+    }
+    if (!ok) return FSDP_ECUDA;
+    if (int rc = plan.pair == 2 ? launch_products<2, false>(products, dev, st) : launch_products<1, false>(products, dev, st))
+      return rc;
+    if (plan.splits > 1) {
+      const JoinParams j{dh.wide, dh.wide_stride, dh.splits, n, a.cols, rows.factor, dhidden, a.dhidden_stride};
+      const int64_t blocks = n * ((a.cols + 255) / 256);
+      if (int rc = launch_after(ce_join, static_cast<int>(blocks), 1, 256, 0, st, j)) return rc;
+    }
+  }
+  return FSDP_OK;
+}
+
+}  // namespace
+}  // namespace fsdp
+
+using namespace fsdp;
+
+extern "C" int fsdp_cross_entropy_workspace(const fsdp_cross_entropy_t* a, int32_t gradients, int64_t* bytes_out) {
+  if (!a || !bytes_out) return FSDP_EINVAL;
+  Plan plan;
+  if (int rc = make_plan(*a, gradients != 0, &plan)) return rc;
+  *bytes_out = plan.bytes;
+  return FSDP_OK;
+}
+
+extern "C" int fsdp_cross_entropy(const fsdp_cross_entropy_t* a, const uint16_t* hidden, const uint16_t* weight,
+                                  const void* targets, const float* dloss, float* loss, float* lse, uint16_t* dhidden,
+                                  uint16_t* dweight, void* workspace, int64_t workspace_bytes, fsdp_stream_t stream) {
+  if (!a || (a->rows > 0 && !dhidden != !dweight)) return FSDP_EINVAL;
+  if (a->target_dtype != FSDP_DTYPE_I32 && a->target_dtype != FSDP_DTYPE_I64) return FSDP_EINVAL;
+  const bool gradients = dweight != nullptr;  // an empty dhidden may have no address
+  if (gradients ? !std::isfinite(static_cast<float>(a->scale)) : dloss != nullptr) return FSDP_EINVAL;
+  Plan plan;
+  if (int rc = make_plan(*a, gradients, &plan)) return rc;
+  const int is = a->target_dtype == FSDP_DTYPE_I64 ? 8 : 4;
+  const Strided sh{hidden, a->rows, a->cols, a->hidden_stride, 2}, sw{weight, a->vocab, a->cols, a->weight_stride, 2},
+      st{targets, 1, a->rows, a->rows, is}, sg{dloss, 1, a->rows, a->rows, 4}, sl{loss, 1, a->rows, a->rows, 4},
+      se{lse, 1, a->rows, a->rows, 4}, sdh{dhidden, a->rows, a->cols, a->dhidden_stride, 2},
+      sdw{dweight, a->vocab, a->cols, a->dweight_stride, 2}, ws{workspace, 1, plan.bytes, plan.bytes, 1};
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (gradients && !sdw.ok()) return FSDP_EINVAL;
+  if (a->rows == 0) {  // no rows: only the weight's gradient, zero
+    if (!gradients) return FSDP_OK;
+    return cudaMemset2DAsync(dweight, static_cast<size_t>(sdw.pitch() ? sdw.pitch() : a->cols * 2), 0,
+                             static_cast<size_t>(a->cols) * 2, static_cast<size_t>(a->vocab), cs) == cudaSuccess
+               ? FSDP_OK
+               : FSDP_ECUDA;
+  }
+  if (!sh.ok() || !sw.ok() || !st.ok() || !sl.ok() || !ws.ok() || (dloss && !sg.ok()) || (lse && !se.ok()) ||
+      (gradients && !sdh.ok()))
+    return FSDP_EINVAL;
+  if (workspace_bytes < plan.bytes) return FSDP_EWORKSPACE;
+  const Strided* in[] = {&sh, &sw, &st, dloss ? &sg : nullptr};
+  const Strided* out[] = {&sl, lse ? &se : nullptr, gradients ? &sdh : nullptr, gradients ? &sdw : nullptr, &ws};
+  for (const Strided* o : out) {
+    if (!o) continue;
+    for (const Strided* q : out)
+      if (q && q != o && o->overlaps(*q)) return FSDP_EALIAS;
+    for (const Strided* i : in)
+      if (i && o->overlaps(*i) && !(o == &sdh && i == &sh && o->same_place(*i))) return FSDP_EALIAS;
+  }
+  return run(*a, plan, Call{hidden, weight, targets, dloss, loss, lse, dhidden, dweight}, workspace, cs);
+}

@@ -38,6 +38,7 @@
 // columns at a time, as tiled stores. A and P are symmetric: tiles above the
 // diagonal are not computed, and the others are written to both places.
 #include "host_internal.h"
+#include "launch.h"
 #include "newton_schulz.h"
 #include "strided.h"
 #include "tensor_core.cuh"
@@ -1367,62 +1368,8 @@ int64_t carve(const NsJob& j, const NsPlan& plan, unsigned char* base, Buffers* 
   return at;
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder() {
-  static const EncodeTiled fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<EncodeTiled>(f);
-  }();
-  return fn;
-}
-
-// Boxes of 64 x 64 elements of a rows x cols fp16 matrix; outside it they read zeros.
 bool make_map(CUtensorMap* map, const __half* base, int64_t rows, int64_t cols, int64_t ld) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-  const cuuint32_t box[2] = {64, 64}, step[2] = {1, 1};
-  return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<__half*>(base), dims, strides, box, step,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-struct Device {
-  int id = 0, sms = 0;
-  unsigned int* status = nullptr;
-};
-
-int device_facts(Device* d) {
-  if (cudaGetDevice(&d->id) != cudaSuccess ||
-      cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, d->id) != cudaSuccess)
-    return FSDP_ECUDA;
-  return device_status_word(&d->status);
-}
-
-// Launches a kernel so that its blocks may be placed while the previous kernel of
-// the stream ends; the kernels wait for that one's results themselves.
-template <typename K, typename P>
-int launch_after(K kernel, int grid, int cluster, int threads, int smem, cudaStream_t stream, const P& p) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FSDP_OK : FSDP_ECUDA;
+  return fsdp::make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, rows, cols, ld, 64);
 }
 
 // How many clusters of the kernel run at once (looked up once per device).

@@ -11,7 +11,13 @@
 namespace fsdp {
 
 inline int size_of_dtype(int32_t dtype) {
-  return dtype == FSDP_DTYPE_F32 ? 4 : dtype == FSDP_DTYPE_BF16 ? 2 : dtype == FSDP_DTYPE_E4M3 ? 1 : 0;
+  switch (dtype) {
+    case FSDP_DTYPE_F32: case FSDP_DTYPE_I32: return 4;
+    case FSDP_DTYPE_BF16: return 2;
+    case FSDP_DTYPE_E4M3: return 1;
+    case FSDP_DTYPE_I64: return 8;
+    default: return 0;
+  }
 }
 
 // A row-major matrix at `p`: rows of `cols` elements of `size` bytes, `stride` elements apart.

@@ -676,6 +676,124 @@ int fsdp_muon_step(const fsdp_muon_unit_t *unit, const fsdp_muon_t *muon, void *
                    fsdp_stream_t stream);
 int fsdp_muon_workspace(const fsdp_muon_unit_t *unit, const fsdp_muon_t *muon, int64_t *bytes_out);
 
+/* ------------------------------------------------------------------------
+ * Operators at a model's two ends and between its blocks: what a root unit's
+ * tensors (embedding tables, the head) are used with. Matrices, workspaces,
+ * EINVAL, EALIAS and EWORKSPACE as above.
+ *
+ * Indexes (tokens, targets) are contiguous 32- or 64-bit integers in device memory,
+ * which the host does not read. A negative one stands for "none"; one that is not below
+ * `vocab` is a mistake of the caller, and what depends on it becomes NaN. */
+
+#define FSDP_DTYPE_I32 3
+#define FSDP_DTYPE_I64 4
+
+/* Embedding lookup: out_r = scale table[token_r] + addend_r, formed in fp32 and rounded
+ * once. table, addend (null: none) and out have type `dtype` (F32 or BF16). A token
+ * below 0 takes a row of zeros (the addend is still added), one from vocab on a row of
+ * NaN. out may be addend in place. rows = 0 launches nothing. EINVAL: cols, vocab < 1; rows < 0;
+ * any of them > 2^30; a stride below cols; a type or a scale (not finite as a float) outside
+ * the above; a missing pointer, one not aligned to its elements. */
+typedef struct {
+  int64_t rows;
+  int64_t cols;
+  int64_t vocab; /* rows of the table */
+  int64_t table_stride;
+  int64_t addend_stride;
+  int64_t out_stride;
+  int32_t dtype;
+  int32_t token_dtype; /* I32 or I64 */
+  double scale;
+} fsdp_embedding_t;
+
+int fsdp_embedding(const fsdp_embedding_t *args, const void *tokens, const void *table, const void *addend, void *out,
+                   fsdp_stream_t stream);
+
+/* Its gradient: dtable_v = scale times the sum of dout_r over the rows r with token_r = v;
+ * accumulate: added to what dtable_v holds (a tied table's other gradient), and the
+ * rows that no token names are left as they are, unread; else these are set to zero.
+ * Rows whose token is below 0, or not below vocab, take no part. Sums are fp32, in an order
+ * fixed by the tokens; each element is rounded once. dtable has table_dtype, dout `dtype` (F32 or
+ * BF16 each), and dtable may lie anywhere in a rank's bf16 gradient row. rows = 0 sets dtable to
+ * zero unless accumulate. */
+typedef struct {
+  int64_t rows;
+  int64_t cols;
+  int64_t vocab;
+  int64_t dout_stride;
+  int64_t dtable_stride;
+  int32_t dtype;
+  int32_t table_dtype;
+  int32_t token_dtype;
+  int32_t accumulate;
+  double scale;
+} fsdp_embedding_backward_t;
+
+int fsdp_embedding_backward(const fsdp_embedding_backward_t *args, const void *tokens, const void *dout, void *dtable,
+                            void *workspace, int64_t workspace_bytes, fsdp_stream_t stream);
+int fsdp_embedding_backward_workspace(int64_t rows, int64_t cols, int64_t vocab, int64_t *bytes_out);
+
+/* Dropout with the residual's addition: out = residual + (kept ? x k : 0), formed in
+ * fp32 and rounded once, with t = round(65536 p), k = 65536 / (65536 - t). Which elements are
+ * kept follows from seed, offset and the element's place alone: element i = row cols + column
+ * has draw i mod 8 of Philox4x32-10 (Salmon et al., 2011) with the 64-bit key `seed` and the
+ * counter (i / 8, offset + *counter), its four words taken as eight 16-bit draws, low half
+ * first, and is kept where its draw is at least t. No mask is stored: the gradient of x is the same
+ * call on out's gradient without a residual. Give each use (layer, step) an offset of its own.
+ * counter (device, may be null: 0) is read when the kernel runs, so that a captured graph can be
+ * replayed with new draws. A dropped element's x has no effect, be it NaN. x, residual (null:
+ * none) and out have type `dtype` (F32 or BF16); out may be x or residual in place. rows = 0
+ * launches nothing. EINVAL: p outside [0, 1), or rounded to 1 in 16 bits; sides > 2^40; as above. */
+typedef struct {
+  int64_t rows;
+  int64_t cols;
+  int64_t x_stride;
+  int64_t residual_stride;
+  int64_t out_stride;
+  uint64_t seed;
+  uint64_t offset;
+  int32_t dtype;
+  double p;
+} fsdp_dropout_t;
+
+int fsdp_dropout(const fsdp_dropout_t *args, const void *x, const void *residual, const uint64_t *counter, void *out,
+                 fsdp_stream_t stream);
+
+/* Softmax cross entropy of a projection onto a vocabulary, with its gradients:
+ *   x = hidden weight^T,  lse_r = log sum_v exp(x_rv),  loss_r = lse_r - x_r,target_r
+ *   G_rv = g_r (exp(x_rv - lse_r) - [v = target_r]),  g_r = scale dloss_r  (dloss null: scale)
+ *   dhidden = G weight,  dweight = G^T hidden
+ * hidden, weight, dhidden and dweight are bf16; dloss, loss and lse (may be null) fp32 [rows].
+ * dhidden and dweight are both given or both null (losses alone; dloss is null then). A row with
+ * a target below 0 has loss 0 and takes no part in the gradients, whatever its hidden row holds
+ * (its dhidden row is zero); its lse is that of its logits. One with a target from vocab on gives NaN.
+ * dweight may lie anywhere in a rank's bf16 gradient row; dhidden may be hidden in place.
+ * The products take bf16 operands on the tensor cores and sum in fp32 (logits in segments of 1024
+ * columns). The logits are not kept: the gradients take exp(x) rounded to bf16, of `piece` rows at a time
+ * (0: as many as keep that below 1 GiB, at least 256; at most 2^20), and dweight's sum over
+ * several pieces is fp32 in the workspace. Rows whose |lse|, or the largest logit of some 128
+ * columns of the vocabulary, is beyond 60 give the same results a little slower. rows = 0 sets
+ * dweight to zero. EINVAL: cols > 2^24, vocab > 2^30, rows > 2^40, piece < 0; a scale that is not
+ * finite as a float; as above. */
+typedef struct {
+  int64_t rows;
+  int64_t cols;
+  int64_t vocab; /* rows of the weight */
+  int64_t hidden_stride;
+  int64_t weight_stride;
+  int64_t dhidden_stride;
+  int64_t dweight_stride;
+  int64_t piece;
+  int32_t target_dtype; /* I32 or I64 */
+  double scale;
+} fsdp_cross_entropy_t;
+
+int fsdp_cross_entropy(const fsdp_cross_entropy_t *args, const uint16_t *hidden, const uint16_t *weight,
+                       const void *targets, const float *dloss, float *loss, float *lse, uint16_t *dhidden,
+                       uint16_t *dweight, void *workspace, int64_t workspace_bytes, fsdp_stream_t stream);
+/* Of the same args (their sizes and piece); gradients: whether dhidden and dweight will be given. */
+int fsdp_cross_entropy_workspace(const fsdp_cross_entropy_t *args, int32_t gradients, int64_t *bytes_out);
+
 /* Text of a status code (static storage). */
 const char *fsdp_status_string(int status);
 
