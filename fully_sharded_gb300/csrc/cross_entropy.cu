@@ -110,6 +110,13 @@ __device__ __forceinline__ float reference_of(float most) {
 
 constexpr float kLog2e = 1.44269504088896341f;
 
+// 2^x to 2^-22 of itself; results below 2^-126 are zero.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ void shared_store(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -359,7 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
           if (target >= 0 && target < kSpan) {
             float score = 0.0f;
 #pragma unroll
-            for (int c = 0; c < kSpan; ++c) score += c == static_cast<int>(target) ? x[c] : 0.0f;  // x stays in registers
+            for (int c = 0; c < kSpan; ++c)  // in this form the compiler does not index x, which would move it out of registers
+              asm("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mov.f32 %0, %2;\n}\n"
+                  : "+f"(score)
+                  : "r"(static_cast<int>(target) - c), "f"(x[c]));
             p.target_score[row] = score;
           }
         }
@@ -370,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
         float sum[4] = {};
 #pragma unroll
         for (int c = 0; c < kSpan; ++c) {
-          x[c] = exp2f(fmaf(x[c], kLog2e, -shift));
+          x[c] = exp2_fast(fmaf(x[c], kLog2e, -shift));
           sum[c & 3] += x[c];
         }
         if (row < g.m) p.stats[row * p.spans + col0 / kSpan] = make_float2(most, (sum[0] + sum[1]) + (sum[2] + sum[3]));
@@ -440,6 +450,7 @@ struct RowParams {
   int64_t hidden_stride;
   uint16_t* scaled;        // s_r H_r
   int64_t scaled_stride;
+  bool vectors;            // H's rows are whole groups of 8 at 16-byte boundaries
 };
 
 __device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
@@ -514,6 +525,20 @@ __global__ void __launch_bounds__(32 * kRowWarps) ce_rows(const __grid_constant_
   if (lane == 0) p.factor[row] = factor;
   const uint16_t* h = p.hidden + row * p.hidden_stride;
   uint16_t* scaled = p.scaled + row * p.scaled_stride;
+  if (p.vectors) {
+    for (int c = lane * 8; c < p.cols; c += 256) {
+      const uint4 v = *reinterpret_cast<const uint4*>(h + c);
+      const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+      uint32_t out[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(in[k] << 16) * factor, __uint_as_float(in[k] & 0xffff0000u) * factor);
+        out[k] = factor == 0.0f ? 0u : *reinterpret_cast<const uint32_t*>(&two);
+      }
+      *reinterpret_cast<uint4*>(scaled + c) = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+    return;
+  }
   for (int c = lane; c < p.cols; c += 32) scaled[c] = factor == 0.0f ? uint16_t(0) : bf16_bits(bf16_value(h[c]) * factor);
 }
 
@@ -733,6 +758,7 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
     const uint16_t* hidden = c.hidden + r0 * a.hidden_stride;
     int64_t hidden_stride = a.hidden_stride;
     rows.hidden = hidden;
+    rows.vectors = mappable(hidden, n, hidden_stride) && a.cols % 8 == 0;
     if (!mappable(hidden, n, hidden_stride)) {
       auto* copy = reinterpret_cast<uint16_t*>(at(plan.hidden));
       if (int rc = copy_rows(hidden, hidden_stride, copy, plan.h_stride, n, a.cols, st)) return rc;

@@ -8,11 +8,14 @@
 // indexes by token, so equal tokens keep the rows' order), and the sorted list is cut into chunks of
 // kChunk rows. A block adds the rows of a chunk, run by run of equal tokens, for
 // its columns: a run that lies in the chunk goes to the table at once, the parts of
-// one that crosses chunks go to the workspace in fp32 and are added in order by a second
-// kernel. Every sum is fp32 in an order fixed by the tokens alone.
+// one that crosses chunks go to the workspace in fp32 and are added in order by a
+// last kernel. Every sum is fp32 in an order fixed by the tokens alone.
+// Where the table is not added to, it is filled with zeros by the blocks that have no
+// part in the sort, meanwhile.
 #include "host_internal.h"
 #include "launch.h"
 #include "strided.h"
+#include "tensor_core.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -90,40 +93,216 @@ struct LookupParams {
   float scale;
 };
 
-constexpr int kLookupThreads = 128;
+constexpr int kLookupWarps = 8;
 
+// How many groups of kVec elements a lane has in flight.
+template <int kVec>
+constexpr int kGroups = kVec == 8 ? 4 : 8;
+
+// A warp takes 32 kGroups kVec consecutive elements of a row at a time. Bound by HBM.
 template <typename T, int kVec>
-__global__ void __launch_bounds__(kLookupThreads) embed_rows(const __grid_constant__ LookupParams p) {
+__global__ void __launch_bounds__(32 * kLookupWarps) embed_rows(const __grid_constant__ LookupParams p) {
   begin_after_previous();
-  const int64_t groups = (p.cols + kVec - 1) / kVec, per_row = (groups + kLookupThreads - 1) / kLookupThreads;
-  const int64_t blocks = p.rows * per_row;
-  for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-    const int64_t row = b / per_row, col = ((b - row * per_row) * kLookupThreads + threadIdx.x) * kVec;
-    if (col >= p.cols) continue;
+  constexpr int kQ = kGroups<kVec>, kUnit = 32 * kQ * kVec;
+  const uint32_t per_row = static_cast<uint32_t>((p.cols + kUnit - 1) / kUnit);
+  const int64_t units = p.rows * per_row;
+  const int lane = threadIdx.x % 32;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kLookupWarps + threadIdx.x / 32; u < units;
+       u += static_cast<int64_t>(gridDim.x) * kLookupWarps) {
+    const int64_t row = units >> 31 ? u / per_row : static_cast<uint32_t>(u) / per_row;
+    const int64_t col = (u - row * per_row) * kUnit + lane * kVec;
     const int64_t token = index_at(p.tokens, p.index_bits, row);
-    float v[kVec];
-    if (token >= 0 && token < p.vocab) {
-      load<kVec>(static_cast<const T*>(p.table) + token * p.table_stride + col, v);
+    const bool there = token >= 0 && token < p.vocab;
+    const T* from = static_cast<const T*>(p.table) + (there ? token : 0) * p.table_stride + col;
+    const T* addend = static_cast<const T*>(p.addend) + row * p.addend_stride + col;
+    float v[kQ][kVec], a[kQ][kVec] = {};
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) v[e] *= p.scale;
-    } else {
+    for (int q = 0; q < kQ; ++q)
+      if (col + q * 32 * kVec < p.cols) {
+        load<kVec>(from + q * 32 * kVec, v[q]);
+        if (p.addend) load<kVec>(addend + q * 32 * kVec, a[q]);
+      }
+    T* out = static_cast<T*>(p.out) + row * p.out_stride + col;
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) v[e] = token < 0 ? 0.0f : NAN;
-    }
-    if (p.addend) {
-      float a[kVec];
-      load<kVec>(static_cast<const T*>(p.addend) + row * p.addend_stride + col, a);
+    for (int q = 0; q < kQ; ++q)
+      if (col + q * 32 * kVec < p.cols) {
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) v[e] += a[e];
-    }
-    store<kVec>(static_cast<T*>(p.out) + row * p.out_stride + col, v);
+        for (int e = 0; e < kVec; ++e) v[q][e] = (there ? v[q][e] * p.scale : token < 0 ? 0.0f : NAN) + a[q][e];
+        store<kVec>(out + q * 32 * kVec, v[q]);
+      }
   }
 }
 
 // ---------------------------------------------------------------------- sort
 
-constexpr int kSortThreads = 256, kSortItems = 8, kSortBlock = kSortThreads * kSortItems;
+// Zeros: rows of `row_bytes` bytes, `pitch` apart, by `parts` blocks of which this is number `part`.
+struct FillParams {
+  unsigned char* to;
+  int64_t rows, row_bytes, pitch;  // row_bytes 0: nothing
+};
+
+__device__ __forceinline__ void fill_zeros(const FillParams& f, int part, int parts) {
+  // a row's bytes (a multiple of 2 from an even address): vectors inside, 2 bytes at a time at the ends
+  const auto fill = [](unsigned char* row, int64_t bytes, int64_t first, int64_t step) {
+    const int64_t head = min(bytes, static_cast<int64_t>(-reinterpret_cast<uintptr_t>(row) & 15u));
+    const int64_t vectors = (bytes - head) / 16, tail = head + vectors * 16;
+    for (int64_t i = first; i < vectors; i += step) reinterpret_cast<uint4*>(row + head)[i] = make_uint4(0, 0, 0, 0);
+    for (int64_t i = first; i < head / 2; i += step) reinterpret_cast<uint16_t*>(row)[i] = 0;
+    for (int64_t i = first; i < (bytes - tail) / 2; i += step) reinterpret_cast<uint16_t*>(row + tail)[i] = 0;
+  };
+  if (f.row_bytes == 0) return;
+  if (f.rows == 1) {
+    fill(f.to, f.row_bytes, static_cast<int64_t>(part) * blockDim.x + threadIdx.x, static_cast<int64_t>(parts) * blockDim.x);
+    return;
+  }
+  const int warps = blockDim.x / 32;
+  for (int64_t r = static_cast<int64_t>(part) * warps + threadIdx.x / 32; r < f.rows; r += static_cast<int64_t>(parts) * warps)
+    fill(f.to + r * f.pitch, f.row_bytes, threadIdx.x % 32, 32);
+}
+
+// Up to 8 x 16384 rows are sorted by one cluster of up to eight blocks, which holds them in
+// registers and moves them through (distributed) shared memory. In a pass each warp ranks its rows by digit, 32 at a
+// time; the places follow from the counts of all digits, blocks and warps. Bound by its own
+// latencies: the passes' barriers and 32-row steps.
 constexpr int kMaxBins = 512;
+constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32, kMaxRounds = 16, kMaxCluster = 8;
+constexpr int kClusterRows = kMaxCluster * kMaxRounds * kClusterThreads;
+
+struct ClusterSortParams {
+  const void* tokens;
+  uint32_t *keys, *rows;
+  uint32_t* active;        // count of the list that embed_sum makes
+  int64_t vocab;
+  int32_t index_bits, n, cluster, rounds, passes, digit;
+  FillParams fill;
+};
+
+__device__ __forceinline__ uint32_t key_of(int64_t token, int64_t vocab) {
+  // tokens that are no row of the table are sorted behind the others
+  return static_cast<uint32_t>(token >= 0 && token < vocab ? token : vocab);
+}
+
+__device__ __forceinline__ void remote_store(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t remote_load(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// A row's place among those of its warp with the same digit (lanes in order, earlier steps first), counted in `count`.
+__device__ __forceinline__ uint32_t rank_in_warp(uint32_t* count, uint32_t bin, bool there, int lane) {
+  const uint32_t same = __match_any_sync(0xffffffffu, there ? bin : 0xffffffffu);
+  const uint32_t below = same & ((1u << lane) - 1);
+  uint32_t old = 0;
+  if (there) old = count[bin];
+  __syncwarp();
+  if (there && below == 0) count[bin] = old + __popc(same);
+  __syncwarp();
+  return old + __popc(below);
+}
+
+__global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_constant__ ClusterSortParams p) {
+  begin_after_previous();
+  if (static_cast<int>(blockIdx.x) >= p.cluster) {
+    fill_zeros(p.fill, blockIdx.x - p.cluster, gridDim.x - p.cluster);
+    return;
+  }
+  extern __shared__ uint32_t sort_shared[];
+  const int each = p.rounds * kClusterThreads, bins = 1 << p.digit;
+  uint32_t *keys = sort_shared, *rows = keys + each, *counts = rows + each;  // counts: [warp][bin]
+  uint32_t *totals = counts + kClusterWarps * bins, *base = totals + bins;
+  __shared__ uint32_t warp_sums[kClusterWarps];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, rank = static_cast<int>(blockIdx.x);
+  if (rank == 0 && threadIdx.x == 0) *p.active = 0;
+  const int mine = warp * 32 * p.rounds + lane;  // of the block's rows: mine, mine + 32, ...
+  const int left = p.n - rank * each;
+  uint32_t key[kMaxRounds], row[kMaxRounds];
+#pragma unroll
+  for (int k = 0; k < kMaxRounds; ++k) {
+    if (k >= p.rounds) break;
+    const int i = mine + 32 * k;
+    row[k] = rank * each + i;
+    key[k] = i < left ? key_of(index_at(p.tokens, p.index_bits, row[k]), p.vocab) : 0;
+  }
+  for (int pass = 0; pass < p.passes; ++pass) {
+    const int shift = pass * p.digit;
+    for (int b = threadIdx.x; b < kClusterWarps * bins; b += kClusterThreads) counts[b] = 0;
+    __syncthreads();
+    uint32_t at[kMaxRounds];
+#pragma unroll
+    for (int k = 0; k < kMaxRounds; ++k) {
+      if (k >= p.rounds) break;
+      at[k] = rank_in_warp(counts + warp * bins, key[k] >> shift & (bins - 1), mine + 32 * k < left, lane);
+    }
+    __syncthreads();
+    // thread b: digit b. The warps' counts become running sums over the warps; totals over the blocks, then over the digits.
+    uint32_t total = 0;
+    if (static_cast<int>(threadIdx.x) < bins) {
+#pragma unroll 8
+      for (int w = 0; w < kClusterWarps; ++w) {
+        const uint32_t c = counts[w * bins + threadIdx.x];
+        counts[w * bins + threadIdx.x] = total;
+        total += c;
+      }
+      totals[threadIdx.x] = total;
+    }
+    tc::cluster_sync();
+    uint32_t all = 0, before = 0;
+    if (static_cast<int>(threadIdx.x) < bins)
+      for (int r = 0; r < p.cluster; ++r) {
+        const uint32_t c = r == rank ? total : remote_load(tc::in_block(tc::smem_addr(&totals[threadIdx.x]), r));
+        if (r < rank) before += c;
+        all += c;
+      }
+    uint32_t run = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += u;
+    }
+    if (lane == 31) warp_sums[warp] = run;
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < bins) {
+      for (int w = 0; w < warp; ++w) before += warp_sums[w];
+      base[threadIdx.x] = before + run - all;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMaxRounds; ++k) {
+      if (k >= p.rounds) break;
+      if (mine + 32 * k >= left) continue;
+      const uint32_t bin = key[k] >> shift & (bins - 1);
+      const uint32_t to = base[bin] + counts[warp * bins + bin] + at[k];
+      const uint32_t block = to / each, slot = to - block * each;
+      remote_store(tc::in_block(tc::smem_addr(&keys[slot]), block), key[k]);
+      remote_store(tc::in_block(tc::smem_addr(&rows[slot]), block), row[k]);
+    }
+    tc::cluster_sync();
+#pragma unroll
+    for (int k = 0; k < kMaxRounds; ++k) {
+      if (k >= p.rounds) break;
+      key[k] = keys[mine + 32 * k];
+      row[k] = rows[mine + 32 * k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kMaxRounds; ++k) {
+    if (k >= p.rounds) break;
+    if (mine + 32 * k >= left) continue;
+    p.keys[rank * each + mine + 32 * k] = key[k];
+    p.rows[rank * each + mine + 32 * k] = row[k];
+  }
+}
+
+__global__ void __launch_bounds__(kClusterThreads) embed_fill(const __grid_constant__ FillParams p) {
+  begin_after_previous();
+  fill_zeros(p, blockIdx.x, gridDim.x);
+}
+
+// More rows: three launches a pass, counts of the blocks' digits in memory.
+constexpr int kSortThreads = 256, kSortItems = 8, kSortBlock = kSortThreads * kSortItems;
 
 struct SortParams {
   const void* tokens;      // first pass: the caller's, else null
@@ -132,14 +311,13 @@ struct SortParams {
   const uint32_t *keys_in, *rows_in;
   uint32_t *keys_out, *rows_out;
   uint32_t* counts;        // [bin][block], then their running sums
+  uint32_t* active;        // as above
   int32_t n, blocks, shift, bins;
 };
 
-// Tokens that are no row of the table are sorted behind the others.
 __device__ __forceinline__ uint32_t sort_key(const SortParams& p, int i) {
   if (!p.tokens) return p.keys_in[i];
-  const int64_t t = index_at(p.tokens, p.index_bits, i);
-  return static_cast<uint32_t>(t >= 0 && t < p.vocab ? t : p.vocab);
+  return key_of(index_at(p.tokens, p.index_bits, i), p.vocab);
 }
 
 __global__ void __launch_bounds__(kSortThreads) sort_count(const __grid_constant__ SortParams p) {
@@ -160,6 +338,7 @@ __global__ void __launch_bounds__(1024) sort_offsets(const __grid_constant__ Sor
   begin_after_previous();
   __shared__ uint32_t warps[32];
   __shared__ uint32_t carry;
+  if (threadIdx.x == 0) *p.active = 0;
   const int n = p.bins * p.blocks, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   if (threadIdx.x == 0) carry = 0;
   for (int i0 = 0; i0 < n; i0 += 4096) {
@@ -206,15 +385,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_move(const __grid_constant_
   for (int k = 0; k < kSortItems; ++k) {
     const int i = first + k * 32;
     key[k] = i < p.n ? sort_key(p, i) : 0;
-    const uint32_t bin = i < p.n ? (key[k] >> p.shift) & (p.bins - 1) : 0xffffffffu;
-    const uint32_t same = __match_any_sync(0xffffffffu, bin);
-    const uint32_t below = same & ((1u << lane) - 1);
-    uint32_t old = 0;
-    if (i < p.n) old = next[warp][bin];
-    __syncwarp();
-    if (i < p.n && below == 0) next[warp][bin] = old + __popc(same);
-    __syncwarp();
-    rank[k] = old + __popc(below);
+    rank[k] = rank_in_warp(next[warp], key[k] >> p.shift & (p.bins - 1), i < p.n, lane);
   }
   __syncthreads();
   for (int b = threadIdx.x; b < p.bins; b += kSortThreads) {
@@ -240,11 +411,12 @@ __global__ void __launch_bounds__(kSortThreads) sort_move(const __grid_constant_
 
 constexpr int kChunk = 32;
 constexpr int kSumThreads = 128;
+constexpr int kSumBatch = 8;  // rows of a thread in flight
 
 struct SumParams {
   const uint32_t *keys, *rows;  // sorted
   int32_t n, chunks;
-  int32_t tiles, join_tiles;    // blocks of columns of a chunk, in the two kernels
+  int32_t tiles, join_tiles;    // parts of the columns, in the two kernels
   int64_t vocab, cols;
   const void* dout;
   int64_t dout_stride;
@@ -252,6 +424,7 @@ struct SumParams {
   int64_t dtable_stride;
   float* parts;                 // [2 chunk + (0: the run that came in, 1: the run that goes on)][part_stride]
   int64_t part_stride;
+  uint32_t* active;             // count, then the chunks where a run begins that goes on behind them
   float scale;
   bool accumulate;
 };
@@ -266,88 +439,132 @@ __device__ __forceinline__ void finish_row(const SumParams& p, uint32_t token, i
   store<kVec>(to, sum);
 }
 
-template <typename T, typename TTable, int kVec>
+// What a thread holds of a row: kVec elements as they lie in memory.
+template <typename T, int kVec>
+struct alignas(sizeof(T) * kVec < 16 ? sizeof(T) * kVec : 16) Piece {
+  T v[kVec];
+  __device__ __forceinline__ void add_to(float (&sum)[kVec]) const {
+    if constexpr (sizeof(T) == 2 && kVec == 8) {
+      float x[8];
+      load<8>(v, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += x[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) sum[e] += static_cast<float>(v[e]);
+    }
+  }
+};
+
+// kQ pieces of kVec columns for each thread. Bound by reading dout (HBM), eight rows at a time.
+template <typename T, typename TTable, int kVec, int kQ>
 __global__ void __launch_bounds__(kSumThreads) embed_sum(const __grid_constant__ SumParams p) {
   begin_after_previous();
   __shared__ uint32_t keys[kChunk + 2], rows[kChunk];  // keys[0]: of the row before the chunk; the last: behind it
   const int chunk = blockIdx.x / p.tiles, tile = blockIdx.x - chunk * p.tiles;
-  const int first = chunk * kChunk, count = min(kChunk, p.n - first);
+  const int first = chunk * kChunk;
   const uint32_t none = static_cast<uint32_t>(p.vocab);
-  for (int i = threadIdx.x; i < kChunk + 2; i += kSumThreads) {
+  int count = 0;
+  for (int i = threadIdx.x; i < kChunk + 2; i += blockDim.x) {
     const int at = first + i - 1;
-    keys[i] = at >= 0 && at < p.n ? p.keys[at] : none;
-    if (i >= 1 && i <= count) rows[i - 1] = p.rows[at];
+    const uint32_t key = at >= 0 && at < p.n ? p.keys[at] : none;
+    keys[i] = key;
+    if (i >= 1 && i <= kChunk && key != none) rows[i - 1] = p.rows[at];
   }
   __syncthreads();
-  const int64_t col = (static_cast<int64_t>(tile) * kSumThreads + threadIdx.x) * kVec;
-  if (col >= p.cols) return;
-  const T* dout = static_cast<const T*>(p.dout) + col;
-  float sum[kVec] = {};
-  int begin = 0;
-  for (int i = 0; i < count && keys[i + 1] != none; ++i) {
-    float v[kVec];
-    load<kVec>(dout + rows[i] * p.dout_stride, v);
+  while (count < kChunk && keys[count + 1] != none) ++count;  // rows with a token come first
+  if (count == 0) return;
+  const bool came = first > 0 && keys[0] == keys[1];                          // the first run began before
+  const bool goes = count == kChunk && keys[kChunk + 1] == keys[kChunk];      // the last one goes on
+  if (tile == 0 && threadIdx.x == 0 && goes && !(came && keys[1] == keys[kChunk]))
+    p.active[1 + atomicAdd(p.active, 1u)] = chunk;
+  const int64_t col0 = (static_cast<int64_t>(tile) * kQ * blockDim.x + threadIdx.x) * kVec, step = blockDim.x * kVec;
+  const T* dout = static_cast<const T*>(p.dout) + col0;
+  float sum[kQ][kVec] = {};
+  bool begun = came;  // whether the present run has rows before the chunk
+  for (int i0 = 0; i0 < count; i0 += kSumBatch) {
+    Piece<T, kVec> v[kSumBatch][kQ];
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) sum[e] += v[e];
-    const bool last = i + 1 == count;
-    if (!last && keys[i + 2] == keys[i + 1]) continue;
-    const bool came = begin == 0 && first > 0 && keys[0] == keys[1];
-    const bool goes = last && keys[count + 1] == keys[count];
-    if (came || goes) {
-      store<kVec>(p.parts + (2 * static_cast<int64_t>(chunk) + (came ? 0 : 1)) * p.part_stride + col, sum);
-    } else {
-      finish_row<TTable, kVec>(p, keys[i + 1], col, sum);
+    for (int k = 0; k < kSumBatch; ++k) {
+      if (i0 + k >= count) break;
+      const T* from = dout + rows[i0 + k] * p.dout_stride;
+#pragma unroll
+      for (int q = 0; q < kQ; ++q)
+        if (col0 + q * step < p.cols) v[k][q] = *reinterpret_cast<const Piece<T, kVec>*>(from + q * step);
     }
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) sum[e] = 0.0f;
-    begin = i + 1;
+    for (int k = 0; k < kSumBatch; ++k) {
+      const int i = i0 + k;
+      if (i >= count) break;
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) v[k][q].add_to(sum[q]);
+      const bool last = i + 1 == count;
+      if (!last && keys[i + 2] == keys[i + 1]) continue;
+      const bool on = last && goes;
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        const int64_t col = col0 + q * step;
+        if (col < p.cols) {
+          if (begun || on)
+            store<kVec>(p.parts + (2 * static_cast<int64_t>(chunk) + (begun ? 0 : 1)) * p.part_stride + col, sum[q]);
+          else
+            finish_row<TTable, kVec>(p, keys[i + 1], col, sum[q]);
+        }
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) sum[q][e] = 0.0f;
+      }
+      begun = false;
+    }
   }
 }
 
-// Adds up a run that begins in this block's chunk and goes on behind it: eight
-// groups of threads each a share of the chunks, then the groups in order.
-constexpr int kJoinGroups = 8;
+// Adds up the runs that cross chunks: eight groups of threads each a share of a run's
+// chunks, then the groups in order.
+constexpr int kJoinGroups = 8, kJoinThreads = 32 * kJoinGroups;
 
 template <typename TTable, int kVec>
-__global__ void __launch_bounds__(32 * kJoinGroups) embed_join(const __grid_constant__ SumParams p) {
+__global__ void __launch_bounds__(kJoinThreads) embed_join(const __grid_constant__ SumParams p) {
   begin_after_previous();
-  const int chunk = blockIdx.x / p.join_tiles, end = min(p.n, (chunk + 1) * kChunk);
-  const uint32_t none = static_cast<uint32_t>(p.vocab);
-  if (end >= p.n) return;
-  const uint32_t token = p.keys[end - 1];
-  if (token == none || p.keys[end] != token) return;
-  if (chunk > 0 && p.keys[chunk * kChunk] == token && p.keys[chunk * kChunk - 1] == token) return;  // began before
-  int lo = end, hi = p.n;  // the run's end: the first key beyond `token`
-  while (lo < hi) {
-    const int mid = lo + (hi - lo) / 2;
-    if (p.keys[mid] == token) lo = mid + 1;
-    else hi = mid;
-  }
-  const int last = (lo - 1) / kChunk, parts = last - chunk;  // after the first one
+  const int64_t items = static_cast<int64_t>(p.active[0]) * p.join_tiles;
   const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
-  const int each = (parts + kJoinGroups - 1) / kJoinGroups;
-  const int from = chunk + 1 + min(parts, group * each), to = chunk + 1 + min(parts, (group + 1) * each);
-  const int64_t col = (static_cast<int64_t>(blockIdx.x - chunk * p.join_tiles) * 32 + lane) * kVec;
   __shared__ float sums[kJoinGroups][kVec][32];
-  float sum[kVec] = {};
-  if (col < p.cols) {
-    if (group == 0) load<kVec>(p.parts + (2 * static_cast<int64_t>(chunk) + 1) * p.part_stride + col, sum);
-    for (int c = from; c < to; ++c) {
-      float v[kVec];
-      load<kVec>(p.parts + 2 * static_cast<int64_t>(c) * p.part_stride + col, v);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) sum[e] += v[e];
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t index = item / p.join_tiles;
+    const int chunk = static_cast<int>(p.active[1 + index]);
+    const uint32_t token = p.keys[(chunk + 1) * kChunk - 1];
+    int parts = 0;  // chunks behind the first that begin with the run
+    for (int c0 = chunk + 1;; c0 += kJoinThreads) {
+      const int64_t at = static_cast<int64_t>(c0 + threadIdx.x) * kChunk;
+      const int more = __syncthreads_count(at < p.n && p.keys[at] == token);
+      parts += more;
+      if (more < kJoinThreads) break;
     }
+    const int each = (parts + kJoinGroups - 1) / kJoinGroups;
+    const int from = chunk + 1 + min(parts, group * each), to = chunk + 1 + min(parts, (group + 1) * each);
+    const int64_t col = ((item - index * p.join_tiles) * 32 + lane) * kVec;
+    float sum[kVec] = {};
+    if (col < p.cols) {
+      if (group == 0) load<kVec>(p.parts + (2 * static_cast<int64_t>(chunk) + 1) * p.part_stride + col, sum);
+#pragma unroll 4
+      for (int c = from; c < to; ++c) {
+        float v[kVec];
+        load<kVec>(p.parts + 2 * static_cast<int64_t>(c) * p.part_stride + col, v);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) sum[e] += v[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) sums[group][e][lane] = sum[e];
+    __syncthreads();
+    if (group == 0 && col < p.cols) {
+#pragma unroll
+      for (int g = 1; g < kJoinGroups; ++g)
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) sum[e] += sums[g][e][lane];
+      finish_row<TTable, kVec>(p, token, col, sum);
+    }
+    __syncthreads();
   }
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) sums[group][e][lane] = sum[e];
-  __syncthreads();
-  if (group != 0 || col >= p.cols) return;
-#pragma unroll
-  for (int g = 1; g < kJoinGroups; ++g)
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) sum[e] += sums[g][e][lane];
-  finish_row<TTable, kVec>(p, token, col, sum);
 }
 
 // ---------------------------------------------------------------------- host
@@ -361,7 +578,7 @@ bool vector_rows(const void* p, int64_t rows, int64_t stride, int size) {
 }
 
 struct Workspace {
-  int64_t keys[2], rows[2], counts, parts, bytes;
+  int64_t keys[2], rows[2], counts, active, parts, bytes;
   int64_t part_stride;
   int32_t chunks, blocks;
 };
@@ -377,30 +594,54 @@ Workspace carve(int64_t rows, int64_t cols) {
   w.chunks = static_cast<int32_t>((rows + kChunk - 1) / kChunk);
   w.blocks = static_cast<int32_t>((rows + kSortBlock - 1) / kSortBlock);
   w.part_stride = round_to(cols, 8);
-  for (int k = 0; k < 2; ++k) {
+  const bool many = rows > kClusterRows;
+  for (int k = 0; k < (many ? 2 : 1); ++k) {
     w.keys[k] = take(rows * 4);
     w.rows[k] = take(rows * 4);
   }
-  w.counts = take(static_cast<int64_t>(w.blocks) * kMaxBins * 4);
+  if (many) w.counts = take(static_cast<int64_t>(w.blocks) * kMaxBins * 4);
+  w.active = take((static_cast<int64_t>(w.chunks) + 1) * 4);
   w.parts = take(2 * static_cast<int64_t>(w.chunks) * w.part_stride * 4);
   w.bytes = at;
   return w;
 }
 
 template <typename T, typename TTable, int kVec>
-int run_sum(SumParams p, cudaStream_t st) {
+int run_sum(SumParams p, int sms, cudaStream_t st) {
+  constexpr int kQ = kVec == 8 ? 1 : 4;
   const int64_t groups = (p.cols + kVec - 1) / kVec;
-  const int64_t tiles = (groups + kSumThreads - 1) / kSumThreads, join_tiles = (groups + 31) / 32;
-  if (join_tiles * p.chunks > INT32_MAX) return FSDP_EINVAL;  // more than any memory holds
+  const int threads = static_cast<int>(std::min<int64_t>(kSumThreads, round_to((groups + kQ - 1) / kQ, 32)));
+  const int64_t tiles = (groups + threads * kQ - 1) / (threads * kQ), join_tiles = (groups + 31) / 32;
+  if (tiles * p.chunks > INT32_MAX || join_tiles > INT32_MAX) return FSDP_EINVAL;  // more than any memory holds
   p.tiles = static_cast<int32_t>(tiles);
   p.join_tiles = static_cast<int32_t>(join_tiles);
-  if (int rc = launch_after(embed_sum<T, TTable, kVec>, p.chunks * p.tiles, 1, kSumThreads, 0, st, p)) return rc;
-  return launch_after(embed_join<TTable, kVec>, p.chunks * p.join_tiles, 1, 32 * kJoinGroups, 0, st, p);
+  if (int rc = launch_after(embed_sum<T, TTable, kVec, kQ>, p.chunks * p.tiles, 1, threads, 0, st, p)) return rc;
+  if (p.chunks == 1) return FSDP_OK;  // no run crosses chunks
+  const int64_t items = p.chunks * join_tiles;  // at most
+  return launch_after(embed_join<TTable, kVec>, static_cast<int>(std::min<int64_t>(items, 4 * sms)), 1, kJoinThreads, 0, st, p);
 }
 
 template <typename T, typename TTable>
-int run_sum_as(const SumParams& p, bool vectors, cudaStream_t st) {
-  return vectors ? run_sum<T, TTable, 8>(p, st) : run_sum<T, TTable, 1>(p, st);
+int run_sum_as(const SumParams& p, bool vectors, int sms, cudaStream_t st) {
+  return vectors ? run_sum<T, TTable, 8>(p, sms, st) : run_sum<T, TTable, 1>(p, sms, st);
+}
+
+// The sort of up to kClusterRows rows; the other blocks fill. As many blocks as leave
+// each four steps of 32 rows a warp, then longer ones.
+int run_cluster_sort(ClusterSortParams p, int sms, cudaStream_t st) {
+  p.cluster = 1;
+  while (p.cluster < kMaxCluster && p.n > p.cluster * 4 * kClusterThreads) p.cluster *= 2;
+  p.rounds = (p.n + p.cluster * kClusterThreads - 1) / (p.cluster * kClusterThreads);
+  const int bins = 1 << p.digit;
+  const int smem = (2 * p.rounds * kClusterThreads + (kClusterWarps + 2) * bins) * 4;
+  constexpr int kMost = (2 * kMaxRounds * kClusterThreads + (kClusterWarps + 2) * kMaxBins) * 4;
+  if (cudaFuncSetAttribute(embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) return FSDP_ECUDA;
+  int grid = p.cluster;
+  if (p.fill.row_bytes) {
+    const int64_t blocks = (p.fill.rows * p.fill.row_bytes + 16383) / 16384;  // a vector for each thread
+    grid += static_cast<int>(std::min<int64_t>(round_to(blocks, p.cluster), sms / p.cluster * p.cluster));
+  }
+  return launch_after(embed_sort, grid, p.cluster, kClusterThreads, smem, st, p);
 }
 
 bool is_index(int32_t dtype) { return dtype == FSDP_DTYPE_I32 || dtype == FSDP_DTYPE_I64; }
@@ -427,12 +668,12 @@ extern "C" int fsdp_embedding(const fsdp_embedding_t* a, const void* tokens, con
   const bool vectors = a->cols % 8 == 0 && vector_rows(table, a->vocab, a->table_stride, es) &&
                        vector_rows(out, a->rows, a->out_stride, es) &&
                        (!addend || vector_rows(addend, a->rows, a->addend_stride, es));
-  const int64_t groups = vectors ? a->cols / 8 : a->cols;
-  const int grid = static_cast<int>(std::min<int64_t>(a->rows * ((groups + kLookupThreads - 1) / kLookupThreads), 1 << 20));
+  const int64_t unit = vectors ? 32 * kGroups<8> * 8 : 32 * kGroups<1>, units = a->rows * ((a->cols + unit - 1) / unit);
+  const int grid = static_cast<int>(std::min<int64_t>((units + kLookupWarps - 1) / kLookupWarps, 1 << 20));
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (a->dtype == FSDP_DTYPE_F32)
-    return launch_after(vectors ? embed_rows<float, 8> : embed_rows<float, 1>, grid, 1, kLookupThreads, 0, cs, p);
-  return launch_after(vectors ? embed_rows<__nv_bfloat16, 8> : embed_rows<__nv_bfloat16, 1>, grid, 1, kLookupThreads, 0, cs, p);
+    return launch_after(vectors ? embed_rows<float, 8> : embed_rows<float, 1>, grid, 1, 32 * kLookupWarps, 0, cs, p);
+  return launch_after(vectors ? embed_rows<__nv_bfloat16, 8> : embed_rows<__nv_bfloat16, 1>, grid, 1, 32 * kLookupWarps, 0, cs, p);
 }
 
 extern "C" int fsdp_embedding_backward_workspace(int64_t rows, int64_t cols, int64_t vocab, int64_t* bytes_out) {
@@ -459,15 +700,18 @@ extern "C" int fsdp_embedding_backward(const fsdp_embedding_backward_t* a, const
     if (sw.overlaps(st) || sw.overlaps(sd) || sw.overlaps(ws) || ws.overlaps(st) || ws.overlaps(sd)) return FSDP_EALIAS;
   }
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (!a->accumulate &&
-      cudaMemset2DAsync(dtable, static_cast<size_t>(sw.pitch() ? sw.pitch() : a->cols * ts), 0,
-                        static_cast<size_t>(a->cols) * ts, static_cast<size_t>(a->vocab), cs) != cudaSuccess)
-    return FSDP_ECUDA;
+  FillParams fill{static_cast<unsigned char*>(dtable), a->vocab, a->accumulate ? 0 : a->cols * ts, sw.pitch()};
+  if (fill.rows > 1 && fill.pitch == fill.row_bytes) fill.row_bytes *= fill.rows, fill.rows = 1;  // one long row
+  Device dev;
+  if (int rc = device_facts(&dev)) return rc;
+  if (fill.row_bytes && (a->rows == 0 || a->rows > kClusterRows)) {
+    if (int rc = launch_after(embed_fill, 2 * dev.sms, 1, kClusterThreads, 0, cs, fill)) return rc;
+  }
   if (a->rows == 0) return FSDP_OK;
 
   const Workspace w = carve(a->rows, a->cols);
   auto* base = reinterpret_cast<unsigned char*>(round_to(reinterpret_cast<intptr_t>(workspace), 256) - 256);
-  uint32_t *keys[2], *rows[2];
+  uint32_t *keys[2], *rows[2], *active = reinterpret_cast<uint32_t*>(base + w.active);
   for (int k = 0; k < 2; ++k) {
     keys[k] = reinterpret_cast<uint32_t*>(base + w.keys[k]);
     rows[k] = reinterpret_cast<uint32_t*>(base + w.rows[k]);
@@ -475,20 +719,28 @@ extern "C" int fsdp_embedding_backward(const fsdp_embedding_backward_t* a, const
   int bits = 1;
   while (a->vocab >> bits) ++bits;  // of the keys 0 .. vocab
   const int passes = (bits + 8) / 9, digit = (bits + passes - 1) / passes;
+  const int32_t n = static_cast<int32_t>(a->rows);
   int now = 0;
-  for (int k = 0; k < passes; ++k, now ^= 1) {
-    const SortParams p{k == 0 ? tokens : nullptr, 8 * is, a->vocab, keys[now], rows[now], keys[now ^ 1], rows[now ^ 1],
-                       reinterpret_cast<uint32_t*>(base + w.counts), static_cast<int32_t>(a->rows), w.blocks, k * digit, 1 << digit};
-    if (int rc = launch_after(sort_count, w.blocks, 1, kSortThreads, 0, cs, p)) return rc;
-    if (int rc = launch_after(sort_offsets, 1, 1, 1024, 0, cs, p)) return rc;
-    if (int rc = launch_after(sort_move, w.blocks, 1, kSortThreads, 0, cs, p)) return rc;
+  if (a->rows <= kClusterRows) {
+    const ClusterSortParams p{tokens, keys[0], rows[0], active, a->vocab, 8 * is, n, 0, 0, passes, digit, fill};
+    if (int rc = run_cluster_sort(p, dev.sms, cs)) return rc;
+  } else {
+    for (int k = 0; k < passes; ++k, now ^= 1) {
+      const SortParams p{k == 0 ? tokens : nullptr, 8 * is, a->vocab, keys[now], rows[now], keys[now ^ 1], rows[now ^ 1],
+                         reinterpret_cast<uint32_t*>(base + w.counts), active, n, w.blocks, k * digit, 1 << digit};
+      if (int rc = launch_after(sort_count, w.blocks, 1, kSortThreads, 0, cs, p)) return rc;
+      if (int rc = launch_after(sort_offsets, 1, 1, 1024, 0, cs, p)) return rc;
+      if (int rc = launch_after(sort_move, w.blocks, 1, kSortThreads, 0, cs, p)) return rc;
+    }
   }
-  const SumParams p{keys[now], rows[now], static_cast<int32_t>(a->rows), w.chunks, 0, 0, a->vocab, a->cols, dout, a->dout_stride,
-                    dtable, a->dtable_stride, reinterpret_cast<float*>(base + w.parts), w.part_stride,
+  const SumParams p{keys[now], rows[now], n, w.chunks, 0, 0, a->vocab, a->cols, dout, a->dout_stride, dtable,
+                    a->dtable_stride, reinterpret_cast<float*>(base + w.parts), w.part_stride, active,
                     static_cast<float>(a->scale), a->accumulate != 0};
   const bool vectors = a->cols % 8 == 0 && vector_rows(dout, a->rows, a->dout_stride, es) &&
                        vector_rows(dtable, a->vocab, a->dtable_stride, ts);
   const bool in32 = a->dtype == FSDP_DTYPE_F32, table32 = a->table_dtype == FSDP_DTYPE_F32;
-  return in32 ? table32 ? run_sum_as<float, float>(p, vectors, cs) : run_sum_as<float, __nv_bfloat16>(p, vectors, cs)
-         : table32 ? run_sum_as<__nv_bfloat16, float>(p, vectors, cs) : run_sum_as<__nv_bfloat16, __nv_bfloat16>(p, vectors, cs);
+  const int sms = dev.sms;
+  return in32 ? table32 ? run_sum_as<float, float>(p, vectors, sms, cs) : run_sum_as<float, __nv_bfloat16>(p, vectors, sms, cs)
+         : table32 ? run_sum_as<__nv_bfloat16, float>(p, vectors, sms, cs)
+                   : run_sum_as<__nv_bfloat16, __nv_bfloat16>(p, vectors, sms, cs);
 }

@@ -10,6 +10,8 @@ Tolerances, element by element, from the operations' roundings:
   - an element of G is rounded to bf16 (2^-8 of itself), shares its row's factor, which carries the rounding of the
     target's element (2^-8), and is off by what its exponent is; in dweight the factor's product with hidden is
     rounded too (2^-8);
+  - exponentials below 2^-126 (of x, where |lse| <= 60, else relative to their row's or span's largest) count as zero, and
+    bf16's subnormal steps are smaller than that: at most 2^-125 in all, over exp(lse) in the former case;
   - the gradients' sums are cut off as the logits' are, in segments of 4096; partial sums add a few 2^-24; each
     output is rounded once (2^-8 of itself).
 """
@@ -91,6 +93,7 @@ def check(hidden, weight, targets, dloss, scale, loss, lse, dh, dw):
     hot = torch.zeros_like(p).scatter_(1, at, 1.0)
     g = f * (p - hot)
     off = g.abs() * (2 * HALF + HALF ** 2 + 2.0 ** -20) + f.abs() * p * 2 * (dx + d_lse[:, None])
+    off = off + f.abs() * 2.0 ** -125 * torch.where(want_lse.abs() <= 60, torch.exp(-want_lse), 1.0)[:, None].clamp(min=1)
     cut = (256 + vocab / 4096 + 8) * 2.0 ** -22
     aw, ah = w.abs(), h.abs()
     want = g @ w
