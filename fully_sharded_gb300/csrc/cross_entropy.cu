@@ -89,6 +89,7 @@ struct Product {
 struct Params {
   Product product[2];
   int32_t count, tiles;
+  int32_t extra, fewer;    // see tile_of
   int32_t segment;         // steps of 64 that are summed in tensor memory
   int32_t index_bits;      // of the targets: 32 or 64
   bool keep;               // E is kept
@@ -129,6 +130,23 @@ __device__ __forceinline__ uint16_t shared_load_half(uint32_t addr) {
 // bf16, bf16 -> fp32.
 __device__ __forceinline__ uint32_t bf16_kind(int m, int n, bool a_mn, bool b_mn) {
   return product_kind(m, n, a_mn, b_mn) | (1u << 7) | (1u << 10);
+}
+
+// The cluster's tile number `turn`, or p.tiles behind its last. The first product's tiles, which take
+// longest, go round the clusters; the `fewer` clusters that get one less than the others take `extra` rounds of
+// the second product's, then those go round all clusters too.
+__device__ __forceinline__ int tile_of(const Params& p, int cluster, int clusters, int turn) {
+  const int first = p.product[0].tiles, more = clusters - p.fewer, own = first / clusters + (p.fewer < clusters && cluster < more && first % clusters ? 1 : 0);
+  if (turn < own) return turn * clusters + cluster;
+  turn -= own;
+  int t;
+  if (cluster >= more && turn < p.extra) {
+    t = first + turn * p.fewer + cluster - more;
+  } else {
+    if (cluster >= more) turn -= p.extra;
+    t = first + p.extra * p.fewer + turn * clusters + cluster;
+  }
+  return min(t, p.tiles);
 }
 
 struct Place {
@@ -236,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
     if (warp == 0) {  // producer: this block's rows of both operands
       uint32_t it = 0;
       bool ok = true;
-      for (int t = cluster; ok && t < p.tiles; t += clusters) {
+      for (int turn = 0, t = tile_of(p, cluster, clusters, 0); ok && t < p.tiles; t = tile_of(p, cluster, clusters, ++turn)) {
         const Place at = place_of(p, t);
         const Product& g = p.product[at.product];
         int from;
@@ -277,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
     } else if (warp == 1 && rank == 0) {  // products, for both blocks of a pair
       uint32_t it = 0, n = 0;             // steps; segments
       bool ok = true;
-      for (int t = cluster; ok && t < p.tiles; t += clusters) {
+      for (int turn = 0, t = tile_of(p, cluster, clusters, 0); ok && t < p.tiles; t = tile_of(p, cluster, clusters, ++turn)) {
         const Place at = place_of(p, t);
         const Product& g = p.product[at.product];
         int from;
@@ -323,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
     uint32_t n = 0, sent = 0;
     bool ok = true;
     await_inputs();
-    for (int t = cluster; ok && t < p.tiles; t += clusters) {
+    for (int turn = 0, t = tile_of(p, cluster, clusters, 0); ok && t < p.tiles; t = tile_of(p, cluster, clusters, ++turn)) {
       const Place at = place_of(p, t);
       const Product& g = p.product[at.product];
       int from;
@@ -616,7 +634,10 @@ int make_plan(const fsdp_cross_entropy_t& a, bool gradients, Plan* out) {
   const int clusters = 152 / p.pair;
   const int64_t tiles = ((p.piece + 128 * p.pair - 1) / (128 * p.pair)) * ((a.cols + kN - 1) / kN);
   const int64_t steps = (a.vocab + kTileK - 1) / kTileK;
+  // Few tiles are cut along the vocabulary where that saves more than the launch that joins them (3 us) costs:
+  // a step takes about 0.3 us.
   p.splits = static_cast<int>(std::max<int64_t>(1, std::min(clusters / tiles, steps / 8)));
+  if (steps < 24) p.splits = 1;
   p.split_steps = static_cast<int>((steps + p.splits - 1) / p.splits);
   p.splits = static_cast<int>((steps + p.split_steps - 1) / p.split_steps);
   int64_t at = 256;  // the caller's pointer may have any alignment
@@ -693,7 +714,14 @@ int launch_products(Params& p, const Device& dev, cudaStream_t stream) {
   }
   const int room = resident_clusters<kPair, kIsScores>(dev);
   if (room < 1) return FSDP_ECUDA;
-  return launch_after(ce_product<kPair, kIsScores>, std::min(p.tiles, room) * kPair, kPair, kThreads, T::kSmemBytes, stream, p);
+  const int clusters = std::min(p.tiles, room);
+  p.fewer = p.extra = 0;
+  if (p.count == 2 && p.product[0].tiles % clusters) {
+    p.fewer = clusters - p.product[0].tiles % clusters;
+    // as many as take as long as one of the first product's
+    p.extra = (2 * p.product[0].split_steps / p.product[1].split_steps + 1) / 2;
+  }
+  return launch_after(ce_product<kPair, kIsScores>, clusters * kPair, kPair, kThreads, T::kSmemBytes, stream, p);
 }
 
 int steps_of(int64_t k) { return static_cast<int>((k + kTileK - 1) / kTileK); }

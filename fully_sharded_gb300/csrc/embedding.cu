@@ -6,7 +6,7 @@
 //
 // Gradient. The rows are put in the order of their tokens (a stable radix sort of row
 // indexes by token, so equal tokens keep the rows' order), and the sorted list is cut into chunks of
-// kChunk rows. A block adds the rows of a chunk, run by run of equal tokens, for
+// 16 or 32 rows. A block adds the rows of a chunk, run by run of equal tokens, for
 // its columns: a run that lies in the chunk goes to the table at once, the parts of
 // one that crosses chunks go to the workspace in fp32 and are added in order by a
 // last kernel. Every sum is fp32 in an order fixed by the tokens alone.
@@ -81,6 +81,13 @@ __device__ __forceinline__ void store(float* p, const float (&v)[kVec]) {
   }
 }
 
+// kVec elements as they lie in memory.
+template <typename T, int kVec>
+struct alignas(sizeof(T) * kVec < 16 ? sizeof(T) * kVec : 16) Piece {
+  T v[kVec];
+  __device__ __forceinline__ void to(float (&x)[kVec]) const { load<kVec>(v, x); }
+};
+
 // -------------------------------------------------------------------- lookup
 
 struct LookupParams {
@@ -99,36 +106,47 @@ constexpr int kLookupWarps = 8;
 template <int kVec>
 constexpr int kGroups = kVec == 8 ? 4 : 8;
 
-// A warp takes 32 kGroups kVec consecutive elements of a row at a time. Bound by HBM.
-template <typename T, int kVec>
+// A warp takes 32 kGroups kVec consecutive elements of a row at a time; the next token is on its way
+// meanwhile. Bound by HBM; the rows stay packed until they are used, so that many warps fit.
+template <typename T, int kVec, bool kAdd>
 __global__ void __launch_bounds__(32 * kLookupWarps) embed_rows(const __grid_constant__ LookupParams p) {
   begin_after_previous();
   constexpr int kQ = kGroups<kVec>, kUnit = 32 * kQ * kVec;
   const uint32_t per_row = static_cast<uint32_t>((p.cols + kUnit - 1) / kUnit);
-  const int64_t units = p.rows * per_row;
+  const int64_t units = p.rows * per_row, step = static_cast<int64_t>(gridDim.x) * kLookupWarps;
   const int lane = threadIdx.x % 32;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kLookupWarps + threadIdx.x / 32; u < units;
-       u += static_cast<int64_t>(gridDim.x) * kLookupWarps) {
-    const int64_t row = units >> 31 ? u / per_row : static_cast<uint32_t>(u) / per_row;
+  const auto row_of = [&](int64_t u) { return units >> 31 ? u / per_row : static_cast<uint32_t>(u) / per_row; };
+  int64_t u = static_cast<int64_t>(blockIdx.x) * kLookupWarps + threadIdx.x / 32;
+  if (u >= units) return;
+  int64_t row = row_of(u), token = index_at(p.tokens, p.index_bits, row);
+  while (u < units) {
     const int64_t col = (u - row * per_row) * kUnit + lane * kVec;
-    const int64_t token = index_at(p.tokens, p.index_bits, row);
     const bool there = token >= 0 && token < p.vocab;
     const T* from = static_cast<const T*>(p.table) + (there ? token : 0) * p.table_stride + col;
     const T* addend = static_cast<const T*>(p.addend) + row * p.addend_stride + col;
-    float v[kQ][kVec], a[kQ][kVec] = {};
+    Piece<T, kVec> v[kQ], a[kAdd ? kQ : 1];
 #pragma unroll
     for (int q = 0; q < kQ; ++q)
       if (col + q * 32 * kVec < p.cols) {
-        load<kVec>(from + q * 32 * kVec, v[q]);
-        if (p.addend) load<kVec>(addend + q * 32 * kVec, a[q]);
+        v[q] = *reinterpret_cast<const Piece<T, kVec>*>(from + q * 32 * kVec);
+        if constexpr (kAdd) a[q] = *reinterpret_cast<const Piece<T, kVec>*>(addend + q * 32 * kVec);
       }
     T* out = static_cast<T*>(p.out) + row * p.out_stride + col;
+    const float none = token < 0 ? 0.0f : NAN;
+    u += step;
+    if (u < units) {
+      row = row_of(u);
+      token = index_at(p.tokens, p.index_bits, row);
+    }
 #pragma unroll
     for (int q = 0; q < kQ; ++q)
       if (col + q * 32 * kVec < p.cols) {
+        float x[kVec], y[kVec] = {};
+        v[q].to(x);
+        if constexpr (kAdd) a[q].to(y);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) v[q][e] = (there ? v[q][e] * p.scale : token < 0 ? 0.0f : NAN) + a[q][e];
-        store<kVec>(out + q * 32 * kVec, v[q]);
+        for (int e = 0; e < kVec; ++e) x[e] = (there ? x[e] * p.scale : none) + (kAdd ? y[e] : 0.0f);
+        store<kVec>(out + q * 32 * kVec, x);
       }
   }
 }
@@ -191,9 +209,15 @@ __device__ __forceinline__ uint32_t remote_load(uint32_t addr) {
   return v;
 }
 
-// A row's place among those of its warp with the same digit (lanes in order, earlier steps first), counted in `count`.
-__device__ __forceinline__ uint32_t rank_in_warp(uint32_t* count, uint32_t bin, bool there, int lane) {
-  const uint32_t same = __match_any_sync(0xffffffffu, there ? bin : 0xffffffffu);
+// A row's place among those of its warp with the same digit (lanes in order, earlier steps first), counted in
+// `count`. The lanes of the same digit by a ballot for each bit: a match of 32 lanes takes several times as long.
+__device__ __forceinline__ uint32_t rank_in_warp(uint32_t* count, uint32_t bin, int bits, bool there, int lane) {
+  uint32_t same = __ballot_sync(0xffffffffu, there);
+  for (int b = 0; b < bits; ++b) {
+    const bool set = bin >> b & 1;
+    const uint32_t others = __ballot_sync(0xffffffffu, set);
+    same &= set ? others : ~others;
+  }
   const uint32_t below = same & ((1u << lane) - 1);
   uint32_t old = 0;
   if (there) old = count[bin];
@@ -234,7 +258,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
 #pragma unroll
     for (int k = 0; k < kMaxRounds; ++k) {
       if (k >= p.rounds) break;
-      at[k] = rank_in_warp(counts + warp * bins, key[k] >> shift & (bins - 1), mine + 32 * k < left, lane);
+      at[k] = rank_in_warp(counts + warp * bins, key[k] >> shift & (bins - 1), p.digit, mine + 32 * k < left, lane);
     }
     __syncthreads();
     // thread b: digit b. The warps' counts become running sums over the warps; totals over the blocks, then over the digits.
@@ -248,14 +272,22 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
       }
       totals[threadIdx.x] = total;
     }
-    tc::cluster_sync();
-    uint32_t all = 0, before = 0;
-    if (static_cast<int>(threadIdx.x) < bins)
-      for (int r = 0; r < p.cluster; ++r) {
-        const uint32_t c = r == rank ? total : remote_load(tc::in_block(tc::smem_addr(&totals[threadIdx.x]), r));
-        if (r < rank) before += c;
-        all += c;
+    uint32_t all = total, before = 0;
+    if (p.cluster > 1) {
+      tc::cluster_sync();
+      if (static_cast<int>(threadIdx.x) < bins) {
+        uint32_t of[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          of[r] = r < p.cluster ? remote_load(tc::in_block(tc::smem_addr(&totals[threadIdx.x]), r)) : 0;
+        all = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          before += r < rank ? of[r] : 0;
+          all += of[r];
+        }
       }
+    }
     uint32_t run = all;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -264,10 +296,9 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
     }
     if (lane == 31) warp_sums[warp] = run;
     __syncthreads();
-    if (static_cast<int>(threadIdx.x) < bins) {
-      for (int w = 0; w < warp; ++w) before += warp_sums[w];
-      base[threadIdx.x] = before + run - all;
-    }
+    // by whole warps: there may be fewer digits than lanes
+    const uint32_t lower = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0);
+    if (static_cast<int>(threadIdx.x) < bins) base[threadIdx.x] = before + run - all + lower;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kMaxRounds; ++k) {
@@ -275,11 +306,19 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
       if (mine + 32 * k >= left) continue;
       const uint32_t bin = key[k] >> shift & (bins - 1);
       const uint32_t to = base[bin] + counts[warp * bins + bin] + at[k];
-      const uint32_t block = to / each, slot = to - block * each;
-      remote_store(tc::in_block(tc::smem_addr(&keys[slot]), block), key[k]);
-      remote_store(tc::in_block(tc::smem_addr(&rows[slot]), block), row[k]);
+      if (p.cluster > 1) {
+        const uint32_t block = to / each, slot = to - block * each;
+        remote_store(tc::in_block(tc::smem_addr(&keys[slot]), block), key[k]);
+        remote_store(tc::in_block(tc::smem_addr(&rows[slot]), block), row[k]);
+      } else {
+        keys[to] = key[k];
+        rows[to] = row[k];
+      }
     }
-    tc::cluster_sync();
+    if (p.cluster > 1)
+      tc::cluster_sync();
+    else
+      __syncthreads();
 #pragma unroll
     for (int k = 0; k < kMaxRounds; ++k) {
       if (k >= p.rounds) break;
@@ -385,7 +424,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_move(const __grid_constant_
   for (int k = 0; k < kSortItems; ++k) {
     const int i = first + k * 32;
     key[k] = i < p.n ? sort_key(p, i) : 0;
-    rank[k] = rank_in_warp(next[warp], key[k] >> p.shift & (p.bins - 1), i < p.n, lane);
+    rank[k] = rank_in_warp(next[warp], key[k] >> p.shift & (p.bins - 1), 31 - __clz(p.bins), i < p.n, lane);
   }
   __syncthreads();
   for (int b = threadIdx.x; b < p.bins; b += kSortThreads) {
@@ -409,13 +448,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_move(const __grid_constant_
 
 // ------------------------------------------------------------------ gradient
 
-constexpr int kChunk = 32;
+constexpr int kMaxChunk = 32;
 constexpr int kSumThreads = 128;
 constexpr int kSumBatch = 8;  // rows of a thread in flight
 
 struct SumParams {
   const uint32_t *keys, *rows;  // sorted
-  int32_t n, chunks;
+  int32_t n, chunk, chunks;     // rows of a chunk
   int32_t tiles, join_tiles;    // parts of the columns, in the two kernels
   int64_t vocab, cols;
   const void* dout;
@@ -424,66 +463,50 @@ struct SumParams {
   int64_t dtable_stride;
   float* parts;                 // [2 chunk + (0: the run that came in, 1: the run that goes on)][part_stride]
   int64_t part_stride;
-  uint32_t* active;             // count, then the chunks where a run begins that goes on behind them
+  uint32_t* active;             // count, then (chunk, token) of the runs that go on behind their first chunk
   float scale;
   bool accumulate;
 };
 
 template <typename TTable, int kVec>
-__device__ __forceinline__ void finish_row(const SumParams& p, uint32_t token, int64_t col, float (&sum)[kVec]) {
-  TTable* to = static_cast<TTable*>(p.dtable) + token * p.dtable_stride + col;
-  float old[kVec] = {};
-  if (p.accumulate) load<kVec>(to, old);
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) sum[e] = old[e] + sum[e] * p.scale;
-  store<kVec>(to, sum);
+__device__ __forceinline__ TTable* table_at(const SumParams& p, uint32_t token, int64_t col) {
+  return static_cast<TTable*>(p.dtable) + token * p.dtable_stride + col;
 }
 
-// What a thread holds of a row: kVec elements as they lie in memory.
-template <typename T, int kVec>
-struct alignas(sizeof(T) * kVec < 16 ? sizeof(T) * kVec : 16) Piece {
-  T v[kVec];
-  __device__ __forceinline__ void add_to(float (&sum)[kVec]) const {
-    if constexpr (sizeof(T) == 2 && kVec == 8) {
-      float x[8];
-      load<8>(v, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += x[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) sum[e] += static_cast<float>(v[e]);
-    }
-  }
-};
-
-// kQ pieces of kVec columns for each thread. Bound by reading dout (HBM), eight rows at a time.
-template <typename T, typename TTable, int kVec, int kQ>
+// kQ pieces of kVec columns for each thread. Bound by reading dout (HBM); kSumBatch rows, and the table's rows
+// that are added to, are on their way together.
+template <typename T, typename TTable, int kVec, int kQ, bool kAccumulate>
 __global__ void __launch_bounds__(kSumThreads) embed_sum(const __grid_constant__ SumParams p) {
   begin_after_previous();
-  __shared__ uint32_t keys[kChunk + 2], rows[kChunk];  // keys[0]: of the row before the chunk; the last: behind it
+  __shared__ uint32_t keys[kMaxChunk + 2], rows[kMaxChunk];  // keys[0]: of the row before the chunk; the last: behind it
   const int chunk = blockIdx.x / p.tiles, tile = blockIdx.x - chunk * p.tiles;
-  const int first = chunk * kChunk;
+  const int first = chunk * p.chunk;
   const uint32_t none = static_cast<uint32_t>(p.vocab);
-  int count = 0;
-  for (int i = threadIdx.x; i < kChunk + 2; i += blockDim.x) {
+  bool token = false;
+  const int i = threadIdx.x;
+  if (i < p.chunk + 2) {
     const int at = first + i - 1;
     const uint32_t key = at >= 0 && at < p.n ? p.keys[at] : none;
     keys[i] = key;
-    if (i >= 1 && i <= kChunk && key != none) rows[i - 1] = p.rows[at];
+    token = i >= 1 && i <= p.chunk && key != none;
+    if (token) rows[i - 1] = p.rows[at];
   }
-  __syncthreads();
-  while (count < kChunk && keys[count + 1] != none) ++count;  // rows with a token come first
+  const int count = __syncthreads_count(token);  // rows with a token come first
   if (count == 0) return;
-  const bool came = first > 0 && keys[0] == keys[1];                          // the first run began before
-  const bool goes = count == kChunk && keys[kChunk + 1] == keys[kChunk];      // the last one goes on
-  if (tile == 0 && threadIdx.x == 0 && goes && !(came && keys[1] == keys[kChunk]))
-    p.active[1 + atomicAdd(p.active, 1u)] = chunk;
-  const int64_t col0 = (static_cast<int64_t>(tile) * kQ * blockDim.x + threadIdx.x) * kVec, step = blockDim.x * kVec;
+  const bool came = first > 0 && keys[0] == keys[1];                              // the first run began before
+  const bool goes = count == p.chunk && keys[p.chunk + 1] == keys[p.chunk];       // the last one goes on
+  if (tile == 0 && i == 0 && goes && !(came && keys[1] == keys[p.chunk])) {
+    uint32_t* to = p.active + 2 + 2 * atomicAdd(p.active, 1u);
+    to[0] = chunk;
+    to[1] = keys[p.chunk];
+  }
+  const int64_t col0 = (static_cast<int64_t>(tile) * kQ * blockDim.x + i) * kVec, step = blockDim.x * kVec;
   const T* dout = static_cast<const T*>(p.dout) + col0;
   float sum[kQ][kVec] = {};
   bool begun = came;  // whether the present run has rows before the chunk
   for (int i0 = 0; i0 < count; i0 += kSumBatch) {
     Piece<T, kVec> v[kSumBatch][kQ];
+    Piece<TTable, kVec> old[kAccumulate ? kSumBatch : 1][kQ];
 #pragma unroll
     for (int k = 0; k < kSumBatch; ++k) {
       if (i0 + k >= count) break;
@@ -491,24 +514,43 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum(const __grid_constant__
 #pragma unroll
       for (int q = 0; q < kQ; ++q)
         if (col0 + q * step < p.cols) v[k][q] = *reinterpret_cast<const Piece<T, kVec>*>(from + q * step);
+      if constexpr (kAccumulate) {
+        const uint32_t key = keys[i0 + k + 1];
+        if (key == keys[i0 + k + 2]) continue;  // the run's last row brings the table's
+#pragma unroll
+        for (int q = 0; q < kQ; ++q)
+          if (col0 + q * step < p.cols)
+            old[k][q] = *reinterpret_cast<const Piece<TTable, kVec>*>(table_at<TTable, kVec>(p, key, col0 + q * step));
+      }
     }
 #pragma unroll
     for (int k = 0; k < kSumBatch; ++k) {
-      const int i = i0 + k;
-      if (i >= count) break;
+      const int r = i0 + k;
+      if (r >= count) break;
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) v[k][q].add_to(sum[q]);
-      const bool last = i + 1 == count;
-      if (!last && keys[i + 2] == keys[i + 1]) continue;
-      const bool on = last && goes;
+      for (int q = 0; q < kQ; ++q) {
+        float x[kVec];
+        v[k][q].to(x);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) sum[q][e] += x[e];
+      }
+      const bool last = r + 1 == count, on = last && goes;
+      if (!last && keys[r + 2] == keys[r + 1]) continue;
+      const bool part = begun || on;
+      float* to = p.parts + (2 * static_cast<int64_t>(chunk) + (begun ? 0 : 1)) * p.part_stride;
 #pragma unroll
       for (int q = 0; q < kQ; ++q) {
         const int64_t col = col0 + q * step;
         if (col < p.cols) {
-          if (begun || on)
-            store<kVec>(p.parts + (2 * static_cast<int64_t>(chunk) + (begun ? 0 : 1)) * p.part_stride + col, sum[q]);
-          else
-            finish_row<TTable, kVec>(p, keys[i + 1], col, sum[q]);
+          if (part) {
+            store<kVec>(to + col, sum[q]);
+          } else {
+            float x[kVec] = {};
+            if constexpr (kAccumulate) old[k][q].to(x);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) x[e] += sum[q][e] * p.scale;
+            store<kVec>(table_at<TTable, kVec>(p, keys[r + 1], col), x);
+          }
         }
 #pragma unroll
         for (int e = 0; e < kVec; ++e) sum[q][e] = 0.0f;
@@ -530,11 +572,11 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join(const __grid_constant
   __shared__ float sums[kJoinGroups][kVec][32];
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
     const int64_t index = item / p.join_tiles;
-    const int chunk = static_cast<int>(p.active[1 + index]);
-    const uint32_t token = p.keys[(chunk + 1) * kChunk - 1];
+    const int chunk = static_cast<int>(p.active[2 + 2 * index]);
+    const uint32_t token = p.active[3 + 2 * index];
     int parts = 0;  // chunks behind the first that begin with the run
     for (int c0 = chunk + 1;; c0 += kJoinThreads) {
-      const int64_t at = static_cast<int64_t>(c0 + threadIdx.x) * kChunk;
+      const int64_t at = static_cast<int64_t>(c0 + threadIdx.x) * p.chunk;
       const int more = __syncthreads_count(at < p.n && p.keys[at] == token);
       parts += more;
       if (more < kJoinThreads) break;
@@ -561,7 +603,12 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join(const __grid_constant
       for (int g = 1; g < kJoinGroups; ++g)
 #pragma unroll
         for (int e = 0; e < kVec; ++e) sum[e] += sums[g][e][lane];
-      finish_row<TTable, kVec>(p, token, col, sum);
+      TTable* to = table_at<TTable, kVec>(p, token, col);
+      float x[kVec] = {};
+      if (p.accumulate) load<kVec>(to, x);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) x[e] += sum[e] * p.scale;
+      store<kVec>(to, x);
     }
     __syncthreads();
   }
@@ -580,7 +627,7 @@ bool vector_rows(const void* p, int64_t rows, int64_t stride, int size) {
 struct Workspace {
   int64_t keys[2], rows[2], counts, active, parts, bytes;
   int64_t part_stride;
-  int32_t chunks, blocks;
+  int32_t chunk, chunks, blocks;
 };
 
 Workspace carve(int64_t rows, int64_t cols) {
@@ -591,7 +638,10 @@ Workspace carve(int64_t rows, int64_t cols) {
     at += round_to(bytes, 256);
     return here;
   };
-  w.chunks = static_cast<int32_t>((rows + kChunk - 1) / kChunk);
+  // Chunks of 16 rows until those of 32 give each SM several blocks: then few rows in sequence count less than
+  // the parts of runs that cross chunks.
+  w.chunk = rows * cols < int64_t(16) << 20 ? 16 : kMaxChunk;
+  w.chunks = static_cast<int32_t>((rows + w.chunk - 1) / w.chunk);
   w.blocks = static_cast<int32_t>((rows + kSortBlock - 1) / kSortBlock);
   w.part_stride = round_to(cols, 8);
   const bool many = rows > kClusterRows;
@@ -600,7 +650,7 @@ Workspace carve(int64_t rows, int64_t cols) {
     w.rows[k] = take(rows * 4);
   }
   if (many) w.counts = take(static_cast<int64_t>(w.blocks) * kMaxBins * 4);
-  w.active = take((static_cast<int64_t>(w.chunks) + 1) * 4);
+  w.active = take((static_cast<int64_t>(w.chunks) + 1) * 8);
   w.parts = take(2 * static_cast<int64_t>(w.chunks) * w.part_stride * 4);
   w.bytes = at;
   return w;
@@ -610,12 +660,13 @@ template <typename T, typename TTable, int kVec>
 int run_sum(SumParams p, int sms, cudaStream_t st) {
   constexpr int kQ = kVec == 8 ? 1 : 4;
   const int64_t groups = (p.cols + kVec - 1) / kVec;
-  const int threads = static_cast<int>(std::min<int64_t>(kSumThreads, round_to((groups + kQ - 1) / kQ, 32)));
+  const int threads = static_cast<int>(std::max<int64_t>(64, std::min<int64_t>(kSumThreads, round_to((groups + kQ - 1) / kQ, 32))));
   const int64_t tiles = (groups + threads * kQ - 1) / (threads * kQ), join_tiles = (groups + 31) / 32;
   if (tiles * p.chunks > INT32_MAX || join_tiles > INT32_MAX) return FSDP_EINVAL;  // more than any memory holds
   p.tiles = static_cast<int32_t>(tiles);
   p.join_tiles = static_cast<int32_t>(join_tiles);
-  if (int rc = launch_after(embed_sum<T, TTable, kVec, kQ>, p.chunks * p.tiles, 1, threads, 0, st, p)) return rc;
+  const auto kernel = p.accumulate ? embed_sum<T, TTable, kVec, kQ, true> : embed_sum<T, TTable, kVec, kQ, false>;
+  if (int rc = launch_after(kernel, p.chunks * p.tiles, 1, threads, 0, st, p)) return rc;
   if (p.chunks == 1) return FSDP_OK;  // no run crosses chunks
   const int64_t items = p.chunks * join_tiles;  // at most
   return launch_after(embed_join<TTable, kVec>, static_cast<int>(std::min<int64_t>(items, 4 * sms)), 1, kJoinThreads, 0, st, p);
@@ -669,11 +720,17 @@ extern "C" int fsdp_embedding(const fsdp_embedding_t* a, const void* tokens, con
                        vector_rows(out, a->rows, a->out_stride, es) &&
                        (!addend || vector_rows(addend, a->rows, a->addend_stride, es));
   const int64_t unit = vectors ? 32 * kGroups<8> * 8 : 32 * kGroups<1>, units = a->rows * ((a->cols + unit - 1) / unit);
-  const int grid = static_cast<int>(std::min<int64_t>((units + kLookupWarps - 1) / kLookupWarps, 1 << 20));
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (a->dtype == FSDP_DTYPE_F32)
-    return launch_after(vectors ? embed_rows<float, 8> : embed_rows<float, 1>, grid, 1, 32 * kLookupWarps, 0, cs, p);
-  return launch_after(vectors ? embed_rows<__nv_bfloat16, 8> : embed_rows<__nv_bfloat16, 1>, grid, 1, 32 * kLookupWarps, 0, cs, p);
+  const auto go = [&](auto kernel, int per_sm) {
+    const int grid = static_cast<int>(std::min<int64_t>((units + kLookupWarps - 1) / kLookupWarps, 152 * per_sm));
+    return launch_after(kernel, grid, 1, 32 * kLookupWarps, 0, cs, p);
+  };
+  if (a->dtype == FSDP_DTYPE_F32) {
+    if (addend) return vectors ? go(embed_rows<float, 8, true>, 2) : go(embed_rows<float, 1, true>, 5);
+    return vectors ? go(embed_rows<float, 8, false>, 4) : go(embed_rows<float, 1, false>, 5);
+  }
+  if (addend) return vectors ? go(embed_rows<__nv_bfloat16, 8, true>, 4) : go(embed_rows<__nv_bfloat16, 1, true>, 5);
+  return vectors ? go(embed_rows<__nv_bfloat16, 8, false>, 5) : go(embed_rows<__nv_bfloat16, 1, false>, 5);
 }
 
 extern "C" int fsdp_embedding_backward_workspace(int64_t rows, int64_t cols, int64_t vocab, int64_t* bytes_out) {
@@ -733,7 +790,7 @@ extern "C" int fsdp_embedding_backward(const fsdp_embedding_backward_t* a, const
       if (int rc = launch_after(sort_move, w.blocks, 1, kSortThreads, 0, cs, p)) return rc;
     }
   }
-  const SumParams p{keys[now], rows[now], n, w.chunks, 0, 0, a->vocab, a->cols, dout, a->dout_stride, dtable,
+  const SumParams p{keys[now], rows[now], n, w.chunk, w.chunks, 0, 0, a->vocab, a->cols, dout, a->dout_stride, dtable,
                     a->dtable_stride, reinterpret_cast<float*>(base + w.parts), w.part_stride, active,
                     static_cast<float>(a->scale), a->accumulate != 0};
   const bool vectors = a->cols % 8 == 0 && vector_rows(dout, a->rows, a->dout_stride, es) &&
