@@ -10,8 +10,9 @@
 // its columns: a run that lies in the chunk goes to the table at once, the parts of
 // one that crosses chunks go to the workspace in fp32 and are added in order by a
 // last kernel. Every sum is fp32 in an order fixed by the tokens alone.
-// Where the table is not added to, it is filled with zeros by the blocks that have no
-// part in the sort, meanwhile.
+// Where the table is not added to, zeros go to its other rows: to all of a small table during the sort,
+// by the SMs that have no part in it; to the rows that no token names (the sort leaves a
+// bit for each row that has one) of a large table, by blocks between those that add.
 #include "host_internal.h"
 #include "launch.h"
 #include "strided.h"
@@ -159,29 +160,31 @@ struct FillParams {
   int64_t rows, row_bytes, pitch;  // row_bytes 0: nothing
 };
 
+// A row's bytes (an even number from an even address): vectors inside, 2 bytes at a time at the ends.
+__device__ __forceinline__ void fill_row(unsigned char* row, int64_t bytes, int64_t first, int64_t step) {
+  const int64_t head = min(bytes, static_cast<int64_t>(-reinterpret_cast<uintptr_t>(row) & 15u));
+  const int64_t vectors = (bytes - head) / 16, tail = head + vectors * 16;
+  for (int64_t i = first; i < vectors; i += step) reinterpret_cast<uint4*>(row + head)[i] = make_uint4(0, 0, 0, 0);
+  for (int64_t i = first; i < head / 2; i += step) reinterpret_cast<uint16_t*>(row)[i] = 0;
+  for (int64_t i = first; i < (bytes - tail) / 2; i += step) reinterpret_cast<uint16_t*>(row + tail)[i] = 0;
+}
+
 __device__ __forceinline__ void fill_zeros(const FillParams& f, int part, int parts) {
-  // a row's bytes (a multiple of 2 from an even address): vectors inside, 2 bytes at a time at the ends
-  const auto fill = [](unsigned char* row, int64_t bytes, int64_t first, int64_t step) {
-    const int64_t head = min(bytes, static_cast<int64_t>(-reinterpret_cast<uintptr_t>(row) & 15u));
-    const int64_t vectors = (bytes - head) / 16, tail = head + vectors * 16;
-    for (int64_t i = first; i < vectors; i += step) reinterpret_cast<uint4*>(row + head)[i] = make_uint4(0, 0, 0, 0);
-    for (int64_t i = first; i < head / 2; i += step) reinterpret_cast<uint16_t*>(row)[i] = 0;
-    for (int64_t i = first; i < (bytes - tail) / 2; i += step) reinterpret_cast<uint16_t*>(row + tail)[i] = 0;
-  };
   if (f.row_bytes == 0) return;
   if (f.rows == 1) {
-    fill(f.to, f.row_bytes, static_cast<int64_t>(part) * blockDim.x + threadIdx.x, static_cast<int64_t>(parts) * blockDim.x);
+    fill_row(f.to, f.row_bytes, static_cast<int64_t>(part) * blockDim.x + threadIdx.x, static_cast<int64_t>(parts) * blockDim.x);
     return;
   }
   const int warps = blockDim.x / 32;
   for (int64_t r = static_cast<int64_t>(part) * warps + threadIdx.x / 32; r < f.rows; r += static_cast<int64_t>(parts) * warps)
-    fill(f.to + r * f.pitch, f.row_bytes, threadIdx.x % 32, 32);
+    fill_row(f.to + r * f.pitch, f.row_bytes, threadIdx.x % 32, 32);
 }
 
 // Up to 8 x 16384 rows are sorted by one cluster of up to eight blocks, which holds them in
 // registers and moves them through (distributed) shared memory. In a pass each warp ranks its rows by digit, 32 at a
-// time; the places follow from the counts of all digits, blocks and warps. Bound by its own
-// latencies: the passes' barriers and 32-row steps.
+// time; the places follow from the counts of all digits, blocks and warps. Bound by its own latencies: of a
+// pass of 16384 rows on eight blocks (cycles, before the stores were paired) ranking took 3000, the counts 3000 and
+// the remote stores 6800.
 constexpr int kMaxBins = 512;
 constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32, kMaxRounds = 16, kMaxCluster = 8;
 constexpr int kClusterRows = kMaxCluster * kMaxRounds * kClusterThreads;
@@ -189,7 +192,8 @@ constexpr int kClusterRows = kMaxCluster * kMaxRounds * kClusterThreads;
 struct ClusterSortParams {
   const void* tokens;
   uint32_t *keys, *rows;
-  uint32_t* active;        // count of the list that embed_sum makes
+  uint32_t* active;        // lists that embed_sum makes: their counts
+  uint32_t* named;         // a bit for each row of the table that a token names (null: not needed)
   int64_t vocab;
   int32_t index_bits, n, cluster, rounds, passes, digit;
   FillParams fill;
@@ -200,8 +204,8 @@ __device__ __forceinline__ uint32_t key_of(int64_t token, int64_t vocab) {
   return static_cast<uint32_t>(token >= 0 && token < vocab ? token : vocab);
 }
 
-__device__ __forceinline__ void remote_store(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+__device__ __forceinline__ void remote_store(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ uint32_t remote_load(uint32_t addr) {
   uint32_t v;
@@ -209,15 +213,21 @@ __device__ __forceinline__ uint32_t remote_load(uint32_t addr) {
   return v;
 }
 
-// A row's place among those of its warp with the same digit (lanes in order, earlier steps first), counted in
-// `count`. The lanes of the same digit by a ballot for each bit: a match of 32 lanes takes several times as long.
-__device__ __forceinline__ uint32_t rank_in_warp(uint32_t* count, uint32_t bin, int bits, bool there, int lane) {
+// The lanes whose `bin` (of nine bits at most) is this lane's, by a ballot for each bit: a match of 32 lanes takes
+// several times as long.
+__device__ __forceinline__ uint32_t same_bin(uint32_t bin, bool there) {
   uint32_t same = __ballot_sync(0xffffffffu, there);
-  for (int b = 0; b < bits; ++b) {
+#pragma unroll
+  for (int b = 0; b < 9; ++b) {
     const bool set = bin >> b & 1;
     const uint32_t others = __ballot_sync(0xffffffffu, set);
     same &= set ? others : ~others;
   }
+  return same;
+}
+
+// A row's place among those of its warp with the same digit (lanes in order, earlier steps first), counted in `count`.
+__device__ __forceinline__ uint32_t rank_in_warp(uint32_t* count, uint32_t bin, uint32_t same, bool there, int lane) {
   const uint32_t below = same & ((1u << lane) - 1);
   uint32_t old = 0;
   if (there) old = count[bin];
@@ -235,11 +245,17 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
   }
   extern __shared__ uint32_t sort_shared[];
   const int each = p.rounds * kClusterThreads, bins = 1 << p.digit;
-  uint32_t *keys = sort_shared, *rows = keys + each, *counts = rows + each;  // counts: [warp][bin]
+  uint2* items = reinterpret_cast<uint2*>(sort_shared);  // key, row
+  uint32_t* counts = sort_shared + 2 * each;             // [warp][bin]
   uint32_t *totals = counts + kClusterWarps * bins, *base = totals + bins;
-  __shared__ uint32_t warp_sums[kClusterWarps];
+  __shared__ uint32_t warp_sums[kClusterWarps], part_sums[kClusterThreads];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, rank = static_cast<int>(blockIdx.x);
-  if (rank == 0 && threadIdx.x == 0) *p.active = 0;
+  // the counts' running sums: thread = part x bins + digit, a part of the warps each
+  const int digit_of = threadIdx.x & (bins - 1), part = threadIdx.x >> p.digit, parts = min(kClusterWarps, kClusterThreads >> p.digit);
+  const int part_warps = kClusterWarps / parts;
+  if (rank == 0 && threadIdx.x < 2) p.active[threadIdx.x] = 0;
+  if (p.named)
+    for (int64_t i = rank * kClusterThreads + threadIdx.x; i < (p.vocab + 31) / 32; i += p.cluster * kClusterThreads) p.named[i] = 0;
   const int mine = warp * 32 * p.rounds + lane;  // of the block's rows: mine, mine + 32, ...
   const int left = p.n - rank * each;
   uint32_t key[kMaxRounds], row[kMaxRounds];
@@ -252,34 +268,53 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
   }
   for (int pass = 0; pass < p.passes; ++pass) {
     const int shift = pass * p.digit;
-    for (int b = threadIdx.x; b < kClusterWarps * bins; b += kClusterThreads) counts[b] = 0;
-    __syncthreads();
-    uint32_t at[kMaxRounds];
+    for (int b = threadIdx.x; b < kClusterWarps * bins / 4; b += kClusterThreads)
+      reinterpret_cast<uint4*>(counts)[b] = make_uint4(0, 0, 0, 0);
+    uint32_t at[kMaxRounds];  // first the lanes of the same digit, then the row's place among its warp's
 #pragma unroll
     for (int k = 0; k < kMaxRounds; ++k) {
       if (k >= p.rounds) break;
-      at[k] = rank_in_warp(counts + warp * bins, key[k] >> shift & (bins - 1), p.digit, mine + 32 * k < left, lane);
+      at[k] = same_bin(key[k] >> shift & (bins - 1), mine + 32 * k < left);
     }
     __syncthreads();
-    // thread b: digit b. The warps' counts become running sums over the warps; totals over the blocks, then over the digits.
-    uint32_t total = 0;
-    if (static_cast<int>(threadIdx.x) < bins) {
+#pragma unroll
+    for (int k = 0; k < kMaxRounds; ++k) {
+      if (k >= p.rounds) break;
+      at[k] = rank_in_warp(counts + warp * bins, key[k] >> shift & (bins - 1), at[k], mine + 32 * k < left, lane);
+    }
+    __syncthreads();
+    uint32_t sum = 0;
+    if (part < parts) {
 #pragma unroll 8
-      for (int w = 0; w < kClusterWarps; ++w) {
-        const uint32_t c = counts[w * bins + threadIdx.x];
-        counts[w * bins + threadIdx.x] = total;
-        total += c;
+      for (int w = 0; w < part_warps; ++w) sum += counts[(part * part_warps + w) * bins + digit_of];
+      part_sums[threadIdx.x] = sum;
+    }
+    __syncthreads();
+    uint32_t total = 0;  // of the digit, in this block (threads of part 0)
+    if (part < parts) {
+      uint32_t run = 0;
+      for (int q = 0; q < parts; ++q) {
+        const uint32_t v = part_sums[(q << p.digit) + digit_of];
+        run += q < part ? v : 0;
+        total += v;
       }
-      totals[threadIdx.x] = total;
+#pragma unroll 8
+      for (int w = 0; w < part_warps; ++w) {
+        uint32_t* c = &counts[(part * part_warps + w) * bins + digit_of];
+        const uint32_t v = *c;
+        *c = run;
+        run += v;
+      }
+      if (part == 0) totals[digit_of] = total;
     }
     uint32_t all = total, before = 0;
     if (p.cluster > 1) {
       tc::cluster_sync();
-      if (static_cast<int>(threadIdx.x) < bins) {
+      if (part == 0) {
         uint32_t of[kMaxCluster];
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r)
-          of[r] = r < p.cluster ? remote_load(tc::in_block(tc::smem_addr(&totals[threadIdx.x]), r)) : 0;
+          of[r] = r < p.cluster ? remote_load(tc::in_block(tc::smem_addr(&totals[digit_of]), r)) : 0;
         all = 0;
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r) {
@@ -288,6 +323,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
         }
       }
     }
+    if (part != 0) all = 0;
     uint32_t run = all;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -298,7 +334,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
     __syncthreads();
     // by whole warps: there may be fewer digits than lanes
     const uint32_t lower = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0);
-    if (static_cast<int>(threadIdx.x) < bins) base[threadIdx.x] = before + run - all + lower;
+    if (part == 0) base[digit_of] = before + run - all + lower;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kMaxRounds; ++k) {
@@ -308,11 +344,9 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
       const uint32_t to = base[bin] + counts[warp * bins + bin] + at[k];
       if (p.cluster > 1) {
         const uint32_t block = to / each, slot = to - block * each;
-        remote_store(tc::in_block(tc::smem_addr(&keys[slot]), block), key[k]);
-        remote_store(tc::in_block(tc::smem_addr(&rows[slot]), block), row[k]);
+        remote_store(tc::in_block(tc::smem_addr(&items[slot]), block), key[k], row[k]);
       } else {
-        keys[to] = key[k];
-        rows[to] = row[k];
+        items[to] = make_uint2(key[k], row[k]);
       }
     }
     if (p.cluster > 1)
@@ -322,16 +356,18 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
 #pragma unroll
     for (int k = 0; k < kMaxRounds; ++k) {
       if (k >= p.rounds) break;
-      key[k] = keys[mine + 32 * k];
-      row[k] = rows[mine + 32 * k];
+      key[k] = items[mine + 32 * k].x;
+      row[k] = items[mine + 32 * k].y;
     }
   }
 #pragma unroll
   for (int k = 0; k < kMaxRounds; ++k) {
     if (k >= p.rounds) break;
-    if (mine + 32 * k >= left) continue;
-    p.keys[rank * each + mine + 32 * k] = key[k];
-    p.rows[rank * each + mine + 32 * k] = row[k];
+    const int i = mine + 32 * k;
+    if (i >= left) continue;
+    p.keys[rank * each + i] = key[k];
+    p.rows[rank * each + i] = row[k];
+    if (p.named && key[k] < p.vocab && (i == 0 || items[i - 1].x != key[k])) atomicOr(&p.named[key[k] / 32], 1u << (key[k] % 32));
   }
 }
 
@@ -377,7 +413,7 @@ __global__ void __launch_bounds__(1024) sort_offsets(const __grid_constant__ Sor
   begin_after_previous();
   __shared__ uint32_t warps[32];
   __shared__ uint32_t carry;
-  if (threadIdx.x == 0) *p.active = 0;
+  if (threadIdx.x < 2) p.active[threadIdx.x] = 0;
   const int n = p.bins * p.blocks, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   if (threadIdx.x == 0) carry = 0;
   for (int i0 = 0; i0 < n; i0 += 4096) {
@@ -424,7 +460,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_move(const __grid_constant_
   for (int k = 0; k < kSortItems; ++k) {
     const int i = first + k * 32;
     key[k] = i < p.n ? sort_key(p, i) : 0;
-    rank[k] = rank_in_warp(next[warp], key[k] >> p.shift & (p.bins - 1), 31 - __clz(p.bins), i < p.n, lane);
+    const uint32_t bin = key[k] >> p.shift & (p.bins - 1);
+    rank[k] = rank_in_warp(next[warp], bin, same_bin(bin, i < p.n), i < p.n, lane);
   }
   __syncthreads();
   for (int b = threadIdx.x; b < p.bins; b += kSortThreads) {
@@ -463,7 +500,12 @@ struct SumParams {
   int64_t dtable_stride;
   float* parts;                 // [2 chunk + (0: the run that came in, 1: the run that goes on)][part_stride]
   int64_t part_stride;
-  uint32_t* active;             // count, then (chunk, token) of the runs that go on behind their first chunk
+  // Runs that go on behind their first chunk, as (chunk, token): counts of the short and the long ones, then the
+  // short ones from the front, the long ones (more than kShortRun chunks behind the first) from the end.
+  uint32_t* active;
+  const uint32_t* named;        // as in the sort; null: the table needs no more zeros
+  int64_t zero_row_bytes;       // of the table's rows
+  int32_t zero_blocks, sum_blocks;
   float scale;
   bool accumulate;
 };
@@ -473,13 +515,34 @@ __device__ __forceinline__ TTable* table_at(const SumParams& p, uint32_t token, 
   return static_cast<TTable*>(p.dtable) + token * p.dtable_stride + col;
 }
 
+constexpr int kShortRun = 16;
+constexpr int kZeroRows = 8;  // rows of the table for each block that writes zeros
+
+__device__ __forceinline__ void zero_unnamed(const SumParams& p, uint32_t part) {
+  for (int64_t v = static_cast<int64_t>(part) * kZeroRows, end = min(v + kZeroRows, p.vocab); v < end; ++v)
+    if (!(p.named[v / 32] >> (v % 32) & 1))
+      fill_row(static_cast<unsigned char*>(p.dtable) + v * p.dtable_stride * (p.zero_row_bytes / p.cols), p.zero_row_bytes,
+               threadIdx.x, blockDim.x);
+}
+
 // kQ pieces of kVec columns for each thread. Bound by reading dout (HBM); kSumBatch rows, and the table's rows
 // that are added to, are on their way together.
 template <typename T, typename TTable, int kVec, int kQ, bool kAccumulate>
 __global__ void __launch_bounds__(kSumThreads) embed_sum(const __grid_constant__ SumParams p) {
   begin_after_previous();
   __shared__ uint32_t keys[kMaxChunk + 2], rows[kMaxChunk];  // keys[0]: of the row before the chunk; the last: behind it
-  const int chunk = blockIdx.x / p.tiles, tile = blockIdx.x - chunk * p.tiles;
+  int block = blockIdx.x;
+  if (!kAccumulate && p.zero_blocks) {  // blocks that write zeros, spread evenly between the others
+    const uint32_t all = p.zero_blocks + p.sum_blocks;
+    const uint32_t zeros = static_cast<uint32_t>(static_cast<uint64_t>(block) * p.zero_blocks / all);
+    const uint32_t next = static_cast<uint32_t>(static_cast<uint64_t>(block + 1) * p.zero_blocks / all);
+    if (next != zeros) {
+      zero_unnamed(p, zeros);
+      return;
+    }
+    block -= zeros;
+  }
+  const int chunk = block / p.tiles, tile = block - chunk * p.tiles;
   const int first = chunk * p.chunk;
   const uint32_t none = static_cast<uint32_t>(p.vocab);
   bool token = false;
@@ -496,7 +559,10 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum(const __grid_constant__
   const bool came = first > 0 && keys[0] == keys[1];                              // the first run began before
   const bool goes = count == p.chunk && keys[p.chunk + 1] == keys[p.chunk];       // the last one goes on
   if (tile == 0 && i == 0 && goes && !(came && keys[1] == keys[p.chunk])) {
-    uint32_t* to = p.active + 2 + 2 * atomicAdd(p.active, 1u);
+    const int64_t far = first + static_cast<int64_t>(kShortRun + 1) * p.chunk;
+    const bool is_long = far < p.n && p.keys[far] == keys[p.chunk];
+    const uint32_t index = atomicAdd(&p.active[is_long], 1u);
+    uint32_t* to = p.active + 2 + 2 * static_cast<int64_t>(is_long ? p.chunks - 1 - index : index);
     to[0] = chunk;
     to[1] = keys[p.chunk];
   }
@@ -560,40 +626,56 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum(const __grid_constant__
   }
 }
 
-// Adds up the runs that cross chunks: eight groups of threads each a share of a run's
-// chunks, then the groups in order.
+// Adds up the runs that cross chunks. Short ones by a warp for each 32 kVec columns, chunk after chunk; long ones
+// by a block: eight groups of threads each a share of the chunks, then the groups in order.
 constexpr int kJoinGroups = 8, kJoinThreads = 32 * kJoinGroups;
+
+template <typename TTable, int kVec>
+__device__ __forceinline__ void add_to_table(const SumParams& p, uint32_t token, int64_t col, const float (&sum)[kVec]) {
+  TTable* to = table_at<TTable, kVec>(p, token, col);
+  float x[kVec] = {};
+  if (p.accumulate) load<kVec>(to, x);
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) x[e] += sum[e] * p.scale;
+  store<kVec>(to, x);
+}
+
+// Adds the parts that chunks [from, to) hold of the run that came in.
+template <int kVec>
+__device__ __forceinline__ void add_parts(const SumParams& p, int from, int to, int64_t col, float (&sum)[kVec]) {
+#pragma unroll 4
+  for (int c = from; c < to; ++c) {
+    float v[kVec];
+    load<kVec>(p.parts + 2 * static_cast<int64_t>(c) * p.part_stride + col, v);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) sum[e] += v[e];
+  }
+}
 
 template <typename TTable, int kVec>
 __global__ void __launch_bounds__(kJoinThreads) embed_join(const __grid_constant__ SumParams p) {
   begin_after_previous();
-  const int64_t items = static_cast<int64_t>(p.active[0]) * p.join_tiles;
+  const int64_t shorts = static_cast<int64_t>(p.active[0]) * p.join_tiles, longs = static_cast<int64_t>(p.active[1]) * p.join_tiles;
   const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
   __shared__ float sums[kJoinGroups][kVec][32];
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+  for (int64_t item = blockIdx.x; item < longs; item += gridDim.x) {
     const int64_t index = item / p.join_tiles;
-    const int chunk = static_cast<int>(p.active[2 + 2 * index]);
-    const uint32_t token = p.active[3 + 2 * index];
+    const uint32_t* run = p.active + 2 + 2 * (p.chunks - 1 - index);
+    const int chunk = static_cast<int>(run[0]);
+    const uint32_t token = run[1];
     int parts = 0;  // chunks behind the first that begin with the run
     for (int c0 = chunk + 1;; c0 += kJoinThreads) {
-      const int64_t at = static_cast<int64_t>(c0 + threadIdx.x) * p.chunk;
+      const int64_t at = (c0 + static_cast<int64_t>(threadIdx.x)) * p.chunk;
       const int more = __syncthreads_count(at < p.n && p.keys[at] == token);
       parts += more;
       if (more < kJoinThreads) break;
     }
     const int each = (parts + kJoinGroups - 1) / kJoinGroups;
-    const int from = chunk + 1 + min(parts, group * each), to = chunk + 1 + min(parts, (group + 1) * each);
     const int64_t col = ((item - index * p.join_tiles) * 32 + lane) * kVec;
     float sum[kVec] = {};
     if (col < p.cols) {
       if (group == 0) load<kVec>(p.parts + (2 * static_cast<int64_t>(chunk) + 1) * p.part_stride + col, sum);
-#pragma unroll 4
-      for (int c = from; c < to; ++c) {
-        float v[kVec];
-        load<kVec>(p.parts + 2 * static_cast<int64_t>(c) * p.part_stride + col, v);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) sum[e] += v[e];
-      }
+      add_parts<kVec>(p, chunk + 1 + min(parts, group * each), chunk + 1 + min(parts, (group + 1) * each), col, sum);
     }
 #pragma unroll
     for (int e = 0; e < kVec; ++e) sums[group][e][lane] = sum[e];
@@ -603,14 +685,23 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join(const __grid_constant
       for (int g = 1; g < kJoinGroups; ++g)
 #pragma unroll
         for (int e = 0; e < kVec; ++e) sum[e] += sums[g][e][lane];
-      TTable* to = table_at<TTable, kVec>(p, token, col);
-      float x[kVec] = {};
-      if (p.accumulate) load<kVec>(to, x);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) x[e] += sum[e] * p.scale;
-      store<kVec>(to, x);
+      add_to_table<TTable, kVec>(p, token, col, sum);
     }
     __syncthreads();
+  }
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kJoinGroups + group; item < shorts; item += static_cast<int64_t>(gridDim.x) * kJoinGroups) {
+    const int64_t index = item / p.join_tiles;
+    const uint32_t* run = p.active + 2 + 2 * index;
+    const int chunk = static_cast<int>(run[0]);
+    const uint32_t token = run[1];
+    const int64_t at = (chunk + 1 + static_cast<int64_t>(lane)) * p.chunk;
+    const int parts = __popc(__ballot_sync(0xffffffffu, lane < kShortRun && at < p.n && p.keys[at] == token));
+    const int64_t col = ((item - index * p.join_tiles) * 32 + lane) * kVec;
+    if (col >= p.cols) continue;
+    float sum[kVec];
+    load<kVec>(p.parts + (2 * static_cast<int64_t>(chunk) + 1) * p.part_stride + col, sum);
+    add_parts<kVec>(p, chunk + 1, chunk + 1 + parts, col, sum);
+    add_to_table<TTable, kVec>(p, token, col, sum);
   }
 }
 
@@ -625,12 +716,12 @@ bool vector_rows(const void* p, int64_t rows, int64_t stride, int size) {
 }
 
 struct Workspace {
-  int64_t keys[2], rows[2], counts, active, parts, bytes;
+  int64_t keys[2], rows[2], counts, active, named, parts, bytes;
   int64_t part_stride;
   int32_t chunk, chunks, blocks;
 };
 
-Workspace carve(int64_t rows, int64_t cols) {
+Workspace carve(int64_t rows, int64_t cols, int64_t vocab) {
   Workspace w{};
   int64_t at = 256;  // the caller's pointer may have any alignment
   const auto take = [&](int64_t bytes) {
@@ -651,6 +742,7 @@ Workspace carve(int64_t rows, int64_t cols) {
   }
   if (many) w.counts = take(static_cast<int64_t>(w.blocks) * kMaxBins * 4);
   w.active = take((static_cast<int64_t>(w.chunks) + 1) * 8);
+  w.named = take((vocab + 31) / 32 * 4);
   w.parts = take(2 * static_cast<int64_t>(w.chunks) * w.part_stride * 4);
   w.bytes = at;
   return w;
@@ -665,11 +757,14 @@ int run_sum(SumParams p, int sms, cudaStream_t st) {
   if (tiles * p.chunks > INT32_MAX || join_tiles > INT32_MAX) return FSDP_EINVAL;  // more than any memory holds
   p.tiles = static_cast<int32_t>(tiles);
   p.join_tiles = static_cast<int32_t>(join_tiles);
+  p.sum_blocks = p.chunks * p.tiles;
+  p.zero_blocks = p.named ? static_cast<int32_t>((p.vocab + kZeroRows - 1) / kZeroRows) : 0;
+  if (static_cast<int64_t>(p.sum_blocks) + p.zero_blocks > INT32_MAX) return FSDP_EINVAL;
   const auto kernel = p.accumulate ? embed_sum<T, TTable, kVec, kQ, true> : embed_sum<T, TTable, kVec, kQ, false>;
-  if (int rc = launch_after(kernel, p.chunks * p.tiles, 1, threads, 0, st, p)) return rc;
+  if (int rc = launch_after(kernel, p.sum_blocks + p.zero_blocks, 1, threads, 0, st, p)) return rc;
   if (p.chunks == 1) return FSDP_OK;  // no run crosses chunks
   const int64_t items = p.chunks * join_tiles;  // at most
-  return launch_after(embed_join<TTable, kVec>, static_cast<int>(std::min<int64_t>(items, 4 * sms)), 1, kJoinThreads, 0, st, p);
+  return launch_after(embed_join<TTable, kVec>, static_cast<int>(std::min<int64_t>(items, 6 * sms)), 1, kJoinThreads, 0, st, p);
 }
 
 template <typename T, typename TTable>
@@ -677,11 +772,11 @@ int run_sum_as(const SumParams& p, bool vectors, int sms, cudaStream_t st) {
   return vectors ? run_sum<T, TTable, 8>(p, sms, st) : run_sum<T, TTable, 1>(p, sms, st);
 }
 
-// The sort of up to kClusterRows rows; the other blocks fill. As many blocks as leave
-// each four steps of 32 rows a warp, then longer ones.
+// The sort of up to kClusterRows rows; the other blocks fill. Two steps of 32 rows for each warp, then more blocks,
+// then more steps.
 int run_cluster_sort(ClusterSortParams p, int sms, cudaStream_t st) {
   p.cluster = 1;
-  while (p.cluster < kMaxCluster && p.n > p.cluster * 4 * kClusterThreads) p.cluster *= 2;
+  while (p.cluster < kMaxCluster && p.n > p.cluster * 2 * kClusterThreads) p.cluster *= 2;
   p.rounds = (p.n + p.cluster * kClusterThreads - 1) / (p.cluster * kClusterThreads);
   const int bins = 1 << p.digit;
   const int smem = (2 * p.rounds * kClusterThreads + (kClusterWarps + 2) * bins) * 4;
@@ -736,7 +831,7 @@ extern "C" int fsdp_embedding(const fsdp_embedding_t* a, const void* tokens, con
 extern "C" int fsdp_embedding_backward_workspace(int64_t rows, int64_t cols, int64_t vocab, int64_t* bytes_out) {
   if (!bytes_out || rows < 0 || rows > kMaxRows || cols < 1 || cols > kMaxCols || vocab < 1 || vocab > kMaxVocab)
     return FSDP_EINVAL;
-  *bytes_out = carve(rows, cols).bytes;
+  *bytes_out = carve(rows, cols, vocab).bytes;
   return FSDP_OK;
 }
 
@@ -761,14 +856,20 @@ extern "C" int fsdp_embedding_backward(const fsdp_embedding_backward_t* a, const
   if (fill.rows > 1 && fill.pitch == fill.row_bytes) fill.row_bytes *= fill.rows, fill.rows = 1;  // one long row
   Device dev;
   if (int rc = device_facts(&dev)) return rc;
+  // A table beyond what is filled during a sort (about 8 us) leaves its zeros to the blocks between the sums' (see
+  // the top): 16384 x 4096, 32000 rows 104 -> 77 us.
+  const bool later = fill.row_bytes && a->rows > 0 && a->rows <= kClusterRows && a->vocab * a->cols * ts > (int64_t(32) << 20) &&
+                     a->cols * ts >= 256;
+  if (later) fill.row_bytes = 0;
   if (fill.row_bytes && (a->rows == 0 || a->rows > kClusterRows)) {
     if (int rc = launch_after(embed_fill, 2 * dev.sms, 1, kClusterThreads, 0, cs, fill)) return rc;
   }
   if (a->rows == 0) return FSDP_OK;
 
-  const Workspace w = carve(a->rows, a->cols);
+  const Workspace w = carve(a->rows, a->cols, a->vocab);
   auto* base = reinterpret_cast<unsigned char*>(round_to(reinterpret_cast<intptr_t>(workspace), 256) - 256);
-  uint32_t *keys[2], *rows[2], *active = reinterpret_cast<uint32_t*>(base + w.active);
+  uint32_t *keys[2], *rows[2], *active = reinterpret_cast<uint32_t*>(base + w.active),
+           *named = later ? reinterpret_cast<uint32_t*>(base + w.named) : nullptr;
   for (int k = 0; k < 2; ++k) {
     keys[k] = reinterpret_cast<uint32_t*>(base + w.keys[k]);
     rows[k] = reinterpret_cast<uint32_t*>(base + w.rows[k]);
@@ -779,7 +880,7 @@ extern "C" int fsdp_embedding_backward(const fsdp_embedding_backward_t* a, const
   const int32_t n = static_cast<int32_t>(a->rows);
   int now = 0;
   if (a->rows <= kClusterRows) {
-    const ClusterSortParams p{tokens, keys[0], rows[0], active, a->vocab, 8 * is, n, 0, 0, passes, digit, fill};
+    const ClusterSortParams p{tokens, keys[0], rows[0], active, named, a->vocab, 8 * is, n, 0, 0, passes, digit, fill};
     if (int rc = run_cluster_sort(p, dev.sms, cs)) return rc;
   } else {
     for (int k = 0; k < passes; ++k, now ^= 1) {
@@ -791,8 +892,8 @@ extern "C" int fsdp_embedding_backward(const fsdp_embedding_backward_t* a, const
     }
   }
   const SumParams p{keys[now], rows[now], n, w.chunk, w.chunks, 0, 0, a->vocab, a->cols, dout, a->dout_stride, dtable,
-                    a->dtable_stride, reinterpret_cast<float*>(base + w.parts), w.part_stride, active,
-                    static_cast<float>(a->scale), a->accumulate != 0};
+                    a->dtable_stride, reinterpret_cast<float*>(base + w.parts), w.part_stride, active, named,
+                    a->cols * ts, 0, 0, static_cast<float>(a->scale), a->accumulate != 0};
   const bool vectors = a->cols % 8 == 0 && vector_rows(dout, a->rows, a->dout_stride, es) &&
                        vector_rows(dtable, a->vocab, a->dtable_stride, ts);
   const bool in32 = a->dtype == FSDP_DTYPE_F32, table32 = a->table_dtype == FSDP_DTYPE_F32;

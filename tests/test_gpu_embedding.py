@@ -136,6 +136,19 @@ def test_gradient_in_a_flat_row(dtype, pad, offset, cols):
         assert untouched(whole, dtable)
 
 
+@pytest.mark.parametrize("cols,dtype,pad,offset", [(256, BF16, 0, 0), (256, BF16, 8, 3), (129, F32, 0, 1), (131, F32, 2, 0)])
+def test_gradient_of_a_large_table(cols, dtype, pad, offset):
+    """Tables whose other rows are set to zero beside the sums: every row, those next to a named one included."""
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    dout = rand(gen, 900, cols, dtype=dtype)
+    tokens = torch.randint(0, 70000, (900,), generator=gen, device="cuda")
+    tokens[:8] = torch.tensor([0, 69999, 31, 32, 33, -1, 70000, 69998], device="cuda")
+    tokens[100:300] = 4096
+    whole, dtable = guarded(70000, cols, dtype, cols + pad, offset)
+    check_gradient(tokens, dout, dtable, 1.5, False)
+    assert untouched(whole, dtable)
+
+
 @pytest.mark.parametrize("tokens", [[-1] * 100, [500] * 100, [-7, 500] * 50, [3] * 100, [0] * 50 + [9] * 50, list(range(9, -1, -1)) * 10],
                          ids=["none", "beyond", "neither", "one", "ends", "falling"])
 @pytest.mark.parametrize("accumulate", [False, True])
