@@ -126,6 +126,11 @@ __device__ __forceinline__ uint16_t shared_load_half(uint32_t addr) {
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ uint32_t shared_load_word(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 
 // bf16, bf16 -> fp32.
 __device__ __forceinline__ uint32_t bf16_kind(int m, int n, bool a_mn, bool b_mn) {
@@ -192,17 +197,24 @@ __device__ __forceinline__ void send_rows(const Product& g, uint32_t box, int ro
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) tma_store(&g.out, col0, row0, box);
-  } else {  // rows off 16-byte alignment, element by element
+  } else {  // rows off 16-byte alignment: by pairs of elements at 4-byte boundaries, and single ones at the ends
     __syncwarp();
-    const int rows = min(32, g.m - row0);
-    for (int r = 0; r < rows; ++r)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = 32 * h + lane;
-        if (col0 + c >= g.n) continue;
-        g.rows[(row0 + r) * g.rows_stride + col0 + c] =
-            shared_load_half(box + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2);
+    const int rows = min(32, g.m - row0), cols = min(64, g.n - col0);
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+      uint16_t* to = g.rows + (row0 + r) * g.rows_stride + col0;
+      const auto at = [=](int c) { return box + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2; };
+      const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(to) >> 1 & 1);
+      const int c = 2 * lane + odd;
+      if (c + 1 < cols) {
+        const uint32_t two = odd ? shared_load_half(at(c)) | static_cast<uint32_t>(shared_load_half(at(c + 1))) << 16
+                                 : shared_load_word(at(c));
+        *reinterpret_cast<uint32_t*>(to + c) = two;
+      } else if (c < cols) {
+        to[c] = shared_load_half(at(c));
       }
+      if (odd && lane == 31) to[0] = shared_load_half(at(0));
+    }
     __syncwarp();
   }
   if (lane == 0) bulk_commit();
@@ -347,19 +359,21 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
       int from;
       const int steps = inner(g, at.split, &from);
       float x[kSpan];
-#pragma unroll
-      for (int c = 0; c < kSpan; ++c) x[c] = 0.0f;
       for (int step0 = 0; ok && step0 < steps; step0 += p.segment, ++n) {
         const uint32_t buf = n & 1u;
         ok = bar_wait_warp(smem_addr(&done_bar[buf]), (n >> 1) & 1u, guard);
         if (!ok) break;
         fence_after();
+        if (step0 == 0) {
+          tmem_load128(lanes + buf * kN, x);
+        } else {
 #pragma unroll
-        for (int c = 0; c < kSpan; c += 32) {
-          float v[32];
-          tmem_load32(lanes + buf * kN + c, v);
+          for (int c = 0; c < kSpan; c += 32) {
+            float v[32];
+            tmem_load32(lanes + buf * kN + c, v);
 #pragma unroll
-          for (int q = 0; q < 32; ++q) x[c + q] += v[q];
+            for (int q = 0; q < 32; ++q) x[c + q] += v[q];
+          }
         }
         fence_before();
         __syncwarp();
@@ -391,9 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
             p.target_score[row] = score;
           }
         }
-        float most = -INFINITY;
+        float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 0; c < kSpan; ++c) most = fmaxf(most, x[c]);
+        for (int c = 4; c < kSpan; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
+        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         const float shift = reference_of(most) * kLog2e;
         float sum[4] = {};
 #pragma unroll
@@ -570,13 +585,33 @@ struct CopyParams {
   int64_t rows, cols;
 };
 
-// Rows off 16-byte alignment into rows that tensor maps can describe.
+// Rows off 16-byte alignment into rows that tensor maps can describe, 8 elements a thread: the (one or two)
+// aligned vectors that hold them, shifted. Bound by HBM.
 __global__ void __launch_bounds__(256) ce_copy(const __grid_constant__ CopyParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x % 32;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32; r < p.rows; r += static_cast<int64_t>(gridDim.x) * 8)
-    for (int64_t c = lane; c < p.cols; c += 32) p.to[r * p.to_stride + c] = p.from[r * p.from_stride + c];
+  const uint32_t per_row = static_cast<uint32_t>((p.cols + 7) / 8);
+  const int64_t vectors = p.rows * per_row;
+  for (int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; v < vectors; v += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = vectors >> 31 ? v / per_row : static_cast<uint32_t>(v) / per_row, c = (v - r * per_row) * 8;
+    const uintptr_t row = reinterpret_cast<uintptr_t>(p.from + r * p.from_stride), from = row + 2 * c, end = row + 2 * p.cols;
+    const uintptr_t base = from & ~uintptr_t(15);
+    const uint32_t off = static_cast<uint32_t>(from & 15);
+    const uint4 a = *reinterpret_cast<const uint4*>(base);
+    uint4 b = make_uint4(0, 0, 0, 0);
+    if (off && base + 16 < end) b = *reinterpret_cast<const uint4*>(base + 16);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (off & 8)
+#pragma unroll
+      for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+    if (off & 4)
+#pragma unroll
+      for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+    if (off & 2)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+    *reinterpret_cast<uint4*>(p.to + r * p.to_stride + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 struct JoinParams {
@@ -589,15 +624,28 @@ struct JoinParams {
   int64_t out_stride;
 };
 
-// The sum of a product's parts, times the row's factor.
-__global__ void __launch_bounds__(256) ce_join(const __grid_constant__ JoinParams p) {
+// The sum of a product's parts, times the row's factor: eight groups of threads each a share of the
+// parts, then the groups in order.
+constexpr int kJoinGroups = 8;
+
+__global__ void __launch_bounds__(32 * kJoinGroups) ce_join(const __grid_constant__ JoinParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t per_row = (p.cols + 255) / 256;
-  const int64_t row = blockIdx.x / per_row, col = (blockIdx.x - row * per_row) * 256 + threadIdx.x;
-  if (col >= p.cols) return;
+  __shared__ float sums[kJoinGroups][32];
+  const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
+  const int64_t per_row = (p.cols + 31) / 32;
+  const int64_t row = blockIdx.x / per_row, col = (blockIdx.x - row * per_row) * 32 + lane;
+  const int each = (p.splits + kJoinGroups - 1) / kJoinGroups;
+  const int from = min(p.splits, group * each), to = min(p.splits, from + each);
   float sum = 0.0f;
-  for (int s = 0; s < p.splits; ++s) sum += p.wide[(s * p.rows + row) * p.wide_stride + col];
+  if (col < p.cols)
+#pragma unroll 8
+    for (int s = from; s < to; ++s) sum += p.wide[(s * p.rows + row) * p.wide_stride + col];
+  sums[group][lane] = sum;
+  __syncthreads();
+  if (group != 0 || col >= p.cols) return;
+#pragma unroll
+  for (int g = 1; g < kJoinGroups; ++g) sum += sums[g][lane];
   const float factor = p.factor[row];
   p.out[row * p.out_stride + col] = bf16_bits(factor == 0.0f ? 0.0f : sum * factor);
 }
@@ -729,7 +777,7 @@ int steps_of(int64_t k) { return static_cast<int>((k + kTileK - 1) / kTileK); }
 int copy_rows(const uint16_t* from, int64_t from_stride, uint16_t* to, int64_t to_stride, int64_t rows, int64_t cols,
               cudaStream_t st) {
   const CopyParams p{from, from_stride, to, to_stride, rows, cols};
-  return launch_after(ce_copy, static_cast<int>(std::min<int64_t>((rows + 7) / 8, 152 * 8)), 1, 256, 0, st, p);
+  return launch_after(ce_copy, static_cast<int>(std::min<int64_t>((rows * ((cols + 7) / 8) + 255) / 256, 152 * 8)), 1, 256, 0, st, p);
 }
 
 struct Call {
@@ -864,8 +912,8 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
       return rc;
     if (plan.splits > 1) {
       const JoinParams j{dh.wide, dh.wide_stride, dh.splits, n, a.cols, rows.factor, dhidden, a.dhidden_stride};
-      const int64_t blocks = n * ((a.cols + 255) / 256);
-      if (int rc = launch_after(ce_join, static_cast<int>(blocks), 1, 256, 0, st, j)) return rc;
+      const int64_t blocks = n * ((a.cols + 31) / 32);  // few: a product is cut only where its result has few tiles
+      if (int rc = launch_after(ce_join, static_cast<int>(blocks), 1, 32 * kJoinGroups, 0, st, j)) return rc;
     }
   }
   return FSDP_OK;

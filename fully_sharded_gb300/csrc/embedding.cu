@@ -182,9 +182,9 @@ __device__ __forceinline__ void fill_zeros(const FillParams& f, int part, int pa
 
 // Up to 8 x 16384 rows are sorted by one cluster of up to eight blocks, which holds them in
 // registers and moves them through (distributed) shared memory. In a pass each warp ranks its rows by digit, 32 at a
-// time; the places follow from the counts of all digits, blocks and warps. Bound by its own latencies: of a
-// pass of 16384 rows on eight blocks (cycles, before the stores were paired) ranking took 3000, the counts 3000 and
-// the remote stores 6800.
+// time; the places follow from the counts of all digits, blocks and warps. Bound by its own latencies (cycles of a
+// pass of 16384 rows on eight blocks: ranking 3000, running sums 1300, exchange of the blocks' totals 2000, their sums
+// 500, moving 2000 and waiting for it 2100).
 constexpr int kMaxBins = 512;
 constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32, kMaxRounds = 16, kMaxCluster = 8;
 constexpr int kClusterRows = kMaxCluster * kMaxRounds * kClusterThreads;
@@ -213,12 +213,13 @@ __device__ __forceinline__ uint32_t remote_load(uint32_t addr) {
   return v;
 }
 
-// The lanes whose `bin` (of nine bits at most) is this lane's, by a ballot for each bit: a match of 32 lanes takes
+// The lanes whose `bin` (of `bits`, at most nine) is this lane's, by a ballot for each bit: a match of 32 lanes takes
 // several times as long.
-__device__ __forceinline__ uint32_t same_bin(uint32_t bin, bool there) {
+__device__ __forceinline__ uint32_t same_bin(uint32_t bin, int bits, bool there) {
   uint32_t same = __ballot_sync(0xffffffffu, there);
 #pragma unroll
   for (int b = 0; b < 9; ++b) {
+    if (b > 4 && b >= bits) break;
     const bool set = bin >> b & 1;
     const uint32_t others = __ballot_sync(0xffffffffu, set);
     same &= set ? others : ~others;
@@ -248,11 +249,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
   uint2* items = reinterpret_cast<uint2*>(sort_shared);  // key, row
   uint32_t* counts = sort_shared + 2 * each;             // [warp][bin]
   uint32_t *totals = counts + kClusterWarps * bins, *base = totals + bins;
-  __shared__ uint32_t warp_sums[kClusterWarps], part_sums[kClusterThreads];
+  __shared__ uint32_t warp_sums[kClusterWarps];
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, rank = static_cast<int>(blockIdx.x);
-  // the counts' running sums: thread = part x bins + digit, a part of the warps each
-  const int digit_of = threadIdx.x & (bins - 1), part = threadIdx.x >> p.digit, parts = min(kClusterWarps, kClusterThreads >> p.digit);
-  const int part_warps = kClusterWarps / parts;
+  const int digit_of = threadIdx.x;
+  const bool has_digit = digit_of < bins;
   if (rank == 0 && threadIdx.x < 2) p.active[threadIdx.x] = 0;
   if (p.named)
     for (int64_t i = rank * kClusterThreads + threadIdx.x; i < (p.vocab + 31) / 32; i += p.cluster * kClusterThreads) p.named[i] = 0;
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
 #pragma unroll
     for (int k = 0; k < kMaxRounds; ++k) {
       if (k >= p.rounds) break;
-      at[k] = same_bin(key[k] >> shift & (bins - 1), mine + 32 * k < left);
+      at[k] = same_bin(key[k] >> shift & (bins - 1), p.digit, mine + 32 * k < left);
     }
     __syncthreads();
 #pragma unroll
@@ -283,34 +283,20 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
       at[k] = rank_in_warp(counts + warp * bins, key[k] >> shift & (bins - 1), at[k], mine + 32 * k < left, lane);
     }
     __syncthreads();
-    uint32_t sum = 0;
-    if (part < parts) {
+    // thread b: digit b. Running sums over the warps; its count in all blocks, and in those before this one.
+    uint32_t all = 0, before = 0;
+    if (has_digit) {
 #pragma unroll 8
-      for (int w = 0; w < part_warps; ++w) sum += counts[(part * part_warps + w) * bins + digit_of];
-      part_sums[threadIdx.x] = sum;
-    }
-    __syncthreads();
-    uint32_t total = 0;  // of the digit, in this block (threads of part 0)
-    if (part < parts) {
-      uint32_t run = 0;
-      for (int q = 0; q < parts; ++q) {
-        const uint32_t v = part_sums[(q << p.digit) + digit_of];
-        run += q < part ? v : 0;
-        total += v;
+      for (int w = 0; w < kClusterWarps; ++w) {
+        const uint32_t c = counts[w * bins + digit_of];
+        counts[w * bins + digit_of] = all;
+        all += c;
       }
-#pragma unroll 8
-      for (int w = 0; w < part_warps; ++w) {
-        uint32_t* c = &counts[(part * part_warps + w) * bins + digit_of];
-        const uint32_t v = *c;
-        *c = run;
-        run += v;
-      }
-      if (part == 0) totals[digit_of] = total;
+      totals[digit_of] = all;
     }
-    uint32_t all = total, before = 0;
     if (p.cluster > 1) {
       tc::cluster_sync();
-      if (part == 0) {
+      if (has_digit) {
         uint32_t of[kMaxCluster];
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r)
@@ -323,7 +309,6 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
         }
       }
     }
-    if (part != 0) all = 0;
     uint32_t run = all;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -334,7 +319,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
     __syncthreads();
     // by whole warps: there may be fewer digits than lanes
     const uint32_t lower = __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0);
-    if (part == 0) base[digit_of] = before + run - all + lower;
+    if (has_digit) base[digit_of] = before + run - all + lower;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kMaxRounds; ++k) {
@@ -461,7 +446,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_move(const __grid_constant_
     const int i = first + k * 32;
     key[k] = i < p.n ? sort_key(p, i) : 0;
     const uint32_t bin = key[k] >> p.shift & (p.bins - 1);
-    rank[k] = rank_in_warp(next[warp], bin, same_bin(bin, i < p.n), i < p.n, lane);
+    rank[k] = rank_in_warp(next[warp], bin, same_bin(bin, 31 - __clz(p.bins), i < p.n), i < p.n, lane);
   }
   __syncthreads();
   for (int b = threadIdx.x; b < p.bins; b += kSortThreads) {
@@ -658,8 +643,9 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join(const __grid_constant
   const int64_t shorts = static_cast<int64_t>(p.active[0]) * p.join_tiles, longs = static_cast<int64_t>(p.active[1]) * p.join_tiles;
   const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
   __shared__ float sums[kJoinGroups][kVec][32];
-  for (int64_t item = blockIdx.x; item < longs; item += gridDim.x) {
-    const int64_t index = item / p.join_tiles;
+  int64_t turn = blockIdx.x;  // the long items, then eight short ones at a time
+  for (; turn < longs; turn += gridDim.x) {
+    const int64_t item = turn, index = item / p.join_tiles;
     const uint32_t* run = p.active + 2 + 2 * (p.chunks - 1 - index);
     const int chunk = static_cast<int>(run[0]);
     const uint32_t token = run[1];
@@ -689,7 +675,9 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join(const __grid_constant
     }
     __syncthreads();
   }
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kJoinGroups + group; item < shorts; item += static_cast<int64_t>(gridDim.x) * kJoinGroups) {
+  for (;; turn += gridDim.x) {
+    const int64_t item = (turn - longs) * kJoinGroups + group;
+    if (item >= shorts) return;
     const int64_t index = item / p.join_tiles;
     const uint32_t* run = p.active + 2 + 2 * index;
     const int chunk = static_cast<int>(run[0]);
