@@ -178,34 +178,45 @@ __device__ __forceinline__ Place place_of(const Params& p, int t) {
   return q;
 }
 
-// Sends 64 columns of the warp's 32 rows (a lane's own row in v, as bf16), from (row0, col0) on.
+// Sends the warp's 32 rows of 128 columns (a lane's own row in value(c), as bf16), from (row0, col0) on: two boxes
+// with one fence between the writes and the copies.
 template <typename F>
-__device__ __forceinline__ void send_rows(const Product& g, uint32_t box, int row0, int col0, int lane, F value) {
-  if (lane == 0) bulk_wait_read<1>();  // the box before the last has left its place
+__device__ __forceinline__ void send_rows(const Product& g, uint32_t boxes, int row0, int col0, int lane, F value) {
+  if (lane == 0) bulk_wait_read<0>();  // the last boxes have left their places
   __syncwarp();
 #pragma unroll
-  for (int q = 0; q < 8; ++q) {
+  for (int q = 0; q < kSpan / 8; ++q) {
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const __nv_bfloat162 two = __floats2bfloat162_rn(value(8 * q + 2 * k), value(8 * q + 2 * k + 1));
       w[k] = *reinterpret_cast<const uint32_t*>(&two);
     }
-    shared_store(box + lane * 128 + ((q ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+    shared_store(boxes + (q >> 3) * kBoxBytes + lane * 128 + (((q & 7) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
   }
   if (!g.rows) {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
-    if (lane == 0) tma_store(&g.out, col0, row0, box);
-  } else {  // rows off 16-byte alignment: by pairs of elements at 4-byte boundaries, and single ones at the ends
-    __syncwarp();
-    const int rows = min(32, g.m - row0), cols = min(64, g.n - col0);
+    if (lane == 0) {
+      tma_store(&g.out, col0, row0, boxes);
+      if (col0 + 64 < g.n) tma_store(&g.out, col0 + 64, row0, boxes + kBoxBytes);
+      bulk_commit();
+    }
+    return;
+  }
+  // rows off 16-byte alignment: by pairs of elements at 4-byte boundaries, and single ones at the ends
+  __syncwarp();
+  const int rows = min(32, g.m - row0), cols = min(kSpan, g.n - col0);
 #pragma unroll 4
-    for (int r = 0; r < rows; ++r) {
-      uint16_t* to = g.rows + (row0 + r) * g.rows_stride + col0;
-      const auto at = [=](int c) { return box + r * 128 + (((c >> 3) ^ (r & 7)) << 4) + (c & 7) * 2; };
-      const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(to) >> 1 & 1);
-      const int c = 2 * lane + odd;
+  for (int r = 0; r < rows; ++r) {
+    uint16_t* to = g.rows + (row0 + r) * g.rows_stride + col0;
+    const auto at = [=](int c) {
+      return boxes + (c >> 6) * kBoxBytes + r * 128 + (((c >> 3 & 7) ^ (r & 7)) << 4) + (c & 7) * 2;
+    };
+    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(to) >> 1 & 1);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = 64 * h + 2 * lane + odd;
       if (c + 1 < cols) {
         const uint32_t two = odd ? shared_load_half(at(c)) | static_cast<uint32_t>(shared_load_half(at(c + 1))) << 16
                                  : shared_load_word(at(c));
@@ -213,11 +224,10 @@ __device__ __forceinline__ void send_rows(const Product& g, uint32_t box, int ro
       } else if (c < cols) {
         to[c] = shared_load_half(at(c));
       }
-      if (odd && lane == 31) to[0] = shared_load_half(at(0));
     }
-    __syncwarp();
+    if (odd && lane == 31) to[0] = shared_load_half(at(0));
   }
-  if (lane == 0) bulk_commit();
+  __syncwarp();
 }
 
 template <int kPair, bool kIsScores>
@@ -350,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
     const int own = warp - 4, quarter = own & 3, half = own >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kSpan;
     const uint32_t box = boxes + own * 2 * kBoxBytes;
-    uint32_t n = 0, sent = 0;
+    uint32_t n = 0;
     bool ok = true;
     await_inputs();
     for (int turn = 0, t = tile_of(p, cluster, clusters, 0); ok && t < p.tiles; t = tile_of(p, cluster, clusters, ++turn)) {
@@ -358,6 +368,16 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
       const Product& g = p.product[at.product];
       int from;
       const int steps = inner(g, at.split, &from);
+      const int row0 = (at.i * kPair + rank) * 128 + quarter * 32, row = row0 + lane;
+      const int col0 = at.j * kN + half * kSpan;
+      int64_t target = -1;    // of the row, on its way during the wait; likewise its factor
+      float factor = 1.0f;
+      if (row < g.m) {
+        if constexpr (kIsScores)
+          target = index_at(p.targets, p.index_bits, row) - col0;
+        else if (g.factor)
+          factor = g.factor[row];
+      }
       float x[kSpan];
       for (int step0 = 0; ok && step0 < steps; step0 += p.segment, ++n) {
         const uint32_t buf = n & 1u;
@@ -385,25 +405,20 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
         }
       }
       if (!ok) break;
-      const int row0 = (at.i * kPair + rank) * 128 + quarter * 32, row = row0 + lane;
-      const int col0 = at.j * kN + half * kSpan;
       if (row0 >= g.m || col0 >= g.n) continue;  // the same for the warp
       if constexpr (kIsScores) {
         if (col0 + kSpan > g.n)
 #pragma unroll
           for (int c = 0; c < kSpan; ++c)
             if (col0 + c >= g.n) x[c] = -INFINITY;
-        if (row < g.m) {
-          const int64_t target = index_at(p.targets, p.index_bits, row) - col0;
-          if (target >= 0 && target < kSpan) {
-            float score = 0.0f;
+        if (target >= 0 && target < kSpan) {
+          float score = 0.0f;
 #pragma unroll
-            for (int c = 0; c < kSpan; ++c)  // in this form the compiler does not index x, which would move it out of registers
-              asm("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mov.f32 %0, %2;\n}\n"
-                  : "+f"(score)
-                  : "r"(static_cast<int>(target) - c), "f"(x[c]));
-            p.target_score[row] = score;
-          }
+          for (int c = 0; c < kSpan; ++c)  // in this form the compiler does not index x, which would move it out of registers
+            asm("{\n .reg .pred p;\n setp.eq.s32 p, %1, 0;\n @p mov.f32 %0, %2;\n}\n"
+                : "+f"(score)
+                : "r"(static_cast<int>(target) - c), "f"(x[c]));
+          p.target_score[row] = score;
         }
         float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
@@ -418,11 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
         }
         if (row < g.m) p.stats[row * p.spans + col0 / kSpan] = make_float2(most, (sum[0] + sum[1]) + (sum[2] + sum[3]));
         if (!p.keep) continue;
-#pragma unroll
-        for (int c = 0; c < kSpan; c += 64) {
-          if (col0 + c >= g.n) continue;
-          send_rows(g, box + (sent++ & 1) * kBoxBytes, row0, col0 + c, lane, [&](int q) { return x[c + q]; });
-        }
+        send_rows(g, box, row0, col0, lane, [&](int c) { return x[c]; });
       } else {
         if (g.result != kRows) {
           float* wide = g.wide + (static_cast<int64_t>(at.split) * g.m + row) * g.wide_stride + col0;
@@ -443,13 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
           if (g.result != kLast) continue;
           __syncwarp();
         }
-        const float factor = g.factor && row < g.m ? g.factor[row] : 1.0f;
+        if (g.factor) {
 #pragma unroll
-        for (int c = 0; c < kSpan; c += 64) {
-          if (col0 + c >= g.n) continue;
-          send_rows(g, box + (sent++ & 1) * kBoxBytes, row0, col0 + c, lane,
-                    [&](int q) { return factor == 0.0f ? 0.0f : x[c + q] * factor; });
+          for (int c = 0; c < kSpan; ++c) x[c] = factor == 0.0f ? 0.0f : x[c] * factor;
         }
+        send_rows(g, box, row0, col0, lane, [&](int c) { return x[c]; });
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -464,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
 
 // ------------------------------------------------------------------ the rows
 
-constexpr int kRowWarps = 8;
+constexpr int kRowThreads = 128;
 
 struct RowParams {
   const float2* stats;
@@ -479,100 +488,101 @@ struct RowParams {
   float* factor;           // s_r
   uint16_t* e;
   int64_t e_stride;
-  const uint16_t* hidden;
+  const uint16_t* hidden;  // rows at 16-byte boundaries, as the scores read them
   int64_t hidden_stride;
   uint16_t* scaled;        // s_r H_r
   int64_t scaled_stride;
-  bool vectors;            // H's rows are whole groups of 8 at 16-byte boundaries
 };
 
 __device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-__device__ __forceinline__ float warp_sum(float v) {
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-__device__ __forceinline__ float warp_max(float v) {
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+// Over the block, the same for all its threads.
+template <typename F>
+__device__ __forceinline__ float block_reduce(float v, float* shared, F f) {
+  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+  __syncthreads();  // the last use of `shared`
+  if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = v;
+  __syncthreads();
+  v = shared[0];
+#pragma unroll
+  for (int w = 1; w < kRowThreads / 32; ++w) v = f(v, shared[w]);
   return v;
 }
 
-// A warp per row of the piece: its lse and loss from the spans' statistics; for the
-// gradients its factor, its target's element of E and its scaled row of H.
-__global__ void __launch_bounds__(32 * kRowWarps) ce_rows(const __grid_constant__ RowParams p) {
+// A block per row of the piece: its lse and loss from the spans' statistics; for the
+// gradients its factor, its target's element of E and its scaled row of H. Bound by HBM for many rows (8192 x
+// 768, vocabulary 50257: 11 us), by its chain of loads for few.
+__global__ void __launch_bounds__(kRowThreads) ce_rows(const __grid_constant__ RowParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x % 32;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowWarps + threadIdx.x / 32;
-  if (row >= p.rows) return;
+  __shared__ float shared[kRowThreads / 32];
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  const auto add = [](float a, float b) { return a + b; };
+  const auto larger = [](float a, float b) { return fmaxf(a, b); };
   const float2* stats = p.stats + row * p.spans;
+  const int64_t target = index_at(p.targets, p.index_bits, row);
+  const bool there = target >= 0, has = there && target < p.vocab;
+  const float score = has ? p.target_score[row] : NAN;
+  const float g = there ? (has ? p.scale * (p.dloss ? p.dloss[row] : 1.0f) : NAN) : 0.0f;
   float most = -INFINITY, far = 0.0f, sum = 0.0f;
-  for (int64_t i = lane; i < p.spans; i += 32) {
+  for (int64_t i = tid; i < p.spans; i += kRowThreads) {
     const float2 s = stats[i];
     most = fmaxf(most, s.x);
     far = fmaxf(far, fabsf(s.x));
     sum += s.y;
   }
-  most = warp_max(most);
-  far = warp_max(far);
+  far = block_reduce(far, shared, larger);
   float lse;
   if (!(far > kPlainRange)) {
-    lse = logf(warp_sum(sum));
+    lse = logf(block_reduce(sum, shared, add));
   } else {
+    most = block_reduce(most, shared, larger);
     sum = 0.0f;
-    for (int64_t i = lane; i < p.spans; i += 32) {
+    for (int64_t i = tid; i < p.spans; i += kRowThreads) {
       const float2 s = stats[i];
       sum += s.y == 0.0f ? 0.0f : s.y * expf(reference_of(s.x) - most);
     }
-    lse = most + logf(warp_sum(sum));
+    lse = most + logf(block_reduce(sum, shared, add));
   }
-  const int64_t target = index_at(p.targets, p.index_bits, row);
-  const bool there = target >= 0;
-  const float score = there && target < p.vocab ? p.target_score[row] : NAN;
-  if (lane == 0) {
+  if (tid == 0) {
     p.loss[row] = there ? lse - score : 0.0f;
     if (p.lse) p.lse[row] = lse;
   }
   if (!p.keep) return;
-  const float g = there ? (target < p.vocab ? p.scale * (p.dloss ? p.dloss[row] : 1.0f) : NAN) : 0.0f;
   uint16_t* e = p.e + row * p.e_stride;
   const bool plain = !(far > kPlainRange) && fabsf(lse) <= kPlainRange;
   // The target's element is the largest of the row's: its rounding to bf16 goes into the row's factor
   // (relative to which the others, rounded too, are then off by one more rounding).
   float factor = g;
-  const bool has = there && target < p.vocab;
   const float exact = has ? (plain ? expf(lse) : 1.0f) * expm1f(score - lse) : 0.0f;
   const uint16_t rounded = bf16_bits(exact);
   if (plain) factor *= expf(-lse);
   if (bf16_value(rounded) != 0.0f) factor *= exact / bf16_value(rounded);
   if (plain) {
-    if (lane == 0 && has) e[target] = rounded;
+    if (tid == 0 && has) e[target] = rounded;
   } else {
-    for (int64_t v = lane; v < p.vocab; v += 32) {
+    for (int64_t v = tid; v < p.vocab; v += kRowThreads) {
       const float kept = bf16_value(e[v]);  // zeros stay: their span's factor may not be finite
       const float own = kept == 0.0f && lse == lse ? 0.0f : kept * expf(reference_of(stats[v / kSpan].x) - lse);
       e[v] = !there ? uint16_t(0) : v == target ? rounded : bf16_bits(own);
     }
   }
-  if (lane == 0) p.factor[row] = factor;
+  if (tid == 0) p.factor[row] = factor;
   const uint16_t* h = p.hidden + row * p.hidden_stride;
   uint16_t* scaled = p.scaled + row * p.scaled_stride;
-  if (p.vectors) {
-    for (int c = lane * 8; c < p.cols; c += 256) {
-      const uint4 v = *reinterpret_cast<const uint4*>(h + c);
-      const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-      uint32_t out[4];
+  for (int c = tid * 8; c < p.cols; c += kRowThreads * 8) {  // what lies behind the row's end is not used
+    const uint4 v = *reinterpret_cast<const uint4*>(h + c);
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+    uint32_t out[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(in[k] << 16) * factor, __uint_as_float(in[k] & 0xffff0000u) * factor);
-        out[k] = factor == 0.0f ? 0u : *reinterpret_cast<const uint32_t*>(&two);
-      }
-      *reinterpret_cast<uint4*>(scaled + c) = make_uint4(out[0], out[1], out[2], out[3]);
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(in[k] << 16) * factor, __uint_as_float(in[k] & 0xffff0000u) * factor);
+      out[k] = factor == 0.0f ? 0u : *reinterpret_cast<const uint32_t*>(&two);
     }
-    return;
+    *reinterpret_cast<uint4*>(scaled + c) = make_uint4(out[0], out[1], out[2], out[3]);
   }
-  for (int c = lane; c < p.cols; c += 32) scaled[c] = factor == 0.0f ? uint16_t(0) : bf16_bits(bf16_value(h[c]) * factor);
 }
 
 // ------------------------------------------------- copies and joined results
@@ -631,23 +641,28 @@ constexpr int kJoinGroups = 8;
 __global__ void __launch_bounds__(32 * kJoinGroups) ce_join(const __grid_constant__ JoinParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float sums[kJoinGroups][32];
+  __shared__ float4 sums[kJoinGroups][32];
   const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
-  const int64_t per_row = (p.cols + 31) / 32;
-  const int64_t row = blockIdx.x / per_row, col = (blockIdx.x - row * per_row) * 32 + lane;
+  const int64_t per_row = (p.cols + 127) / 128;
+  const int64_t row = blockIdx.x / per_row, col = ((blockIdx.x - row * per_row) * 32 + lane) * 4;
   const int each = (p.splits + kJoinGroups - 1) / kJoinGroups;
   const int from = min(p.splits, group * each), to = min(p.splits, from + each);
-  float sum = 0.0f;
-  if (col < p.cols)
-#pragma unroll 8
-    for (int s = from; s < to; ++s) sum += p.wide[(s * p.rows + row) * p.wide_stride + col];
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const auto add = [&](const float4& v) { sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w; };
+  if (col < p.cols)  // the parts' rows are whole groups of 8
+#pragma unroll 4
+    for (int s = from; s < to; ++s) add(*reinterpret_cast<const float4*>(p.wide + (s * p.rows + row) * p.wide_stride + col));
   sums[group][lane] = sum;
+  const float factor = p.factor[row];
   __syncthreads();
   if (group != 0 || col >= p.cols) return;
 #pragma unroll
-  for (int g = 1; g < kJoinGroups; ++g) sum += sums[g][lane];
-  const float factor = p.factor[row];
-  p.out[row * p.out_stride + col] = bf16_bits(factor == 0.0f ? 0.0f : sum * factor);
+  for (int g = 1; g < kJoinGroups; ++g) add(sums[g][lane]);
+  const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+  uint16_t* out = p.out + row * p.out_stride + col;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (col + e < p.cols) out[e] = bf16_bits(factor == 0.0f ? 0.0f : v[e] * factor);
 }
 
 // ---------------------------------------------------------------------- host
@@ -766,8 +781,10 @@ int launch_products(Params& p, const Device& dev, cudaStream_t stream) {
   p.fewer = p.extra = 0;
   if (p.count == 2 && p.product[0].tiles % clusters) {
     p.fewer = clusters - p.product[0].tiles % clusters;
-    // as many as take as long as one of the first product's
-    p.extra = (2 * p.product[0].split_steps / p.product[1].split_steps + 1) / 2;
+    // As many as take as long as one of the first product's: a tile takes its steps or, with few, its epilogue and
+    // store, about as long as 6 steps (61 x 4096, vocabulary 32000: by the steps alone a few SMs had most of the
+    // one-step tiles, 130 us, now 75).
+    p.extra = (2 * p.product[0].split_steps / std::max(6, p.product[1].split_steps) + 1) / 2;
   }
   return launch_after(ce_product<kPair, kIsScores>, clusters * kPair, kPair, kThreads, T::kSmemBytes, stream, p);
 }
@@ -827,20 +844,19 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
     rows.scaled = reinterpret_cast<uint16_t*>(at(plan.scaled));
     rows.scaled_stride = plan.h_stride;
   }
-  rows.hidden_stride = a.hidden_stride;
 
   for (int64_t r0 = 0; r0 < a.rows; r0 += plan.piece) {
     const int64_t n = std::min(plan.piece, a.rows - r0);
     const uint16_t* hidden = c.hidden + r0 * a.hidden_stride;
     int64_t hidden_stride = a.hidden_stride;
-    rows.hidden = hidden;
-    rows.vectors = mappable(hidden, n, hidden_stride) && a.cols % 8 == 0;
     if (!mappable(hidden, n, hidden_stride)) {
       auto* copy = reinterpret_cast<uint16_t*>(at(plan.hidden));
       if (int rc = copy_rows(hidden, hidden_stride, copy, plan.h_stride, n, a.cols, st)) return rc;
       hidden = copy;
       hidden_stride = plan.h_stride;
     }
+    rows.hidden = hidden;
+    rows.hidden_stride = hidden_stride;
     scores.targets = static_cast<const unsigned char*>(c.targets) + r0 * index_bytes;
     rows.targets = scores.targets;
     rows.rows = static_cast<int32_t>(n);
@@ -862,7 +878,7 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
     if (!ok) return FSDP_ECUDA;
     if (int rc = plan.pair == 2 ? launch_products<2, true>(scores, dev, st) : launch_products<1, true>(scores, dev, st))
       return rc;
-    if (int rc = launch_after(ce_rows, static_cast<int>((n + kRowWarps - 1) / kRowWarps), 1, 32 * kRowWarps, 0, st, rows))
+    if (int rc = launch_after(ce_rows, static_cast<int>(n), 1, kRowThreads, 0, st, rows))
       return rc;
     if (!gradients) continue;
 
@@ -912,7 +928,7 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
       return rc;
     if (plan.splits > 1) {
       const JoinParams j{dh.wide, dh.wide_stride, dh.splits, n, a.cols, rows.factor, dhidden, a.dhidden_stride};
-      const int64_t blocks = n * ((a.cols + 31) / 32);  // few: a product is cut only where its result has few tiles
+      const int64_t blocks = n * ((a.cols + 127) / 128);  // few: a product is cut only where its result has few tiles
       if (int rc = launch_after(ce_join, static_cast<int>(blocks), 1, 32 * kJoinGroups, 0, st, j)) return rc;
     }
   }

@@ -46,21 +46,27 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&two);
 }
 
-// kVec consecutive elements (kVec > 1: at a 16-byte boundary).
+// kVec consecutive elements (kVec > 1: at a boundary of their size, 16 bytes at most).
 template <int kVec>
 __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[kVec]) {
   if constexpr (kVec == 8) {
     const uint4 a = *reinterpret_cast<const uint4*>(p);
     unpack_bf16(a.x, v), unpack_bf16(a.y, v + 2), unpack_bf16(a.z, v + 4), unpack_bf16(a.w, v + 6);
+  } else if constexpr (kVec == 4) {
+    const uint2 a = *reinterpret_cast<const uint2*>(p);
+    unpack_bf16(a.x, v), unpack_bf16(a.y, v + 2);
   } else {
     v[0] = __bfloat162float(*p);
   }
 }
 template <int kVec>
 __device__ __forceinline__ void load(const float* p, float (&v)[kVec]) {
-  if constexpr (kVec == 8) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  if constexpr (kVec >= 4) {
+#pragma unroll
+    for (int e = 0; e < kVec; e += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(p + e);
+      v[e] = a.x, v[e + 1] = a.y, v[e + 2] = a.z, v[e + 3] = a.w;
+    }
   } else {
     v[0] = *p;
   }
@@ -69,14 +75,16 @@ template <int kVec>
 __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[kVec]) {
   if constexpr (kVec == 8)
     *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  else if constexpr (kVec == 4)
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
   else
     *p = __float2bfloat16_rn(v[0]);
 }
 template <int kVec>
 __device__ __forceinline__ void store(float* p, const float (&v)[kVec]) {
-  if constexpr (kVec == 8) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  if constexpr (kVec >= 4) {
+#pragma unroll
+    for (int e = 0; e < kVec; e += 4) *reinterpret_cast<float4*>(p + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
   } else {
     *p = v[0];
   }
@@ -105,7 +113,7 @@ constexpr int kLookupWarps = 8;
 
 // How many groups of kVec elements a lane has in flight.
 template <int kVec>
-constexpr int kGroups = kVec == 8 ? 4 : 8;
+constexpr int kGroups = kVec > 1 ? 4 : 8;
 
 // A warp takes 32 kGroups kVec consecutive elements of a row at a time; the next token is on its way
 // meanwhile. Bound by HBM; the rows stay packed until they are used, so that many warps fit.
@@ -180,13 +188,13 @@ __device__ __forceinline__ void fill_zeros(const FillParams& f, int part, int pa
     fill_row(f.to + r * f.pitch, f.row_bytes, threadIdx.x % 32, 32);
 }
 
-// Up to 8 x 16384 rows are sorted by one cluster of up to eight blocks, which holds them in
+// Up to 8 x 8192 rows are sorted by one cluster of up to eight blocks, which holds them in
 // registers and moves them through (distributed) shared memory. In a pass each warp ranks its rows by digit, 32 at a
 // time; the places follow from the counts of all digits, blocks and warps. Bound by its own latencies (cycles of a
 // pass of 16384 rows on eight blocks: ranking 3000, running sums 1300, exchange of the blocks' totals 2000, their sums
 // 500, moving 2000 and waiting for it 2100).
 constexpr int kMaxBins = 512;
-constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32, kMaxRounds = 16, kMaxCluster = 8;
+constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32, kMaxRounds = 8, kMaxCluster = 8;
 constexpr int kClusterRows = kMaxCluster * kMaxRounds * kClusterThreads;
 
 struct ClusterSortParams {
@@ -361,7 +369,8 @@ __global__ void __launch_bounds__(kClusterThreads) embed_fill(const __grid_const
   fill_zeros(p, blockIdx.x, gridDim.x);
 }
 
-// More rows: three launches a pass, counts of the blocks' digits in memory.
+// More rows: three launches a pass, counts of the blocks' digits in memory (the whole gradient with 64 columns, in
+// this form and on a cluster: 36000 rows 44 and 37 us, 65536 53 and 53, 131072 75 and 92).
 constexpr int kSortThreads = 256, kSortItems = 8, kSortBlock = kSortThreads * kSortItems;
 
 struct SortParams {
@@ -478,6 +487,7 @@ struct SumParams {
   const uint32_t *keys, *rows;  // sorted
   int32_t n, chunk, chunks;     // rows of a chunk
   int32_t tiles, join_tiles;    // parts of the columns, in the two kernels
+  int32_t join_lanes;           // threads that the columns of a part take (a power of two, 32 at most)
   int64_t vocab, cols;
   const void* dout;
   int64_t dout_stride;
@@ -612,8 +622,9 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum(const __grid_constant__
 }
 
 // Adds up the runs that cross chunks. Short ones by a warp for each 32 kVec columns, chunk after chunk; long ones
-// by a block: eight groups of threads each a share of the chunks, then the groups in order.
-constexpr int kJoinGroups = 8, kJoinThreads = 32 * kJoinGroups;
+// by a block: groups of as many threads as the columns take, up to 32, each a share of the chunks, then the groups
+// pair by pair.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
 template <typename TTable, int kVec>
 __device__ __forceinline__ void add_to_table(const SumParams& p, uint32_t token, int64_t col, const float (&sum)[kVec]) {
@@ -641,9 +652,10 @@ template <typename TTable, int kVec>
 __global__ void __launch_bounds__(kJoinThreads) embed_join(const __grid_constant__ SumParams p) {
   begin_after_previous();
   const int64_t shorts = static_cast<int64_t>(p.active[0]) * p.join_tiles, longs = static_cast<int64_t>(p.active[1]) * p.join_tiles;
-  const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
-  __shared__ float sums[kJoinGroups][kVec][32];
+  const int lane = threadIdx.x % 32;
+  __shared__ float sums[kVec][kJoinThreads];
   int64_t turn = blockIdx.x;  // the long items, then eight short ones at a time
+  const int lanes = p.join_lanes, groups = kJoinThreads / lanes, in_group = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes;
   for (; turn < longs; turn += gridDim.x) {
     const int64_t item = turn, index = item / p.join_tiles;
     const uint32_t* run = p.active + 2 + 2 * (p.chunks - 1 - index);
@@ -656,27 +668,28 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join(const __grid_constant
       parts += more;
       if (more < kJoinThreads) break;
     }
-    const int each = (parts + kJoinGroups - 1) / kJoinGroups;
-    const int64_t col = ((item - index * p.join_tiles) * 32 + lane) * kVec;
+    const int each = (parts + groups - 1) / groups;
+    const int64_t col = ((item - index * p.join_tiles) * 32 + in_group) * kVec;
     float sum[kVec] = {};
     if (col < p.cols) {
       if (group == 0) load<kVec>(p.parts + (2 * static_cast<int64_t>(chunk) + 1) * p.part_stride + col, sum);
-      add_parts<kVec>(p, chunk + 1 + min(parts, group * each), chunk + 1 + min(parts, (group + 1) * each), col, sum);
+      const int64_t from = min(static_cast<int64_t>(parts), static_cast<int64_t>(group) * each);
+      const int64_t to = min(static_cast<int64_t>(parts), from + each);
+      add_parts<kVec>(p, chunk + 1 + static_cast<int>(from), chunk + 1 + static_cast<int>(to), col, sum);
     }
+    for (int half = groups / 2; half > 0; half /= 2) {
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) sums[group][e][lane] = sum[e];
-    __syncthreads();
-    if (group == 0 && col < p.cols) {
+      for (int e = 0; e < kVec; ++e) sums[e][threadIdx.x] = sum[e];
+      __syncthreads();
+      if (group < half)
 #pragma unroll
-      for (int g = 1; g < kJoinGroups; ++g)
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) sum[e] += sums[g][e][lane];
-      add_to_table<TTable, kVec>(p, token, col, sum);
+        for (int e = 0; e < kVec; ++e) sum[e] += sums[e][threadIdx.x + half * lanes];
+      __syncthreads();
     }
-    __syncthreads();
+    if (group == 0 && col < p.cols) add_to_table<TTable, kVec>(p, token, col, sum);
   }
   for (;; turn += gridDim.x) {
-    const int64_t item = (turn - longs) * kJoinGroups + group;
+    const int64_t item = (turn - longs) * kJoinWarps + threadIdx.x / 32;
     if (item >= shorts) return;
     const int64_t index = item / p.join_tiles;
     const uint32_t* run = p.active + 2 + 2 * index;
@@ -738,13 +751,15 @@ Workspace carve(int64_t rows, int64_t cols, int64_t vocab) {
 
 template <typename T, typename TTable, int kVec>
 int run_sum(SumParams p, int sms, cudaStream_t st) {
-  constexpr int kQ = kVec == 8 ? 1 : 4;
+  constexpr int kQ = kVec == 8 ? 1 : kVec == 4 ? 2 : 4;
   const int64_t groups = (p.cols + kVec - 1) / kVec;
   const int threads = static_cast<int>(std::max<int64_t>(64, std::min<int64_t>(kSumThreads, round_to((groups + kQ - 1) / kQ, 32))));
   const int64_t tiles = (groups + threads * kQ - 1) / (threads * kQ), join_tiles = (groups + 31) / 32;
   if (tiles * p.chunks > INT32_MAX || join_tiles > INT32_MAX) return FSDP_EINVAL;  // more than any memory holds
   p.tiles = static_cast<int32_t>(tiles);
   p.join_tiles = static_cast<int32_t>(join_tiles);
+  p.join_lanes = 1;
+  while (p.join_lanes < 32 && p.join_lanes < groups) p.join_lanes *= 2;
   p.sum_blocks = p.chunks * p.tiles;
   p.zero_blocks = p.named ? static_cast<int32_t>((p.vocab + kZeroRows - 1) / kZeroRows) : 0;
   if (static_cast<int64_t>(p.sum_blocks) + p.zero_blocks > INT32_MAX) return FSDP_EINVAL;
@@ -757,7 +772,9 @@ int run_sum(SumParams p, int sms, cudaStream_t st) {
 
 template <typename T, typename TTable>
 int run_sum_as(const SumParams& p, bool vectors, int sms, cudaStream_t st) {
-  return vectors ? run_sum<T, TTable, 8>(p, sms, st) : run_sum<T, TTable, 1>(p, sms, st);
+  // vectors of 16 bytes of the wider type
+  constexpr int kVec = sizeof(T) == 2 && sizeof(TTable) == 2 ? 8 : 4;
+  return vectors ? run_sum<T, TTable, kVec>(p, sms, st) : run_sum<T, TTable, 1>(p, sms, st);
 }
 
 // The sort of up to kClusterRows rows; the other blocks fill. Two steps of 32 rows for each warp, then more blocks,
@@ -802,18 +819,18 @@ extern "C" int fsdp_embedding(const fsdp_embedding_t* a, const void* tokens, con
   const bool vectors = a->cols % 8 == 0 && vector_rows(table, a->vocab, a->table_stride, es) &&
                        vector_rows(out, a->rows, a->out_stride, es) &&
                        (!addend || vector_rows(addend, a->rows, a->addend_stride, es));
-  const int64_t unit = vectors ? 32 * kGroups<8> * 8 : 32 * kGroups<1>, units = a->rows * ((a->cols + unit - 1) / unit);
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  const auto go = [&](auto kernel, int per_sm) {
+  const auto go = [&](auto kernel, int vec, int groups, int per_sm) {  // per_sm: blocks that run at once
+    const int64_t unit = 32 * groups * vec, units = a->rows * ((a->cols + unit - 1) / unit);
     const int grid = static_cast<int>(std::min<int64_t>((units + kLookupWarps - 1) / kLookupWarps, 152 * per_sm));
     return launch_after(kernel, grid, 1, 32 * kLookupWarps, 0, cs, p);
   };
   if (a->dtype == FSDP_DTYPE_F32) {
-    if (addend) return vectors ? go(embed_rows<float, 8, true>, 2) : go(embed_rows<float, 1, true>, 5);
-    return vectors ? go(embed_rows<float, 8, false>, 4) : go(embed_rows<float, 1, false>, 5);
+    if (addend) return vectors ? go(embed_rows<float, 4, true>, 4, 4, 4) : go(embed_rows<float, 1, true>, 1, 8, 4);
+    return vectors ? go(embed_rows<float, 4, false>, 4, 4, 5) : go(embed_rows<float, 1, false>, 1, 8, 5);
   }
-  if (addend) return vectors ? go(embed_rows<__nv_bfloat16, 8, true>, 4) : go(embed_rows<__nv_bfloat16, 1, true>, 5);
-  return vectors ? go(embed_rows<__nv_bfloat16, 8, false>, 5) : go(embed_rows<__nv_bfloat16, 1, false>, 5);
+  if (addend) return vectors ? go(embed_rows<__nv_bfloat16, 8, true>, 8, 4, 3) : go(embed_rows<__nv_bfloat16, 1, true>, 1, 8, 4);
+  return vectors ? go(embed_rows<__nv_bfloat16, 8, false>, 8, 4, 4) : go(embed_rows<__nv_bfloat16, 1, false>, 1, 8, 5);
 }
 
 extern "C" int fsdp_embedding_backward_workspace(int64_t rows, int64_t cols, int64_t vocab, int64_t* bytes_out) {
@@ -879,7 +896,7 @@ extern "C" int fsdp_embedding_backward(const fsdp_embedding_backward_t* a, const
       if (int rc = launch_after(sort_move, w.blocks, 1, kSortThreads, 0, cs, p)) return rc;
     }
   }
-  const SumParams p{keys[now], rows[now], n, w.chunk, w.chunks, 0, 0, a->vocab, a->cols, dout, a->dout_stride, dtable,
+  const SumParams p{keys[now], rows[now], n, w.chunk, w.chunks, 0, 0, 0, a->vocab, a->cols, dout, a->dout_stride, dtable,
                     a->dtable_stride, reinterpret_cast<float*>(base + w.parts), w.part_stride, active, named,
                     a->cols * ts, 0, 0, static_cast<float>(a->scale), a->accumulate != 0};
   const bool vectors = a->cols % 8 == 0 && vector_rows(dout, a->rows, a->dout_stride, es) &&
