@@ -118,17 +118,40 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// Two values at once: half the instructions.
+struct Two {
+  uint64_t bits;
+  __device__ __forceinline__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(bits) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ void to(float* a, float* b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(*a), "=f"(*b) : "l"(bits)); }
+};
+__device__ __forceinline__ Two fma_two(const Two& a, const Two& b, const Two& c) {
+  Two d = a;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.bits) : "l"(a.bits), "l"(b.bits), "l"(c.bits));
+  return d;
+}
+__device__ __forceinline__ Two add_two(const Two& a, const Two& b) {
+  Two d = a;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.bits) : "l"(a.bits), "l"(b.bits));
+  return d;
+}
+// The largest of three (a NaN among them counts for nothing).
+__device__ __forceinline__ float max_of(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 __device__ __forceinline__ void shared_store(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ uint16_t shared_load_half(uint32_t addr) {
   uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ uint32_t shared_load_word(uint32_t addr) {
   uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
 
@@ -207,25 +230,39 @@ __device__ __forceinline__ void send_rows(const Product& g, uint32_t boxes, int 
   // rows off 16-byte alignment: by pairs of elements at 4-byte boundaries, and single ones at the ends
   __syncwarp();
   const int rows = min(32, g.m - row0), cols = min(kSpan, g.n - col0);
-#pragma unroll 4
-  for (int r = 0; r < rows; ++r) {
-    uint16_t* to = g.rows + (row0 + r) * g.rows_stride + col0;
-    const auto at = [=](int c) {
-      return boxes + (c >> 6) * kBoxBytes + r * 128 + (((c >> 3 & 7) ^ (r & 7)) << 4) + (c & 7) * 2;
-    };
-    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(to) >> 1 & 1);
+  const int64_t stride = g.rows_stride;
+  uint16_t* to = g.rows + row0 * stride + col0;
+  constexpr int kAtOnce = 4;  // rows whose loads are in flight
+  for (int r0 = 0; r0 < rows; r0 += kAtOnce) {
+    uint32_t two[kAtOnce][2];
+    bool odd[kAtOnce];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = 64 * h + 2 * lane + odd;
-      if (c + 1 < cols) {
-        const uint32_t two = odd ? shared_load_half(at(c)) | static_cast<uint32_t>(shared_load_half(at(c + 1))) << 16
-                                 : shared_load_word(at(c));
-        *reinterpret_cast<uint32_t*>(to + c) = two;
-      } else if (c < cols) {
-        to[c] = shared_load_half(at(c));
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int r = r0 + k;
+      odd[k] = (reinterpret_cast<uintptr_t>(to + k * stride) >> 1 & 1) != 0;
+      const auto at = [=](int c) {
+        return boxes + (c >> 6) * kBoxBytes + r * 128 + (((c >> 3 & 7) ^ (r & 7)) << 4) + (c & 7) * 2;
+      };
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // columns 64 h + 2 lane + odd, and the next one (the last lane's wraps to column 0)
+        const int c = 64 * h + 2 * lane;
+        two[k][h] = odd[k] ? shared_load_half(at(c + 1)) | static_cast<uint32_t>(shared_load_half(at((c + 2) % kSpan))) << 16
+                           : shared_load_word(at(c));
       }
     }
-    if (odd && lane == 31) to[0] = shared_load_half(at(0));
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k, to += stride) {
+      if (r0 + k >= rows) break;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = 64 * h + 2 * lane + odd[k];
+        if (c + 1 < cols)
+          *reinterpret_cast<uint32_t*>(to + c) = two[k][h];
+        else if (c < cols)
+          to[c] = static_cast<uint16_t>(two[k][h]);
+      }
+      if (odd[k] && lane == 31) to[0] = static_cast<uint16_t>(two[k][1] >> 16);
+    }
   }
   __syncwarp();
 }
@@ -422,16 +459,24 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
         }
         float top[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int c = 4; c < kSpan; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
-        const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        const float shift = reference_of(most) * kLog2e;
-        float sum[4] = {};
+        for (int c = 4; c < kSpan - 4; c += 8)
 #pragma unroll
-        for (int c = 0; c < kSpan; ++c) {
-          x[c] = exp2_fast(fmaf(x[c], kLog2e, -shift));
-          sum[c & 3] += x[c];
+          for (int k = 0; k < 4; ++k) top[k] = max_of(top[k], x[c + 2 * k], x[c + 2 * k + 1]);
+        const float most = max_of(max_of(top[0], top[1], top[2]), max_of(top[3], x[kSpan - 4], x[kSpan - 3]),
+                                  fmaxf(x[kSpan - 2], x[kSpan - 1]));
+        const float shift = reference_of(most) * kLog2e;
+        const Two slope(kLog2e, kLog2e), offset(-shift, -shift);
+        Two sums[2] = {Two(0.0f, 0.0f), Two(0.0f, 0.0f)};
+#pragma unroll
+        for (int c = 0; c < kSpan; c += 2) {
+          fma_two(Two(x[c], x[c + 1]), slope, offset).to(&x[c], &x[c + 1]);
+          x[c] = exp2_fast(x[c]);
+          x[c + 1] = exp2_fast(x[c + 1]);
+          sums[c / 2 & 1] = add_two(sums[c / 2 & 1], Two(x[c], x[c + 1]));
         }
-        if (row < g.m) p.stats[row * p.spans + col0 / kSpan] = make_float2(most, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+        float sum[2];
+        add_two(sums[0], sums[1]).to(&sum[0], &sum[1]);
+        if (row < g.m) p.stats[row * p.spans + col0 / kSpan] = make_float2(most, sum[0] + sum[1]);
         if (!p.keep) continue;
         send_rows(g, box, row0, col0, lane, [&](int c) { return x[c]; });
       } else {
@@ -688,7 +733,7 @@ int make_plan(const fsdp_cross_entropy_t& a, bool gradients, Plan* out) {
   Plan p{};
   p.spans = (a.vocab + kSpan - 1) / kSpan;
   p.e_stride = round_to(a.vocab, 64);
-  p.h_stride = round_to(a.cols, 8);
+  p.h_stride = round_to(a.cols, 64);  // whole lines: a box's row of 128 bytes is then one
   int64_t piece = a.piece;
   if (!piece) piece = std::max<int64_t>(256, kPieceBytes / (p.e_stride * 2) / 256 * 256);
   p.piece = std::max<int64_t>(1, std::min({piece, a.rows, kMaxPiece}));
