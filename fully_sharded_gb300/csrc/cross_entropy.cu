@@ -43,7 +43,7 @@ constexpr int kN = 256;                           // columns of a tile
 constexpr int kSpan = 128;                        // columns of a tile that one thread holds; of one statistic
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;  // producer, products, two idle warps, epilogue
-constexpr int kBoxBytes = 32 * 64 * 2;            // what a warp sends at once: 32 rows of 64 columns
+constexpr int kBoxBytes = 32 * 128;               // what a warp sends at once: 32 rows of 128 bytes
 constexpr int kOutBytes = kEpilogueWarps * 2 * kBoxBytes;
 // Registers after the start: 384 threads come with 168 each.
 constexpr int kLeanRegisters = 56, kEpilogueRegisters = 224;
@@ -65,25 +65,23 @@ enum Result : int32_t {
   kScores,   // E and the statistics of a piece's logits
   kRows,     // bf16 rows, times a factor per row
   kPartial,  // fp32, a part of the inner dimension: joined later
-  kAdd,      // fp32 sum over the pieces: written by the first, added to by the others
-  kLast,     // bf16 rows of that sum and the last piece's
+  kSum,      // fp32, the first piece's; kAdd: a later piece's, added to it in memory
+  kAdd,
 };
 
 // C[m, n] = sum_k A[m, k] B[n, k].
 struct Product {
-  CUtensorMap a, b, out;   // boxes of 64 x 64 of the operands; of 32 x 64 of the result
+  CUtensorMap a, b, out;   // boxes of 64 x 64 of the operands; of the result 32 rows of 128 bytes (bf16 or fp32)
   int32_t m, n, k;
   int32_t row_tiles, col_tiles, tiles;
   int32_t splits, split_steps;  // parts of the inner dimension, and their length in steps of 64
+  int32_t split_rows;      // kPartial: from one part's rows to the next's
   uint8_t a_mn, b_mn;      // the operand's row index (of C's rows, columns) is the contiguous one
   uint8_t rows_first;      // order of the tiles
-  uint8_t first;           // kAdd: the first piece
   int32_t result;
-  uint16_t* rows;          // kRows, kLast: where the bf16 rows go if `out` cannot describe them, else null
+  uint16_t* rows;          // kRows: where the rows go if `out` cannot describe them, else null
   int64_t rows_stride;
   const float* factor;     // kRows: of each row (null: 1)
-  float* wide;             // kPartial, kAdd, kLast: fp32, a row `wide_stride` from the next
-  int64_t wide_stride;
 };
 
 struct Params {
@@ -265,6 +263,36 @@ __device__ __forceinline__ void send_rows(const Product& g, uint32_t boxes, int 
     }
   }
   __syncwarp();
+}
+
+// The same in fp32, 64 columns at a time: stored, or added to what is there (each element by one block in a
+// launch, and launches follow one another: the order of the additions is fixed).
+__device__ __forceinline__ void send_wide(const Product& g, uint32_t boxes, int row0, int col0, int lane, const float (&x)[kSpan]) {
+  const bool add = g.result == kAdd;
+#pragma unroll
+  for (int h = 0; h < kSpan; h += 64) {
+    if (col0 + h >= g.n) break;
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+#pragma unroll
+    for (int q = 0; q < 16; ++q)
+      shared_store(boxes + (q >> 3) * kBoxBytes + lane * 128 + (((q & 7) ^ (lane & 7)) << 4), __float_as_uint(x[h + 4 * q]),
+                   __float_as_uint(x[h + 4 * q + 1]), __float_as_uint(x[h + 4 * q + 2]), __float_as_uint(x[h + 4 * q + 3]));
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int col = col0 + h + 32 * b;
+        if (col >= g.n) break;
+        if (add)
+          tma_add(&g.out, col, row0, boxes + b * kBoxBytes);
+        else
+          tma_store(&g.out, col, row0, boxes + b * kBoxBytes);
+      }
+      bulk_commit();
+    }
+  }
 }
 
 template <int kPair, bool kIsScores>
@@ -481,23 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
         send_rows(g, box, row0, col0, lane, [&](int c) { return x[c]; });
       } else {
         if (g.result != kRows) {
-          float* wide = g.wide + (static_cast<int64_t>(at.split) * g.m + row) * g.wide_stride + col0;
-          const bool add = g.result == kLast || (g.result == kAdd && !g.first);
-          // a row holds whole groups of 8 elements
-          if (row < g.m) {
-#pragma unroll
-            for (int c = 0; c < kSpan; c += 4) {
-              if (col0 + c >= g.wide_stride) continue;
-              float4* to = reinterpret_cast<float4*>(wide + c);
-              if (add) {
-                const float4 old = *to;
-                x[c] += old.x, x[c + 1] += old.y, x[c + 2] += old.z, x[c + 3] += old.w;
-              }
-              if (g.result != kLast) *to = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
-            }
-          }
-          if (g.result != kLast) continue;
-          __syncwarp();
+          send_wide(g, box, at.split * g.split_rows + row0, col0, lane, x);
+          continue;
         }
         if (g.factor) {
 #pragma unroll
@@ -671,7 +684,7 @@ __global__ void __launch_bounds__(256) ce_copy(const __grid_constant__ CopyParam
 
 struct JoinParams {
   const float* wide;
-  int64_t wide_stride;
+  int64_t wide_stride, split_rows;
   int32_t splits;
   int64_t rows, cols;
   const float* factor;
@@ -696,7 +709,7 @@ __global__ void __launch_bounds__(32 * kJoinGroups) ce_join(const __grid_constan
   const auto add = [&](const float4& v) { sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w; };
   if (col < p.cols)  // the parts' rows are whole groups of 8
 #pragma unroll 4
-    for (int s = from; s < to; ++s) add(*reinterpret_cast<const float4*>(p.wide + (s * p.rows + row) * p.wide_stride + col));
+    for (int s = from; s < to; ++s) add(*reinterpret_cast<const float4*>(p.wide + (s * p.split_rows + row) * p.wide_stride + col));
   sums[group][lane] = sum;
   const float factor = p.factor[row];
   __syncthreads();
@@ -708,6 +721,37 @@ __global__ void __launch_bounds__(32 * kJoinGroups) ce_join(const __grid_constan
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     if (col + e < p.cols) out[e] = bf16_bits(factor == 0.0f ? 0.0f : v[e] * factor);
+}
+
+struct RoundParams {
+  const float* sum;
+  int64_t sum_stride;
+  uint16_t* out;
+  int64_t out_stride;
+  int64_t rows, cols;
+};
+
+// The sum over the pieces, rounded: 8 elements a thread at 16-byte boundaries, else one. Bound by HBM.
+template <int kVec>
+__global__ void __launch_bounds__(256) ce_round(const __grid_constant__ RoundParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const uint32_t per_row = static_cast<uint32_t>((p.cols + kVec - 1) / kVec);
+  const int64_t groups = p.rows * per_row;
+#pragma unroll 2
+  for (int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; v < groups; v += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = groups >> 31 ? v / per_row : static_cast<uint32_t>(v) / per_row, c = (v - r * per_row) * kVec;
+    const float* from = p.sum + r * p.sum_stride + c;
+    uint16_t* to = p.out + r * p.out_stride + c;
+    if constexpr (kVec == 8) {
+      const float4 a = *reinterpret_cast<const float4*>(from), b = *reinterpret_cast<const float4*>(from + 4);
+      const __nv_bfloat162 two[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w), __floats2bfloat162_rn(b.x, b.y),
+                                     __floats2bfloat162_rn(b.z, b.w)};
+      *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(two);
+    } else {
+      *to = bf16_bits(*from);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------- host
@@ -763,7 +807,7 @@ int make_plan(const fsdp_cross_entropy_t& a, bool gradients, Plan* out) {
     p.e = take(p.piece * p.e_stride * 2);
     p.scaled = take(p.piece * p.h_stride * 2);
     if (p.pieces > 1) p.sum = take(a.vocab * p.h_stride * 4);
-    if (p.splits > 1) p.partial = take(p.splits * p.piece * p.h_stride * 4);
+    if (p.splits > 1) p.partial = take(p.splits * round_to(p.piece, 256) * p.h_stride * 4);
   }
   p.bytes = at;
   *out = p;
@@ -775,9 +819,13 @@ bool mappable(const void* p, int64_t rows, int64_t stride) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows < 2 || stride % 8 == 0);
 }
 
+bool f32_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t stride) {
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, rows, cols, stride, 32);
+}
+
 bool bf16_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t stride, int box_rows) {
   if (rows < 2) stride = round_to(cols, 8);  // not used
-  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows, cols, stride, box_rows);
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, cols, stride, box_rows);
 }
 
 // How many clusters of the kernel run at once (looked up once per device).
@@ -882,6 +930,7 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
   rows.cols = static_cast<int32_t>(a.cols);
   rows.vocab = static_cast<int32_t>(a.vocab);
   rows.scale = static_cast<float>(a.scale);
+  auto* sum = reinterpret_cast<float*>(at(plan.sum));  // several pieces: dweight's
   if (gradients) {
     rows.factor = reinterpret_cast<float*>(at(plan.factor));
     rows.e = reinterpret_cast<uint16_t*>(at(plan.e));
@@ -937,16 +986,21 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
     dh.b_mn = 1;
     dh.splits = plan.splits;
     dh.split_steps = plan.split_steps;
-    dh.result = plan.splits > 1 ? kPartial : kRows;
     dh.factor = rows.factor;
-    dh.wide = reinterpret_cast<float*>(at(plan.partial));
-    dh.wide_stride = plan.h_stride;
+    auto* partial = reinterpret_cast<float*>(at(plan.partial));
     ok = bf16_map(&dh.a, rows.e, n, a.vocab, plan.e_stride, 64) && bf16_map(&dh.b, weight, a.vocab, a.cols, weight_stride, 64);
-    if (mappable(dhidden, n, a.dhidden_stride)) {
-      ok = ok && bf16_map(&dh.out, dhidden, n, a.cols, a.dhidden_stride, 32);
+    if (plan.splits > 1) {
+      dh.result = kPartial;
+      dh.split_rows = static_cast<int32_t>(round_to(n, 256));
+      ok = ok && f32_map(&dh.out, partial, plan.splits * static_cast<int64_t>(dh.split_rows), a.cols, plan.h_stride);
     } else {
-      dh.rows = dhidden;
-      dh.rows_stride = a.dhidden_stride;
+      dh.result = kRows;
+      if (mappable(dhidden, n, a.dhidden_stride)) {
+        ok = ok && bf16_map(&dh.out, dhidden, n, a.cols, a.dhidden_stride, 32);
+      } else {
+        dh.rows = dhidden;
+        dh.rows_stride = a.dhidden_stride;
+      }
     }
     Product& dw = products.product[1];
     dw = Product{};
@@ -956,26 +1010,35 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
     dw.a_mn = dw.b_mn = 1;
     dw.splits = 1;
     dw.split_steps = steps_of(n);
-    dw.first = r0 == 0;
-    dw.result = plan.pieces == 1 ? kRows : r0 + n < a.rows ? kAdd : kLast;
-    dw.wide = reinterpret_cast<float*>(at(plan.sum));
-    dw.wide_stride = plan.h_stride;
     dw.a = dh.a;
     ok = ok && bf16_map(&dw.b, rows.scaled, n, a.cols, plan.h_stride, 64);
-    if (mappable(c.dweight, a.vocab, a.dweight_stride)) {
-      ok = ok && bf16_map(&dw.out, c.dweight, a.vocab, a.cols, a.dweight_stride, 32);
+    if (plan.pieces > 1) {
+      dw.result = r0 == 0 ? kSum : kAdd;
+      ok = ok && f32_map(&dw.out, sum, a.vocab, a.cols, plan.h_stride);
     } else {
-      dw.rows = c.dweight;
-      dw.rows_stride = a.dweight_stride;
+      dw.result = kRows;
+      if (mappable(c.dweight, a.vocab, a.dweight_stride)) {
+        ok = ok && bf16_map(&dw.out, c.dweight, a.vocab, a.cols, a.dweight_stride, 32);
+      } else {
+        dw.rows = c.dweight;
+        dw.rows_stride = a.dweight_stride;
+      }
     }
     if (!ok) return FSDP_ECUDA;
     if (int rc = plan.pair == 2 ? launch_products<2, false>(products, dev, st) : launch_products<1, false>(products, dev, st))
       return rc;
     if (plan.splits > 1) {
-      const JoinParams j{dh.wide, dh.wide_stride, dh.splits, n, a.cols, rows.factor, dhidden, a.dhidden_stride};
+      const JoinParams j{partial, plan.h_stride, dh.split_rows, dh.splits, n, a.cols, rows.factor, dhidden, a.dhidden_stride};
       const int64_t blocks = n * ((a.cols + 127) / 128);  // few: a product is cut only where its result has few tiles
       if (int rc = launch_after(ce_join, static_cast<int>(blocks), 1, 32 * kJoinGroups, 0, st, j)) return rc;
     }
+  }
+  if (gradients && plan.pieces > 1) {
+    const RoundParams p{sum, plan.h_stride, c.dweight, a.dweight_stride, a.vocab, a.cols};
+    const bool vectors = mappable(c.dweight, a.vocab, a.dweight_stride) && a.cols % 8 == 0;
+    const int64_t groups = a.vocab * (vectors ? a.cols / 8 : a.cols);
+    const int grid = static_cast<int>(std::min<int64_t>((groups + 255) / 256, 152 * 8));
+    return launch_after(vectors ? ce_round<8> : ce_round<1>, grid, 1, 256, 0, st, p);
   }
   return FSDP_OK;
 }

@@ -28,13 +28,13 @@ inline EncodeTiled encoder() {
   return fn;
 }
 
-// Boxes of box_rows x 64 elements of a rows x cols matrix of a two-byte type, 128-byte
+// Boxes of box_rows rows of 128 bytes of a rows x cols matrix whose elements have `size` bytes, 128-byte
 // swizzled in shared memory; outside the matrix they read zeros.
-inline bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows, int64_t cols, int64_t ld,
-                     int box_rows) {
+inline bool make_map(CUtensorMap* map, CUtensorMapDataType type, int size, const void* base, int64_t rows, int64_t cols,
+                     int64_t ld, int box_rows) {
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * size};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
   return encoder()(map, type, 2, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

@@ -1369,7 +1369,7 @@ int64_t carve(const NsJob& j, const NsPlan& plan, unsigned char* base, Buffers* 
 }
 
 bool make_map(CUtensorMap* map, const __half* base, int64_t rows, int64_t cols, int64_t ld) {
-  return fsdp::make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, rows, cols, ld, 64);
+  return fsdp::make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, rows, cols, ld, 64);
 }
 
 // How many clusters of the kernel run at once (looked up once per device).

@@ -131,6 +131,12 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, 
                "r"(y), "r"(src)
                : "memory");
 }
+// As tma_store, of fp32 values that are added to what the matrix holds.
+__device__ __forceinline__ void tma_add(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // At most kLeft of the thread's groups have yet to read shared memory.
 template <int kLeft>
