@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
 
 // ------------------------------------------------------------------ the rows
 
-constexpr int kRowThreads = 128;
+constexpr int kRowThreads = 128;  // of a block: for one row, or for four
 
 struct RowParams {
   const float2* stats;
@@ -555,10 +555,11 @@ struct RowParams {
 __device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-// Over the block, the same for all its threads.
-template <typename F>
-__device__ __forceinline__ float block_reduce(float v, float* shared, F f) {
+// Over the threads of a row (the block, or a warp of it), the same for all of them.
+template <int kLanes, typename F>
+__device__ __forceinline__ float row_reduce(float v, float* shared, F f) {
   for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if constexpr (kLanes == 32) return v;
   __syncthreads();  // the last use of `shared`
   if (threadIdx.x % 32 == 0) shared[threadIdx.x / 32] = v;
   __syncthreads();
@@ -568,15 +569,18 @@ __device__ __forceinline__ float block_reduce(float v, float* shared, F f) {
   return v;
 }
 
-// A block per row of the piece: its lse and loss from the spans' statistics; for the
-// gradients its factor, its target's element of E and its scaled row of H. Bound by HBM for many rows (8192 x
-// 768, vocabulary 50257: 11 us), by its chain of loads for few.
+// A row of the piece by kLanes threads: its lse and loss from the spans' statistics; for the
+// gradients its factor, its target's element of E and its scaled row of H. Bound by HBM for many rows, a warp each
+// (8192 x 768, vocabulary 50257: 11 us; by blocks 21), by its chain of loads for few, a block each (61 x 4096,
+// 32000: 8 us; by warps 13).
+template <int kLanes>
 __global__ void __launch_bounds__(kRowThreads) ce_rows(const __grid_constant__ RowParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ float shared[kRowThreads / 32];
-  const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x % kLanes;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRowThreads / kLanes) + threadIdx.x / kLanes;
+  if (row >= p.rows) return;  // a whole warp, or a whole block
   const auto add = [](float a, float b) { return a + b; };
   const auto larger = [](float a, float b) { return fmaxf(a, b); };
   const float2* stats = p.stats + row * p.spans;
@@ -585,24 +589,24 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows(const __grid_constant__ R
   const float score = has ? p.target_score[row] : NAN;
   const float g = there ? (has ? p.scale * (p.dloss ? p.dloss[row] : 1.0f) : NAN) : 0.0f;
   float most = -INFINITY, far = 0.0f, sum = 0.0f;
-  for (int64_t i = tid; i < p.spans; i += kRowThreads) {
+  for (int64_t i = tid; i < p.spans; i += kLanes) {
     const float2 s = stats[i];
     most = fmaxf(most, s.x);
     far = fmaxf(far, fabsf(s.x));
     sum += s.y;
   }
-  far = block_reduce(far, shared, larger);
+  far = row_reduce<kLanes>(far, shared, larger);
   float lse;
   if (!(far > kPlainRange)) {
-    lse = logf(block_reduce(sum, shared, add));
+    lse = logf(row_reduce<kLanes>(sum, shared, add));
   } else {
-    most = block_reduce(most, shared, larger);
+    most = row_reduce<kLanes>(most, shared, larger);
     sum = 0.0f;
-    for (int64_t i = tid; i < p.spans; i += kRowThreads) {
+    for (int64_t i = tid; i < p.spans; i += kLanes) {
       const float2 s = stats[i];
       sum += s.y == 0.0f ? 0.0f : s.y * expf(reference_of(s.x) - most);
     }
-    lse = most + logf(block_reduce(sum, shared, add));
+    lse = most + logf(row_reduce<kLanes>(sum, shared, add));
   }
   if (tid == 0) {
     p.loss[row] = there ? lse - score : 0.0f;
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows(const __grid_constant__ R
   if (plain) {
     if (tid == 0 && has) e[target] = rounded;
   } else {
-    for (int64_t v = tid; v < p.vocab; v += kRowThreads) {
+    for (int64_t v = tid; v < p.vocab; v += kLanes) {
       const float kept = bf16_value(e[v]);  // zeros stay: their span's factor may not be finite
       const float own = kept == 0.0f && lse == lse ? 0.0f : kept * expf(reference_of(stats[v / kSpan].x) - lse);
       e[v] = !there ? uint16_t(0) : v == target ? rounded : bf16_bits(own);
@@ -630,7 +634,7 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows(const __grid_constant__ R
   if (tid == 0) p.factor[row] = factor;
   const uint16_t* h = p.hidden + row * p.hidden_stride;
   uint16_t* scaled = p.scaled + row * p.scaled_stride;
-  for (int c = tid * 8; c < p.cols; c += kRowThreads * 8) {  // what lies behind the row's end is not used
+  for (int c = tid * 8; c < p.cols; c += kLanes * 8) {  // what lies behind the row's end is not used
     const uint4 v = *reinterpret_cast<const uint4*>(h + c);
     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
     uint32_t out[4];
@@ -972,8 +976,9 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
     if (!ok) return FSDP_ECUDA;
     if (int rc = plan.pair == 2 ? launch_products<2, true>(scores, dev, st) : launch_products<1, true>(scores, dev, st))
       return rc;
-    if (int rc = launch_after(ce_rows, static_cast<int>(n), 1, kRowThreads, 0, st, rows))
-      return rc;
+    const bool many = n >= 2048;
+    const int row_blocks = static_cast<int>(many ? (n + kRowThreads / 32 - 1) / (kRowThreads / 32) : n);
+    if (int rc = launch_after(many ? ce_rows<32> : ce_rows<kRowThreads>, row_blocks, 1, kRowThreads, 0, st, rows)) return rc;
     if (!gradients) continue;
 
     products.count = 2;

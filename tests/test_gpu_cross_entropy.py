@@ -107,7 +107,7 @@ def check(hidden, weight, targets, dloss, scale, loss, lse, dh, dw):
 
 
 SIZES = [(1, 1, 1), (1, 8, 2), (3, 7, 5), (2, 64, 129), (37, 64, 1000), (128, 128, 256), (129, 72, 257), (200, 769, 1009),
-         (300, 1030, 4097), (256, 4096, 640), (64, 96, 50257), (513, 2056, 700), (1000, 40, 130)]
+         (300, 1030, 4097), (256, 4096, 640), (64, 96, 50257), (513, 2056, 700), (1000, 40, 130), (2050, 24, 300)]
 
 
 @pytest.mark.parametrize("rows,cols,vocab", SIZES)
