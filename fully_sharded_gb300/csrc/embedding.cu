@@ -11,8 +11,8 @@
 // one that crosses chunks go to the workspace in fp32 and are added in order by a
 // last kernel. Every sum is fp32 in an order fixed by the tokens alone.
 // Where the table is not added to, zeros go to its other rows: to all of a small table during the sort,
-// by the SMs that have no part in it; to the rows that no token names (the sort leaves a
-// bit for each row that has one) of a large table, by blocks between those that add.
+// by the SMs that have no part in it; to the rows that no token names of a large table, by blocks between
+// those that add.
 #include "host_internal.h"
 #include "launch.h"
 #include "strided.h"
@@ -188,6 +188,85 @@ __device__ __forceinline__ void fill_zeros(const FillParams& f, int part, int pa
     fill_row(f.to + r * f.pitch, f.row_bytes, threadIdx.x % 32, 32);
 }
 
+// Up to 8192 rows: every row's place is counted, as the number of rows with a smaller token, or the same token before
+// it. A block finds the places of 64 rows, 8 by each warp, whose lanes share out the comparisons with all rows.
+// Bound by those, 2 instructions each; in fp32 (tokens below 2^24 are exact), because integer additions and all
+// comparisons run at half its rate (8192 rows 13 us by integers).
+constexpr int kRankRows = 8192, kRankTile = 64, kRankEach = 8, kRankThreads = 1024, kRankWarps = kRankThreads / 32;
+constexpr int64_t kRankVocab = (1 << 24) - 2;
+
+struct RankParams {
+  const void* tokens;
+  uint32_t *keys, *rows;
+  uint32_t* active;        // lists that embed_sum makes: their counts
+  int64_t vocab;
+  int32_t index_bits, n, tiles;
+  FillParams fill;
+};
+
+__device__ __forceinline__ uint32_t key_of(int64_t token, int64_t vocab) {
+  // tokens that are no row of the table are sorted behind the others
+  return static_cast<uint32_t>(token >= 0 && token < vocab ? token : vocab);
+}
+
+__global__ void __launch_bounds__(kRankThreads) embed_rank(const __grid_constant__ RankParams p) {
+  begin_after_previous();
+  if (static_cast<int>(blockIdx.x) >= p.tiles) {
+    fill_zeros(p.fill, blockIdx.x - p.tiles, gridDim.x - p.tiles);
+    return;
+  }
+  extern __shared__ float4 rank_shared[];  // the rows' keys, four to a vector
+  constexpr int kShares = kRankWarps * kRankEach / kRankTile;  // warps that share 8 rows
+  __shared__ float counts[kShares][kRankTile];
+  float* keys = reinterpret_cast<float*>(rank_shared);
+  if (blockIdx.x == 0 && threadIdx.x < 2) p.active[threadIdx.x] = 0;
+  const int vectors = (p.n + 3) / 4;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < 4 * vectors; i += kRankThreads)  // behind the last row: smaller than none
+    keys[i] = i < p.n ? static_cast<float>(key_of(index_at(p.tokens, p.index_bits, i), p.vocab)) : 3e38f;
+  __syncthreads();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, first = blockIdx.x * kRankTile;
+  const int group = warp / kShares * kRankEach, share = warp % kShares * 32 + lane;
+  float own[kRankEach], count[kRankEach] = {};
+#pragma unroll
+  for (int k = 0; k < kRankEach; ++k) own[k] = first + group + k < p.n ? keys[first + group + k] : 0.0f;
+  const auto compare = [&](int from, int to, float or_same) {
+#pragma unroll 2
+    for (int v = from + share; v < to; v += 32 * kShares) {
+      const float4 other = rank_shared[v];
+#pragma unroll
+      for (int k = 0; k < kRankEach; ++k) {  // bound - other, cut to [0, 1], is 1 where other is smaller and 0 elsewhere
+        const float bound = own[k] + or_same;
+        count[k] += __saturatef(bound - other.x);
+        count[k] += __saturatef(bound - other.y);
+        count[k] += __saturatef(bound - other.z);
+        count[k] += __saturatef(bound - other.w);
+      }
+    }
+  };
+  compare(0, first / 4, 1.0f);                                 // rows before the tile: the same token counts too
+  compare((first + kRankTile) / 4, vectors, 0.0f);             // rows behind it
+  for (int j = first + share; j < min(first + kRankTile, p.n); j += 32 * kShares) {
+    const float other = keys[j];
+#pragma unroll
+    for (int k = 0; k < kRankEach; ++k) count[k] += other < own[k] || (other == own[k] && j < first + group + k) ? 1.0f : 0.0f;
+  }
+#pragma unroll
+  for (int k = 0; k < kRankEach; ++k) {
+    const uint32_t sum = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(count[k]));
+    if (lane == 0) counts[warp % kShares][group + k] = static_cast<float>(sum);
+  }
+  __syncthreads();
+  const int row = first + static_cast<int>(threadIdx.x);
+  if (threadIdx.x >= kRankTile || row >= p.n) return;
+  float sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kShares; ++w) sum += counts[w][threadIdx.x];
+  const int place = static_cast<int>(sum);
+  p.keys[place] = static_cast<uint32_t>(keys[row]);
+  p.rows[place] = row;
+}
+
 // Up to 8 x 8192 rows are sorted by one cluster of up to eight blocks, which holds them in
 // registers and moves them through (distributed) shared memory. In a pass each warp ranks its rows by digit, 32 at a
 // time; the places follow from the counts of all digits, blocks and warps. Bound by its own latencies (cycles of a
@@ -200,17 +279,11 @@ constexpr int kClusterRows = kMaxCluster * kMaxRounds * kClusterThreads;
 struct ClusterSortParams {
   const void* tokens;
   uint32_t *keys, *rows;
-  uint32_t* active;        // lists that embed_sum makes: their counts
-  uint32_t* named;         // a bit for each row of the table that a token names (null: not needed)
+  uint32_t* active;        // as above
   int64_t vocab;
   int32_t index_bits, n, cluster, rounds, passes, digit;
   FillParams fill;
 };
-
-__device__ __forceinline__ uint32_t key_of(int64_t token, int64_t vocab) {
-  // tokens that are no row of the table are sorted behind the others
-  return static_cast<uint32_t>(token >= 0 && token < vocab ? token : vocab);
-}
 
 __device__ __forceinline__ void remote_store(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
@@ -262,8 +335,6 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
   const int digit_of = threadIdx.x;
   const bool has_digit = digit_of < bins;
   if (rank == 0 && threadIdx.x < 2) p.active[threadIdx.x] = 0;
-  if (p.named)
-    for (int64_t i = rank * kClusterThreads + threadIdx.x; i < (p.vocab + 31) / 32; i += p.cluster * kClusterThreads) p.named[i] = 0;
   const int mine = warp * 32 * p.rounds + lane;  // of the block's rows: mine, mine + 32, ...
   const int left = p.n - rank * each;
   uint32_t key[kMaxRounds], row[kMaxRounds];
@@ -360,7 +431,6 @@ __global__ void __launch_bounds__(kClusterThreads, 1) embed_sort(const __grid_co
     if (i >= left) continue;
     p.keys[rank * each + i] = key[k];
     p.rows[rank * each + i] = row[k];
-    if (p.named && key[k] < p.vocab && (i == 0 || items[i - 1].x != key[k])) atomicOr(&p.named[key[k] / 32], 1u << (key[k] % 32));
   }
 }
 
@@ -498,8 +568,7 @@ struct SumParams {
   // Runs that go on behind their first chunk, as (chunk, token): counts of the short and the long ones, then the
   // short ones from the front, the long ones (more than kShortRun chunks behind the first) from the end.
   uint32_t* active;
-  const uint32_t* named;        // as in the sort; null: the table needs no more zeros
-  int64_t zero_row_bytes;       // of the table's rows
+  int64_t zero_row_bytes;       // of the table's rows; 0: the table needs no more zeros
   int32_t zero_blocks, sum_blocks;
   float scale;
   bool accumulate;
@@ -513,11 +582,24 @@ __device__ __forceinline__ TTable* table_at(const SumParams& p, uint32_t token, 
 constexpr int kShortRun = 16;
 constexpr int kZeroRows = 8;  // rows of the table for each block that writes zeros
 
+// Zeros to the rows of its part that no token names, a warp for each row: whether the row is among the sorted
+// keys is found in steps of 32 lanes (16384 keys: 3).
 __device__ __forceinline__ void zero_unnamed(const SumParams& p, uint32_t part) {
-  for (int64_t v = static_cast<int64_t>(part) * kZeroRows, end = min(v + kZeroRows, p.vocab); v < end; ++v)
-    if (!(p.named[v / 32] >> (v % 32) & 1))
-      fill_row(static_cast<unsigned char*>(p.dtable) + v * p.dtable_stride * (p.zero_row_bytes / p.cols), p.zero_row_bytes,
-               threadIdx.x, blockDim.x);
+  const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
+  const int64_t end = min(static_cast<int64_t>(part + 1) * kZeroRows, p.vocab);
+  for (int64_t v = static_cast<int64_t>(part) * kZeroRows + threadIdx.x / 32; v < end; v += warps) {
+    int lo = 0, left = p.n;  // the first key that is not below v lies in [lo, lo + left]
+    while (left > 0) {
+      const int step = (left + 31) / 32;
+      const bool below = lane * step < left && p.keys[lo + lane * step] < v;
+      const int count = __popc(__ballot_sync(0xffffffffu, below));
+      if (count == 0) break;
+      left = min(count * step, left) - (count - 1) * step - 1;
+      lo += (count - 1) * step + 1;
+    }
+    if (lo < p.n && p.keys[lo] == v) continue;
+    fill_row(static_cast<unsigned char*>(p.dtable) + v * p.dtable_stride * (p.zero_row_bytes / p.cols), p.zero_row_bytes, lane, 32);
+  }
 }
 
 // kQ pieces of kVec columns for each thread. Bound by reading dout (HBM); kSumBatch rows, and the table's rows
@@ -544,10 +626,11 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum(const __grid_constant__
   const int i = threadIdx.x;
   if (i < p.chunk + 2) {
     const int at = first + i - 1;
-    const uint32_t key = at >= 0 && at < p.n ? p.keys[at] : none;
+    const bool there = at >= 0 && at < p.n, inside = i >= 1 && i <= p.chunk;
+    const uint32_t key = there ? p.keys[at] : none, row = there && inside ? p.rows[at] : 0;
     keys[i] = key;
-    token = i >= 1 && i <= p.chunk && key != none;
-    if (token) rows[i - 1] = p.rows[at];
+    token = inside && key != none;
+    if (inside) rows[i - 1] = row;
   }
   const int count = __syncthreads_count(token);  // rows with a token come first
   if (count == 0) return;
@@ -696,13 +779,24 @@ __global__ void __launch_bounds__(kJoinThreads) embed_join(const __grid_constant
     const int chunk = static_cast<int>(run[0]);
     const uint32_t token = run[1];
     const int64_t at = (chunk + 1 + static_cast<int64_t>(lane)) * p.chunk;
-    const int parts = __popc(__ballot_sync(0xffffffffu, lane < kShortRun && at < p.n && p.keys[at] == token));
     const int64_t col = ((item - index * p.join_tiles) * 32 + lane) * kVec;
+    // on their way together: the keys that tell how far the run goes, its first two parts and the table's row
+    const bool more = lane < kShortRun && at < p.n && p.keys[at] == token;
+    float sum[kVec] = {}, next[kVec] = {}, old[kVec] = {};
+    if (col < p.cols) {
+      const float* from = p.parts + (2 * static_cast<int64_t>(chunk) + 1) * p.part_stride + col;
+      load<kVec>(from, sum);
+      load<kVec>(from + p.part_stride, next);
+      if (p.accumulate) load<kVec>(table_at<TTable, kVec>(p, token, col), old);
+    }
+    const int parts = __popc(__ballot_sync(0xffffffffu, more));  // at least one
     if (col >= p.cols) continue;
-    float sum[kVec];
-    load<kVec>(p.parts + (2 * static_cast<int64_t>(chunk) + 1) * p.part_stride + col, sum);
-    add_parts<kVec>(p, chunk + 1, chunk + 1 + parts, col, sum);
-    add_to_table<TTable, kVec>(p, token, col, sum);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) sum[e] += next[e];
+    add_parts<kVec>(p, chunk + 2, chunk + 1 + parts, col, sum);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) old[e] += sum[e] * p.scale;
+    store<kVec>(table_at<TTable, kVec>(p, token, col), old);
   }
 }
 
@@ -717,12 +811,12 @@ bool vector_rows(const void* p, int64_t rows, int64_t stride, int size) {
 }
 
 struct Workspace {
-  int64_t keys[2], rows[2], counts, active, named, parts, bytes;
+  int64_t keys[2], rows[2], counts, active, parts, bytes;
   int64_t part_stride;
   int32_t chunk, chunks, blocks;
 };
 
-Workspace carve(int64_t rows, int64_t cols, int64_t vocab) {
+Workspace carve(int64_t rows, int64_t cols) {
   Workspace w{};
   int64_t at = 256;  // the caller's pointer may have any alignment
   const auto take = [&](int64_t bytes) {
@@ -743,7 +837,6 @@ Workspace carve(int64_t rows, int64_t cols, int64_t vocab) {
   }
   if (many) w.counts = take(static_cast<int64_t>(w.blocks) * kMaxBins * 4);
   w.active = take((static_cast<int64_t>(w.chunks) + 1) * 8);
-  w.named = take((vocab + 31) / 32 * 4);
   w.parts = take(2 * static_cast<int64_t>(w.chunks) * w.part_stride * 4);
   w.bytes = at;
   return w;
@@ -761,7 +854,7 @@ int run_sum(SumParams p, int sms, cudaStream_t st) {
   p.join_lanes = 1;
   while (p.join_lanes < 32 && p.join_lanes < groups) p.join_lanes *= 2;
   p.sum_blocks = p.chunks * p.tiles;
-  p.zero_blocks = p.named ? static_cast<int32_t>((p.vocab + kZeroRows - 1) / kZeroRows) : 0;
+  p.zero_blocks = p.zero_row_bytes ? static_cast<int32_t>((p.vocab + kZeroRows - 1) / kZeroRows) : 0;
   if (static_cast<int64_t>(p.sum_blocks) + p.zero_blocks > INT32_MAX) return FSDP_EINVAL;
   const auto kernel = p.accumulate ? embed_sum<T, TTable, kVec, kQ, true> : embed_sum<T, TTable, kVec, kQ, false>;
   if (int rc = launch_after(kernel, p.sum_blocks + p.zero_blocks, 1, threads, 0, st, p)) return rc;
@@ -777,6 +870,16 @@ int run_sum_as(const SumParams& p, bool vectors, int sms, cudaStream_t st) {
   return vectors ? run_sum<T, TTable, kVec>(p, sms, st) : run_sum<T, TTable, 1>(p, sms, st);
 }
 
+// Blocks that fill beside a sort: a vector for each thread, at most `most`.
+int fill_blocks(const FillParams& f, int most) {
+  return static_cast<int>(std::min<int64_t>((f.rows * f.row_bytes + 16383) / 16384, most));
+}
+
+int run_rank(RankParams p, int sms, cudaStream_t st) {
+  p.tiles = (p.n + kRankTile - 1) / kRankTile;
+  return launch_after(embed_rank, p.tiles + fill_blocks(p.fill, sms), 1, kRankThreads, (p.n + 3) / 4 * 16, st, p);
+}
+
 // The sort of up to kClusterRows rows; the other blocks fill. Two steps of 32 rows for each warp, then more blocks,
 // then more steps.
 int run_cluster_sort(ClusterSortParams p, int sms, cudaStream_t st) {
@@ -787,11 +890,7 @@ int run_cluster_sort(ClusterSortParams p, int sms, cudaStream_t st) {
   const int smem = (2 * p.rounds * kClusterThreads + (kClusterWarps + 2) * bins) * 4;
   constexpr int kMost = (2 * kMaxRounds * kClusterThreads + (kClusterWarps + 2) * kMaxBins) * 4;
   if (cudaFuncSetAttribute(embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost) != cudaSuccess) return FSDP_ECUDA;
-  int grid = p.cluster;
-  if (p.fill.row_bytes) {
-    const int64_t blocks = (p.fill.rows * p.fill.row_bytes + 16383) / 16384;  // a vector for each thread
-    grid += static_cast<int>(std::min<int64_t>(round_to(blocks, p.cluster), sms / p.cluster * p.cluster));
-  }
+  const int grid = p.cluster + static_cast<int>(round_to(fill_blocks(p.fill, (sms / p.cluster - 1) * p.cluster), p.cluster));
   return launch_after(embed_sort, grid, p.cluster, kClusterThreads, smem, st, p);
 }
 
@@ -836,7 +935,7 @@ extern "C" int fsdp_embedding(const fsdp_embedding_t* a, const void* tokens, con
 extern "C" int fsdp_embedding_backward_workspace(int64_t rows, int64_t cols, int64_t vocab, int64_t* bytes_out) {
   if (!bytes_out || rows < 0 || rows > kMaxRows || cols < 1 || cols > kMaxCols || vocab < 1 || vocab > kMaxVocab)
     return FSDP_EINVAL;
-  *bytes_out = carve(rows, cols, vocab).bytes;
+  *bytes_out = carve(rows, cols).bytes;
   return FSDP_OK;
 }
 
@@ -862,19 +961,19 @@ extern "C" int fsdp_embedding_backward(const fsdp_embedding_backward_t* a, const
   Device dev;
   if (int rc = device_facts(&dev)) return rc;
   // A table beyond what is filled during a sort (about 8 us) leaves its zeros to the blocks between the sums' (see
-  // the top): 16384 x 4096, 32000 rows 104 -> 77 us.
-  const bool later = fill.row_bytes && a->rows > 0 && a->rows <= kClusterRows && a->vocab * a->cols * ts > (int64_t(32) << 20) &&
-                     a->cols * ts >= 256;
+  // the top): 16384 x 4096, 32000 rows 104 -> 88 us. Not narrow rows, which take a warp each there.
+  const bool sorted_at_once = a->rows <= kClusterRows;
+  const bool later = fill.row_bytes && a->rows > 0 && a->cols * ts >= 256 &&
+                     (!sorted_at_once || a->vocab * a->cols * ts > (int64_t(32) << 20));
   if (later) fill.row_bytes = 0;
-  if (fill.row_bytes && (a->rows == 0 || a->rows > kClusterRows)) {
+  if (fill.row_bytes && (a->rows == 0 || !sorted_at_once)) {
     if (int rc = launch_after(embed_fill, 2 * dev.sms, 1, kClusterThreads, 0, cs, fill)) return rc;
   }
   if (a->rows == 0) return FSDP_OK;
 
-  const Workspace w = carve(a->rows, a->cols, a->vocab);
+  const Workspace w = carve(a->rows, a->cols);
   auto* base = reinterpret_cast<unsigned char*>(round_to(reinterpret_cast<intptr_t>(workspace), 256) - 256);
-  uint32_t *keys[2], *rows[2], *active = reinterpret_cast<uint32_t*>(base + w.active),
-           *named = later ? reinterpret_cast<uint32_t*>(base + w.named) : nullptr;
+  uint32_t *keys[2], *rows[2], *active = reinterpret_cast<uint32_t*>(base + w.active);
   for (int k = 0; k < 2; ++k) {
     keys[k] = reinterpret_cast<uint32_t*>(base + w.keys[k]);
     rows[k] = reinterpret_cast<uint32_t*>(base + w.rows[k]);
@@ -884,8 +983,10 @@ extern "C" int fsdp_embedding_backward(const fsdp_embedding_backward_t* a, const
   const int passes = (bits + 8) / 9, digit = (bits + passes - 1) / passes;
   const int32_t n = static_cast<int32_t>(a->rows);
   int now = 0;
-  if (a->rows <= kClusterRows) {
-    const ClusterSortParams p{tokens, keys[0], rows[0], active, named, a->vocab, 8 * is, n, 0, 0, passes, digit, fill};
+  if (a->rows <= kRankRows && a->vocab <= kRankVocab) {
+    if (int rc = run_rank(RankParams{tokens, keys[0], rows[0], active, a->vocab, 8 * is, n, 0, fill}, dev.sms, cs)) return rc;
+  } else if (sorted_at_once) {
+    const ClusterSortParams p{tokens, keys[0], rows[0], active, a->vocab, 8 * is, n, 0, 0, passes, digit, fill};
     if (int rc = run_cluster_sort(p, dev.sms, cs)) return rc;
   } else {
     for (int k = 0; k < passes; ++k, now ^= 1) {
@@ -897,8 +998,8 @@ extern "C" int fsdp_embedding_backward(const fsdp_embedding_backward_t* a, const
     }
   }
   const SumParams p{keys[now], rows[now], n, w.chunk, w.chunks, 0, 0, 0, a->vocab, a->cols, dout, a->dout_stride, dtable,
-                    a->dtable_stride, reinterpret_cast<float*>(base + w.parts), w.part_stride, active, named,
-                    a->cols * ts, 0, 0, static_cast<float>(a->scale), a->accumulate != 0};
+                    a->dtable_stride, reinterpret_cast<float*>(base + w.parts), w.part_stride, active,
+                    later ? a->cols * ts : 0, 0, 0, static_cast<float>(a->scale), a->accumulate != 0};
   const bool vectors = a->cols % 8 == 0 && vector_rows(dout, a->rows, a->dout_stride, es) &&
                        vector_rows(dtable, a->vocab, a->dtable_stride, ts);
   const bool in32 = a->dtype == FSDP_DTYPE_F32, table32 = a->table_dtype == FSDP_DTYPE_F32;

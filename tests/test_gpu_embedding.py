@@ -103,7 +103,7 @@ def check_gradient(tokens, dout, dtable, scale, accumulate):
 
 
 GRADIENT = [(1, 1, 1), (1, 64, 5), (31, 8, 3), (32, 24, 1), (33, 769, 100), (700, 40, 1000), (64, 1000, 2), (5000, 48, 300),
-            (3000, 17, 70000), (40000, 8, 50257), (20000, 128, 3), (70000, 3, 500)]
+            (3000, 17, 70000), (40000, 8, 50257), (20000, 128, 3), (70000, 3, 500), (300, 2, (1 << 24) + 10)]
 
 
 @pytest.mark.parametrize("rows,cols,vocab", GRADIENT)
