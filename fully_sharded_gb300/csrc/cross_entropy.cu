@@ -11,8 +11,8 @@
 // so that normalising takes a factor per row (in the epilogue of the first product, in a scaled
 // copy of H for the second) and no pass over E, and the targets' -1 is one element of each
 // row: E_rt = exp(lse_r) expm1(x_rt - lse_r). bf16's exponents hold exp(x) for |x| up to 87; a row
-// with |lse| or the largest logit of some 128 columns beyond 60 (or not finite) goes by the
-// general form instead: its E is kept relative to each such span's own maximum and
+// with |lse| or the largest logit of some 128 columns beyond 40 (or not finite; s_r H_r then keeps 20 decades
+// above bf16's smallest values for g_r) goes by the general form instead: its E is kept relative to each such span's own maximum and
 // rescaled to exp(x - lse) once lse is known.
 //
 // Launches for each piece: the scores (product and statistics), the rows (lse, loss,
@@ -36,7 +36,7 @@ namespace {
 using namespace tc;
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
-constexpr float kPlainRange = 60.0f;              // of the logits of a row whose E is exp(x) itself
+constexpr float kPlainRange = 40.0f;              // of the logits of a row whose E is exp(x) itself
 
 constexpr int kTileK = 64;
 constexpr int kN = 256;                           // columns of a tile
@@ -818,9 +818,9 @@ int make_plan(const fsdp_cross_entropy_t& a, bool gradients, Plan* out) {
   return FSDP_OK;
 }
 
-// Whether a tensor map can describe these bf16 rows.
+// Whether a tensor map can describe these bf16 rows (its strides are below 2^40 bytes).
 bool mappable(const void* p, int64_t rows, int64_t stride) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows < 2 || stride % 8 == 0);
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows < 2 || (stride % 8 == 0 && stride < (int64_t(1) << 39)));
 }
 
 bool f32_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t stride) {

@@ -772,7 +772,7 @@ int fsdp_dropout(const fsdp_dropout_t *args, const void *x, const void *residual
  * columns). The logits are not kept: the gradients take exp(x) rounded to bf16, of `piece` rows at a time
  * (0: as many as keep that below 1 GiB, at least 256; at most 2^20), and dweight's sum over
  * several pieces is fp32 in the workspace. Rows whose |lse|, or the largest logit of some 128
- * columns of the vocabulary, is beyond 60 give the same results a little slower. rows = 0 sets
+ * columns of the vocabulary, is beyond 40 give the same results a little slower. rows = 0 sets
  * dweight to zero. EINVAL: cols > 2^24, vocab > 2^30, rows > 2^40, piece < 0; a scale that is not
  * finite as a float; as above. */
 typedef struct {

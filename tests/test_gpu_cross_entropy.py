@@ -10,7 +10,7 @@ Tolerances, element by element, from the operations' roundings:
   - an element of G is rounded to bf16 (2^-8 of itself), shares its row's factor, which carries the rounding of the
     target's element (2^-8), and is off by what its exponent is; in dweight the factor's product with hidden is
     rounded too (2^-8);
-  - exponentials below 2^-126 (of x, where |lse| <= 60, else relative to their row's or span's largest) count as zero, and
+  - exponentials below 2^-126 (of x, where |lse| <= 40, else relative to their row's or span's largest) count as zero, and
     bf16's subnormal steps are smaller than that: at most 2^-125 in all, over exp(lse) in the former case;
   - the gradients' sums are cut off as the logits' are, in segments of 4096; partial sums add a few 2^-24; each
     output is rounded once (2^-8 of itself).
@@ -93,7 +93,7 @@ def check(hidden, weight, targets, dloss, scale, loss, lse, dh, dw):
     hot = torch.zeros_like(p).scatter_(1, at, 1.0)
     g = f * (p - hot)
     off = g.abs() * (2 * HALF + HALF ** 2 + 2.0 ** -20) + f.abs() * p * 2 * (dx + d_lse[:, None])
-    off = off + f.abs() * 2.0 ** -125 * torch.where(want_lse.abs() <= 60, torch.exp(-want_lse), 1.0)[:, None].clamp(min=1)
+    off = off + f.abs() * 2.0 ** -125 * torch.where(want_lse.abs() <= 40.01, torch.exp(-want_lse), 1.0)[:, None].clamp(min=1)
     cut = (256 + vocab / 4096 + 8) * 2.0 ** -22
     aw, ah = w.abs(), h.abs()
     want = g @ w
@@ -180,7 +180,18 @@ def test_rows_without_a_target_may_hold_anything(bad):
     assert bool(torch.isfinite(dw).all()) and bool((dh[targets < 0] == 0).all()) and bool((loss[targets < 0] == 0).all())
 
 
-@pytest.mark.parametrize("size,shift", [(40.0, 0.0), (200.0, 0.0), (1.0, 90.0), (1.0, -90.0), (1.0, -200.0), (1.0, 59.0), (1.0, -62.0)])
+def test_small_factors_of_rows_with_large_logits():
+    """Factors down to 1e-18 keep their rows' gradients: what is scaled stays above bf16's smallest normal values."""
+    hidden, weight, targets, _ = inputs(140, 64, 700, without=0)
+    hidden = torch.cat([hidden, torch.ones(140, 8, device="cuda", dtype=BF16)], 1)
+    weight = torch.cat([weight, torch.full((700, 8), 4.5, device="cuda", dtype=BF16)], 1)
+    dloss = torch.logspace(0, -18, 140, device="cuda")
+    check(hidden, weight, targets, dloss, 1.0, *call(hidden, weight, targets, dloss))
+    one = torch.full_like(dloss, 1e-18)
+    check(hidden, weight, targets, one, 1.0, *call(hidden, weight, targets, one))
+
+
+@pytest.mark.parametrize("size,shift", [(40.0, 0.0), (200.0, 0.0), (1.0, 90.0), (1.0, -90.0), (1.0, -200.0), (1.0, 59.0), (1.0, -62.0), (1.0, 39.0), (1.0, -46.0), (6.0, 0.0)])
 def test_logits_far_from_zero(size, shift):
     """Rows beyond the range of the plain exponentials: wide ones, and ones that are shifted as a whole."""
     hidden, weight, targets, dloss = inputs(140, 64, 700)
