@@ -657,8 +657,23 @@ struct CopyParams {
   int64_t rows, cols;
 };
 
+// Eight two-byte elements from byte `off` (even) of two vectors on.
+__device__ __forceinline__ uint4 eight_from(const uint4& a, const uint4& b, uint32_t off) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (off & 8)
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+  if (off & 4)
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+  if (off & 2)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Rows off 16-byte alignment into rows that tensor maps can describe, 8 elements a thread: the (one or two)
-// aligned vectors that hold them, shifted. Bound by HBM.
+// aligned vectors that hold them, shifted. Bound by HBM (65536 x 1795: 70 us, 6.7 TB/s).
 __global__ void __launch_bounds__(256) ce_copy(const __grid_constant__ CopyParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -672,17 +687,37 @@ __global__ void __launch_bounds__(256) ce_copy(const __grid_constant__ CopyParam
     const uint4 a = *reinterpret_cast<const uint4*>(base);
     uint4 b = make_uint4(0, 0, 0, 0);
     if (off && base + 16 < end) b = *reinterpret_cast<const uint4*>(base + 16);
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    if (off & 8)
+    *reinterpret_cast<uint4*>(p.to + r * p.to_stride + c) = eight_from(a, b, off);
+  }
+}
+
+// The other way: rows at 16-byte boundaries to where they belong, an aligned vector of the result a thread,
+// single elements at the rows' ends.
+__global__ void __launch_bounds__(256) ce_place(const __grid_constant__ CopyParams p) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const uint32_t per_row = static_cast<uint32_t>((p.cols + 14) / 8);
+  const int64_t vectors = p.rows * per_row;
+  for (int64_t v = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; v < vectors; v += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = vectors >> 31 ? v / per_row : static_cast<uint32_t>(v) / per_row;
+    uint16_t* to = p.to + r * p.to_stride;
+    const int64_t c = (v - r * per_row) * 8 - static_cast<int64_t>(reinterpret_cast<uintptr_t>(to) >> 1 & 7);  // the vector's first column
+    if (c >= p.cols) continue;
+    const int64_t first = c >= 0 ? c / 8 : -1;  // the row's vector that holds it
+    const uint32_t off = static_cast<uint32_t>(c - 8 * first) * 2;
+    const uint4* from = reinterpret_cast<const uint4*>(p.from + r * p.from_stride);
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    if (first >= 0) a = from[first];
+    if (off && 8 * (first + 1) < p.cols) b = from[first + 1];
+    const uint4 w = eight_from(a, b, off);
+    if (c >= 0 && c + 8 <= p.cols) {
+      *reinterpret_cast<uint4*>(to + c) = w;
+    } else {
+      const uint32_t words[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
-    if (off & 4)
-#pragma unroll
-      for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
-    if (off & 2)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
-    *reinterpret_cast<uint4*>(p.to + r * p.to_stride + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int e = 0; e < 8; ++e)
+        if (c + e >= 0 && c + e < p.cols) to[c + e] = static_cast<uint16_t>(words[e / 2] >> (e & 1) * 16);
+    }
   }
 }
 
@@ -771,7 +806,7 @@ struct Plan {
   int64_t piece, pieces;   // rows of a piece
   int64_t spans, e_stride, h_stride;
   int pair, splits, split_steps;
-  int64_t stats, target_score, factor, e, scaled, hidden, weight, sum, partial, bytes;  // offsets
+  int64_t stats, target_score, factor, e, scaled, hidden, weight, sum, aside, partial, bytes;  // offsets (0: not there)
 };
 
 int make_plan(const fsdp_cross_entropy_t& a, bool gradients, Plan* out) {
@@ -810,7 +845,10 @@ int make_plan(const fsdp_cross_entropy_t& a, bool gradients, Plan* out) {
     p.factor = take(p.piece * 4);
     p.e = take(p.piece * p.e_stride * 2);
     p.scaled = take(p.piece * p.h_stride * 2);
-    if (p.pieces > 1) p.sum = take(a.vocab * p.h_stride * 4);
+    if (p.pieces > 1)
+      p.sum = take(a.vocab * p.h_stride * 4);
+    else if (a.cols % 8 != 0 && a.rows <= 2048)  // see run()
+      p.aside = take(a.vocab * p.h_stride * 2);
     if (p.splits > 1) p.partial = take(p.splits * round_to(p.piece, 256) * p.h_stride * 4);
   }
   p.bytes = at;
@@ -935,6 +973,11 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
   rows.vocab = static_cast<int32_t>(a.vocab);
   rows.scale = static_cast<float>(a.scale);
   auto* sum = reinterpret_cast<float*>(at(plan.sum));  // several pieces: dweight's
+  // Few rows: dweight's rows off 16-byte boundaries go there by a pass of their own (73 x 1795, 65536 348 us; stored by
+  // the products in words 403; 1123 x 741, 43094 237 and 243), where odd widths make that certain enough for the workspace
+  // to have room. With many the products hide their stores (4000 x 769, 50257: 752 and 725).
+  auto* aside = plan.aside ? reinterpret_cast<uint16_t*>(at(plan.aside)) : nullptr;
+  bool put_aside = false;
   if (gradients) {
     rows.factor = reinterpret_cast<float*>(at(plan.factor));
     rows.e = reinterpret_cast<uint16_t*>(at(plan.e));
@@ -1024,6 +1067,9 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
       dw.result = kRows;
       if (mappable(c.dweight, a.vocab, a.dweight_stride)) {
         ok = ok && bf16_map(&dw.out, c.dweight, a.vocab, a.cols, a.dweight_stride, 32);
+      } else if (aside) {
+        ok = ok && bf16_map(&dw.out, aside, a.vocab, a.cols, plan.h_stride, 32);
+        put_aside = true;
       } else {
         dw.rows = c.dweight;
         dw.rows_stride = a.dweight_stride;
@@ -1037,6 +1083,11 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
       const int64_t blocks = n * ((a.cols + 127) / 128);  // few: a product is cut only where its result has few tiles
       if (int rc = launch_after(ce_join, static_cast<int>(blocks), 1, 32 * kJoinGroups, 0, st, j)) return rc;
     }
+  }
+  if (put_aside) {
+    const CopyParams p{aside, plan.h_stride, c.dweight, a.dweight_stride, a.vocab, a.cols};
+    const int64_t blocks = (a.vocab * ((a.cols + 14) / 8) + 255) / 256;
+    return launch_after(ce_place, static_cast<int>(std::min<int64_t>(blocks, 152 * 8)), 1, 256, 0, st, p);
   }
   if (gradients && plan.pieces > 1) {
     const RoundParams p{sum, plan.h_stride, c.dweight, a.dweight_stride, a.vocab, a.cols};

@@ -137,11 +137,12 @@ def test_pieces(rows, piece):
     check(hidden, weight, targets, dloss, 2.0, *call(hidden, weight, targets, dloss, 2.0, piece=piece))
 
 
-@pytest.mark.parametrize("offset,pad", [(1, 0), (0, 1), (3, 5), (8, 8), (4, 0)])
-def test_strides_and_alignment(offset, pad):
-    hidden, weight, targets, dloss = inputs(150, 136, 300)
-    h, w = place(hidden, 136 + pad, offset), place(weight, 136 + pad, offset)
-    loss, lse, dh, dw = call(h, w, targets, dloss, 1.0, strides=(136 + pad, 136 + pad), offsets=(offset, offset))
+@pytest.mark.parametrize("offset,pad", [(1, 0), (0, 1), (3, 5), (8, 8), (4, 0), (7, 2)])
+@pytest.mark.parametrize("cols", [136, 131, 5])
+def test_strides_and_alignment(cols, offset, pad):
+    hidden, weight, targets, dloss = inputs(150, cols, 300)
+    h, w = place(hidden, cols + pad, offset), place(weight, cols + pad, offset)
+    loss, lse, dh, dw = call(h, w, targets, dloss, 1.0, strides=(cols + pad, cols + pad), offsets=(offset, offset))
     check(hidden, weight, targets, dloss, 1.0, loss, lse, dh, dw)
     plain = call(hidden, weight, targets, dloss, 1.0)
     for a, b in zip((loss, lse, dh, dw), plain):
