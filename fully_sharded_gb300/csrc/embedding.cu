@@ -4,8 +4,8 @@
 //   out_r = scale table[token_r] + addend_r
 //   dtable_v (+)= scale sum over the rows r with token_r = v of dout_r
 //
-// Gradient. The rows are put in the order of their tokens (a stable radix sort of row
-// indexes by token, so equal tokens keep the rows' order), and the sorted list is cut into chunks of
+// Gradient. The rows are put in the order of their tokens (places counted, or a stable radix sort of row
+// indexes by token: equal tokens keep the rows' order), and the sorted list is cut into chunks of
 // 16 or 32 rows. A block adds the rows of a chunk, run by run of equal tokens, for
 // its columns: a run that lies in the chunk goes to the table at once, the parts of
 // one that crosses chunks go to the workspace in fp32 and are added in order by a
@@ -961,7 +961,7 @@ extern "C" int fsdp_embedding_backward(const fsdp_embedding_backward_t* a, const
   Device dev;
   if (int rc = device_facts(&dev)) return rc;
   // A table beyond what is filled during a sort (about 8 us) leaves its zeros to the blocks between the sums' (see
-  // the top): 16384 x 4096, 32000 rows 104 -> 88 us. Not narrow rows, which take a warp each there.
+  // the top): 16384 x 4096, 32000 rows 104 -> 84 us. Not narrow rows, which take a warp each there.
   const bool sorted_at_once = a->rows <= kClusterRows;
   const bool later = fill.row_bytes && a->rows > 0 && a->cols * ts >= 256 &&
                      (!sorted_at_once || a->vocab * a->cols * ts > (int64_t(32) << 20));

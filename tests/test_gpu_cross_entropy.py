@@ -107,7 +107,7 @@ def check(hidden, weight, targets, dloss, scale, loss, lse, dh, dw):
 
 
 SIZES = [(1, 1, 1), (1, 8, 2), (3, 7, 5), (2, 64, 129), (37, 64, 1000), (128, 128, 256), (129, 72, 257), (200, 769, 1009),
-         (300, 1030, 4097), (256, 4096, 640), (64, 96, 50257), (513, 2056, 700), (1000, 40, 130), (2050, 24, 300)]
+         (300, 1030, 4097), (256, 4096, 640), (64, 96, 50257), (513, 2056, 700), (1000, 40, 130), (2050, 24, 300), (2050, 21, 300)]
 
 
 @pytest.mark.parametrize("rows,cols,vocab", SIZES)
@@ -129,12 +129,12 @@ def test_losses_alone(rows, cols, vocab):
     assert torch.equal(loss, with_gradients[0]) and torch.equal(lse, with_gradients[1])
 
 
-@pytest.mark.parametrize("rows,piece", [(700, 256), (513, 512), (300, 100), (600, 1), (257, 256)])
-def test_pieces(rows, piece):
-    if piece == 1:
-        rows = 9
-    hidden, weight, targets, dloss = inputs(rows, 200, 515)
-    check(hidden, weight, targets, dloss, 2.0, *call(hidden, weight, targets, dloss, 2.0, piece=piece))
+@pytest.mark.parametrize("rows,piece", [(700, 256), (513, 512), (300, 100), (9, 1), (257, 256)])
+@pytest.mark.parametrize("cols,pad,offset", [(200, 0, 0), (131, 0, 0), (64, 3, 1)])
+def test_pieces(rows, piece, cols, pad, offset):
+    hidden, weight, targets, dloss = inputs(rows, cols, 515)
+    check(hidden, weight, targets, dloss, 2.0, *call(hidden, weight, targets, dloss, 2.0, piece=piece, strides=(cols + pad, cols + pad),
+                                                     offsets=(offset, offset)))
 
 
 @pytest.mark.parametrize("offset,pad", [(1, 0), (0, 1), (3, 5), (8, 8), (4, 0), (7, 2)])

@@ -14,8 +14,6 @@ import math
 
 import pytest
 
-import gpu_util as gu
-
 pytestmark = pytest.mark.gpu
 
 fs = pytest.importorskip("fully_sharded_gb300")
