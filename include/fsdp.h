@@ -769,7 +769,7 @@ int fsdp_dropout(const fsdp_dropout_t *args, const void *x, const void *residual
  * (its dhidden row is zero); its lse is that of its logits. One with a target from vocab on gives NaN.
  * dweight may lie anywhere in a rank's bf16 gradient row; dhidden may be hidden in place.
  * The products take bf16 operands on the tensor cores and sum in fp32 (logits in segments of 1024
- * columns). The logits are not kept: the gradients take exp(x) rounded to bf16, of `piece` rows at a time
+ * columns, 256 up to 128 rows). The logits are not kept: the gradients take exp(x) rounded to bf16, of `piece` rows at a time
  * (0: as many as keep that below 1 GiB, at least 256; at most 2^20), and dweight's sum over
  * several pieces is fp32 in the workspace. Rows whose |lse|, or the largest logit of some 128
  * columns of the vocabulary, is beyond 40 give the same results a little slower. rows = 0 sets

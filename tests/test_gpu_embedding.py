@@ -193,12 +193,13 @@ def test_gradient_is_the_lookups():
     assert abs(float(left - right)) <= 16 * U * float(size)
 
 
-def test_on_a_stream_and_in_a_graph():
+@pytest.mark.parametrize("rows", [500, 20000, 70000])
+def test_on_a_stream_and_in_a_graph(rows):
     gen = torch.Generator(device="cuda").manual_seed(7)
-    tokens = torch.randint(0, 50, (500,), generator=gen, device="cuda")
-    dout, dtable = rand(gen, 500, 64, dtype=BF16), torch.empty(50, 64, dtype=BF16, device="cuda")
-    ws = torch.empty(fs.fsdp_embedding_backward_workspace(500, 64, 50), dtype=torch.uint8, device="cuda")
-    out = torch.empty(500, 64, dtype=BF16, device="cuda")
+    tokens = torch.randint(0, 50, (rows,), generator=gen, device="cuda")
+    dout, dtable = rand(gen, rows, 64, dtype=BF16), torch.empty(50, 64, dtype=BF16, device="cuda")
+    ws = torch.empty(fs.fsdp_embedding_backward_workspace(rows, 64, 50), dtype=torch.uint8, device="cuda")
+    out = torch.empty(rows, 64, dtype=BF16, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         fs.fsdp_embedding_backward(tokens, dout, dtable, ws)
