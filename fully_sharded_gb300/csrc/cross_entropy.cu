@@ -861,6 +861,9 @@ bool mappable(const void* p, int64_t rows, int64_t stride) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows < 2 || (stride % 8 == 0 && stride < (int64_t(1) << 39)));
 }
 
+// Whether tiled stores can write them: whole vectors of 16 bytes, for a store fills a row's last one up.
+bool storable(const void* p, int64_t rows, int64_t cols, int64_t stride) { return cols % 8 == 0 && mappable(p, rows, stride); }
+
 bool f32_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t stride) {
   return make_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, rows, cols, stride, 32);
 }
@@ -1040,14 +1043,15 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
     dh.split_steps = plan.split_steps;
     dh.factor = rows.factor;
     auto* partial = reinterpret_cast<float*>(at(plan.partial));
-    ok = bf16_map(&dh.a, rows.e, n, a.vocab, plan.e_stride, 64) && bf16_map(&dh.b, weight, a.vocab, a.cols, weight_stride, 64);
+    ok = bf16_map(&dh.a, rows.e, n, a.vocab, plan.e_stride, 64);
+    dh.b = s.b;
     if (plan.splits > 1) {
       dh.result = kPartial;
       dh.split_rows = static_cast<int32_t>(round_to(n, 256));
       ok = ok && f32_map(&dh.out, partial, plan.splits * static_cast<int64_t>(dh.split_rows), a.cols, plan.h_stride);
     } else {
       dh.result = kRows;
-      if (mappable(dhidden, n, a.dhidden_stride)) {
+      if (storable(dhidden, n, a.cols, a.dhidden_stride)) {
         ok = ok && bf16_map(&dh.out, dhidden, n, a.cols, a.dhidden_stride, 32);
       } else {
         dh.rows = dhidden;
@@ -1069,7 +1073,7 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
       ok = ok && f32_map(&dw.out, sum, a.vocab, a.cols, plan.h_stride);
     } else {
       dw.result = kRows;
-      if (mappable(c.dweight, a.vocab, a.dweight_stride)) {
+      if (storable(c.dweight, a.vocab, a.cols, a.dweight_stride)) {
         ok = ok && bf16_map(&dw.out, c.dweight, a.vocab, a.cols, a.dweight_stride, 32);
       } else if (aside) {
         ok = ok && bf16_map(&dw.out, aside, a.vocab, a.cols, plan.h_stride, 32);
@@ -1095,7 +1099,7 @@ int run(const fsdp_cross_entropy_t& a, const Plan& plan, const Call& c, void* wo
   }
   if (gradients && plan.pieces > 1) {
     const RoundParams p{sum, plan.h_stride, c.dweight, a.dweight_stride, a.vocab, a.cols};
-    const bool vectors = mappable(c.dweight, a.vocab, a.dweight_stride) && a.cols % 8 == 0;
+    const bool vectors = storable(c.dweight, a.vocab, a.cols, a.dweight_stride);
     const int64_t groups = a.vocab * (vectors ? a.cols / 8 : a.cols);
     const int grid = static_cast<int>(std::min<int64_t>((groups + 255) / 256, 152 * 8));
     return launch_after(vectors ? ce_round<8> : ce_round<1>, grid, 1, 256, 0, st, p);

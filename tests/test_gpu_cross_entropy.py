@@ -137,7 +137,7 @@ def test_pieces(rows, piece, cols, pad, offset):
                                                      offsets=(offset, offset)))
 
 
-@pytest.mark.parametrize("offset,pad", [(1, 0), (0, 1), (3, 5), (8, 8), (4, 0), (7, 2)])
+@pytest.mark.parametrize("offset,pad", [(1, 0), (0, 1), (3, 5), (8, 8), (4, 0), (7, 2), (0, 5), (8, 3)])
 @pytest.mark.parametrize("cols", [136, 131, 5])
 def test_strides_and_alignment(cols, offset, pad):
     hidden, weight, targets, dloss = inputs(150, cols, 300)
