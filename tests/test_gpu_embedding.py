@@ -40,7 +40,7 @@ def untouched(whole, view):
     return bool((rest == 7.0).all())
 
 
-SIZES = [(1, 1, 1), (1, 4096, 10), (5, 8, 3), (33, 769, 100), (300, 24, 1000), (70, 1000, 17), (2, 5000, 7), (1000, 33, 4)]
+SIZES = [(1, 1, 1), (1, 4096, 10), (9000, 1024, 40), (5000, 520, 9), (5, 8, 3), (33, 769, 100), (300, 24, 1000), (70, 1000, 17), (2, 5000, 7), (1000, 33, 4)]
 
 
 @pytest.mark.parametrize("rows,cols,vocab", SIZES)
