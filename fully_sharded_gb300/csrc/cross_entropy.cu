@@ -608,8 +608,10 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows(const __grid_constant__ R
     }
     lse = most + logf(row_reduce<kLanes>(sum, shared, add));
   }
+  // A confident row's lse may round to less than its target's logit: its loss is then 0, and p - 1 not above 0.
+  const float behind = score - lse > 0.0f ? 0.0f : score - lse;
   if (tid == 0) {
-    p.loss[row] = there ? lse - score : 0.0f;
+    p.loss[row] = there ? 0.0f - behind : 0.0f;
     if (p.lse) p.lse[row] = lse;
   }
   if (!p.keep) return;
@@ -618,7 +620,7 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows(const __grid_constant__ R
   // The target's element is the largest of the row's: its rounding to bf16 goes into the row's factor
   // (relative to which the others, rounded too, are then off by one more rounding).
   float factor = g;
-  const float exact = has ? (plain ? expf(lse) : 1.0f) * expm1f(score - lse) : 0.0f;
+  const float exact = has ? (plain ? expf(lse) : 1.0f) * expm1f(behind) : 0.0f;
   const uint16_t rounded = bf16_bits(exact);
   if (plain) factor *= expf(-lse);
   if (bf16_value(rounded) != 0.0f) factor *= exact / bf16_value(rounded);

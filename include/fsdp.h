@@ -764,7 +764,7 @@ int fsdp_dropout(const fsdp_dropout_t *args, const void *x, const void *residual
  *   G_rv = g_r (exp(x_rv - lse_r) - [v = target_r]),  g_r = scale dloss_r  (dloss null: scale)
  *   dhidden = G weight,  dweight = G^T hidden
  * hidden, weight, dhidden and dweight are bf16; dloss, loss and lse (may be null) fp32 [rows].
- * dhidden and dweight are both given or both null (losses alone; dloss is null then). A row with
+ * A loss is never below 0. dhidden and dweight are both given or both null (losses alone; dloss is null then). A row with
  * a target below 0 has loss 0 and takes no part in the gradients, whatever its hidden row holds
  * (its dhidden row is zero); its lse is that of its logits. One with a target from vocab on gives NaN.
  * dweight may lie anywhere in a rank's bf16 gradient row; dhidden may be hidden in place.
