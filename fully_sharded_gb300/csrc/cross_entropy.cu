@@ -6,14 +6,14 @@
 //
 // The logits x exist only as tiles in tensor memory and registers. What is kept of a
 // piece of rows is E = exp(x) in bf16, which the gradients' products read as it
-// is: with s_r = g_r exp(-lse_r),
+// is: with S_r = exp(lse_r) and s_r = g_r / S_r,
 //   dH_r = s_r sum_v E_rv W_v,   dW_v = sum_r E_rv (s_r H_r),
 // so that normalising takes a factor per row (in the epilogue of the first product, in a scaled
 // copy of H for the second) and no pass over E, and the targets' -1 is one element of each
-// row: E_rt = exp(lse_r) expm1(x_rt - lse_r). bf16's exponents hold exp(x) for |x| up to 87; a row
+// row: E_rt = S_r expm1(x_rt - lse_r). bf16's exponents hold exp(x) for |x| up to 87; a row
 // with |lse| or the largest logit of some 128 columns beyond 40 (or not finite; s_r H_r then keeps 20 decades
-// above bf16's smallest values for g_r) goes by the general form instead: its E is kept relative to each such span's own maximum and
-// rescaled to exp(x - lse) once lse is known.
+// above bf16's smallest values for g_r) goes by the general form instead: such a span's E is kept in units of a power of
+// two near its largest, and brought to units of one near S_r once that is known, which rounds nothing again.
 //
 // Launches for each piece: the scores (product and statistics), the rows (lse, loss,
 // targets, scaled H), the gradients' two products together.
@@ -92,7 +92,7 @@ struct Params {
   int32_t index_bits;      // of the targets: 32 or 64
   bool keep;               // E is kept
   const void* targets;
-  float2* stats;           // [row][span]: largest logit, sum of exp(x - reference)
+  float2* stats;           // [row][span]: largest logit, sum of exp(x) in its unit
   int64_t spans;
   float* target_score;
   unsigned int* status;
@@ -102,12 +102,12 @@ __device__ __forceinline__ int64_t index_at(const void* p, int bits, int64_t i) 
   return bits == 64 ? static_cast<const int64_t*>(p)[i] : static_cast<const int32_t*>(p)[i];
 }
 
-// The reference of a span's exponentials: none where exp(x) itself can be kept.
-__device__ __forceinline__ float reference_of(float most) {
-  return !(fabsf(most) > kPlainRange) || most == -INFINITY ? 0.0f : most;
-}
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
-constexpr float kLog2e = 1.44269504088896341f;
+// The unit of a span's exponentials, as a power of two: 1 where exp(x) itself can be kept.
+__device__ __forceinline__ float unit_of(float most) {
+  return !(fabsf(most) > kPlainRange) || most == -INFINITY ? 0.0f : rintf(most * kLog2e);
+}
 
 // 2^x to 2^-22 of itself; results below 2^-126 are zero.
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -492,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
           for (int k = 0; k < 4; ++k) top[k] = max_of(top[k], x[c + 2 * k], x[c + 2 * k + 1]);
         const float most = max_of(max_of(top[0], top[1], top[2]), max_of(top[3], x[kSpan - 4], x[kSpan - 3]),
                                   fmaxf(x[kSpan - 2], x[kSpan - 1]));
-        const float shift = reference_of(most) * kLog2e;
-        const Two slope(kLog2e, kLog2e), offset(-shift, -shift);
+        const float unit = unit_of(most);
+        const Two slope(kLog2e, kLog2e), offset(-unit, -unit);
         Two sums[2] = {Two(0.0f, 0.0f), Two(0.0f, 0.0f)};
 #pragma unroll
         for (int c = 0; c < kSpan; c += 2) {
@@ -555,6 +555,11 @@ struct RowParams {
 __device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
+// From one power of two to another, as far as a float's exponents go (a NaN counts as very small).
+__device__ __forceinline__ int between(float from, float to) {
+  return static_cast<int>(fminf(fmaxf(from - to, -300.0f), 300.0f));
+}
+
 // Over the threads of a row (the block, or a warp of it), the same for all of them.
 template <int kLanes, typename F>
 __device__ __forceinline__ float row_reduce(float v, float* shared, F f) {
@@ -596,20 +601,23 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows(const __grid_constant__ R
     sum += s.y;
   }
   far = row_reduce<kLanes>(far, shared, larger);
-  float lse;
+  float unit = 0.0f;  // of the sum
   if (!(far > kPlainRange)) {
-    lse = logf(row_reduce<kLanes>(sum, shared, add));
+    sum = row_reduce<kLanes>(sum, shared, add);
   } else {
-    most = row_reduce<kLanes>(most, shared, larger);
+    unit = unit_of(row_reduce<kLanes>(most, shared, larger));
     sum = 0.0f;
     for (int64_t i = tid; i < p.spans; i += kLanes) {
       const float2 s = stats[i];
-      sum += s.y == 0.0f ? 0.0f : s.y * expf(reference_of(s.x) - most);
+      sum += ldexpf(s.y, between(unit_of(s.x), unit));
     }
-    lse = most + logf(row_reduce<kLanes>(sum, shared, add));
+    sum = row_reduce<kLanes>(sum, shared, add);
   }
-  // A confident row's lse may round to less than its target's logit: its loss is then 0, and p - 1 not above 0.
-  const float behind = score - lse > 0.0f ? 0.0f : score - lse;
+  const float log_sum = logf(sum), lse = fmaf(unit, kLn2, log_sum);
+  // x_t - lse, in the sum's unit if it has one. A confident row's lse may round to less than its target's logit: its
+  // loss is then 0, and p - 1 not above 0.
+  float behind = (unit == 0.0f ? score : fmaf(score, kLog2e, -unit) * kLn2) - log_sum;
+  if (behind > 0.0f) behind = 0.0f;
   if (tid == 0) {
     p.loss[row] = there ? 0.0f - behind : 0.0f;
     if (p.lse) p.lse[row] = lse;
@@ -617,20 +625,39 @@ __global__ void __launch_bounds__(kRowThreads) ce_rows(const __grid_constant__ R
   if (!p.keep) return;
   uint16_t* e = p.e + row * p.e_stride;
   const bool plain = !(far > kPlainRange) && fabsf(lse) <= kPlainRange;
+  if (!plain && sum > 0.0f && sum < INFINITY) {  // E in a unit near the sum
+    const int more = ilogbf(sum);
+    unit += static_cast<float>(more);
+    sum = ldexpf(sum, -more);
+  }
   // The target's element is the largest of the row's: its rounding to bf16 goes into the row's factor
   // (relative to which the others, rounded too, are then off by one more rounding).
-  float factor = g;
-  const float exact = has ? (plain ? expf(lse) : 1.0f) * expm1f(behind) : 0.0f;
+  const float exact = has ? sum * expm1f(behind) : 0.0f;
   const uint16_t rounded = bf16_bits(exact);
-  if (plain) factor *= expf(-lse);
+  float factor = g == 0.0f ? 0.0f : g / sum;
   if (bf16_value(rounded) != 0.0f) factor *= exact / bf16_value(rounded);
   if (plain) {
     if (tid == 0 && has) e[target] = rounded;
   } else {
-    for (int64_t v = tid; v < p.vocab; v += kLanes) {
-      const float kept = bf16_value(e[v]);  // zeros stay: their span's factor may not be finite
-      const float own = kept == 0.0f && lse == lse ? 0.0f : kept * expf(reference_of(stats[v / kSpan].x) - lse);
-      e[v] = !there ? uint16_t(0) : v == target ? rounded : bf16_bits(own);
+    for (int64_t v = tid * 8; v < p.vocab; v += kLanes * 8) {  // whole vectors: E's rows are whole lines
+      const int by = between(unit_of(stats[v / kSpan].x), unit);
+      const bool own = has && target >= v && target < v + 8;
+      if (there && by == 0 && !own) continue;
+      uint4* at = reinterpret_cast<uint4*>(e + v);
+      const uint4 kept = *at;
+      const uint32_t in[4] = {kept.x, kept.y, kept.z, kept.w};
+      uint32_t out[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t two[2] = {in[k] & 0xffffu, in[k] >> 16};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          two[h] = there ? bf16_bits(ldexpf(bf16_value(static_cast<uint16_t>(two[h])), by)) : 0u;
+          if (own && target == v + 2 * k + h) two[h] = rounded;
+        }
+        out[k] = two[0] | two[1] << 16;
+      }
+      *at = make_uint4(out[0], out[1], out[2], out[3]);
     }
   }
   if (tid == 0) p.factor[row] = factor;

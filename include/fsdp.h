@@ -772,8 +772,10 @@ int fsdp_dropout(const fsdp_dropout_t *args, const void *x, const void *residual
  * columns, 256 up to 128 rows). The logits are not kept: the gradients take exp(x) rounded to bf16, of `piece` rows at a time
  * (0: as many as keep that below 1 GiB, at least 256; at most 2^20), and dweight's sum over
  * several pieces is fp32 in the workspace. Rows whose |lse|, or the largest logit of some 128
- * columns of the vocabulary, is beyond 40 give the same results a little slower. rows = 0 sets
- * dweight to zero. EINVAL: cols > 2^24, vocab > 2^30, rows > 2^40, piece < 0; a scale that is not
+ * columns of the vocabulary, is beyond 40 (all of them where the logits are not centred) take one more pass over
+ * what is kept, which rounds nothing again: 8192 of them through a 50257 x 768 head take 1.5 ms in place
+ * of 1.2, 4096 through 32000 x 4096 2.06 ms in place of 1.92, 64 through 50257 x 768 0.14 to 0.17 ms in place
+ * of 0.06; losses alone take no longer. rows = 0 sets dweight to zero. EINVAL: cols > 2^24, vocab > 2^30, rows > 2^40, piece < 0; a scale that is not
  * finite as a float; as above. */
 typedef struct {
   int64_t rows;

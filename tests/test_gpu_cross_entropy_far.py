@@ -42,3 +42,33 @@ def test_no_loss_is_below_zero(rows, others, scale):
     assert bool((loss >= 0).all()) and bool((loss.double() <= off).all())
     assert bool(((lse.double() - logit).abs() <= off).all())
     assert bool((dh[:, 0] <= 0).all()) and bool((dh[:, 0].double().abs() <= off * (1 + 2 * HALF)).all())
+
+
+@pytest.mark.parametrize("rows", [1, 200, 2100])
+@pytest.mark.parametrize("shift", [-88.0, -50.0, 0.0, 44.0, 96.0])
+def test_exponentials_are_rounded_once(rows, shift):
+    """Entries of the vocabulary that are the same have the same gradient, in whatever span of columns they lie: what is kept
+    of a row is exp(x) rounded once, although spans have units of their own. In fp32 two such exponentials differ by at most
+    2^-19 of themselves (2^-22 each by the instruction, 2^-19.5 by the rounding of an argument below 64), so their roundings
+    to bf16 differ where a boundary, at least 2^-8 from the next, lies between: for 2^-11 of the pairs, with room 2^-9, and by one
+    step, 2 h for h = 2^-8, which the results' own rounding may make 4 h."""
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    half, row = 128 * 100, rows // 2
+    weight = torch.randn(half, 16, generator=gen, device="cuda") * 0.3
+    weight[:, :8] = shift / 8
+    weight = torch.cat([weight, weight])
+    weight[half::128, 8:] = 0.05 * torch.arange(100, device="cuda")[:, None]  # the spans' largest: 0 to 40 above the others
+    hidden = torch.randn(rows, 16, generator=gen, device="cuda") * 0.1
+    hidden[row] = 1
+    hidden, weight = hidden.to(BF16), weight.to(BF16)
+    dloss = torch.zeros(rows, device="cuda")
+    dloss[row] = 1
+    targets = torch.full((rows,), half, device="cuda")
+    _, _, _, dw = call(hidden, weight, targets, dloss)
+    first, second = dw[:half], dw[half:]
+    pairs = torch.ones(half, dtype=torch.bool, device="cuda")
+    pairs[::128] = False
+    first, second = first[pairs, 0].double(), second[pairs, 0].double()
+    assert bool((first > 0).all())
+    assert float((first != second).double().mean()) <= 2.0 ** -9
+    assert bool(((first - second).abs() <= 4 * HALF * first).all())
