@@ -38,11 +38,11 @@ struct Strided {
     return p == o.p && size == o.size && rows == o.rows && cols == o.cols && pitch() == o.pitch();
   }
   // True when some byte belongs to both. Column slices of one buffer (equal
-  // pitch, columns apart) do not overlap although their spans do.
+  // pitch, or a single row beside a matrix; columns apart) do not overlap although their spans do.
   bool overlaps(const Strided& o) const {
     if (rows < 1 || o.rows < 1 || hi() <= o.lo() || o.hi() <= lo()) return false;
-    const int64_t s = pitch();
-    if (s == 0 || s != o.pitch()) return true;
+    const int64_t s = std::max(pitch(), o.pitch());
+    if (s == 0 || (pitch() && o.pitch() && pitch() != o.pitch())) return true;
     const int64_t d = static_cast<int64_t>((o.lo() - lo()) % static_cast<uintptr_t>(s));
     const int64_t at = o.lo() >= lo() ? d : (s - static_cast<int64_t>((lo() - o.lo()) % static_cast<uintptr_t>(s))) % s;
     return !(at >= cols * size && at + o.cols * o.size <= s);
