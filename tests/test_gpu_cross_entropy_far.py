@@ -72,3 +72,54 @@ def test_exponentials_are_rounded_once(rows, shift):
     assert bool((first > 0).all())
     assert float((first != second).double().mean()) <= 2.0 ** -9
     assert bool(((first - second).abs() <= 4 * HALF * first).all())
+
+
+def far_inputs(rows, cols, vocab, shifts):
+    """Rows whose logits are all shifted by one of `shifts`, in turn."""
+    hidden, weight, targets, dloss = inputs(rows, cols, vocab)
+    by = torch.tensor(shifts, device="cuda")[torch.arange(rows, device="cuda") % len(shifts)]
+    hidden = torch.cat([hidden, (by / 8)[:, None].expand(rows, 8).to(BF16)], 1)
+    weight = torch.cat([weight, torch.ones(vocab, 8, device="cuda", dtype=BF16)], 1)
+    return hidden, weight, targets, dloss
+
+
+@pytest.mark.parametrize("rows", [140, 2050])
+@pytest.mark.parametrize("shifts", [(-80.0,), (64.0,), (0.0, 90.0, -90.0), (-39.0, -41.0, 39.0, 41.0), (-128.0, 240.0)])
+@pytest.mark.parametrize("vocab,index", [(700, torch.int64), (4097, torch.int32)])
+def test_rows_far_from_zero(rows, shifts, vocab, index):
+    hidden, weight, targets, dloss = far_inputs(rows, 64, vocab, shifts)
+    targets = targets.to(index)
+    check(hidden, weight, targets, dloss, 1.0, *call(hidden, weight, targets, dloss))
+    for piece in (128, 1000):
+        check(hidden, weight, targets, dloss, 1.0, *call(hidden, weight, targets, dloss, piece=piece))
+
+
+@pytest.mark.parametrize("rows", [140, 2050])
+def test_wide_rows(rows):
+    """Logits spread over some hundreds, so that spans of the vocabulary have units of their own."""
+    hidden, weight, targets, dloss = inputs(rows, 64, 1000)
+    weight = (weight.float() * torch.linspace(1, 60, 1000, device="cuda")[:, None]).to(BF16)
+    check(hidden, weight, targets, dloss, 1.0, *call(hidden, weight, targets, dloss))
+
+
+@pytest.mark.parametrize("rows", [140, 2050])
+@pytest.mark.parametrize("shift", [0.0, 70.0])
+def test_bad_rows_among_rows_far_from_zero(rows, shift):
+    hidden, weight, targets, _ = far_inputs(rows, 64, 700, (shift, -70.0))
+    targets = targets.clamp(min=0)
+    hidden[9, 3] = float("nan")       # a row with a target: loud, and alone
+    targets[17], targets[18] = 700, 1 << 40
+    hidden[20, 5], targets[20] = float("nan"), -1   # one without: nothing
+    hidden[21, 5], targets[21] = float("inf"), -100
+    loss, lse, dh, dw = call(hidden, weight, targets)
+    loud = [9, 17, 18]
+    assert torch.isnan(loss).nonzero()[:, 0].tolist() == loud and torch.isnan(dh).any(1).nonzero()[:, 0].tolist() == loud
+    assert bool(torch.isnan(dh[loud]).all()) and bool(torch.isnan(dw).all())
+    assert bool((dh[[20, 21]] == 0).all()) and bool((loss[[20, 21]] == 0).all())
+    targets[loud] = -1
+    hidden[[9, 20, 21]] = 0
+    loss2, lse, dh2, dw2 = call(hidden, weight, targets)
+    check(hidden, weight, targets, None, 1.0, loss2, lse, dh2, dw2)
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    rest[loud] = False
+    assert torch.equal(loss[rest], loss2[rest]) and torch.equal(dh[rest], dh2[rest])
