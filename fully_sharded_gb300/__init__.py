@@ -933,7 +933,8 @@ def fsdp_dropout(x, out, p: float, seed: int, offset: int = 0, residual=None, co
 
 
 def fsdp_cross_entropy_workspace(rows: int, cols: int, vocab: int, gradients: bool = True, piece: int = 0) -> int:
-    """Bytes of workspace that fsdp_cross_entropy needs (host only)."""
+    """Bytes of workspace that fsdp_cross_entropy needs (host only); room for a copy of the weight among them, which is
+    made where it lies off 16 bytes."""
     n = _c_i64(0)
     a = CrossEntropyArgs(rows, cols, vocab, cols, cols, cols, cols, piece, FSDP_DTYPE_I64, 1.0)
     _check("fsdp_cross_entropy_workspace",
@@ -945,8 +946,9 @@ def fsdp_cross_entropy(hidden, weight, targets, loss, workspace, lse=None, dhidd
                        scale: float = 1.0, dloss=None, piece: int = 0, stream=None):
     """Softmax cross entropy of hidden @ weight.T against targets: loss (and lse) fp32 [rows]; with dhidden and dweight
     also the gradients of scale * sum(dloss * loss) (dloss None: ones). hidden, weight and their gradients are
-    bfloat16; a row with a negative target has loss 0 and no part in the gradients. The logits are
-    never stored; `piece` rows are worked on at a time (0: chosen; as given to the workspace's size)."""
+    bfloat16; a row with a negative target has loss 0 and no part in the gradients. The logits are never stored in
+    fp32; for the gradients exp of `piece` rows' logits at a time is kept in the workspace in bf16 (0: chosen, 1 GiB
+    of them or 256 rows; as given to the workspace's size)."""
     torch = _torch()
     shape = _shape2(hidden, "hidden")
     rows, cols = shape

@@ -15,6 +15,12 @@
 // above bf16's smallest values for g_r) goes by the general form instead: such a span's E is kept in units of a power of
 // two near its largest, and brought to units of one near S_r once that is known, which rounds nothing again.
 //
+// Fewer bits than fp32, each for the tensor cores' sake: E and s_r H_r are rounded to bf16 (a product's operands have one
+// type, and the other ones are bf16 parameters; wider operands halve the rate and double E's bytes); sums are cut off
+// at each addition in tensor memory (hence the segments); exp(x) is one instruction on a rounded x log2(e). Together with the
+// results' own rounding the gradients are within 1.9e-3 to 2.3e-3 of 64 bits (1.65e-3 is that rounding alone), losses and lse
+// within 4e-7 to 7e-7.
+//
 // Launches for each piece: the scores (product and statistics), the rows (lse, loss,
 // targets, scaled H), the gradients' two products together.
 #include "host_internal.h"
@@ -320,8 +326,9 @@ __global__ void __launch_bounds__(kThreads, 1) ce_product(const __grid_constant_
     stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  // Held while this grid waits for the previous one, which is safe: with its 220 KB a block shares its SM
-  // with no other block that has tensor memory, and the next launch starts after this barrier.
+  // Held while this grid waits for the previous one, which is safe: that grid's blocks have their own columns
+  // before they let this one start (and so does this one, below), so none of them waits for these; with 209 KB of
+  // shared memory or more no second block of such products is on the SM.
   if (warp == 1) tmem_alloc<kPair>(smem_addr(&tmem_slot), T::kTmemCols);
   fence_before();
   __syncthreads();

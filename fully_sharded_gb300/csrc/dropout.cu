@@ -106,8 +106,9 @@ __device__ __forceinline__ void drop_singly(const DropoutParams& p, int64_t g, u
 }
 
 // kVector: every group of 8 elements lies in one row, at 16-byte boundaries (the last one of one long row may be
-// short). Bound by HBM there: 16384 x 4096 bf16 with the residual 58 us, 6.9 TB/s; ten rounds for 8 elements are a
-// third of the instructions that the memory leaves room for.
+// short). Bound by HBM there: 16384 x 4096 bf16 with the residual 60 us, 6.7 TB/s (without it 54 us; rows 4104
+// apart 61); ten rounds for 8 elements are a third of the instructions that the memory leaves room for. Else
+// one element after another, bound by their loads and stores: the same matrix 2 bytes off a boundary 168 us.
 template <typename T, bool kVector>
 __global__ void __launch_bounds__(kThreads) dropout_rows(const __grid_constant__ DropoutParams p) {
   asm volatile("griddepcontrol.launch_dependents;");
