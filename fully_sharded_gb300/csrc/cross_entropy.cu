@@ -957,7 +957,7 @@ int launch_products(Params& p, const Device& dev, cudaStream_t stream) {
     p.fewer = clusters - p.product[0].tiles % clusters;
     // As many as take as long as one of the first product's: a tile takes its steps or, with few, its epilogue and
     // store, about as long as 6 steps (61 x 4096, vocabulary 32000: by the steps alone a few SMs had most of the
-    // one-step tiles, 130 us, now 75).
+    // one-step tiles, the launch took 130 us, now 75).
     p.extra = (2 * p.product[0].split_steps / std::max(6, p.product[1].split_steps) + 1) / 2;
   }
   return launch_after(ce_product<kPair, kIsScores>, clusters * kPair, kPair, kThreads, T::kSmemBytes, stream, p);

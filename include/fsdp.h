@@ -520,7 +520,8 @@ int fsdp_account(double P, double U, int32_t N, int32_t F, int32_t prefetch,
  * orthogonalises every matrix's update. (The FSDP pages have no counterpart.)
  *
  * Matrices are row-major with a row stride in elements (>= the row's length;
- * any value for a single row). A workspace is device memory of the caller, of
+ * any value for a single row). Bytes beside a row in the 16-byte units that hold its ends may be
+ * read, without effect; they are never written. A workspace is device memory of the caller, of
  * any alignment, at least as large as the call's ..._workspace function says
  * for the same arguments; it holds nothing between calls, and calls whose
  * work overlaps on the GPU need workspaces of their own. */
@@ -775,8 +776,7 @@ int fsdp_dropout(const fsdp_dropout_t *args, const void *x, const void *residual
  * for dweight. Together with the results' own rounding the gradients are within 0.0023 of their norm. Factors g_r are 0
  * or between 1e-18 and 1e18 (beyond, a row's gradients may be cut to zero or infinite).
  * The workspace always has room for a copy of the weight and of a piece's hidden rows (2 vocab cols bytes and more, with
- * cols rounded up to 64, for losses alone too), made where one lies off 16 bytes. Bytes beside a row of hidden or weight in the same
- * 16-byte units may be read; they are never written and have no effect. Rows whose |lse|, or the largest logit of some 128
+ * cols rounded up to 64, for losses alone too), made where one lies off 16 bytes. Rows whose |lse|, or the largest logit of some 128
  * columns of the vocabulary, is beyond 40 (all of them where the logits are not centred) take one more pass over
  * what is kept, which rounds nothing again: 8192 of them through a 50257 x 768 head take 1.5 ms in place
  * of 1.2, 4096 through 32000 x 4096 2.06 ms in place of 1.92, 64 through 50257 x 768 0.14 to 0.17 ms in place
