@@ -765,23 +765,25 @@ int fsdp_dropout(const fsdp_dropout_t *args, const void *x, const void *residual
  *   G_rv = g_r (exp(x_rv - lse_r) - [v = target_r]),  g_r = scale dloss_r  (dloss null: scale)
  *   dhidden = G weight,  dweight = G^T hidden
  * hidden, weight, dhidden and dweight are bf16; dloss, loss and lse (may be null) fp32 [rows].
- * A loss is never below 0. dhidden and dweight are both given or both null (losses alone; dloss is null then). A row with
- * a target below 0 has loss 0 and takes no part in the gradients, whatever its hidden row holds
- * (its dhidden row is zero); its lse is that of its logits. One with a target from vocab on gives NaN.
- * dweight may lie anywhere in a rank's bf16 gradient row; dhidden may be hidden in place.
- * The products take bf16 operands on the tensor cores and sum in fp32 (logits in segments of 1024
- * columns, 256 up to 128 rows). The fp32 logits are not stored: losses alone keep nothing of them, the gradients
- * exp(x) rounded to bf16 in the workspace, of `piece` rows at a time (0: as many as keep that below 1 GiB, at least 256; at most
- * 2^20); dweight's sum over several pieces is fp32 in the workspace. hidden's rows times their factors are rounded to bf16
- * for dweight. Together with the results' own rounding the gradients are within 0.0023 of their norm. Factors g_r are 0
- * or between 1e-18 and 1e18 (beyond, a row's gradients may be cut to zero or infinite).
- * The workspace always has room for a copy of the weight and of a piece's hidden rows (2 vocab cols bytes and more, with
- * cols rounded up to 64, for losses alone too), made where one lies off 16 bytes. Rows whose |lse|, or the largest logit of some 128
- * columns of the vocabulary, is beyond 40 (all of them where the logits are not centred) take one more pass over
- * what is kept, which rounds nothing again: 8192 of them through a 50257 x 768 head take 1.5 ms in place
- * of 1.2, 4096 through 32000 x 4096 2.06 ms in place of 1.92, 64 through 50257 x 768 0.14 to 0.17 ms in place
- * of 0.06; losses alone take no longer. rows = 0 sets dweight to zero. EINVAL: cols > 2^24, vocab > 2^30, rows > 2^40, piece < 0; a scale that is not
- * finite as a float; as above. */
+ * A loss is never below 0. dhidden and dweight are both given or both null (losses alone; dloss is
+ * null then). A row with a target below 0 has loss 0 and takes no part in the gradients, whatever
+ * its hidden row holds (its dhidden row is zero); its lse is that of its logits. One with a target
+ * from vocab on gives NaN. dweight may lie anywhere in a rank's bf16 gradient row; dhidden may be
+ * hidden in place. The products take bf16 operands on the tensor cores and sum in fp32 (logits in
+ * segments of 1024 columns, 256 up to 128 rows). The fp32 logits are not stored: losses alone keep
+ * nothing of them, the gradients exp(x) rounded to bf16 in the workspace, of `piece` rows at a time
+ * (0: as many as keep that below 1 GiB, at least 256; at most 2^20); dweight's sum over several
+ * pieces is fp32 in the workspace. hidden's rows times their factors are rounded to bf16 for
+ * dweight. Together with the results' own rounding the gradients are within 0.0023 of their norm.
+ * Factors g_r are 0 or between 1e-18 and 1e18 (beyond, a row's gradients may be cut to zero or
+ * infinite). The workspace always has room for a copy of the weight and of a piece's hidden rows (2
+ * vocab cols bytes and more, with cols rounded up to 64, for losses alone too), made where one lies
+ * off 16 bytes. Rows whose |lse|, or the largest logit of some 128 columns of the vocabulary, is
+ * beyond 40 (all of them where the logits are not centred) take one more pass over what is kept,
+ * which rounds nothing again: 8192 of them through a 50257 x 768 head take 1.5 ms in place of 1.2,
+ * 4096 through 32000 x 4096 2.06 ms in place of 1.92, 64 through 50257 x 768 0.14 to 0.17 ms in
+ * place of 0.06; losses alone take no longer. rows = 0 sets dweight to zero. EINVAL: cols > 2^24,
+ * vocab > 2^30, rows > 2^40, piece < 0; a scale that is not finite as a float; as above. */
 typedef struct {
   int64_t rows;
   int64_t cols;
