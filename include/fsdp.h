@@ -774,7 +774,7 @@ int fsdp_dropout(const fsdp_dropout_t *args, const void *x, const void *residual
  * nothing of them, the gradients exp(x) rounded to bf16 in the workspace, of `piece` rows at a time
  * (0: as many as keep that below 1 GiB, at least 256; at most 2^20); dweight's sum over several
  * pieces is fp32 in the workspace. hidden's rows times their factors are rounded to bf16 for
- * dweight. Together with the results' own rounding the gradients are within 0.0023 of their norm.
+ * dweight. Together with the results' own rounding the gradients are typically within 0.0023 of their norm.
  * Factors g_r are 0 or between 1e-18 and 1e18 (beyond, a row's gradients may be cut to zero or
  * infinite). The workspace always has room for a copy of the weight and of a piece's hidden rows (2
  * vocab cols bytes and more, with cols rounded up to 64, for losses alone too), made where one lies
